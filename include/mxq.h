@@ -502,6 +502,171 @@ mxq_status mxq_grouped_gemm_noalloc(const void* a_q, const void* a_s, const void
                                     const int64_t* group_offsets, int32_t G, int64_t M_total,
                                     int64_t N, int64_t K, void* y, mxq_stream_t stream);
 
+/*
+ * ---- Operators around the experts' products --------------------------------
+ *
+ * What a mixture-of-experts block does before, between and after the GEMMs of
+ * this library, in training and in serving: layer norm, routing to experts,
+ * rows into expert order (which gives mxq_grouped_gemm its rows and offsets)
+ * and back, and clipping by the norm over all gradients.  Tensors are BF16 or FP32
+ * (mxq_dtype); arithmetic, statistics and sums are in FP32 or more and a result
+ * is rounded once.  Matrices are row-major with unit stride along a row and a row
+ * stride (ld) in elements; rows may start at any multiple of the element
+ * size (16-byte aligned rows of a multiple of 16 bytes run fastest).  Outputs
+ * must not overlap inputs unless a call says so.  Results are the same on
+ * every call (no floating-point atomics).  Errors: MXQ_ERR_INVALID_ARG,
+ * MXQ_ERR_UNSUPPORTED_SHAPE (a size past the stated limit; rows and slots are
+ * limited to 2^31 - 4096, elements of a row to 2^23), MXQ_ERR_UNSUPPORTED_DEVICE,
+ * MXQ_ERR_CUDA.
+ */
+typedef enum {
+    MXQ_BF16 = 0,
+    MXQ_F32 = 1
+} mxq_dtype;
+
+typedef enum {
+    MXQ_SCORE_SOFTMAX = 0,   /* s = softmax of the token's logits */
+    MXQ_SCORE_SIGMOID = 1    /* s = 1 / (1 + exp(-x)) of each logit */
+} mxq_route_score;
+
+typedef enum {
+    MXQ_GROUP_MAX = 0,       /* a group scores its largest choice value */
+    MXQ_GROUP_TOP2SUM = 1    /* the sum of its two largest (of s, or s + bias) */
+} mxq_group_score;
+
+/*
+ * Routing: the k experts of every token and their weights.
+ *
+ *   s = score(x) in FP32;  c = s + bias, or x itself where there is no bias (the
+ *   same order as s, without its rounding);
+ *   the experts of the topk_group best of n_group groups (groups of
+ *   experts / n_group consecutive experts) are eligible;
+ *   ids = the topk largest c among them, largest first, ties to the lowest expert;
+ *   w_j = scale * s_j,  with renorm  scale * s_j / (sum_i s_i + 1e-20).
+ *
+ * logits      [tokens, experts] of dtype, row stride ld.  A logit of -inf takes the
+ *             expert out for that token.
+ * bias        optional FP32 [experts], added for the choice only (a bias that
+ *             balances the experts' load); -inf takes the expert out.
+ * token_mask  optional bytes [tokens]: 0 marks a padding token, whose logits are not
+ *             read and which gets no expert.
+ * ids         int32 [tokens, topk]; -1 in the last places where fewer than topk
+ *             experts are left.
+ * weights     FP32 [tokens, topk]; 0 where ids is -1.
+ * A NaN choice value ranks below every number and stays eligible: the ids are
+ * always distinct and in range, and a chosen NaN shows in the weights.
+ * Limits: experts <= 1024, topk <= 32 and <= the experts of topk_group groups,
+ * n_group <= 32 and a divisor of experts.
+ */
+mxq_status mxq_route(const void* logits, mxq_dtype dtype, int64_t tokens, int32_t experts, int64_t ld,
+                     const float* bias, const uint8_t* token_mask, mxq_route_score score, int32_t n_group,
+                     int32_t topk_group, mxq_group_score group_score, int32_t topk, int32_t renorm, float scale,
+                     int32_t* ids, float* weights, mxq_stream_t stream);
+
+/*
+ * Gradient of mxq_route's weights by its logits (the choice itself has none):
+ * dlogits [tokens, experts] of dtype, row stride ld_out, from dweights FP32 and the
+ * ids [tokens, topk] that mxq_route gave for these logits, score, renorm and scale.
+ * Places with id -1 (or out of range) add nothing; a token that has only such
+ * places gets zeros and its logits are not read.
+ */
+mxq_status mxq_route_backward(const float* dweights, const int32_t* ids, const void* logits, mxq_dtype dtype,
+                              int64_t tokens, int32_t experts, int64_t ld, mxq_route_score score, int32_t topk,
+                              int32_t renorm, float scale, void* dlogits, int64_t ld_out, mxq_stream_t stream);
+
+/*
+ * Expert order: a stable counting sort of the tokens * k slots by expert.
+ *
+ * ids      int32 [tokens, k] as mxq_route gives them (any number outside
+ *          [0, experts) is a dropped slot).
+ * offsets  int64 [experts + 1]: the rows of expert g are offsets[g] ..
+ *          offsets[g+1] - 1, in the order of the tokens: the group_offsets of
+ *          mxq_grouped_gemm and mxq_quant_1x32_cols_grouped.
+ * rows     int32 [tokens, k]: the row of every slot.  Dropped slots have the rows
+ *          from offsets[experts] on, each given as -1 - row.
+ * experts <= 1024.  With dropped slots offsets[experts] < tokens * k: the grouped
+ * calls, given M_total = tokens * k, leave the rows behind it alone, and the calls
+ * below never read them.  tokens == 0 writes zero offsets.
+ */
+mxq_status mxq_moe_plan(const int32_t* ids, int64_t tokens, int32_t k, int32_t experts, int64_t* offsets, int32_t* rows,
+                        mxq_stream_t stream);
+
+/* a[rows[t, j]] = x[t] (zeros for a dropped slot): x [tokens, H], a [tokens * k, H].
+ * rows as mxq_moe_plan gives it: every row exactly once. */
+mxq_status mxq_moe_dispatch(const void* x, mxq_dtype dtype, int64_t tokens, int32_t k, int64_t H, int64_t ldx,
+                            const int32_t* rows, void* a, int64_t lda, mxq_stream_t stream);
+
+/* out[t] = sum_j w_j y[rows[t, j]] over the slots that are not dropped, in FP32:
+ * y [tokens * k, H], weights FP32 [tokens, k] (NULL: 1, which makes the call the
+ * gradient of mxq_moe_dispatch), out [tokens, H]; a token without slots gets zeros. */
+mxq_status mxq_moe_combine(const void* y, mxq_dtype dtype, int64_t tokens, int32_t k, int64_t H, int64_t ldy,
+                           const int32_t* rows, const float* weights, void* out, int64_t ldo, mxq_stream_t stream);
+
+/* Gradients of mxq_moe_combine: dy[rows[t, j]] = w_j dout[t] ([tokens * k, H]; zeros
+ * for a dropped slot) and dweights[t, j] = <dout[t], y[rows[t, j]]> (FP32; 0 for a
+ * dropped slot). */
+mxq_status mxq_moe_combine_backward(const void* dout, const void* y, mxq_dtype dtype, int64_t tokens, int32_t k,
+                                    int64_t H, int64_t ldd, int64_t ldy, const int32_t* rows, const float* weights,
+                                    void* dy, int64_t lddy, float* dweights, mxq_stream_t stream);
+
+/*
+ * Layer norm of every row of x [rows, cols]:
+ *   mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   y = (x - mean) rstd weight + shift.
+ * weight, shift  [cols] of param_dtype, either may be NULL (1 and 0).
+ * y              [rows, cols] of dtype; may be x itself.
+ * mean, rstd     FP32 [rows], for the backward pass.
+ * eps            finite, >= 0.
+ */
+mxq_status mxq_layer_norm(const void* x, mxq_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, const void* weight,
+                          const void* shift, mxq_dtype param_dtype, float eps, void* y, int64_t ldy, float* mean,
+                          float* rstd, mxq_stream_t stream);
+
+/*
+ * Its gradients from dy [rows, cols] and what the forward pass kept:
+ *   h = (x - mean) rstd, u = dy weight,
+ *   dx = rstd (u - mean(u) - h mean(u h)),  dweight = sum over rows of dy h,
+ *   dshift = sum over rows of dy   (both FP32 [cols]; either may be NULL).
+ * dx may be dy itself.  workspace: DEVICE scratch, 16-byte aligned, of at least
+ * mxq_layer_norm_backward_workspace_size(rows, cols) bytes, not used by other
+ * work until this call's work has finished.  rows == 0 gives zero sums.
+ */
+mxq_status mxq_layer_norm_backward(const void* dy, const void* x, mxq_dtype dtype, int64_t rows, int64_t cols,
+                                   int64_t lddy, int64_t ldx, const void* weight, mxq_dtype param_dtype,
+                                   const float* mean, const float* rstd, void* dx, int64_t lddx, float* dweight,
+                                   float* dshift, void* workspace, size_t workspace_bytes, mxq_stream_t stream);
+
+/* Host only; 0 for shapes the call refuses. */
+size_t mxq_layer_norm_backward_workspace_size(int64_t rows, int64_t cols);
+
+/* One gradient of mxq_grad_norm and mxq_clip_grad_norm: numel contiguous elements. */
+typedef struct {
+    const void* grad;
+    void* out;          /* mxq_clip_grad_norm: the scaled gradient (may be grad itself) */
+    int64_t numel;
+    mxq_dtype dtype;
+} mxq_grad_desc;
+
+#define MXQ_MAX_GRADS 65536
+
+/* norm (DEVICE FP32) = sqrt(sum over all gradients of the sum of squares).  Squares
+ * are summed in FP32 within a thread's share and in FP64 from there on, so a
+ * gradient beyond about 1e19 gives inf.  grads: host array, read during the call.
+ * workspace: DEVICE scratch, 16-byte aligned, of at least
+ * mxq_grad_norm_workspace_size(count) bytes.  count <= MXQ_MAX_GRADS; 0 gives 0. */
+mxq_status mxq_grad_norm(const mxq_grad_desc* grads, int32_t count, float* norm, void* workspace, size_t workspace_bytes,
+                         mxq_stream_t stream);
+
+/* mxq_grad_norm, then out = grad * min(1, max_norm / (norm + eps)) for every
+ * gradient, without the host learning the norm.  A norm that is NaN makes every
+ * output NaN, an infinite one scales by 0 (0 * inf is NaN), as the formula says.
+ * max_norm >= 0, eps finite and >= 0. */
+mxq_status mxq_clip_grad_norm(const mxq_grad_desc* grads, int32_t count, float max_norm, float eps, float* norm,
+                              void* workspace, size_t workspace_bytes, mxq_stream_t stream);
+
+/* Host only; 0 for a bad count. */
+size_t mxq_grad_norm_workspace_size(int32_t count);
+
 /* Waits for the work queued on `stream` (synchronizes the host with it), then
  * returns MXQ_ERR_TIMEOUT if any kernel of this library on the current device
  * recorded a bounded wait that ran out since the last call, MXQ_ERR_CUDA if

@@ -19,8 +19,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libmxq.so")
-SOURCES = ["api.cu", "quant.cu", "gemm.cu", "tensor_map.cu", "fsdp.cu", "noalloc.cu"]
-HEADERS = ["mxq_device.cuh", "mxq_internal.h", "mxq_quant_math.cuh"]
+SOURCES = ["api.cu", "quant.cu", "gemm.cu", "tensor_map.cu", "fsdp.cu", "noalloc.cu",
+           "api_block.cu", "route.cu", "permute.cu", "norm.cu", "clip.cu"]
+HEADERS = ["mxq_device.cuh", "mxq_internal.h", "mxq_quant_math.cuh", "mxq_elem.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]

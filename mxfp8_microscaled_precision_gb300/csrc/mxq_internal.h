@@ -117,4 +117,80 @@ cudaError_t launch_grouped_gemm_wgrad(const DeviceInfo& dev, const void* a_q, co
 
 cudaError_t launch_wait_probe(const DeviceInfo& dev, uint64_t limit_ns, cudaStream_t stream);
 
+// ---- the operators around the GEMMs (route.cu, permute.cu, norm.cu, clip.cu) ----
+
+// Routing of tokens to experts (see mxq_route).  token_mask and bias may be null.
+struct RouteArgs {
+    int64_t tokens, ld;
+    int experts, topk, n_group, topk_group, top2sum, renorm;
+    float scale;
+    const float* bias;
+    const uint8_t* token_mask;
+    int32_t* ids;
+    float* weights;
+};
+cudaError_t launch_route(const void* logits, bool f32, const RouteArgs& a, bool softmax, cudaStream_t stream);
+
+// Gradient of the routing weights by the logits (see mxq_route_backward).
+struct RouteBackwardArgs {
+    int64_t tokens, ld, ld_out;
+    int experts, topk, renorm;
+    float scale;
+    const int32_t* ids;
+    const float* dweights;
+};
+cudaError_t launch_route_backward(const void* logits, void* dlogits, bool f32, const RouteBackwardArgs& a,
+                                  bool softmax, cudaStream_t stream);
+
+// Expert order of the routed slots (see mxq_moe_plan).
+cudaError_t launch_moe_plan(const int32_t* ids, int64_t slots, int experts, int64_t* offsets, int32_t* rows,
+                            cudaStream_t stream);
+
+// Rows of H elements of `tokens` tokens and of their tokens * k slots.
+struct PermuteArgs {
+    int64_t tokens, H;
+    int k;
+    const int32_t* rows;
+    int64_t ld_tokens, ld_rows;   // row strides of the matrix by tokens and of the (written) matrix by rows
+};
+cudaError_t launch_moe_dispatch(const PermuteArgs& a, bool f32, const void* x, void* out, cudaStream_t stream);
+cudaError_t launch_moe_combine(const PermuteArgs& a, bool f32, const void* y, const float* weights, void* out,
+                               cudaStream_t stream);
+cudaError_t launch_moe_combine_backward(const PermuteArgs& a, bool f32, const void* dout, const void* y, int64_t ldy,
+                                        const float* weights, void* dy, float* dweights, cudaStream_t stream);
+
+// Layer norm (see mxq_layer_norm).  weight and shift may be null.
+struct NormArgs {
+    int64_t rows, cols, ldx, ldy;
+    const void *x, *weight, *shift;
+    float eps;
+    void* y;
+    float *mean, *rstd;
+};
+cudaError_t launch_layer_norm(const NormArgs& a, bool f32, bool params_f32, cudaStream_t stream);
+
+// Its backward pass: partial holds norm_partials(rows) x 2 x cols floats.
+constexpr int64_t kNormPartials = 304;
+int64_t norm_partials(int64_t rows);
+struct NormBackwardArgs {
+    int64_t rows, cols, lddy, ldx, lddx;
+    const void *dy, *x, *weight;
+    const float *mean, *rstd;
+    void* dx;
+    float *dweight, *dshift, *partial;
+};
+cudaError_t launch_layer_norm_backward(const NormBackwardArgs& a, bool f32, bool params_f32, cudaStream_t stream);
+
+// Norm over all gradients and scaling to a largest norm (see mxq_clip_grad_norm).
+struct ClipTensor {
+    const void* in;
+    void* out;
+    int64_t n;
+    bool f32;
+};
+constexpr int kClipBlocks = 608;   // partial sums of one launch
+int clip_partials(int count);
+cudaError_t launch_clip(const ClipTensor* tensors, int count, bool scale_too, float max_norm, float eps, float* norm,
+                        double* partial, cudaStream_t stream);
+
 }  // namespace mxq

@@ -1,0 +1,302 @@
+// permute.cu -- rows into expert order and back, around the grouped GEMMs:
+// the plan (a stable counting sort of the routed slots by expert), dispatch
+// (copies of the tokens' rows in expert order), combine (the weighted sum of a
+// token's rows) and the gradients of combine.
+//
+// A slot (t, j) is the j-th expert of token t; rows[t, j] is its row in expert
+// order.  A dropped slot (no expert) has a row too, behind all experts' rows:
+// it is given as -1 - row, so that every row is written by exactly one slot and
+// nothing needs clearing beforehand.  No atomics: results do not depend on the
+// order in which blocks run.
+
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "mxq_elem.cuh"
+#include "mxq_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace mxq {
+namespace {
+
+// ---- plan ------------------------------------------------------------------------
+
+// One cluster counts and places all slots: warp w of the cluster's warps owns
+// the slots [w * chunk, (w + 1) * chunk).  Bucket E takes the dropped slots.
+// Shared memory: hist[warps][E + 1] slots per warp and bucket (then: where the
+// warp's next slot of the bucket goes), count[E + 1] of the block, base[E + 1].
+__global__ void __launch_bounds__(1024) plan_kernel(const int32_t* ids, int64_t slots, int E, int64_t chunk,
+                                                    int64_t* offsets, int32_t* rows) {
+    extern __shared__ int sh[];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int B = E + 1;
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int* hist = sh;
+    int* count = hist + warps * B;
+    int* base = count + B;
+    const unsigned rank = cluster.block_rank(), blocks = cluster.num_blocks();
+
+    for (int i = threadIdx.x; i < warps * B; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    const int64_t lo = (static_cast<int64_t>(rank) * warps + warp) * chunk;
+    const int64_t hi = min(slots, lo + chunk);
+    int* mine = hist + warp * B;
+    for (int64_t s0 = lo; s0 < hi; s0 += 32) {
+        const int64_t s = s0 + lane;
+        int e = -1;
+        if (s < hi) {
+            e = ids[s];
+            if (e < 0 || e >= E) e = E;
+        }
+        const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
+        if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < B; e += blockDim.x) {   // exclusive over the block's warps
+        int sum = 0;
+        for (int w = 0; w < warps; ++w) {
+            const int n = hist[w * B + e];
+            hist[w * B + e] = sum;
+            sum += n;
+        }
+        count[e] = sum;
+    }
+    cluster.sync();
+    // base[e] = slots of the cluster's earlier blocks in bucket e; total in count's place is
+    // kept apart (count is read by the other blocks until the next cluster barrier).
+    if (warp == 0) {
+        int carry = 0;
+        for (int e0 = 0; e0 < B; e0 += 32) {
+            const int e = e0 + lane;
+            int before = 0, total = 0;
+            if (e < B) {
+                for (unsigned b = 0; b < blocks; ++b) {
+                    const int n = cluster.map_shared_rank(count, b)[e];
+                    total += n;
+                    if (b < rank) before += n;
+                }
+            }
+            int scan = total;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, scan, d);
+                if (lane >= d) scan += v;
+            }
+            if (e < B) {
+                const int first = carry + scan - total;
+                base[e] = first + before;
+                if (rank == 0) offsets[e] = first;   // bucket E starts where the experts' rows end
+            }
+            carry += __shfl_sync(0xFFFFFFFFu, scan, 31);
+        }
+    }
+    cluster.sync();
+    for (int64_t s0 = lo; s0 < hi; s0 += 32) {
+        const int64_t s = s0 + lane;
+        int e = -1;
+        if (s < hi) {
+            e = ids[s];
+            if (e < 0 || e >= E) e = E;
+        }
+        const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
+        if (e >= 0) {
+            const int row = base[e] + mine[e] + __popc(peers & ((1u << lane) - 1u));
+            rows[s] = e == E ? -1 - row : row;
+        }
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+        __syncwarp();
+    }
+}
+
+// ---- rows ------------------------------------------------------------------------
+
+constexpr int kThreads = 256;
+
+// Where a slot's entry of `rows` points: the row and whether the slot is kept.
+// Entries that mxq_moe_plan does not give (a row that does not exist) point nowhere.
+struct Place {
+    int64_t row;
+    bool kept, exists;
+};
+__device__ __forceinline__ Place place_of(int entry, int64_t slots) {
+    const bool kept = entry >= 0;
+    const int row = kept ? entry : -1 - entry;
+    return {row, kept, row < slots};
+}
+
+// a[rows[t, j]] = x[t], zeros for a dropped slot.  Token blockIdx.x; one vector
+// of the row per thread, blockIdx.y over the row: x is read once, whatever k.
+template <typename V>
+__global__ void __launch_bounds__(kThreads) dispatch_kernel(const V* x, int64_t ldx, V* a, int64_t lda, int64_t n,
+                                                            const int32_t* rows, int k) {
+    const int64_t t = blockIdx.x;
+    const int64_t i = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x;
+    if (i >= n) return;
+    const V v = x[t * ldx + i];
+    const int32_t* r = rows + t * k;
+    const int64_t slots = static_cast<int64_t>(gridDim.x) * k;
+    for (int j = 0; j < k; ++j) {
+        const Place p = place_of(r[j], slots);
+        if (p.exists) a[p.row * lda + i] = p.kept ? v : V{};
+    }
+}
+
+// out[t] = sum_j w_j y[rows[t, j]] (w_j = 1 without weights), summed in FP32 in
+// the order of j and rounded once.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const T* y, int64_t ldy, const int32_t* rows,
+                                                           const float* weights, int k, T* out, int64_t ldo,
+                                                           int64_t H) {
+    const int64_t t = blockIdx.x;
+    const int64_t i = (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x) * V;
+    if (i >= H) return;
+    const int32_t* r = rows + t * k;
+    const int64_t slots = static_cast<int64_t>(gridDim.x) * k;
+    float acc[V] = {};
+    for (int j = 0; j < k; ++j) {
+        const Place p = place_of(r[j], slots);
+        if (!p.kept || !p.exists) continue;   // a dropped slot: its row of y is not read
+        const float w = weights != nullptr ? weights[t * k + j] : 1.0f;
+        float f[V];
+        load_vec<T, V>(y + p.row * ldy + i, f);
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(w, f[c], acc[c]);
+    }
+    store_vec<T, V>(out + t * ldo + i, acc);
+}
+
+// dy[rows[t, j]] = w_j dout[t], dw_j = <dout[t], y[rows[t, j]]>: one warp per slot.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) combine_backward_kernel(const T* dout, int64_t ldd, const T* y, int64_t ldy,
+                                                                    const int32_t* rows, const float* weights, int k,
+                                                                    int64_t slots, T* dy, int64_t lddy,
+                                                                    float* dweights, int64_t H) {
+    const int64_t s = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (s >= slots) return;
+    const Place p = place_of(rows[s], slots);
+    if (!p.kept || !p.exists) {
+        T* to = dy + p.row * lddy;
+        const float zero[V] = {};
+        for (int64_t i = lane * V; p.exists && i < H; i += 32 * V) store_vec<T, V>(to + i, zero);
+        if (lane == 0) dweights[s] = 0.0f;
+        return;
+    }
+    const T* d = dout + (s / k) * ldd;
+    const T* from = y + p.row * ldy;
+    T* to = dy + p.row * lddy;
+    const float w = weights[s];
+    float dot = 0.0f;
+    for (int64_t i = lane * V; i < H; i += 32 * V) {
+        float g[V], f[V];
+        load_vec<T, V>(d + i, g);
+        load_vec<T, V>(from + i, f);
+#pragma unroll
+        for (int c = 0; c < V; ++c) dot = fmaf(g[c], f[c], dot);
+#pragma unroll
+        for (int c = 0; c < V; ++c) g[c] *= w;
+        store_vec<T, V>(to + i, g);
+    }
+    dot = warp_sum(dot);
+    if (lane == 0) dweights[s] = dot;
+}
+
+bool vectors16(int64_t H, size_t size, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
+    if (H * size % 16 != 0) return false;
+    for (const void* p : ptrs)
+        if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
+    for (int64_t ld : lds)
+        if (ld * size % 16 != 0) return false;
+    return true;
+}
+
+dim3 row_grid(int64_t tokens, int64_t vectors) {
+    return dim3(static_cast<unsigned>(tokens), static_cast<unsigned>((vectors + kThreads - 1) / kThreads));
+}
+
+template <typename T, int V>
+cudaError_t combine_launch(const PermuteArgs& a, const void* y, const float* weights, void* out, cudaStream_t stream) {
+    combine_kernel<T, V><<<row_grid(a.tokens, (a.H + V - 1) / V), kThreads, 0, stream>>>(
+        static_cast<const T*>(y), a.ld_rows, a.rows, weights, a.k, static_cast<T*>(out), a.ld_tokens, a.H);
+    return cudaGetLastError();
+}
+
+template <typename T, int V>
+cudaError_t combine_backward_launch(const PermuteArgs& a, const void* dout, const void* y, int64_t ldy,
+                                    const float* weights, void* dy, float* dweights, cudaStream_t stream) {
+    const int64_t slots = a.tokens * a.k;
+    const int64_t blocks = (slots + kThreads / 32 - 1) / (kThreads / 32);
+    combine_backward_kernel<T, V><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
+        static_cast<const T*>(dout), a.ld_tokens, static_cast<const T*>(y), ldy, a.rows, weights, a.k, slots,
+        static_cast<T*>(dy), a.ld_rows, dweights, a.H);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_moe_plan(const int32_t* ids, int64_t slots, int experts, int64_t* offsets, int32_t* rows,
+                            cudaStream_t stream) {
+    const int B = experts + 1;
+    int blocks = 1, warps = 32;
+    if (slots > 4096) blocks = 8;
+    if (slots <= 32 * 32) warps = static_cast<int>((slots + 31) / 32);
+    if (warps < 4) warps = 4;
+    const int64_t all = static_cast<int64_t>(blocks) * warps;
+    const int64_t chunk = ((slots + all - 1) / all + 31) / 32 * 32;
+    const size_t smem = sizeof(int) * (static_cast<size_t>(warps) * B + 2 * static_cast<size_t>(B));
+    cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(blocks), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, plan_kernel, ids, slots, experts, chunk, offsets, rows);
+}
+
+cudaError_t launch_moe_dispatch(const PermuteArgs& a, bool f32, const void* x, void* out, cudaStream_t stream) {
+    const size_t size = f32 ? 4 : 2;
+    if (vectors16(a.H, size, {x, out}, {a.ld_tokens, a.ld_rows})) {
+        const int64_t per = 16 / static_cast<int64_t>(size), n = a.H / per;
+        dispatch_kernel<uint4><<<row_grid(a.tokens, n), kThreads, 0, stream>>>(
+            static_cast<const uint4*>(x), a.ld_tokens / per, static_cast<uint4*>(out), a.ld_rows / per, n, a.rows, a.k);
+    } else if (f32) {
+        dispatch_kernel<uint32_t><<<row_grid(a.tokens, a.H), kThreads, 0, stream>>>(
+            static_cast<const uint32_t*>(x), a.ld_tokens, static_cast<uint32_t*>(out), a.ld_rows, a.H, a.rows, a.k);
+    } else {
+        dispatch_kernel<bf16_bits><<<row_grid(a.tokens, a.H), kThreads, 0, stream>>>(
+            static_cast<const bf16_bits*>(x), a.ld_tokens, static_cast<bf16_bits*>(out), a.ld_rows, a.H, a.rows, a.k);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_moe_combine(const PermuteArgs& a, bool f32, const void* y, const float* weights, void* out,
+                               cudaStream_t stream) {
+    const bool vec = vectors16(a.H, f32 ? 4 : 2, {y, out}, {a.ld_tokens, a.ld_rows});
+    if (f32) return vec ? combine_launch<float, 4>(a, y, weights, out, stream)
+                        : combine_launch<float, 1>(a, y, weights, out, stream);
+    return vec ? combine_launch<bf16_bits, 8>(a, y, weights, out, stream)
+               : combine_launch<bf16_bits, 1>(a, y, weights, out, stream);
+}
+
+cudaError_t launch_moe_combine_backward(const PermuteArgs& a, bool f32, const void* dout, const void* y, int64_t ldy,
+                                        const float* weights, void* dy, float* dweights, cudaStream_t stream) {
+    const bool vec = vectors16(a.H, f32 ? 4 : 2, {dout, y, dy}, {a.ld_tokens, ldy, a.ld_rows});
+    if (f32) return vec ? combine_backward_launch<float, 4>(a, dout, y, ldy, weights, dy, dweights, stream)
+                        : combine_backward_launch<float, 1>(a, dout, y, ldy, weights, dy, dweights, stream);
+    return vec ? combine_backward_launch<bf16_bits, 8>(a, dout, y, ldy, weights, dy, dweights, stream)
+               : combine_backward_launch<bf16_bits, 1>(a, dout, y, ldy, weights, dy, dweights, stream);
+}
+
+}  // namespace mxq

@@ -89,13 +89,31 @@ def lib() -> ctypes.CDLL:
         L.mxq_grouped_gemm_noalloc.argtypes = [P, P, P, P, P, I32, I64, I64, I64, P, P]
         L.mxq_grouped_gemm_noalloc.restype = S
         L.mxq_debug_wait_timeout.argtypes = [U32, P]
+        F = ctypes.c_float
+        L.mxq_route.argtypes = [P, S, I64, I32, I64, P, P, S, I32, I32, S, I32, I32, F, P, P, P]
+        L.mxq_route_backward.argtypes = [P, P, P, S, I64, I32, I64, S, I32, I32, F, P, I64, P]
+        L.mxq_moe_plan.argtypes = [P, I64, I32, I32, P, P, P]
+        L.mxq_moe_dispatch.argtypes = [P, S, I64, I32, I64, I64, P, P, I64, P]
+        L.mxq_moe_combine.argtypes = [P, S, I64, I32, I64, I64, P, P, P, I64, P]
+        L.mxq_moe_combine_backward.argtypes = [P, P, S, I64, I32, I64, I64, I64, P, P, P, I64, P, P]
+        L.mxq_layer_norm.argtypes = [P, S, I64, I64, I64, P, P, S, F, P, I64, P, P, P]
+        L.mxq_layer_norm_backward.argtypes = [P, P, S, I64, I64, I64, I64, P, S, P, P, P, I64, P, P, P, SZ, P]
+        L.mxq_layer_norm_backward_workspace_size.argtypes = [I64, I64]
+        L.mxq_layer_norm_backward_workspace_size.restype = SZ
+        L.mxq_grad_norm.argtypes = [P, I32, P, P, SZ, P]
+        L.mxq_clip_grad_norm.argtypes = [P, I32, F, F, P, P, SZ, P]
+        L.mxq_grad_norm_workspace_size.argtypes = [I32]
+        L.mxq_grad_norm_workspace_size.restype = SZ
         for f in ("mxq_quant_1x32_dual", "mxq_quant_32x32", "mxq_gemm_bf16out",
                   "mxq_grouped_gemm", "mxq_get_device_status", "mxq_debug_wait_timeout",
                   "mxq_quant_1x32_dual_batched", "mxq_quant_1x32_cols_grouped",
                   "mxq_grouped_gemm_wgrad", "mxq_gemm_bf16out_fmt", "mxq_gemm_mxfp8out",
                   "mxq_fsdp_payload_layout", "mxq_fsdp_unpack", "mxq_quant_1x32_cols_grouped_fmt",
                   "mxq_grouped_gemm_fmt", "mxq_grouped_gemm_wgrad_fmt", "mxq_gemm_bf16out_multi",
-                  "mxq_grouped_gemm_group_tiled", "mxq_scale_regroup_rows", "mxq_quant_32x32_fmt"):
+                  "mxq_grouped_gemm_group_tiled", "mxq_scale_regroup_rows", "mxq_quant_32x32_fmt",
+                  "mxq_route", "mxq_route_backward", "mxq_moe_plan", "mxq_moe_dispatch", "mxq_moe_combine",
+                  "mxq_moe_combine_backward", "mxq_layer_norm", "mxq_layer_norm_backward", "mxq_grad_norm",
+                  "mxq_clip_grad_norm"):
             getattr(L, f).restype = S
         _lib = L
         return L
@@ -470,6 +488,285 @@ def grouped_gemm_group_tiled(a_q, a_s_grouped, b_q, b_s, offsets: torch.Tensor, 
                                               _fmt(b_fmt), _ptr(offsets), G, M_total, N, K, bands_cap, _ptr(out),
                                               out.stride(0), _stream()), "mxq_grouped_gemm_group_tiled")
     return out
+
+
+# ---- operators around the experts' products (see the same section of mxq.h) ----
+
+BF16, F32 = 0, 1
+_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "top2sum": 1}
+MAX_GRADS = 65536
+
+
+def _matrix(t: torch.Tensor, name: str) -> int:
+    """The dtype code of a 2-D bf16 or fp32 CUDA tensor with unit last stride."""
+    code = _DTYPES.get(t.dtype)
+    if code is None or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D bfloat16 or float32 CUDA tensor")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must have unit stride along its last axis")
+    return code
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride in elements; a single row has any (its stride says nothing)."""
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _dense(t: torch.Tensor, name: str, dtype, shape):
+    """A contiguous CUDA tensor of this dtype and shape."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor {list(shape)}")
+    return t
+
+
+def _out_like(out, name, shape, like):
+    """`out` checked against what the call writes, or a new tensor."""
+    if out is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    _matrix(out, name)
+    if out.dtype != like.dtype or tuple(out.shape) != shape:
+        raise ValueError(f"{name} must be {str(like.dtype)[6:]} {list(shape)}")
+    return out
+
+
+def _of(table, key, what):
+    if key not in table:
+        raise ValueError(f"unknown {what} {key!r} ({' or '.join(table)})")
+    return table[key]
+
+
+def route(logits: torch.Tensor, topk: int, score="softmax", bias=None, n_group: int = 1, topk_group: int = 1,
+          group_score="max", renorm: bool = True, scale: float = 1.0, token_mask=None, out=None):
+    """The topk experts of every token and their weights (see mxq_route).
+    logits: bf16 or fp32 [T, E]; bias: fp32 [E], added for the choice only; token_mask:
+    bool or uint8 [T], 0 for padding tokens.  Returns (ids int32 [T, topk], weights
+    fp32 [T, topk]); ids is -1 (weight 0) where no expert is left."""
+    code = _matrix(logits, "logits")
+    T, E = logits.shape
+    if bias is not None:
+        _dense(bias, "bias", torch.float32, (E,))
+    if token_mask is not None:
+        _dense(token_mask, "token_mask", torch.bool if token_mask.dtype == torch.bool else torch.uint8, (T,))
+    if out is None:
+        ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+    else:
+        ids, weights = out
+        _dense(ids, "ids", torch.int32, (T, topk))
+        _dense(weights, "weights", torch.float32, (T, topk))
+    _check(lib().mxq_route(_ptr(logits), code, T, E, _ld(logits), _ptr(bias), _ptr(token_mask),
+                           _of(_SCORES, score, "score"), n_group, topk_group,
+                           _of(_GROUP_SCORES, group_score, "group score"), topk, 1 if renorm else 0, scale, _ptr(ids),
+                           _ptr(weights), _stream()), "mxq_route")
+    return ids, weights
+
+
+def route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score="softmax",
+                   renorm: bool = True, scale: float = 1.0, out=None):
+    """Gradient of route's weights by its logits (see mxq_route_backward), in the
+    logits' dtype; score, renorm and scale as in the forward call."""
+    code = _matrix(logits, "logits")
+    T, E = logits.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must be 2-D")
+    topk = ids.shape[1]
+    _dense(ids, "ids", torch.int32, (T, topk))
+    _dense(dweights, "dweights", torch.float32, (T, topk))
+    out = _out_like(out, "out", (T, E), logits)
+    _check(lib().mxq_route_backward(_ptr(dweights), _ptr(ids), _ptr(logits), code, T, E, _ld(logits),
+                                    _of(_SCORES, score, "score"), topk, 1 if renorm else 0, scale, _ptr(out), _ld(out),
+                                    _stream()), "mxq_route_backward")
+    return out
+
+
+def moe_plan(ids: torch.Tensor, experts: int, out=None):
+    """Expert order of the routed slots (see mxq_moe_plan).  ids: int32 [T, k] from
+    route.  Returns (offsets int64 [experts + 1], rows int32 [T, k]): offsets are the
+    group offsets of the grouped calls, rows[t, j] the row of slot (t, j), -1 - row
+    for a dropped slot."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be 2-D")
+    T, k = ids.shape
+    _dense(ids, "ids", torch.int32, (T, k))
+    if out is None:
+        offsets = torch.empty(experts + 1 if experts > 0 else 1, dtype=torch.int64, device=ids.device)
+        rows = torch.empty((T, k), dtype=torch.int32, device=ids.device)
+    else:
+        offsets, rows = out
+        _dense(offsets, "offsets", torch.int64, (experts + 1,))
+        _dense(rows, "rows", torch.int32, (T, k))
+    _check(lib().mxq_moe_plan(_ptr(ids), T, k, experts, _ptr(offsets), _ptr(rows), _stream()), "mxq_moe_plan")
+    return offsets, rows
+
+
+def _rows_shape(rows: torch.Tensor):
+    if rows.dim() != 2:
+        raise ValueError("rows must be 2-D")
+    T, k = rows.shape
+    _dense(rows, "rows", torch.int32, (T, k))
+    return T, k
+
+
+def moe_dispatch(x: torch.Tensor, rows: torch.Tensor, out=None) -> torch.Tensor:
+    """The tokens' rows in expert order (see mxq_moe_dispatch): x [T, H], rows from
+    moe_plan.  Returns [T * k, H], zeros in the rows of dropped slots."""
+    code = _matrix(x, "x")
+    T, k = _rows_shape(rows)
+    if x.shape[0] != T:
+        raise ValueError("x and rows must have the same number of tokens")
+    H = x.shape[1]
+    out = _out_like(out, "out", (T * k, H), x)
+    _check(lib().mxq_moe_dispatch(_ptr(x), code, T, k, H, _ld(x), _ptr(rows), _ptr(out), _ld(out), _stream()),
+           "mxq_moe_dispatch")
+    return out
+
+
+def moe_combine(y: torch.Tensor, rows: torch.Tensor, weights=None, out=None) -> torch.Tensor:
+    """out[t] = sum over a token's slots of weight * y[row] (see mxq_moe_combine):
+    y [T * k, H] in expert order, weights fp32 [T, k] from route.  Without weights it
+    is the plain sum, the gradient of moe_dispatch.  Returns [T, H]."""
+    code = _matrix(y, "y")
+    T, k = _rows_shape(rows)
+    if y.shape[0] != T * k:
+        raise ValueError("y must have a row for every slot")
+    if weights is not None:
+        _dense(weights, "weights", torch.float32, (T, k))
+    H = y.shape[1]
+    out = _out_like(out, "out", (T, H), y)
+    _check(lib().mxq_moe_combine(_ptr(y), code, T, k, H, _ld(y), _ptr(rows), _ptr(weights), _ptr(out), _ld(out),
+                                 _stream()), "mxq_moe_combine")
+    return out
+
+
+def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor, out=None):
+    """Gradients of moe_combine (see mxq_moe_combine_backward): returns
+    (dy [T * k, H], dweights fp32 [T, k]); `out` may supply both."""
+    code = _matrix(y, "y")
+    T, k = _rows_shape(rows)
+    H = y.shape[1]
+    if y.shape[0] != T * k:
+        raise ValueError("y must have a row for every slot")
+    if _matrix(dout, "dout") != code or tuple(dout.shape) != (T, H):
+        raise ValueError(f"dout must be {str(y.dtype)[6:]} {[T, H]}")
+    _dense(weights, "weights", torch.float32, (T, k))
+    dy, dweights = (None, None) if out is None else out
+    dy = _out_like(dy, "dy", (T * k, H), y)
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    else:
+        _dense(dweights, "dweights", torch.float32, (T, k))
+    _check(lib().mxq_moe_combine_backward(_ptr(dout), _ptr(y), code, T, k, H, _ld(dout), _ld(y), _ptr(rows),
+                                          _ptr(weights), _ptr(dy), _ld(dy), _ptr(dweights), _stream()),
+           "mxq_moe_combine_backward")
+    return dy, dweights
+
+
+def _param(t, name, cols):
+    """dtype code of a weight or shift [cols]."""
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    _dense(t, name, t.dtype, (cols,))
+    return code
+
+
+def layer_norm(x: torch.Tensor, weight=None, shift=None, eps: float = 1e-5, out=None):
+    """Layer norm of every row of x [M, C] (see mxq_layer_norm); weight and shift [C],
+    bf16 or fp32 (both alike), optional.  Returns (y [M, C], mean fp32 [M], rstd fp32
+    [M]); `out` may supply the three (y may be x)."""
+    code = _matrix(x, "x")
+    M, C = x.shape
+    pcode = _param(weight, "weight", C) if weight is not None else None
+    if shift is not None:
+        scode = _param(shift, "shift", C)
+        if pcode is not None and scode != pcode:
+            raise ValueError("weight and shift must have the same dtype")
+        pcode = scode
+    y, mean, rstd = (None, None, None) if out is None else out
+    y = _out_like(y, "y", (M, C), x)
+    if mean is None:
+        mean = torch.empty(M, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    else:
+        _dense(mean, "mean", torch.float32, (M,))
+        _dense(rstd, "rstd", torch.float32, (M,))
+    _check(lib().mxq_layer_norm(_ptr(x), code, M, C, _ld(x), _ptr(weight), _ptr(shift), pcode or 0, eps, _ptr(y), _ld(y),
+                                _ptr(mean), _ptr(rstd), _stream()), "mxq_layer_norm")
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight, mean: torch.Tensor, rstd: torch.Tensor, out=None):
+    """Gradients of layer_norm (see mxq_layer_norm_backward): returns (dx [M, C],
+    dweight fp32 [C], dshift fp32 [C]); `out` may supply dx (which may be dy)."""
+    code = _matrix(x, "x")
+    M, C = x.shape
+    if _matrix(dy, "dy") != code or tuple(dy.shape) != (M, C):
+        raise ValueError(f"dy must be {str(x.dtype)[6:]} {[M, C]}")
+    pcode = _param(weight, "weight", C) if weight is not None else 0
+    _dense(mean, "mean", torch.float32, (M,))
+    _dense(rstd, "rstd", torch.float32, (M,))
+    dx = _out_like(out, "out", (M, C), x)
+    sums = torch.empty((2, C), dtype=torch.float32, device=x.device)
+    size = int(lib().mxq_layer_norm_backward_workspace_size(M, C))
+    workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
+    _check(lib().mxq_layer_norm_backward(_ptr(dy), _ptr(x), code, M, C, _ld(dy), _ld(x), _ptr(weight), pcode, _ptr(mean),
+                                         _ptr(rstd), _ptr(dx), _ld(dx), _ptr(sums[0]), _ptr(sums[1]), _ptr(workspace),
+                                         size, _stream()), "mxq_layer_norm_backward")
+    return dx, sums[0], sums[1]
+
+
+class GradDesc(ctypes.Structure):
+    """mxq_grad_desc of include/mxq.h."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+def _grad_descs(grads, outs):
+    descs = (GradDesc * max(1, len(grads)))()
+    for d, g, o in zip(descs, grads, outs):
+        code = _DTYPES.get(g.dtype)
+        if code is None or not g.is_cuda or not g.is_contiguous():
+            raise ValueError("gradients must be contiguous bfloat16 or float32 CUDA tensors")
+        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous()):
+            raise ValueError("every output must be contiguous and match its gradient")
+        d.grad, d.out, d.numel, d.dtype = g.data_ptr(), o.data_ptr(), g.numel(), code
+    return descs
+
+
+def _norm_buffers(grads):
+    if len(grads) > MAX_GRADS:
+        raise ValueError(f"at most {MAX_GRADS} gradients")
+    size = int(lib().mxq_grad_norm_workspace_size(len(grads)))
+    device = grads[0].device if grads else torch.device("cuda")
+    return (torch.empty((), dtype=torch.float32, device=device), torch.empty(size, dtype=torch.uint8, device=device),
+            size)
+
+
+def grad_norm(grads) -> torch.Tensor:
+    """The 2-norm over all of a list of gradients (bf16 and fp32 mixed), an fp32
+    scalar on the device (see mxq_grad_norm)."""
+    grads = list(grads)
+    descs = _grad_descs(grads, grads)
+    norm, workspace, size = _norm_buffers(grads)
+    _check(lib().mxq_grad_norm(descs, len(grads), _ptr(norm), _ptr(workspace), size, _stream()), "mxq_grad_norm")
+    return norm
+
+
+def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None):
+    """Every gradient times min(1, max_norm / (norm + eps)), norm being that over all
+    of them (see mxq_clip_grad_norm).  out: a list of tensors like the gradients, the
+    gradients themselves to scale in place, or None for new ones.  Returns (norm fp32
+    scalar on the device, the list of outputs)."""
+    grads = list(grads)
+    out = [torch.empty_like(g) for g in grads] if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError("out must have a tensor for every gradient")
+    descs = _grad_descs(grads, out)
+    norm, workspace, size = _norm_buffers(grads)
+    _check(lib().mxq_clip_grad_norm(descs, len(grads), max_norm, eps, _ptr(norm), _ptr(workspace), size, _stream()),
+           "mxq_clip_grad_norm")
+    return norm, out
 
 
 def get_device_status() -> int:
