@@ -25,10 +25,14 @@ inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_
 inline bool bad_dtype(mxq_dtype d) { return d != MXQ_BF16 && d != MXQ_F32; }
 inline size_t size_of(mxq_dtype d) { return d == MXQ_F32 ? 4 : 2; }
 
+mxq_status device_ok(DeviceInfo* info) {
+    if (mxq::current_device_info(info) != cudaSuccess) return MXQ_ERR_CUDA;
+    return info->cc_major == 10 && info->cc_minor == 3 ? MXQ_OK : MXQ_ERR_UNSUPPORTED_DEVICE;
+}
+
 mxq_status device_ok() {
     DeviceInfo info;
-    if (mxq::current_device_info(&info) != cudaSuccess) return MXQ_ERR_CUDA;
-    return info.cc_major == 10 && info.cc_minor == 3 ? MXQ_OK : MXQ_ERR_UNSUPPORTED_DEVICE;
+    return device_ok(&info);
 }
 
 inline mxq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA; }
@@ -204,7 +208,7 @@ mxq_status mxq_layer_norm(const void* x, mxq_dtype dtype, int64_t rows, int64_t 
 
 size_t mxq_layer_norm_backward_workspace_size(int64_t rows, int64_t cols) {
     if (rows < 0 || cols < 0 || rows > kMaxRows || cols > kMaxCols) return 0;
-    return static_cast<size_t>(mxq::norm_partials(rows) * 2 * cols) * sizeof(float);
+    return static_cast<size_t>(mxq::norm_partials(rows, cols) * 2 * cols) * sizeof(float);
 }
 
 mxq_status mxq_layer_norm_backward(const void* dy, const void* x, mxq_dtype dtype, int64_t rows, int64_t cols,
@@ -224,7 +228,8 @@ mxq_status mxq_layer_norm_backward(const void* dy, const void* x, mxq_dtype dtyp
             return MXQ_ERR_INVALID_ARG;
         if (workspace_bytes < mxq_layer_norm_backward_workspace_size(rows, cols)) return MXQ_ERR_INVALID_ARG;
     }
-    st = device_ok();
+    DeviceInfo info;
+    st = device_ok(&info);
     if (st != MXQ_OK) return st;
     if (rows == 0) {   // sums over no rows
         cudaError_t e = cudaSuccess;
@@ -233,7 +238,8 @@ mxq_status mxq_layer_norm_backward(const void* dy, const void* x, mxq_dtype dtyp
         return from_cuda(e);
     }
     return from_cuda(mxq::launch_layer_norm_backward({rows, cols, lddy, ldx, lddx, dy, x, weight, mean, rstd, dx,
-                                                      dweight, dshift, static_cast<float*>(workspace)},
+                                                      dweight, dshift, static_cast<float*>(workspace),
+                                                      info.status},
                                                      dtype == MXQ_F32, param_dtype == MXQ_F32, cu(stream)));
 }
 

@@ -169,15 +169,15 @@ struct NormArgs {
 };
 cudaError_t launch_layer_norm(const NormArgs& a, bool f32, bool params_f32, cudaStream_t stream);
 
-// Its backward pass: partial holds norm_partials(rows) x 2 x cols floats.
-constexpr int64_t kNormPartials = 304;
-int64_t norm_partials(int64_t rows);
+// Its backward pass: partial holds norm_partials(rows, cols) x 2 x cols floats.
+int64_t norm_partials(int64_t rows, int64_t cols);
 struct NormBackwardArgs {
     int64_t rows, cols, lddy, ldx, lddx;
     const void *dy, *x, *weight;
     const float *mean, *rstd;
     void* dx;
     float *dweight, *dshift, *partial;
+    unsigned int* status;   // device status word
 };
 cudaError_t launch_layer_norm_backward(const NormBackwardArgs& a, bool f32, bool params_f32, cudaStream_t stream);
 

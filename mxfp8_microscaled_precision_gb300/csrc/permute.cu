@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "mxq_elem.cuh"
 #include "mxq_internal.h"
@@ -129,61 +130,63 @@ __device__ __forceinline__ Place place_of(int entry, int64_t slots) {
     return {row, kept, row < slots};
 }
 
-// a[rows[t, j]] = x[t], zeros for a dropped slot.  Token blockIdx.x; one vector
-// of the row per thread, blockIdx.y over the row: x is read once, whatever k.
-template <typename V>
-__global__ void __launch_bounds__(kThreads) dispatch_kernel(const V* x, int64_t ldx, V* a, int64_t lda, int64_t n,
-                                                            const int32_t* rows, int k) {
+// a[rows[t, j]] = x[t], zeros for a dropped slot.  Token blockIdx.x; 16 bytes of
+// the row per thread, blockIdx.y over the row: x is read once, whatever k.
+template <int kSize, bool kAny>
+__global__ void __launch_bounds__(kThreads) dispatch_kernel(const unsigned char* x, int64_t ldx, unsigned char* a,
+                                                            int64_t lda, int64_t H, const int32_t* rows, int k) {
     const int64_t t = blockIdx.x;
-    const int64_t i = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x;
-    if (i >= n) return;
-    const V v = x[t * ldx + i];
+    const int64_t i = (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x) * (16 / kSize);
+    if (!kAny && i >= H) return;
+    const uint4 v = load16<kSize, kAny>(x + t * ldx * kSize, i, H);
     const int32_t* r = rows + t * k;
     const int64_t slots = static_cast<int64_t>(gridDim.x) * k;
     for (int j = 0; j < k; ++j) {
         const Place p = place_of(r[j], slots);
-        if (p.exists) a[p.row * lda + i] = p.kept ? v : V{};
+        if (p.exists) store16<kSize, kAny>(a + p.row * lda * kSize, i, H, p.kept ? v : make_uint4(0u, 0u, 0u, 0u));
     }
 }
 
 // out[t] = sum_j w_j y[rows[t, j]] (w_j = 1 without weights), summed in FP32 in
 // the order of j and rounded once.
-template <typename T, int V>
+template <typename T, bool kAny>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const T* y, int64_t ldy, const int32_t* rows,
                                                            const float* weights, int k, T* out, int64_t ldo,
                                                            int64_t H) {
+    constexpr int V = kVec16<T>;
     const int64_t t = blockIdx.x;
     const int64_t i = (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x) * V;
-    if (i >= H) return;
+    if (!kAny && i >= H) return;
     const int32_t* r = rows + t * k;
     const int64_t slots = static_cast<int64_t>(gridDim.x) * k;
     float acc[V] = {};
+#pragma unroll 4
     for (int j = 0; j < k; ++j) {
         const Place p = place_of(r[j], slots);
         if (!p.kept || !p.exists) continue;   // a dropped slot: its row of y is not read
         const float w = weights != nullptr ? weights[t * k + j] : 1.0f;
         float f[V];
-        load_vec<T, V>(y + p.row * ldy + i, f);
+        unpack<T>(load16<sizeof(T), kAny>(y + p.row * ldy, i, H), f);
 #pragma unroll
         for (int c = 0; c < V; ++c) acc[c] = fmaf(w, f[c], acc[c]);
     }
-    store_vec<T, V>(out + t * ldo + i, acc);
+    store16<sizeof(T), kAny>(out + t * ldo, i, H, pack<T>(acc));
 }
 
 // dy[rows[t, j]] = w_j dout[t], dw_j = <dout[t], y[rows[t, j]]>: one warp per slot.
-template <typename T, int V>
+template <typename T, bool kAny>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const T* dout, int64_t ldd, const T* y, int64_t ldy,
                                                                     const int32_t* rows, const float* weights, int k,
                                                                     int64_t slots, T* dy, int64_t lddy,
                                                                     float* dweights, int64_t H) {
+    constexpr int V = kVec16<T>;
     const int64_t s = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (s >= slots) return;
     const Place p = place_of(rows[s], slots);
     if (!p.kept || !p.exists) {
-        T* to = dy + p.row * lddy;
-        const float zero[V] = {};
-        for (int64_t i = lane * V; p.exists && i < H; i += 32 * V) store_vec<T, V>(to + i, zero);
+        for (int64_t i = 0; p.exists && i < H; i += 32 * V)
+            store16<sizeof(T), kAny>(dy + p.row * lddy, i + lane * V, H, make_uint4(0u, 0u, 0u, 0u));
         if (lane == 0) dweights[s] = 0.0f;
         return;
     }
@@ -192,21 +195,24 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const T* dou
     T* to = dy + p.row * lddy;
     const float w = weights[s];
     float dot = 0.0f;
-    for (int64_t i = lane * V; i < H; i += 32 * V) {
+#pragma unroll 4
+    for (int64_t i0 = 0; i0 < H; i0 += 32 * V) {
+        const int64_t i = i0 + lane * V;
         float g[V], f[V];
-        load_vec<T, V>(d + i, g);
-        load_vec<T, V>(from + i, f);
+        unpack<T>(load16<sizeof(T), kAny>(d, i, H), g);
+        unpack<T>(load16<sizeof(T), kAny>(from, i, H), f);
 #pragma unroll
         for (int c = 0; c < V; ++c) dot = fmaf(g[c], f[c], dot);
 #pragma unroll
         for (int c = 0; c < V; ++c) g[c] *= w;
-        store_vec<T, V>(to + i, g);
+        store16<sizeof(T), kAny>(to, i, H, pack<T>(g));
     }
     dot = warp_sum(dot);
     if (lane == 0) dweights[s] = dot;
 }
 
-bool vectors16(int64_t H, size_t size, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
+// Whether every row lies on the 16-byte grid in whole vectors.
+bool on_grid(int64_t H, size_t size, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
     if (H * size % 16 != 0) return false;
     for (const void* p : ptrs)
         if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;
@@ -215,23 +221,32 @@ bool vectors16(int64_t H, size_t size, std::initializer_list<const void*> ptrs, 
     return true;
 }
 
-dim3 row_grid(int64_t tokens, int64_t vectors) {
+dim3 row_grid(int64_t tokens, int64_t H, int64_t size) {
+    const int64_t vectors = (H * size + 15) / 16;
     return dim3(static_cast<unsigned>(tokens), static_cast<unsigned>((vectors + kThreads - 1) / kThreads));
 }
 
-template <typename T, int V>
+template <int kSize, bool kAny>
+cudaError_t dispatch_launch(const PermuteArgs& a, const void* x, void* out, cudaStream_t stream) {
+    dispatch_kernel<kSize, kAny><<<row_grid(a.tokens, a.H, kSize), kThreads, 0, stream>>>(
+        static_cast<const unsigned char*>(x), a.ld_tokens, static_cast<unsigned char*>(out), a.ld_rows, a.H, a.rows,
+        a.k);
+    return cudaGetLastError();
+}
+
+template <typename T, bool kAny>
 cudaError_t combine_launch(const PermuteArgs& a, const void* y, const float* weights, void* out, cudaStream_t stream) {
-    combine_kernel<T, V><<<row_grid(a.tokens, (a.H + V - 1) / V), kThreads, 0, stream>>>(
+    combine_kernel<T, kAny><<<row_grid(a.tokens, a.H, sizeof(T)), kThreads, 0, stream>>>(
         static_cast<const T*>(y), a.ld_rows, a.rows, weights, a.k, static_cast<T*>(out), a.ld_tokens, a.H);
     return cudaGetLastError();
 }
 
-template <typename T, int V>
+template <typename T, bool kAny>
 cudaError_t combine_backward_launch(const PermuteArgs& a, const void* dout, const void* y, int64_t ldy,
                                     const float* weights, void* dy, float* dweights, cudaStream_t stream) {
     const int64_t slots = a.tokens * a.k;
     const int64_t blocks = (slots + kThreads / 32 - 1) / (kThreads / 32);
-    combine_backward_kernel<T, V><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
+    combine_backward_kernel<T, kAny><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
         static_cast<const T*>(dout), a.ld_tokens, static_cast<const T*>(y), ldy, a.rows, weights, a.k, slots,
         static_cast<T*>(dy), a.ld_rows, dweights, a.H);
     return cudaGetLastError();
@@ -266,37 +281,27 @@ cudaError_t launch_moe_plan(const int32_t* ids, int64_t slots, int experts, int6
 }
 
 cudaError_t launch_moe_dispatch(const PermuteArgs& a, bool f32, const void* x, void* out, cudaStream_t stream) {
-    const size_t size = f32 ? 4 : 2;
-    if (vectors16(a.H, size, {x, out}, {a.ld_tokens, a.ld_rows})) {
-        const int64_t per = 16 / static_cast<int64_t>(size), n = a.H / per;
-        dispatch_kernel<uint4><<<row_grid(a.tokens, n), kThreads, 0, stream>>>(
-            static_cast<const uint4*>(x), a.ld_tokens / per, static_cast<uint4*>(out), a.ld_rows / per, n, a.rows, a.k);
-    } else if (f32) {
-        dispatch_kernel<uint32_t><<<row_grid(a.tokens, a.H), kThreads, 0, stream>>>(
-            static_cast<const uint32_t*>(x), a.ld_tokens, static_cast<uint32_t*>(out), a.ld_rows, a.H, a.rows, a.k);
-    } else {
-        dispatch_kernel<bf16_bits><<<row_grid(a.tokens, a.H), kThreads, 0, stream>>>(
-            static_cast<const bf16_bits*>(x), a.ld_tokens, static_cast<bf16_bits*>(out), a.ld_rows, a.H, a.rows, a.k);
-    }
-    return cudaGetLastError();
+    const bool grid = on_grid(a.H, f32 ? 4 : 2, {x, out}, {a.ld_tokens, a.ld_rows});
+    if (f32) return grid ? dispatch_launch<4, false>(a, x, out, stream) : dispatch_launch<4, true>(a, x, out, stream);
+    return grid ? dispatch_launch<2, false>(a, x, out, stream) : dispatch_launch<2, true>(a, x, out, stream);
 }
 
 cudaError_t launch_moe_combine(const PermuteArgs& a, bool f32, const void* y, const float* weights, void* out,
                                cudaStream_t stream) {
-    const bool vec = vectors16(a.H, f32 ? 4 : 2, {y, out}, {a.ld_tokens, a.ld_rows});
-    if (f32) return vec ? combine_launch<float, 4>(a, y, weights, out, stream)
-                        : combine_launch<float, 1>(a, y, weights, out, stream);
-    return vec ? combine_launch<bf16_bits, 8>(a, y, weights, out, stream)
-               : combine_launch<bf16_bits, 1>(a, y, weights, out, stream);
+    const bool grid = on_grid(a.H, f32 ? 4 : 2, {y, out}, {a.ld_tokens, a.ld_rows});
+    if (f32) return grid ? combine_launch<float, false>(a, y, weights, out, stream)
+                         : combine_launch<float, true>(a, y, weights, out, stream);
+    return grid ? combine_launch<bf16_bits, false>(a, y, weights, out, stream)
+                : combine_launch<bf16_bits, true>(a, y, weights, out, stream);
 }
 
 cudaError_t launch_moe_combine_backward(const PermuteArgs& a, bool f32, const void* dout, const void* y, int64_t ldy,
                                         const float* weights, void* dy, float* dweights, cudaStream_t stream) {
-    const bool vec = vectors16(a.H, f32 ? 4 : 2, {dout, y, dy}, {a.ld_tokens, ldy, a.ld_rows});
-    if (f32) return vec ? combine_backward_launch<float, 4>(a, dout, y, ldy, weights, dy, dweights, stream)
-                        : combine_backward_launch<float, 1>(a, dout, y, ldy, weights, dy, dweights, stream);
-    return vec ? combine_backward_launch<bf16_bits, 8>(a, dout, y, ldy, weights, dy, dweights, stream)
-               : combine_backward_launch<bf16_bits, 1>(a, dout, y, ldy, weights, dy, dweights, stream);
+    const bool grid = on_grid(a.H, f32 ? 4 : 2, {dout, y, dy}, {a.ld_tokens, ldy, a.ld_rows});
+    if (f32) return grid ? combine_backward_launch<float, false>(a, dout, y, ldy, weights, dy, dweights, stream)
+                         : combine_backward_launch<float, true>(a, dout, y, ldy, weights, dy, dweights, stream);
+    return grid ? combine_backward_launch<bf16_bits, false>(a, dout, y, ldy, weights, dy, dweights, stream)
+                : combine_backward_launch<bf16_bits, true>(a, dout, y, ldy, weights, dy, dweights, stream);
 }
 
 }  // namespace mxq
