@@ -69,7 +69,7 @@ __device__ __forceinline__ float squares(const T* p, int64_t lo, int64_t hi) {
     float s = 0.0f;
     for (int64_t i = threadIdx.x; i < vectors; i += kThreads) {
         float f[V];
-        unpack<T>(load16<sizeof(T), false>(p + head, i * V, n), f);
+        unpack<T>(*reinterpret_cast<const uint4*>(p + head + i * V), f);
 #pragma unroll
         for (int c = 0; c < V; ++c) s = fmaf(f[c], f[c], s);
     }
@@ -125,10 +125,10 @@ __device__ __forceinline__ void scale(const T* in, T* out, int64_t lo, int64_t h
     const int64_t vectors = (n - head) / V;
     for (int64_t i = threadIdx.x; i < vectors; i += kThreads) {
         float f[V];
-        unpack<T>(load16<sizeof(T), false>(in + head, i * V, n), f);
+        unpack<T>(*reinterpret_cast<const uint4*>(in + head + i * V), f);
 #pragma unroll
         for (int k = 0; k < V; ++k) f[k] *= c;
-        store16<sizeof(T), false>(out + head, i * V, n, pack<T>(f));
+        *reinterpret_cast<uint4*>(out + head + i * V) = pack<T>(f);
     }
     const int64_t tail = head + vectors * V;
     const int64_t i = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;

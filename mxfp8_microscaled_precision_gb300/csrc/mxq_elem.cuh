@@ -55,14 +55,66 @@ __device__ __forceinline__ uint4 pack(const float (&f)[kVec16<T>]) {
                           __float_as_uint(f[3]));
 }
 
+// ---- pairs of floats -----------------------------------------------------------------
+//
+// Two FP32 values in one 64-bit register: sm_103 adds, multiplies and fuses pairs in one
+// instruction (each half rounded as the scalar instruction rounds it).
+
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    return static_cast<f32x2>(__float_as_uint(lo)) | (static_cast<f32x2>(__float_as_uint(hi)) << 32);
+}
+__device__ __forceinline__ float lo_of(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi_of(f32x2 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// 16 bytes as pairs and back.
+template <typename T>
+__device__ __forceinline__ void unpack2(const uint4 w, f32x2 (&f)[kVec16<T> / 2]) {
+    float s[kVec16<T>];
+    unpack<T>(w, s);
+#pragma unroll
+    for (int i = 0; i < kVec16<T> / 2; ++i) f[i] = pair(s[2 * i], s[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack2(const f32x2 (&f)[kVec16<T> / 2]) {
+    float s[kVec16<T>];
+#pragma unroll
+    for (int i = 0; i < kVec16<T> / 2; ++i) s[2 * i] = lo_of(f[i]), s[2 * i + 1] = hi_of(f[i]);
+    return pack<T>(s);
+}
+
 // ---- rows that start at any element ------------------------------------------------
 //
 // A row whose length is odd leaves the next one off the 16-byte grid.  Element by element such rows
-// move at a third of the bandwidth (64 bytes a request), so they are moved in
-// vectors too: a load takes the two aligned vectors that its elements lie in
-// and shifts them together, a store gets the missing elements of an aligned
-// vector from the next lane.  Only a row's first and last vectors go element by
-// element, so nothing outside the row is touched.
+// move at a third of the bandwidth (64 bytes a request), so they are moved in vectors
+// too, on the 16-byte grid of the memory itself: with `lead` the elements between the last
+// boundary and the row's first one, vector q holds the elements [q V - lead, q V - lead + V).  Only a row's
+// first and last vectors, which it shares with its neighbours, go element by element,
+// so nothing outside the row is touched.  Where another tensor's row has another lead, the two
+// aligned vectors that the wanted elements lie in are loaded and shifted together.
+
+// Elements of the row at p before its first one on the 16-byte grid.
+template <int kSize>
+__device__ __forceinline__ int lead_of(const void* p) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u) / kSize;
+}
 
 // Bytes off .. off + 15 of the 32 bytes a, b (off even, the same for most lanes).
 __device__ __forceinline__ uint4 shift16(const uint4 a, const uint4 b, unsigned off) {
@@ -82,113 +134,133 @@ __device__ __forceinline__ uint4 shift16(const uint4 a, const uint4 b, unsigned 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Elements [i, i + V) of a row of n as 16 bytes, zeros from n on (i a multiple
-// of V = 16 / kSize).  kAny: the row may start at any element; otherwise it is
-// 16-byte aligned and n a multiple of V.
-template <int kSize, bool kAny>
-__device__ __forceinline__ uint4 load16(const void* row, int64_t i, int64_t n) {
-    constexpr int V = 16 / kSize;
-    const unsigned char* p = static_cast<const unsigned char*>(row) + i * kSize;
-    if (i >= n) return make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (!kAny) {
-        return *reinterpret_cast<const uint4*>(p);
-    } else {
-        const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 15u);
-        if (off == 0u && i + V <= n) return *reinterpret_cast<const uint4*>(p);
-        if (i > 0 && i + 2 * V - static_cast<int>(off) / kSize <= n) {
-            const uint4* q = reinterpret_cast<const uint4*>(p - off);
-            return shift16(q[0], q[1], off);
-        }
-        uint32_t w[4] = {};
+// Elements [i, i + V) (V = 16 / kSize) of a row of n, one by one; 0 outside the row.
+template <int kSize>
+__device__ __noinline__ uint4 load_ends(const void* row, int i, int n) {
+    uint32_t w[4] = {};
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-            if (i + c < n) {
-                if constexpr (kSize == 2)
-                    w[c / 2] |= static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(p)[c]) << (16 * (c & 1));
-                else
-                    w[c] = reinterpret_cast<const uint32_t*>(p)[c];
-            }
+    for (int c = 0; c < 16 / kSize; ++c) {
+        if (i + c >= 0 && i + c < n) {
+            if constexpr (kSize == 2)
+                w[c / 2] |= static_cast<uint32_t>(static_cast<const unsigned short*>(row)[i + c]) << (16 * (c & 1));
+            else
+                w[c] = static_cast<const uint32_t*>(row)[i + c];
         }
-        return make_uint4(w[0], w[1], w[2], w[3]);
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Elements a .. b - 1 (of the V that v holds) to p, one by one.
 template <int kSize>
-__device__ __forceinline__ void store_some(unsigned char* p, const uint4 v, int a, int b) {
+__device__ __noinline__ void store_ends(void* row, int i, int n, const uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int c = 0; c < 16 / kSize; ++c) {
-        if (c >= a && c < b) {
+        if (i + c >= 0 && i + c < n) {
             if constexpr (kSize == 2)
-                reinterpret_cast<unsigned short*>(p)[c] = static_cast<unsigned short>(w[c / 2] >> (16 * (c & 1)));
+                static_cast<unsigned short*>(row)[i + c] = static_cast<unsigned short>(w[c / 2] >> (16 * (c & 1)));
             else
-                reinterpret_cast<uint32_t*>(p)[c] = w[c];
+                static_cast<uint32_t*>(row)[i + c] = w[c];
         }
     }
 }
 
-// Stores elements [i, i + V) of a row of n.  With kAny every lane of the warp
-// takes part (a lane with nothing to store has i >= n), and within each `width` lanes
-// (a power of two) lane l + 1 holds the V elements after lane l's of the same row.
+// Elements [i, i + V) of a row of n, where element i lies on the 16-byte grid; 0 outside the
+// row.  Without kAny the row holds whole vectors, from its first element on.
 template <int kSize, bool kAny>
-__device__ __forceinline__ void store16(void* row, int64_t i, int64_t n, const uint4 v, int width = 32) {
-    constexpr int V = 16 / kSize;
-    unsigned char* p = static_cast<unsigned char*>(row) + i * kSize;
-    if constexpr (!kAny) {
-        if (i < n) *reinterpret_cast<uint4*>(p) = v;
-    } else {
-        const int lane = static_cast<int>(threadIdx.x) & (width - 1);
-        uint4 next;
-        next.x = __shfl_down_sync(0xFFFFFFFFu, v.x, 1);
-        next.y = __shfl_down_sync(0xFFFFFFFFu, v.y, 1);
-        next.z = __shfl_down_sync(0xFFFFFFFFu, v.z, 1);
-        next.w = __shfl_down_sync(0xFFFFFFFFu, v.w, 1);
-        const int m = i >= n ? 0 : (n - i < V ? static_cast<int>(n - i) : V);   // elements of this lane
-        const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 15u);
-        if (off == 0u) {
-            if (m == V) *reinterpret_cast<uint4*>(p) = v;
-            else store_some<kSize>(p, v, 0, m);
-            return;
-        }
-        const int head = V - static_cast<int>(off) / kSize;   // elements before the aligned vector
-        if (m == V && lane < width - 1 && n - i - V >= head)
-            *reinterpret_cast<uint4*>(p + (16u - off)) = shift16(v, next, 16u - off);
-        else
-            store_some<kSize>(p, v, head, m);
-        if (lane == 0 || m < head)   // not in the vector that the lane before stored
-            store_some<kSize>(p, v, 0, m < head ? m : head);
-    }
+__device__ __forceinline__ uint4 load16(const void* row, int i, int n) {
+    const void* p = static_cast<const unsigned char*>(row) + static_cast<int64_t>(i) * kSize;
+    if (kAny ? i >= 0 && i + 16 / kSize <= n : i < n) return *static_cast<const uint4*>(p);
+    if (kAny && i < n) return load_ends<kSize>(row, i, n);
+    return make_uint4(0u, 0u, 0u, 0u);
 }
 
-// V = kVec16<T> parameters [i, i + V) of W (weights and the like, n of them, read
-// by many rows) as floats; `otherwise` without a tensor.  kAny as for load16; the tensor
-// starts on 16 bytes otherwise.
+// alike: element i lies on the 16-byte grid of this row too (kAny only).
+template <int kSize, bool kAny>
+__device__ __forceinline__ void store16(void* row, int i, int n, const uint4 v, bool alike = true) {
+    void* p = static_cast<unsigned char*>(row) + static_cast<int64_t>(i) * kSize;
+    if (kAny ? alike && i >= 0 && i + 16 / kSize <= n : i < n) *static_cast<uint4*>(p) = v;
+    else if (kAny && i < n) store_ends<kSize>(row, i, n, v);
+}
+
+// Whether the elements [i, i + V) of rows of n with any lead can be loaded by two vectors
+// each without leaving the row.
+template <int kSize>
+__device__ __forceinline__ bool is_inner(int i, int n) {
+    constexpr int V = 16 / kSize;
+    return i >= V - 1 && i + 2 * V <= n;
+}
+
+// Elements [i, i + V) of a row with any lead (is_inner holds).
+template <int kSize>
+__device__ __forceinline__ uint4 load_inner(const void* row, int i) {
+    const unsigned char* p = static_cast<const unsigned char*>(row) + static_cast<int64_t>(i) * kSize;
+    const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 15u);
+    const uint4* q = reinterpret_cast<const uint4*>(p - off);
+    return shift16(q[0], q[1], off);
+}
+
+// V parameters [i, i + V) of W (weights and the like, n of them, read by many rows) as
+// pairs; `otherwise` without a tensor, 0 outside it.  Without kAny the tensor starts on 16 bytes and
+// i is a multiple of V.
 template <typename W, int V, bool kAny>
-__device__ __forceinline__ void load_params(const W* p, int64_t i, int64_t n, float otherwise, float (&f)[V]) {
+__device__ __forceinline__ void load_params2(const W* p, int i, int n, float otherwise, f32x2 (&f)[V / 2]) {
     if (p == nullptr) {
 #pragma unroll
-        for (int c = 0; c < V; ++c) f[c] = otherwise;
-    } else if constexpr (V * sizeof(W) == 16) {
-        unpack<W>(load16<sizeof(W), kAny>(p, i, n), f);
-    } else if constexpr (V * sizeof(W) == 32) {   // 8 FP32 parameters of 8 BF16 elements
-        float lo[4], hi[4];
-        unpack<W>(load16<sizeof(W), kAny>(p, i, n), lo);
-        unpack<W>(load16<sizeof(W), kAny>(p, i + 4, n), hi);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) f[c] = lo[c], f[c + 4] = hi[c];
-    } else {   // 4 BF16 parameters of 4 FP32 elements
-        static_assert(V * sizeof(W) == 8, "vectors of 4 or 8");
-        if (!kAny && i < n) {
-            const uint2 w = *reinterpret_cast<const uint2*>(p + i);
-            f[0] = __uint_as_float(w.x << 16), f[1] = __uint_as_float(w.x & 0xFFFF0000u);
-            f[2] = __uint_as_float(w.y << 16), f[3] = __uint_as_float(w.y & 0xFFFF0000u);
+        for (int c = 0; c < V / 2; ++c) f[c] = pair(otherwise, otherwise);
+    } else if constexpr (V * sizeof(W) == 8) {   // 4 BF16 parameters of 4 FP32 elements
+        uint2 w = make_uint2(0u, 0u);
+        if (!kAny) {
+            if (i < n) w = *reinterpret_cast<const uint2*>(p + i);
         } else {
+            const uint4 v = load_ends<2>(p, i, i + 4 < n ? i + 4 : n);
+            w = make_uint2(v.x, v.y);
+        }
+        f[0] = pair(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u));
+        f[1] = pair(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+    } else {
+        constexpr int kPer = kVec16<W>;   // parameters of 16 bytes: V, or half of it
 #pragma unroll
-            for (int c = 0; c < V; ++c) f[c] = i + c < n ? to_float(p[i + c]) : 0.0f;
+        for (int k = 0; k < V / kPer; ++k) {
+            const int at = i + k * kPer;
+            uint4 v;
+            if (!kAny) v = load16<sizeof(W), false>(p, at, n);
+            else v = is_inner<sizeof(W)>(at, n) ? load_inner<sizeof(W)>(p, at) : load_ends<sizeof(W)>(p, at, n);
+            f32x2 s[kPer / 2];
+            unpack2<W>(v, s);
+#pragma unroll
+            for (int c = 0; c < kPer / 2; ++c) f[k * kPer / 2 + c] = s[c];
         }
     }
 }
+
+// V parameters of a thread's columns in the registers of their own type, for a loop over rows.
+template <typename W, int V>
+struct Params {
+    uint32_t u[V * sizeof(W) / 4];
+    template <bool kAny>
+    __device__ __forceinline__ void load(const W* p, int i, int n, float otherwise) {
+        f32x2 f[V / 2];
+        load_params2<W, V, kAny>(p, i, n, otherwise, f);
+#pragma unroll
+        for (int c = 0; c < V / 2; ++c) {
+            if constexpr (sizeof(W) == 2) {
+                u[c] = cvt_bf16x2(lo_of(f[c]), hi_of(f[c]));   // exact: 0, 1 or a BF16 value
+            } else {
+                u[2 * c] = __float_as_uint(lo_of(f[c]));
+                u[2 * c + 1] = __float_as_uint(hi_of(f[c]));
+            }
+        }
+    }
+    __device__ __forceinline__ void get(f32x2 (&f)[V / 2]) const {
+#pragma unroll
+        for (int c = 0; c < V / 2; ++c) {
+            if constexpr (sizeof(W) == 2)
+                f[c] = pair(__uint_as_float(u[c] << 16), __uint_as_float(u[c] & 0xFFFF0000u));
+            else
+                f[c] = pair(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1]));
+        }
+    }
+};
 
 // Sum over the warp, the same order on every call, the result in all lanes.
 __device__ __forceinline__ float warp_sum(float v) {

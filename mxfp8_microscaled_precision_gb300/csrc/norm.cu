@@ -9,7 +9,11 @@
 // (no cancellation of mean(x^2) - mu^2).  Backward: a fixed number of blocks
 // walks over the rows; a thread owns the same columns in every row and keeps its
 // share of dw and db in FP32 registers, the shares meet in a workspace and are
-// added in a fixed order.  Both are bound by memory.
+// added in a fixed order.
+//
+// kAny: rows that start at any element (mxq_elem.cuh), in vectors of x's rows.  dy and the
+// result mostly start like x, as rows of the same length in buffers of their own do; where
+// one does not, it goes element by element.  The sums are formed in the same order either way.
 
 #include <cuda_runtime.h>
 
@@ -24,90 +28,152 @@ namespace mxq {
 namespace {
 
 constexpr int kSMs = 152;
-constexpr int64_t kRingBytes = 200 * 1024;   // rows in flight of an SM's blocks (backward)
+constexpr int64_t kShortCols = 512;   // rows up to this long need no ring (backward)
 
 // ---- sums over the threads of a row ---------------------------------------------------
 //
-// A row belongs to tpr threads: a part of a warp (4 .. 32 lanes), or the whole
-// block.  Sums are taken in the same order on every call and known to all of them.
+// A row belongs to tpr threads: a part of a warp (4 .. 32 lanes), or several
+// warps.  Sums are taken in the same order on every call and known to all of them.
 
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
     for (int d = lanes >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
     return v;
 }
 
-// sh: 32 floats per call site, not written again before every thread of the
-// block has passed another barrier.
+// Rows of whole blocks.  sh: 32 floats per call site, not written again before every
+// thread of the block has passed another barrier.
 __device__ __forceinline__ float row_sum(float v, int tpr, float* sh) {
     if (tpr <= 32) return lanes_sum(v, tpr);
     v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
     __syncthreads();
-    float s = 0.0f;
-    for (int w = 0; w < (tpr >> 5); ++w) s += sh[w];
-    return s;
+    return warp_sum((threadIdx.x & 31) < (tpr >> 5) ? sh[threadIdx.x & 31] : 0.0f);
+}
+
+__device__ __forceinline__ f32x2 warp_sum2(f32x2 v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    return v;
+}
+
+// 1 / sqrt(v): the approximation (2 ulp) and a step of Newton's method.
+__device__ __forceinline__ float inverse_root(float v) {
+    const float r = rsqrtf(v);
+    const float better = r * fmaf(-0.5f * v * r, r, 1.5f);
+    return v > 0.0f && v < INFINITY ? better : r;   // 0 and infinity: r is exact, the step would be NaN
+}
+
+// v with the elements outside [0, cols) set to 0; i: index of its first element.
+template <typename T>
+__device__ __forceinline__ uint4 inside(const uint4 v, int i, int cols) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if constexpr (sizeof(T) == 2) {
+            const int e = i + 2 * c;
+            w[c] &= (e >= 0 && e < cols ? 0xFFFFu : 0u) | (e + 1 >= 0 && e + 1 < cols ? 0xFFFF0000u : 0u);
+        } else {
+            w[c] = i + c >= 0 && i + c < cols ? w[c] : 0u;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // ---- forward ----------------------------------------------------------------------------
 
-// Thread i of a row holds the vectors i, i + tpr, ... (kN of 16 bytes).
+// Thread i of a row holds the vectors i, i + tpr, ... (kN of 16 bytes), packed as they
+// came: unpacking them in each pass costs less than the registers of 32-bit copies.  On
+// the grid a block has one row (or one for each group of lanes), and the parameters come from the
+// L1; with kAny they would have to be shifted for every row, so the blocks are fewer, each
+// keeps its threads' parameters and walks over rows that are a multiple of 8
+// apart and so all start alike.
 template <typename T, typename W, int kN, bool kAny>
 __global__ void __launch_bounds__(kN == 8 ? 512 : 1024) norm_kernel(const NormArgs a, int tpr) {
-    constexpr int V = kVec16<T>;
+    constexpr int V = kVec16<T>, H = V / 2, S = sizeof(T);
+    constexpr bool kHeld = kAny && kN <= 2;
     __shared__ float sh[2][32];
     const int group = threadIdx.x / tpr, at = threadIdx.x % tpr;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + group;
-    const bool live = row < a.rows;
-    const int64_t cols = live ? a.cols : 0;   // a row past the end loads and stores nothing
-    const T* x = static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx;
-    T* y = static_cast<T*>(a.y) + (live ? row : 0) * a.ldy;
+    const int64_t row_first = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + group;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x / tpr);
+    const int first = at * V - (kAny ? lead_of<S>(static_cast<const T*>(a.x) + row_first * a.ldx) : 0);
     const float inv = 1.0f / static_cast<float>(a.cols);
-    uint4 q[kN];
-#pragma unroll
-    for (int n = 0; n < kN; ++n) q[n] = load16<sizeof(T), kAny>(x, (n * tpr + at) * V, cols);
-    float sum = 0.0f;
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-        float f[V];
-        unpack<T>(q[n], f);
-#pragma unroll
-        for (int c = 0; c < V; ++c) sum += f[c];   // elements past the row are 0
-    }
-    const float mu = row_sum(sum, tpr, sh[0]) * inv;
-    float sq = 0.0f;
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-        float f[V];
-        unpack<T>(q[n], f);
-        const int64_t i = (n * tpr + at) * V;
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-            const float d = f[c] - mu;
-            if (kAny ? i + c < cols : i < cols) sq = fmaf(d, d, sq);
-        }
-    }
-    const float r = 1.0f / sqrtf(row_sum(sq, tpr, sh[1]) * inv + a.eps);
-    if (live && at == 0) {
-        a.mean[row] = mu;
-        a.rstd[row] = r;
-    }
     const W* w = static_cast<const W*>(a.weight);
     const W* b = static_cast<const W*>(a.shift);
+    Params<W, V> held_w[kHeld ? kN : 1], held_b[kHeld ? kN : 1];
+    if constexpr (kHeld) {
 #pragma unroll
-    for (int n = 0; n < kN; ++n) {
-        const int64_t i = (n * tpr + at) * V;
-        float f[V], fw[V], fb[V];
-        unpack<T>(q[n], f);
-        load_params<W, V, kAny>(w, i, cols, 1.0f, fw);
-        load_params<W, V, kAny>(b, i, cols, 0.0f, fb);
+        for (int n = 0; n < kN; ++n) {
+            held_w[n].template load<true>(w, first + n * tpr * V, static_cast<int>(a.cols), 1.0f);
+            held_b[n].template load<true>(b, first + n * tpr * V, static_cast<int>(a.cols), 0.0f);
+        }
+    }
+    for (int64_t row0 = row_first - group; row0 < a.rows; row0 += step) {   // one turn without kAny
+        const int64_t row = row0 + group;
+        const bool live = row < a.rows;
+        const int cols = live ? static_cast<int>(a.cols) : -V;   // a row past the end loads and stores nothing
+        const T* x = static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx;
+        T* y = static_cast<T*>(a.y) + (live ? row : 0) * a.ldy;
+        uint4 q[kN];
 #pragma unroll
-        for (int c = 0; c < V; ++c) f[c] = fmaf((f[c] - mu) * r, fw[c], fb[c]);
-        store16<sizeof(T), kAny>(y, i, cols, pack<T>(f), tpr < 32 ? tpr : 32);
+        for (int n = 0; n < kN; ++n) q[n] = load16<S, kAny>(x, first + n * tpr * V, cols);
+        f32x2 sum = 0;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            f32x2 f[H];
+            unpack2<T>(q[n], f);
+#pragma unroll
+            for (int c = 0; c < H; ++c) sum = add2(sum, f[c]);   // elements outside the row are 0
+        }
+        const float mu = row_sum(lo_of(sum) + hi_of(sum), tpr, sh[0]) * inv;
+        const f32x2 minus = pair(-mu, -mu);
+        f32x2 sq = 0;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int i = first + n * tpr * V;
+            if (i >= cols) continue;
+            f32x2 f[H], part = 0;
+            unpack2<T>(q[n], f);
+#pragma unroll
+            for (int c = 0; c < H; ++c) {
+                f32x2 d = add2(f[c], minus);
+                if (kAny && (i < 0 || i + V > cols)) {   // a vector that the row has a part of
+                    const int e = i + 2 * c;
+                    d = pair(e >= 0 && e < cols ? lo_of(d) : 0.0f, e + 1 >= 0 && e + 1 < cols ? hi_of(d) : 0.0f);
+                }
+                part = fma2(d, d, part);
+            }
+            sq = add2(sq, part);
+        }
+        const float r = inverse_root(row_sum(lo_of(sq) + hi_of(sq), tpr, sh[1]) * inv + a.eps);
+        if (live && at == 0) {
+            a.mean[row] = mu;
+            a.rstd[row] = r;
+        }
+        const f32x2 rr = pair(r, r);
+        const bool alike = kAny && lead_of<S>(y) == lead_of<S>(x);
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int i = first + n * tpr * V;
+            if (i >= cols) continue;
+            f32x2 f[H], fw[H], fb[H];
+            unpack2<T>(q[n], f);
+            if constexpr (kHeld) {
+                held_w[n].get(fw);
+                held_b[n].get(fb);
+            } else {
+                load_params2<W, V, kAny>(w, i, cols, 1.0f, fw);
+                load_params2<W, V, kAny>(b, i, cols, 0.0f, fb);
+            }
+#pragma unroll
+            for (int c = 0; c < H; ++c) f[c] = fma2(mul2(add2(f[c], minus), rr), fw[c], fb[c]);
+            store16<S, kAny>(y, i, cols, pack2<T>(f), alike);
+        }
+        if (!kAny) return;
     }
 }
 
-// Rows longer than the registers of a block hold (512 threads x 8 vectors):
-// read again in each pass, one block per row.
+// Rows longer than the registers of a block hold: element by element, read again in
+// each pass, one block per row.
 template <typename T, typename W>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
     __shared__ float sh[2][32];
@@ -116,276 +182,452 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
     T* y = static_cast<T*>(a.y) + row * a.ldy;
     const W* w = static_cast<const W*>(a.weight);
     const W* b = static_cast<const W*>(a.shift);
-    const float inv = 1.0f / static_cast<float>(a.cols);
+    const int cols = static_cast<int>(a.cols);
+    const float inv = 1.0f / static_cast<float>(cols);
     float sum = 0.0f, sq = 0.0f;
-    for (int64_t i = threadIdx.x; i < a.cols; i += blockDim.x) sum += to_float(x[i]);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < cols; i += blockDim.x) sum += to_float(x[i]);
     const float mu = row_sum(sum, blockDim.x, sh[0]) * inv;
-    for (int64_t i = threadIdx.x; i < a.cols; i += blockDim.x) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < cols; i += blockDim.x) {
         const float d = to_float(x[i]) - mu;
         sq = fmaf(d, d, sq);
     }
-    const float r = 1.0f / sqrtf(row_sum(sq, blockDim.x, sh[1]) * inv + a.eps);
+    const float r = inverse_root(row_sum(sq, blockDim.x, sh[1]) * inv + a.eps);
     if (threadIdx.x == 0) {
         a.mean[row] = mu;
         a.rstd[row] = r;
     }
-    for (int64_t i = threadIdx.x; i < a.cols; i += blockDim.x)
+    for (int i = threadIdx.x; i < cols; i += blockDim.x)
         y[i] = from_float<T>(fmaf((to_float(x[i]) - mu) * r, w ? to_float(w[i]) : 1.0f, b ? to_float(b[i]) : 0.0f));
 }
 
 // ---- backward ---------------------------------------------------------------------------
 
-// One vector of x and dy: adds to the column sums, and to sum(u), sum(u h) of the row.
-template <int V>
-__device__ __forceinline__ void add_vector(const float (&fx)[V], const float (&g)[V], const float (&fw)[V], float mu,
-                                           float r, float (&dw)[V], float (&db)[V], float2& sum) {
+// One vector of x and dy: adds to the column sums, and to sum(u), sum(u h) of the row;
+// leaves h = x r - mu r in x and u in g.  rr = (r, r), off = (-mu r, -mu r).  Elements outside the
+// row are 0 in both and add nothing.
+template <int H>
+__device__ __forceinline__ void add_vector(f32x2 (&x)[H], f32x2 (&g)[H], const f32x2 (&w)[H], f32x2 rr, f32x2 off,
+                                           f32x2 (&dw)[H], f32x2 (&db)[H], f32x2& s1, f32x2& s2) {
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-        const float h = (fx[c] - mu) * r;
-        dw[c] = fmaf(g[c], h, dw[c]);
-        db[c] += g[c];
-        const float u = g[c] * fw[c];
-        sum.x += u;
-        sum.y = fmaf(u, h, sum.y);
+    for (int c = 0; c < H; ++c) {
+        x[c] = fma2(x[c], rr, off);
+        dw[c] = fma2(g[c], x[c], dw[c]);
+        db[c] = add2(db[c], g[c]);
+        g[c] = mul2(g[c], w[c]);
+        s1 = add2(s1, g[c]);
+        s2 = fma2(g[c], x[c], s2);
     }
 }
 
-// dx of one vector; m1 = mean(u), m2 = mean(u h).
-template <int V>
-__device__ __forceinline__ void dx_vector(const float (&fx)[V], float (&g)[V], const float (&fw)[V], float mu, float r,
-                                          float m1, float m2) {
+// dx = u r + (-m1 r) + h (-m2 r) of one vector, in u; c1 = -m1 r, c2 = -m2 r.
+template <int H>
+__device__ __forceinline__ void dx_vector(const f32x2 (&h)[H], f32x2 (&u)[H], f32x2 rr, f32x2 c1, f32x2 c2) {
 #pragma unroll
-    for (int c = 0; c < V; ++c) g[c] = r * (g[c] * fw[c] - m1 - (fx[c] - mu) * r * m2);
+    for (int c = 0; c < H; ++c) u[c] = fma2(u[c], rr, fma2(h[c], c2, c1));
 }
 
-// Short rows (up to 512 elements): tpr = 4 .. 32 lanes a row, no barrier per row.
-// The groups' column sums meet by shuffles within a warp and in shared memory over the warps.
+// One thread's column sums of one vector into (or onto) those of the block.
+template <int H>
+__device__ __forceinline__ void put_columns(float* sums, int i, int cols, bool add, const f32x2 (&dw)[H],
+                                            const f32x2 (&db)[H]) {
+#pragma unroll
+    for (int c = 0; c < 2 * H; ++c) {
+        if (i + c < 0 || i + c >= cols) continue;
+        const float fw = c & 1 ? hi_of(dw[c / 2]) : lo_of(dw[c / 2]);
+        const float fb = c & 1 ? hi_of(db[c / 2]) : lo_of(db[c / 2]);
+        sums[i + c] = (add ? sums[i + c] : 0.0f) + fw;
+        sums[cols + i + c] = (add ? sums[cols + i + c] : 0.0f) + fb;
+    }
+}
+
+// Short rows: tpr = 4 .. 32 lanes a row, no barrier per row.  A group's rows are gridDim.x x
+// groups apart, a multiple of 8 rows, so they all start alike and the group's threads
+// keep their columns.
 constexpr int kShortThreads = 256;
 template <typename T, typename W, int kN, bool kAny>
 __global__ void __launch_bounds__(kShortThreads, 2) norm_backward_short_kernel(const NormBackwardArgs a, int tpr) {
-    constexpr int V = kVec16<T>;
+    constexpr int V = kVec16<T>, H = V / 2, S = sizeof(T);
     extern __shared__ float cols_sh[];   // [2][cols]: column sums of the block
-    const int per = kShortThreads / tpr;
+    const int groups = kShortThreads / tpr;
     const int group = threadIdx.x / tpr, at = threadIdx.x % tpr, lane = threadIdx.x & 31;
-    const W* w = static_cast<const W*>(a.weight);
-    const float inv = 1.0f / static_cast<float>(a.cols);
-    float dw[kN][V] = {}, db[kN][V] = {};
-    const int64_t step = static_cast<int64_t>(gridDim.x) * per;
-    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * per; row0 < a.rows; row0 += step) {
+    const int64_t row_first = static_cast<int64_t>(blockIdx.x) * groups + group;
+    const int all = static_cast<int>(a.cols);
+    const int first = at * V - (kAny ? lead_of<S>(static_cast<const T*>(a.x) + row_first * a.ldx) : 0);
+    const float inv = 1.0f / static_cast<float>(all);
+    f32x2 w[kN][H];
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+        load_params2<W, V, kAny>(static_cast<const W*>(a.weight), first + n * tpr * V, all, 1.0f, w[n]);
+    f32x2 dw[kN][H] = {}, db[kN][H] = {};
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < a.rows; row0 += step) {
         const int64_t row = row0 + group;
         const bool live = row < a.rows;
-        const int64_t cols = live ? a.cols : 0, at_row = live ? row : 0;
+        const int64_t at_row = live ? row : 0;
+        const int cols = live ? all : -V;   // a row past the end loads and stores nothing
         const T* x = static_cast<const T*>(a.x) + at_row * a.ldx;
         const T* dy = static_cast<const T*>(a.dy) + at_row * a.lddy;
         T* dx = static_cast<T*>(a.dx) + at_row * a.lddx;
         uint4 qx[kN], qg[kN];
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-            qx[n] = load16<sizeof(T), kAny>(x, (n * tpr + at) * V, cols);
-            qg[n] = load16<sizeof(T), kAny>(dy, (n * tpr + at) * V, cols);   // 0 past the row: adds nothing
+            qx[n] = load16<S, kAny>(x, first + n * tpr * V, cols);
+            if (!kAny || lead_of<S>(dy) == lead_of<S>(x)) qg[n] = load16<S, kAny>(dy, first + n * tpr * V, cols);
+            else qg[n] = load_ends<S>(dy, first + n * tpr * V, cols);
         }
-        // elements past the row, and rows past the end, add nothing: their dy is 0
         const float mu = live ? a.mean[at_row] : 0.0f, r = live ? a.rstd[at_row] : 0.0f;
-        float2 sum = make_float2(0.0f, 0.0f);
+        const f32x2 rr = pair(r, r), off = pair(-mu * r, -mu * r);
+        f32x2 h[kN][H], u[kN][H], s1 = 0, s2 = 0;
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-            float fx[V], g[V], fw[V];
-            unpack<T>(qx[n], fx);
-            unpack<T>(qg[n], g);
-            load_params<W, V, kAny>(w, (n * tpr + at) * V, a.cols, 1.0f, fw);
-            add_vector<V>(fx, g, fw, mu, r, dw[n], db[n], sum);
+            unpack2<T>(qx[n], h[n]);
+            unpack2<T>(qg[n], u[n]);
+            add_vector<H>(h[n], u[n], w[n], rr, off, dw[n], db[n], s1, s2);
         }
-        const float m1 = lanes_sum(sum.x, tpr) * inv, m2 = lanes_sum(sum.y, tpr) * inv;
+        const float m1 = lanes_sum(lo_of(s1) + hi_of(s1), tpr) * inv, m2 = lanes_sum(lo_of(s2) + hi_of(s2), tpr) * inv;
+        const f32x2 c1 = pair(-m1 * r, -m1 * r), c2 = pair(-m2 * r, -m2 * r);
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-            float fx[V], g[V], fw[V];
-            unpack<T>(qx[n], fx);
-            unpack<T>(qg[n], g);
-            load_params<W, V, kAny>(w, (n * tpr + at) * V, a.cols, 1.0f, fw);
-            dx_vector<V>(fx, g, fw, mu, r, m1, m2);
-            store16<sizeof(T), kAny>(dx, (n * tpr + at) * V, cols, pack<T>(g), tpr);
+            dx_vector<H>(h[n], u[n], rr, c1, c2);
+            store16<S, kAny>(dx, first + n * tpr * V, cols, pack2<T>(u[n]), !kAny || lead_of<S>(dx) == lead_of<S>(x));
         }
     }
-    // groups of the warp, then the block's warps one after the other
+    // The groups' sums one after the other; those of a warp, which start alike on the grid, meet by shuffles.
+    const int turns = kAny ? groups : kShortThreads / 32;
+    const int turn = kAny ? group : static_cast<int>(threadIdx.x >> 5);
+    if (!kAny) {
 #pragma unroll
-    for (int n = 0; n < kN; ++n) {
+        for (int n = 0; n < kN; ++n) {
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-            for (int d = tpr; d < 32; d <<= 1) {
-                dw[n][c] += __shfl_xor_sync(0xFFFFFFFFu, dw[n][c], d);
-                db[n][c] += __shfl_xor_sync(0xFFFFFFFFu, db[n][c], d);
-            }
-        }
-    }
-    for (int warp = 0; warp < kShortThreads / 32; ++warp) {
-        if ((threadIdx.x >> 5) == warp && lane < tpr) {
-#pragma unroll
-            for (int n = 0; n < kN; ++n) {
-#pragma unroll
-                for (int c = 0; c < V; ++c) {
-                    const int i = (n * tpr + at) * V + c;
-                    if (i < a.cols) {
-                        cols_sh[i] = (warp ? cols_sh[i] : 0.0f) + dw[n][c];
-                        cols_sh[a.cols + i] = (warp ? cols_sh[a.cols + i] : 0.0f) + db[n][c];
-                    }
+            for (int c = 0; c < H; ++c) {
+                for (int d = tpr; d < 32; d <<= 1) {
+                    dw[n][c] = add2(dw[n][c], __shfl_xor_sync(0xFFFFFFFFu, dw[n][c], d));
+                    db[n][c] = add2(db[n][c], __shfl_xor_sync(0xFFFFFFFFu, db[n][c], d));
                 }
             }
         }
+    }
+    for (int i = 0; i < turns; ++i) {
+        if (turn == i && (kAny || lane < tpr)) {
+#pragma unroll
+            for (int n = 0; n < kN; ++n) put_columns<H>(cols_sh, first + n * tpr * V, all, i > 0, dw[n], db[n]);
+        }
         __syncthreads();
     }
-    float* part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-    for (int i = threadIdx.x; i < 2 * a.cols; i += kShortThreads) part[i] = cols_sh[i];
+    float* part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * all;
+    for (int i = threadIdx.x; i < 2 * all; i += kShortThreads) part[i] = cols_sh[i];
 }
 
-// Rows of up to 512 threads x kN vectors.  With kRing the rows of x and dy come
-// through a ring of `stages` bulk copies in shared memory, so that some 100 KB a
-// SM are in flight while a row's sums are formed; without (rows off the 16-byte grid, or
-// too long for two stages) they are read from memory.  dx reads a row a second time from there:
-// registers hold the column sums.
-template <typename T, typename W, int kN, bool kAny, bool kRing>
-__global__ void __launch_bounds__(512, kN * kVec16<T> > 16 ? 1 : 2) norm_backward_kernel(const NormBackwardArgs a, int stages) {
-    constexpr int V = kVec16<T>;
-    extern __shared__ __align__(128) unsigned char ring[];   // [stages][x row, dy row]
-    __shared__ float2 sh[2][16];
-    __shared__ __align__(8) uint64_t bars[8];
-    __shared__ int abort_flag;
-    const int tpr = blockDim.x, warp = threadIdx.x >> 5, warps = tpr >> 5;
-    const uint32_t bytes = static_cast<uint32_t>(a.cols * sizeof(T));
-    const W* w = static_cast<const W*>(a.weight);
-    const float inv = 1.0f / static_cast<float>(a.cols);
-    const uint32_t bar0 = smem_u32(bars), ring0 = smem_u32(ring);
-    const WaitGuard guard{&abort_flag, a.status, kDefaultWaitLimitNs};
-    int64_t fetched = blockIdx.x;   // the next row to fetch (thread 0)
-    int to = 0;                     // and its stage
-    auto fetch = [&]() {
-        if (fetched >= a.rows) return;
-        const uint32_t bar = bar0 + 8 * to, dst = ring0 + 2 * to * bytes;
-        mbar_arrive_expect_tx(bar, 2 * bytes);
-        bulk_load(dst, static_cast<const T*>(a.x) + fetched * a.ldx, bytes, bar);
-        bulk_load(dst + bytes, static_cast<const T*>(a.dy) + fetched * a.lddy, bytes, bar);
-        fetched += gridDim.x;
-        if (++to == stages) to = 0;
-    };
-    if (kRing) {
+// ---- a ring of rows in shared memory (longer rows) ---------------------------------------
+//
+// One block an SM reads its rows (row blockIdx.x, + gridDim.x, ...) of x and dy through a
+// ring of bulk copies in shared memory, so that some 100 KB an SM are in flight while
+// sums are formed.  The block's threads form groups of tpr; its row i belongs to group
+// i % groups and lies in stage i % stages.  At the barrier that a group needs for a row's sums
+// anyway all its threads have read the row, and one thread copies the row `stages`
+// further into that stage.  stages is a multiple of groups: a stage belongs to one
+// group, which takes its phases one after the other.  (A group that asked for a phase while the
+// one before it, another group's row, was on its way would be answered by the
+// parity of the phase before that.)
+//
+// With kAny a row's copy takes the whole 16-byte blocks that it lies in: inside the
+// matrix, as rows lie before and after it; the first and the last row's ends go
+// element by element.  The block's rows are gridDim.x apart, a multiple of 8 (or
+// there is one row), so they all start alike.
+
+constexpr int kMaxStages = 32;
+constexpr int kMaxGroups = 14;               // named barriers: one each, and one for all
+constexpr int kRingThreads = 512;
+constexpr int64_t kRingBytes = 204 * 1024;
+
+struct RingBars {
+    uint64_t full[kMaxStages];
+    int copies[kMaxStages];    // into each stage, by now
+    int abort_flag;            // a wait ran out
+    int stop[kMaxGroups][2];   // it as a group's first thread saw it before the barrier of a row (by parity):
+                               // the whole group acts on that
+};
+
+template <typename T, bool kAny>
+struct RowRing {
+    const T* src[2];
+    int64_t ld[2], rows;
+    unsigned char* buf;    // [stages][2][row_bytes]
+    RingBars* bars;
+    uint32_t full;         // shared address of the mbarriers
+    int cols, row_bytes, stages;
+
+    static int64_t bytes_of(int64_t cols) {   // of one row in the ring: the blocks that it can lie in
+        return (cols * static_cast<int64_t>(sizeof(T)) + 15) / 16 * 16 + (kAny ? 16 : 0);
+    }
+
+    // By all threads; a __syncthreads must follow.  Starts the first copies.
+    __device__ __forceinline__ void init(const NormBackwardArgs& a, RingBars* all, unsigned char* memory, int stage_count) {
+        src[0] = static_cast<const T*>(a.x);
+        src[1] = static_cast<const T*>(a.dy);
+        ld[0] = a.ldx;
+        ld[1] = a.lddy;
+        rows = a.rows;
+        cols = static_cast<int>(a.cols);
+        buf = memory;
+        bars = all;
+        full = smem_u32(bars->full);
+        row_bytes = (cols * static_cast<int>(sizeof(T)) + 15) / 16 * 16 + (kAny ? 16 : 0);
+        stages = stage_count;
         if (threadIdx.x == 0) {
-            abort_flag = 0;
-            for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8 * s, 1);
+            bars->abort_flag = 0;
+            for (int s = 0; s < stages; ++s) {
+                bars->copies[s] = 0;
+                mbar_init(full + 8 * s, 1);
+            }
             fence_mbar_init();
+            int64_t row = blockIdx.x;
+            for (int s = 0; s < stages && row < rows; ++s, row += gridDim.x) fetch(row, s);
         }
+    }
+
+    // Copies a row of x and of dy into a stage (one thread).
+    __device__ __forceinline__ void fetch(int64_t at, int stage) {
+        const bool ends = kAny && (at == 0 || at == rows - 1);
+        unsigned char* dst = buf + 2 * stage * row_bytes;
+        const unsigned char* from[2];
+        uint32_t skip[2], bytes[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const T* row = src[k] + at * ld[k];
+            const unsigned char* p = reinterpret_cast<const unsigned char*>(row);
+            const uint32_t lead = kAny ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u) : 0u;
+            const uint32_t size = static_cast<uint32_t>(cols * static_cast<int>(sizeof(T)));
+            uint32_t lo = 0, hi = (lead + size + 15u) & ~15u;   // blocks, from the one that holds the first element
+            if (ends) {
+                if (lead != 0) lo = 16;
+                hi = (lead + size) & ~15u;
+                T* to_row = reinterpret_cast<T*>(dst + k * row_bytes + lead);
+                const int head = static_cast<int>((lo - (lo ? lead : 0u)) / sizeof(T));
+                for (int i = 0; i < head; ++i) to_row[i] = row[i];
+                for (int i = static_cast<int>((hi - lead) / sizeof(T)); i < cols; ++i) to_row[i] = row[i];
+            }
+            from[k] = p - lead + lo;
+            skip[k] = lo;
+            bytes[k] = hi - lo;
+        }
+        const uint32_t bar = full + 8 * stage;
+        ++bars->copies[stage];
+        mbar_arrive_expect_tx(bar, bytes[0] + bytes[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) bulk_load(smem_u32(dst + k * row_bytes + skip[k]), from[k], bytes[k], bar);
+    }
+
+    // All threads of its group have read a row: its stage takes the row `stages` further.
+    __device__ __forceinline__ void refill(int64_t row, int stage) {
+        const int64_t next = row + static_cast<int64_t>(stages) * gridDim.x;
+        if (next >= rows) return;
+        fence_proxy_async_smem();   // the group's reads of the stage before the copy's writes
+        fetch(next, stage);
+    }
+
+    // After a wait that ran out, by all threads that have not ended: one of each group that
+    // gave up waits (bounded) for the copies in flight before the block ends.
+    __device__ __noinline__ void drain(const WaitGuard& guard, bool first_of_group) {
         __syncthreads();
-        if (threadIdx.x == 0)
-            for (int s = 0; s < stages; ++s) fetch();
+        if (!first_of_group) return;
+        int again = 0;
+        const WaitGuard last{&again, guard.status, guard.limit_ns};
+        for (int s = 0; s < stages; ++s)
+            if (bars->copies[s] > 0) mbar_wait(full + 8 * s, (bars->copies[s] - 1) & 1, last);
     }
-    float dw[kN][V] = {}, db[kN][V] = {};
-    int stage = 0, phase = 0;
-    bool odd = false;
-    float mu = a.mean[blockIdx.x], r = a.rstd[blockIdx.x];
-    int64_t row = blockIdx.x;
-    for (; row < a.rows; row += gridDim.x) {
-        const int64_t after = row + gridDim.x;
-        float mu_next = 0.0f, r_next = 0.0f;
-        if (after < a.rows) mu_next = a.mean[after], r_next = a.rstd[after];
-        const void* x = static_cast<const T*>(a.x) + row * a.ldx;
-        const void* dy = static_cast<const T*>(a.dy) + row * a.lddy;
-        if (kRing) {
-            x = ring + 2 * stage * bytes;
-            dy = ring + (2 * stage + 1) * bytes;
-            mbar_wait(bar0 + 8 * stage, phase, guard);   // false: abort_flag is set, seen below
-        }
-        float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-            const int i = (n * tpr + static_cast<int>(threadIdx.x)) * V;
-            float fx[V], g[V], fw[V];
-            unpack<T>(load16<sizeof(T), kAny>(x, i, a.cols), fx);
-            unpack<T>(load16<sizeof(T), kAny>(dy, i, a.cols), g);
-            load_params<W, V, kAny>(w, i, a.cols, 1.0f, fw);
-            add_vector<V>(fx, g, fw, mu, r, dw[n], db[n], sum);
-        }
-        sum.x = warp_sum(sum.x);
-        sum.y = warp_sum(sum.y);
-        if ((threadIdx.x & 31) == 0) sh[odd][warp] = sum;
-        __syncthreads();   // every thread is done with the row before this one: its stage is free
-        if (kRing && abort_flag) break;
-        if (kRing && threadIdx.x == 0 && row != blockIdx.x) fetch();
-        float m1 = 0.0f, m2 = 0.0f;
-        for (int i = 0; i < warps; ++i) {
-            m1 += sh[odd][i].x;
-            m2 += sh[odd][i].y;
-        }
-        m1 *= inv;
-        m2 *= inv;
-        T* dx = static_cast<T*>(a.dx) + row * a.lddx;
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-            const int i = (n * tpr + static_cast<int>(threadIdx.x)) * V;
-            float fx[V], g[V], fw[V];
-            unpack<T>(load16<sizeof(T), kAny>(x, i, a.cols), fx);
-            unpack<T>(load16<sizeof(T), kAny>(dy, i, a.cols), g);
-            load_params<W, V, kAny>(w, i, a.cols, 1.0f, fw);
-            dx_vector<V>(fx, g, fw, mu, r, m1, m2);
-            store16<sizeof(T), kAny>(dx, i, a.cols, pack<T>(g));
-        }
-        mu = mu_next, r = r_next;
-        odd = !odd;
-        if (++stage == stages) stage = 0, phase ^= 1;
+
+    __device__ __forceinline__ void wait(int stage, int phase, const WaitGuard& guard) const {
+        if (!mbar_try_wait(full + 8 * stage, phase)) mbar_wait(full + 8 * stage, phase, guard);
     }
-    if (kRing && abort_flag) {   // a copy did not arrive in time: wait for those in flight (bounded) and give up
-        if (threadIdx.x == 0) {
-            int again = 0;
-            const WaitGuard last{&again, a.status, kDefaultWaitLimitNs};
-            for (; row < fetched; row += gridDim.x) {
-                mbar_wait(bar0 + 8 * stage, phase, last);
-                if (++stage == stages) stage = 0, phase ^= 1;
-            }
-        }
-        return;
+
+    // Vector q of x's row (k = 0) in `stage`, elements [i, i + V), or the same elements of dy's,
+    // which starts `lead` elements into its first block and alike or not: 0 outside the row.
+    __device__ __forceinline__ uint4 read(int k, int stage, int q, int i, int lead = 0, bool alike = true) const {
+        const unsigned char* row = buf + (2 * stage + k) * row_bytes;
+        if (kAny && !alike) return load_ends<sizeof(T)>(row + lead * sizeof(T), i, cols);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (i < cols) v = *reinterpret_cast<const uint4*>(row + 16 * q);
+        if (kAny && (i < 0 || i + kVec16<T> > cols)) v = inside<T>(v, i, cols);
+        return v;
     }
-    float* part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-        const int i = (n * tpr + static_cast<int>(threadIdx.x)) * V;
-#pragma unroll
-        for (int c = 0; c < V; ++c)
-            if (i + c < a.cols) {
-                part[i + c] = dw[n][c];
-                part[a.cols + i + c] = db[n][c];
-            }
+};
+
+// Place of a group in the ring and in the rows.
+struct RingPlace {
+    int64_t row;
+    int stage, phase;
+    __device__ __forceinline__ void move(int by, int stages) {   // to the block's row that many further
+        row += static_cast<int64_t>(by) * gridDim.x;
+        stage += by;
+        while (stage >= stages) stage -= stages, phase ^= 1;
     }
+};
+
+// The group's barrier for a row; true if the group has to give up (the same for all its threads).
+__device__ __forceinline__ bool group_barrier(RingBars& bars, int group, int at, int tpr, int parity) {
+    if (at == 0) bars.stop[group][parity] = *static_cast<volatile int*>(&bars.abort_flag);
+    if (tpr == 32) __syncwarp();
+    else named_bar_sync(1 + group, tpr);
+    return bars.stop[group][parity] != 0;
 }
 
-// Longer rows: dw and db by columns, one thread each, over the block's rows (their
-// shares in the workspace), then dx from two passes over each row.
+// A thread of 16 elements a row (kKeep) keeps h and u of the row between the two passes; a
+// longer row is read a second time from the ring: registers hold the column sums.
+template <typename T, typename W, int kN, bool kAny>
+__global__ void __launch_bounds__(kRingThreads, 1) norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
+    constexpr int V = kVec16<T>, H = V / 2, S = sizeof(T);
+    constexpr bool kKeep = kN * V <= 16;
+    constexpr bool kHeld = kN * V * sizeof(W) <= (kAny ? 64 : 32);   // weights in 8 registers (16 where each use would shift them)
+    extern __shared__ __align__(128) unsigned char buf[];
+    __shared__ f32x2 sums[kMaxGroups][2][16];    // [group][row parity][warp]: of u and of u h
+    __shared__ float2 stats[kMaxGroups][2];      // mean and rstd of the group's row
+    __shared__ __align__(8) RingBars bars;
+    const int groups = blockDim.x / tpr, group = threadIdx.x / tpr, at = threadIdx.x - group * tpr;
+    const int warp = at >> 5, lane = threadIdx.x & 31;
+    RowRing<T, kAny> ring;
+    ring.init(a, &bars, buf, stages);
+    for (int i = threadIdx.x; i < kMaxGroups * 2 * 16; i += blockDim.x)
+        (&sums[0][0][0])[i] = 0;   // warps that a group does not have
+    RingPlace place{blockIdx.x, 0, 0};
+    place.move(group, stages);
+    const int64_t stride = static_cast<int64_t>(groups) * gridDim.x;
+    // The group's first thread loads mean and rstd two rows ahead.
+    auto statistics = [&](int64_t row) {
+        return row < a.rows ? make_float2(a.mean[row], a.rstd[row]) : make_float2(0.0f, 0.0f);
+    };
+    float2 later = make_float2(0.0f, 0.0f);
+    if (at == 0) {
+        stats[group][0] = statistics(place.row);
+        later = statistics(place.row + stride);
+    }
+    __syncthreads();
+    const WaitGuard guard{&bars.abort_flag, a.status, kDefaultWaitLimitNs};
+    const int cols = static_cast<int>(a.cols);
+    const float inv = 1.0f / static_cast<float>(cols);
+    const int lead_x = kAny ? lead_of<S>(static_cast<const T*>(a.x) + blockIdx.x * a.ldx) : 0;
+    const int lead_g = kAny ? lead_of<S>(static_cast<const T*>(a.dy) + blockIdx.x * a.lddy) : 0;
+    const int first = at * V - lead_x;
+    const bool alike = lead_g == lead_x;
+    const W* wp = static_cast<const W*>(a.weight);
+    Params<W, V> w[kHeld ? kN : 1];
+    if constexpr (kHeld) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) w[n].template load<kAny>(wp, first + n * tpr * V, cols, 1.0f);
+    }
+    f32x2 dw[kN][H] = {}, db[kN][H] = {};
+    bool stop = false;
+    int odd = 0;
+    while (place.row < a.rows) {
+        const float2 st = stats[group][odd];
+        const f32x2 rr = pair(st.y, st.y), off = pair(-st.x * st.y, -st.x * st.y);
+        ring.wait(place.stage, place.phase, guard);   // if it runs out, abort_flag is set: seen after the barrier
+        f32x2 h[kKeep ? kN : 1][H], u[kKeep ? kN : 1][H];
+        f32x2 s1 = 0, s2 = 0;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int q = n * tpr + at, i = first + n * tpr * V, m = kKeep ? n : 0;
+            f32x2 fw[H];
+            unpack2<T>(ring.read(0, place.stage, q, i), h[m]);
+            unpack2<T>(ring.read(1, place.stage, q, i, lead_g, alike), u[m]);
+            if constexpr (kHeld) w[n].get(fw);
+            else load_params2<W, V, kAny>(wp, i, cols, 1.0f, fw);
+            add_vector<H>(h[m], u[m], fw, rr, off, dw[n], db[n], s1, s2);
+        }
+        const f32x2 both = warp_sum2(pair(lo_of(s1) + hi_of(s1), lo_of(s2) + hi_of(s2)));
+        if (lane == 0) sums[group][odd][warp] = both;
+        if (at == 0) {
+            stats[group][odd ^ 1] = later;
+            later = statistics(place.row + 2 * stride);
+        }
+        stop = group_barrier(bars, group, at, tpr, odd);
+        if (stop) break;
+        if (kKeep && at == 0) ring.refill(place.row, place.stage);
+        f32x2 total = sums[group][odd][lane & 15];
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) total = add2(total, __shfl_xor_sync(0xFFFFFFFFu, total, d));
+        const float m1 = -lo_of(total) * inv * st.y, m2 = -hi_of(total) * inv * st.y;
+        const f32x2 c1 = pair(m1, m1), c2 = pair(m2, m2);
+        T* dx = static_cast<T*>(a.dx) + place.row * a.lddx;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int q = n * tpr + at, i = first + n * tpr * V, m = kKeep ? n : 0;
+            if constexpr (!kKeep) {
+                f32x2 fw[H];
+                unpack2<T>(ring.read(0, place.stage, q, i), h[m]);
+                unpack2<T>(ring.read(1, place.stage, q, i, lead_g, alike), u[m]);
+                if constexpr (kHeld) w[n].get(fw);
+                else load_params2<W, V, kAny>(wp, i, cols, 1.0f, fw);
+#pragma unroll
+                for (int c = 0; c < H; ++c) {
+                    h[m][c] = fma2(h[m][c], rr, off);
+                    u[m][c] = mul2(u[m][c], fw[c]);
+                }
+            }
+            dx_vector<H>(h[m], u[m], rr, c1, c2);
+            store16<S, kAny>(dx, i, cols, pack2<T>(u[m]), !kAny || lead_of<S>(dx) == lead_x);
+        }
+        if constexpr (!kKeep) {   // the row has been read a second time
+            stop = group_barrier(bars, group, at, tpr, odd);
+            if (stop) break;
+            if (at == 0) ring.refill(place.row, place.stage);
+        }
+        place.move(groups, stages);
+        odd ^= 1;
+    }
+    // The groups' column sums one after the other, in the ring (all rows have been read).
+    float* part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+    float* meet = groups == 1 ? part : reinterpret_cast<float*>(buf);
+    for (int g = 0; g < groups; ++g) {
+        if (groups > 1) named_bar_sync(15, groups * tpr);
+        if (g != group) continue;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) put_columns<H>(meet, first + n * tpr * V, cols, g > 0, dw[n], db[n]);
+    }
+    if (groups > 1) {
+        named_bar_sync(15, groups * tpr);
+        for (int i = threadIdx.x; i < 2 * cols; i += groups * tpr) part[i] = meet[i];
+    }
+    if (stop) ring.drain(guard, at == 0);   // a group that gave up
+}
+
+// The longest rows: element by element.  dw and db by columns, one thread each, over the block's rows (their shares in the workspace),
+// then dx from two passes over each row.
 template <typename T, typename W>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormBackwardArgs a) {
     __shared__ float sh[2][32];
     const W* w = static_cast<const W*>(a.weight);
-    const float inv = 1.0f / static_cast<float>(a.cols);
-    float* part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-    for (int64_t i = threadIdx.x; i < a.cols; i += blockDim.x) {
+    const int cols = static_cast<int>(a.cols);
+    const float inv = 1.0f / static_cast<float>(cols);
+    float* part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+    for (int i = threadIdx.x; i < cols; i += blockDim.x) {
         float dw = 0.0f, db = 0.0f;
+#pragma unroll 4
         for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
             const float g = to_float(static_cast<const T*>(a.dy)[row * a.lddy + i]);
             dw = fmaf(g, (to_float(static_cast<const T*>(a.x)[row * a.ldx + i]) - a.mean[row]) * a.rstd[row], dw);
             db += g;
         }
         part[i] = dw;
-        part[a.cols + i] = db;
+        part[cols + i] = db;
     }
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T* x = static_cast<const T*>(a.x) + row * a.ldx;
         const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
         T* dx = static_cast<T*>(a.dx) + row * a.lddx;
         const float mu = a.mean[row], r = a.rstd[row];
-        float2 sum = make_float2(0.0f, 0.0f);
-        for (int64_t i = threadIdx.x; i < a.cols; i += blockDim.x) {
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < cols; i += blockDim.x) {
             const float u = to_float(dy[i]) * (w ? to_float(w[i]) : 1.0f);
-            sum.x += u;
-            sum.y = fmaf(u, (to_float(x[i]) - mu) * r, sum.y);
+            s1 += u;
+            s2 = fmaf(u, (to_float(x[i]) - mu) * r, s2);
         }
         __syncthreads();   // the sums of the row before, and (dx may be dy) the pass over columns
-        const float m1 = row_sum(sum.x, blockDim.x, sh[0]) * inv, m2 = row_sum(sum.y, blockDim.x, sh[1]) * inv;
-        for (int64_t i = threadIdx.x; i < a.cols; i += blockDim.x) {
+        const float m1 = row_sum(s1, blockDim.x, sh[0]) * inv, m2 = row_sum(s2, blockDim.x, sh[1]) * inv;
+        for (int i = threadIdx.x; i < cols; i += blockDim.x) {
             const float u = to_float(dy[i]) * (w ? to_float(w[i]) : 1.0f);
             dx[i] = from_float<T>(r * (u - m1 - (to_float(x[i]) - mu) * r * m2));
         }
@@ -417,7 +659,7 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float* partial, 
 
 // ---- launches ---------------------------------------------------------------------------
 
-// Whether every row (and the parameters) lies on the 16-byte grid in whole vectors.
+// Whether the rows of several tensors all lie on the 16-byte grid in whole vectors.
 bool on_grid(int64_t cols, size_t size, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
     if (cols * size % 16 != 0) return false;
     for (const void* p : ptrs)
@@ -441,80 +683,90 @@ int lanes_of(int64_t vectors) {   // 4 .. 32 lanes, a power of two
     return lanes;
 }
 
+// Vectors that a row lies in: one more where x's rows start anywhere.
+template <typename T>
+int64_t vectors_of(const void* x, int64_t ldx, int64_t cols) {
+    return (cols + kVec16<T> - 1) / kVec16<T> + (on_grid(cols, sizeof(T), {x}, {ldx}) ? 0 : 1);
+}
+
 template <typename T, typename W, bool kAny>
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t stream) {
-    const int64_t vectors = (a.cols + kVec16<T> - 1) / kVec16<T>;
-    // Few rows: as many threads to a row as it has vectors for (latency).  Many
-    // rows: up to 8 vectors a thread, which keeps 128 bytes a thread in flight and needs few barriers.
-    const int64_t most = a.rows <= 2 * kSMs ? 2 : 8;
+    const int64_t vectors = vectors_of<T>(a.x, a.ldx, a.cols);
     if (vectors > 8 * 512) {
         norm_long_kernel<T, W><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a);
         return cudaGetLastError();
     }
+    // Few rows: 2 vectors a thread (latency).  Many: 4, and 8 for the longest rows, so that
+    // several blocks with a row each share an SM (16384 x 4096 BF16: 52 us with 4, 61 with 8, 72 with 2).
+    const int64_t most = kAny || a.rows <= 2 * kSMs ? 2 : 4;
     int64_t n = (vectors + 31) / 32;   // vectors of a thread if a warp has the row
     if (n > most) n = most;
-    if (vectors > n * 512) n = (vectors + 511) / 512;
+    while (n < 8 && vectors > n * 512) n *= 2;
     return by_count<8>(n, [&](auto count) {
         constexpr int kN = count.value;
         int tpr = lanes_of(vectors);
         if (vectors > 32 * kN) tpr = static_cast<int>((vectors + 32 * kN - 1) / (32 * kN)) * 32;
         const int threads = tpr <= 32 ? 128 : tpr;
         const int64_t per = threads / tpr;
-        norm_kernel<T, W, kN, kAny><<<static_cast<unsigned>((a.rows + per - 1) / per), threads, 0, stream>>>(a, tpr);
+        int64_t grid = (a.rows + per - 1) / per;
+        if (kAny) {   // what the SMs hold at a time, by registers
+            const int64_t most = kSMs * (65536 / (threads * (kN == 8 ? 128 : 64)));
+            if (grid > most) grid = most;
+        }
+        norm_kernel<T, W, kN, kAny><<<static_cast<unsigned>(grid), threads, 0, stream>>>(a, tpr);
         return cudaGetLastError();
     });
 }
 
 template <typename T, typename W, int kN, bool kAny>
-cudaError_t backward_short(const NormBackwardArgs& a, int64_t vectors, unsigned grid, cudaStream_t stream) {
-    const size_t smem = static_cast<size_t>(2 * a.cols) * sizeof(float);
-    norm_backward_short_kernel<T, W, kN, kAny><<<grid, kShortThreads, smem, stream>>>(a, lanes_of(vectors));
-    return cudaGetLastError();
-}
-
-template <typename T, typename W, int kN, bool kAny>
-cudaError_t backward_block(const NormBackwardArgs& a, int64_t vectors, int64_t* grid, cudaStream_t stream) {
-    const int threads = static_cast<int>((vectors + 32 * kN - 1) / (32 * kN)) * 32;
-    const int64_t stage = 2 * a.cols * sizeof(T);
-    int64_t blocks = (*grid + kSMs - 1) / kSMs;   // of an SM
-    if (!kAny)   // fewer blocks where that makes room for two stages
-        while (blocks > 1 && kRingBytes / blocks / stage < 2) --blocks;
-    if (*grid > blocks * kSMs) *grid = blocks * kSMs;
-    int64_t stages = kRingBytes / blocks / stage;
-    if (stages > 8) stages = 8;
-    if (!kAny && stages >= 2) {
-        auto kernel = norm_backward_kernel<T, W, kN, false, true>;
-        const int smem = static_cast<int>(stages * stage);
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        kernel<<<static_cast<unsigned>(*grid), threads, smem, stream>>>(a, static_cast<int>(stages));
-    } else {
-        norm_backward_kernel<T, W, kN, kAny, false><<<static_cast<unsigned>(*grid), threads, 0, stream>>>(a, 1);
-    }
+cudaError_t backward_ring(const NormBackwardArgs& a, int64_t vectors, int64_t grid, cudaStream_t stream) {
+    const int64_t stage = 2 * RowRing<T, kAny>::bytes_of(a.cols);
+    const int tpr = static_cast<int>((vectors + 32 * kN - 1) / (32 * kN)) * 32;
+    int64_t stages = kRingBytes / stage;
+    if (stages > kMaxStages) stages = kMaxStages;
+    // as many groups as there are threads for, with two stages each, and none without a row
+    int64_t groups = kRingThreads / tpr;
+    const int64_t rows = (a.rows + grid - 1) / grid;
+    if (groups > kMaxGroups) groups = kMaxGroups;
+    if (groups > stages / 2) groups = stages / 2;
+    if (groups > rows) groups = rows;
+    if (groups < 1) groups = 1;
+    stages -= stages % groups;
+    auto kernel = norm_backward_kernel<T, W, kN, kAny>;
+    const int smem = static_cast<int>(stages * stage);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(grid), static_cast<unsigned>(tpr * groups), smem, stream>>>(
+        a, static_cast<int>(stages), tpr);
     return cudaGetLastError();
 }
 
 template <typename T, typename W, bool kAny>
 cudaError_t norm_backward_launch(const NormBackwardArgs& a, cudaStream_t stream) {
     constexpr int V = kVec16<T>;
-    const int64_t vectors = (a.cols + V - 1) / V;
+    const int64_t vectors = vectors_of<T>(a.x, a.ldx, a.cols);
     int64_t parts = norm_partials(a.rows, a.cols);
     cudaError_t e;
-    if (a.cols <= 512) {
-        constexpr int kMost = 16 / V;   // 16 elements a lane
-        e = by_count<kMost>((vectors + 31) / 32, [&](auto count) {
-            const int64_t per = kShortThreads / lanes_of(vectors);
-            const int64_t cap = count.value * V > 8 ? 2 * kSMs : 3 * kSMs;   // what fits the SMs by registers
-            if (parts > cap) parts = cap;
+    if (a.cols <= kShortCols) {
+        constexpr int kMost = 16 / V;   // 16 elements a lane, one vector more for a row off the grid
+        const int64_t n = (vectors + 31) / 32;
+        auto go = [&](auto count) {
+            const int tpr = lanes_of(vectors);
+            const int64_t per = kShortThreads / tpr;
             if (parts > (a.rows + per - 1) / per) parts = (a.rows + per - 1) / per;
-            return backward_short<T, W, count.value, kAny>(a, vectors, static_cast<unsigned>(parts), stream);
-        });
-    } else if (vectors <= 512 * (8 / V)) {   // 8 elements a thread
-        e = backward_block<T, W, 8 / V, kAny>(a, vectors, &parts, stream);
-    } else if (vectors <= 512 * (16 / V)) {
-        e = backward_block<T, W, 16 / V, kAny>(a, vectors, &parts, stream);
-    } else if (vectors <= 512 * (32 / V)) {
-        e = backward_block<T, W, 32 / V, kAny>(a, vectors, &parts, stream);
+            if (count.value * V > 8 && parts > 2 * kSMs) parts = 2 * kSMs;   // what the registers leave room for
+            const size_t smem = static_cast<size_t>(2 * a.cols) * sizeof(float);
+            norm_backward_short_kernel<T, W, count.value, kAny>
+                <<<static_cast<unsigned>(parts), kShortThreads, smem, stream>>>(a, tpr);
+            return cudaGetLastError();
+        };
+        e = n <= 1 ? go(std::integral_constant<int, 1>{}) : n <= 2 ? go(std::integral_constant<int, 2>{})
+            : n <= kMost ? go(std::integral_constant<int, kMost>{}) : go(std::integral_constant<int, kMost + 1>{});
+    } else if (vectors <= kRingThreads * (16 / V)) {
+        if (parts > kSMs) parts = kSMs;
+        e = backward_ring<T, W, 16 / V, kAny>(a, vectors, parts, stream);
+    } else if (vectors <= kRingThreads * (32 / V) && 4 * RowRing<T, kAny>::bytes_of(a.cols) <= kRingBytes) {
+        e = backward_ring<T, W, 32 / V, kAny>(a, vectors, parts, stream);
     } else {
         norm_backward_long_kernel<T, W><<<static_cast<unsigned>(parts), 1024, 0, stream>>>(a);
         e = cudaGetLastError();
@@ -534,15 +786,10 @@ cudaError_t by_types(bool f32, bool params_f32, F f) {
 
 }  // namespace
 
-// Blocks of the backward pass at most, each with 2 x cols column sums: what fits 1024
-// threads of an SM, so that rows of few threads still fill it and the sums stay near
-// 10 MB; one a SM for rows whose sums take the registers of 512 threads.
+// Blocks of the backward pass at most, each with 2 x cols column sums: one an SM, three for
+// the short rows that need no ring.
 int64_t norm_partials(int64_t rows, int64_t cols) {
-    const int64_t held = cols <= 4096 ? 8 : cols <= 8192 ? 16 : 32;   // elements of a row in a thread
-    const int64_t threads = (cols + 32 * held - 1) / (32 * held) * 32;
-    int64_t per = held == 32 ? 1 : 1024 / (threads < 32 ? 32 : threads);
-    if (per > 8) per = 8;
-    const int64_t most = per * kSMs;
+    const int64_t most = cols <= kShortCols ? 3 * kSMs : kSMs;
     return rows < most ? rows : most;
 }
 

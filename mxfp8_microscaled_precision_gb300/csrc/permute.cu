@@ -131,84 +131,114 @@ __device__ __forceinline__ Place place_of(int entry, int64_t slots) {
 }
 
 // a[rows[t, j]] = x[t], zeros for a dropped slot.  Token blockIdx.x; 16 bytes of
-// the row per thread, blockIdx.y over the row: x is read once, whatever k.
+// the row per thread, blockIdx.y over the row: x is read once, whatever k.  With kAny
+// the vectors are those of the row that is written.
 template <int kSize, bool kAny>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const unsigned char* x, int64_t ldx, unsigned char* a,
-                                                            int64_t lda, int64_t H, const int32_t* rows, int k) {
+                                                            int64_t lda, int H, const int32_t* rows, int k) {
+    constexpr int V = 16 / kSize;
     const int64_t t = blockIdx.x;
-    const int64_t i = (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x) * (16 / kSize);
-    if (!kAny && i >= H) return;
-    const uint4 v = load16<kSize, kAny>(x + t * ldx * kSize, i, H);
+    const int at = (blockIdx.y * kThreads + threadIdx.x) * V;
     const int32_t* r = rows + t * k;
     const int64_t slots = static_cast<int64_t>(gridDim.x) * k;
-    for (int j = 0; j < k; ++j) {
-        const Place p = place_of(r[j], slots);
-        if (p.exists) store16<kSize, kAny>(a + p.row * lda * kSize, i, H, p.kept ? v : make_uint4(0u, 0u, 0u, 0u));
+    const unsigned char* from = x + t * ldx * kSize;
+    if constexpr (!kAny) {
+        if (at >= H) return;
+        const uint4 v = load16<kSize, false>(from, at, H);
+        for (int j = 0; j < k; ++j) {
+            const Place p = place_of(r[j], slots);
+            if (p.exists)
+                store16<kSize, false>(a + p.row * lda * kSize, at, H, p.kept ? v : make_uint4(0u, 0u, 0u, 0u));
+        }
+    } else {
+        if (at >= H + V) return;
+#pragma unroll 2
+        for (int j = 0; j < k; ++j) {
+            const Place p = place_of(r[j], slots);
+            if (!p.exists) continue;
+            unsigned char* to = a + p.row * lda * kSize;
+            const int i = at - lead_of<kSize>(to);
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (p.kept) v = is_inner<kSize>(i, H) ? load_inner<kSize>(from, i) : load_ends<kSize>(from, i, H);
+            store16<kSize, true>(to, i, H, v);
+        }
     }
 }
 
 // out[t] = sum_j w_j y[rows[t, j]] (w_j = 1 without weights), summed in FP32 in
-// the order of j and rounded once.
+// the order of j and rounded once.  With kAny the vectors are those of out's row.
 template <typename T, bool kAny>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const T* y, int64_t ldy, const int32_t* rows,
-                                                           const float* weights, int k, T* out, int64_t ldo,
-                                                           int64_t H) {
-    constexpr int V = kVec16<T>;
+                                                           const float* weights, int k, T* out, int64_t ldo, int H) {
+    constexpr int V = kVec16<T>, S = sizeof(T);
     const int64_t t = blockIdx.x;
-    const int64_t i = (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x) * V;
-    if (!kAny && i >= H) return;
+    const int at = (blockIdx.y * kThreads + threadIdx.x) * V;
+    T* to = out + t * ldo;
+    const int i = kAny ? at - lead_of<S>(to) : at;
+    if (i >= H) return;
     const int32_t* r = rows + t * k;
     const int64_t slots = static_cast<int64_t>(gridDim.x) * k;
-    float acc[V] = {};
-#pragma unroll 4
-    for (int j = 0; j < k; ++j) {
+    f32x2 acc[V / 2] = {};
+    auto add = [&](int j, auto load) {
         const Place p = place_of(r[j], slots);
-        if (!p.kept || !p.exists) continue;   // a dropped slot: its row of y is not read
+        if (!p.kept || !p.exists) return;   // a dropped slot: its row of y is not read
         const float w = weights != nullptr ? weights[t * k + j] : 1.0f;
-        float f[V];
-        unpack<T>(load16<sizeof(T), kAny>(y + p.row * ldy, i, H), f);
+        f32x2 f[V / 2];
+        unpack2<T>(load(y + p.row * ldy), f);
 #pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = fmaf(w, f[c], acc[c]);
+        for (int c = 0; c < V / 2; ++c) acc[c] = fma2(pair(w, w), f[c], acc[c]);
+    };
+    if (!kAny || is_inner<S>(i, H)) {
+#pragma unroll 4
+        for (int j = 0; j < k; ++j)
+            add(j, [&](const T* row) { return kAny ? load_inner<S>(row, i) : load16<S, false>(row, i, H); });
+    } else {
+        for (int j = 0; j < k; ++j) add(j, [&](const T* row) { return load_ends<S>(row, i, H); });
     }
-    store16<sizeof(T), kAny>(out + t * ldo, i, H, pack<T>(acc));
+    store16<S, kAny>(to, i, H, pack2<T>(acc));
 }
 
 // dy[rows[t, j]] = w_j dout[t], dw_j = <dout[t], y[rows[t, j]]>: one warp per slot.
+// With kAny the vectors are those of dy's row.
 template <typename T, bool kAny>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const T* dout, int64_t ldd, const T* y, int64_t ldy,
                                                                     const int32_t* rows, const float* weights, int k,
                                                                     int64_t slots, T* dy, int64_t lddy,
-                                                                    float* dweights, int64_t H) {
-    constexpr int V = kVec16<T>;
+                                                                    float* dweights, int H) {
+    constexpr int V = kVec16<T>, S = sizeof(T);
     const int64_t s = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (s >= slots) return;
     const Place p = place_of(rows[s], slots);
+    T* to = dy + (p.exists ? p.row : 0) * lddy;
+    const int first = lane * V - (kAny ? lead_of<S>(to) : 0);
     if (!p.kept || !p.exists) {
-        for (int64_t i = 0; p.exists && i < H; i += 32 * V)
-            store16<sizeof(T), kAny>(dy + p.row * lddy, i + lane * V, H, make_uint4(0u, 0u, 0u, 0u));
+        for (int i = first; p.exists && i < H; i += 32 * V) store16<S, kAny>(to, i, H, make_uint4(0u, 0u, 0u, 0u));
         if (lane == 0) dweights[s] = 0.0f;
         return;
     }
     const T* d = dout + (s / k) * ldd;
     const T* from = y + p.row * ldy;
-    T* to = dy + p.row * lddy;
     const float w = weights[s];
-    float dot = 0.0f;
-#pragma unroll 4
-    for (int64_t i0 = 0; i0 < H; i0 += 32 * V) {
-        const int64_t i = i0 + lane * V;
-        float g[V], f[V];
-        unpack<T>(load16<sizeof(T), kAny>(d, i, H), g);
-        unpack<T>(load16<sizeof(T), kAny>(from, i, H), f);
+    const f32x2 ww = pair(w, w);
+    f32x2 dot = 0;
+    auto step = [&](int i, const uint4 vg, const uint4 vf) {
+        f32x2 g[V / 2], f[V / 2];
+        unpack2<T>(vg, g);
+        unpack2<T>(vf, f);
 #pragma unroll
-        for (int c = 0; c < V; ++c) dot = fmaf(g[c], f[c], dot);
+        for (int c = 0; c < V / 2; ++c) dot = fma2(g[c], f[c], dot);
 #pragma unroll
-        for (int c = 0; c < V; ++c) g[c] *= w;
-        store16<sizeof(T), kAny>(to, i, H, pack<T>(g));
+        for (int c = 0; c < V / 2; ++c) g[c] = mul2(g[c], ww);
+        store16<S, kAny>(to, i, H, pack2<T>(g));
+    };
+    for (int i = first; i < H; i += 32 * V) {
+        if constexpr (!kAny) step(i, load16<S, false>(d, i, H), load16<S, false>(from, i, H));
+        else if (is_inner<S>(i, H)) step(i, load_inner<S>(d, i), load_inner<S>(from, i));
+        else step(i, load_ends<S>(d, i, H), load_ends<S>(from, i, H));
     }
-    dot = warp_sum(dot);
-    if (lane == 0) dweights[s] = dot;
+    const float total = warp_sum(lo_of(dot) + hi_of(dot));
+    if (lane == 0) dweights[s] = total;
 }
 
 // Whether every row lies on the 16-byte grid in whole vectors.
@@ -221,23 +251,25 @@ bool on_grid(int64_t H, size_t size, std::initializer_list<const void*> ptrs, st
     return true;
 }
 
-dim3 row_grid(int64_t tokens, int64_t H, int64_t size) {
-    const int64_t vectors = (H * size + 15) / 16;
+// kAny: a row off the grid lies in one vector more.
+dim3 row_grid(int64_t tokens, int64_t H, int64_t size, bool any) {
+    const int64_t vectors = (H * size + 15) / 16 + (any ? 1 : 0);
     return dim3(static_cast<unsigned>(tokens), static_cast<unsigned>((vectors + kThreads - 1) / kThreads));
 }
 
 template <int kSize, bool kAny>
 cudaError_t dispatch_launch(const PermuteArgs& a, const void* x, void* out, cudaStream_t stream) {
-    dispatch_kernel<kSize, kAny><<<row_grid(a.tokens, a.H, kSize), kThreads, 0, stream>>>(
-        static_cast<const unsigned char*>(x), a.ld_tokens, static_cast<unsigned char*>(out), a.ld_rows, a.H, a.rows,
-        a.k);
+    dispatch_kernel<kSize, kAny><<<row_grid(a.tokens, a.H, kSize, kAny), kThreads, 0, stream>>>(
+        static_cast<const unsigned char*>(x), a.ld_tokens, static_cast<unsigned char*>(out), a.ld_rows, static_cast<int>(a.H),
+        a.rows, a.k);
     return cudaGetLastError();
 }
 
 template <typename T, bool kAny>
 cudaError_t combine_launch(const PermuteArgs& a, const void* y, const float* weights, void* out, cudaStream_t stream) {
-    combine_kernel<T, kAny><<<row_grid(a.tokens, a.H, sizeof(T)), kThreads, 0, stream>>>(
-        static_cast<const T*>(y), a.ld_rows, a.rows, weights, a.k, static_cast<T*>(out), a.ld_tokens, a.H);
+    combine_kernel<T, kAny><<<row_grid(a.tokens, a.H, sizeof(T), kAny), kThreads, 0, stream>>>(
+        static_cast<const T*>(y), a.ld_rows, a.rows, weights, a.k, static_cast<T*>(out), a.ld_tokens,
+        static_cast<int>(a.H));
     return cudaGetLastError();
 }
 
@@ -248,7 +280,7 @@ cudaError_t combine_backward_launch(const PermuteArgs& a, const void* dout, cons
     const int64_t blocks = (slots + kThreads / 32 - 1) / (kThreads / 32);
     combine_backward_kernel<T, kAny><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
         static_cast<const T*>(dout), a.ld_tokens, static_cast<const T*>(y), ldy, a.rows, weights, a.k, slots,
-        static_cast<T*>(dy), a.ld_rows, dweights, a.H);
+        static_cast<T*>(dy), a.ld_rows, dweights, static_cast<int>(a.H));
     return cudaGetLastError();
 }
 

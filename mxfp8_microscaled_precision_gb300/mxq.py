@@ -15,6 +15,7 @@ block-scaled FP8 matmuls with BF16 output.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -499,42 +500,55 @@ _GROUP_SCORES = {"max": 0, "top2sum": 1}
 MAX_GRADS = 65536
 
 
-def _matrix(t: torch.Tensor, name: str) -> int:
-    """The dtype code of a 2-D bf16 or fp32 CUDA tensor with unit last stride."""
+# These calls are made for single tokens too, where the host's share is most of the
+# time: addresses go to ctypes as integers, the stream comes without building a Stream object, and a
+# check looks only at what the library cannot see.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(t: torch.Tensor) -> int:
+    """The current stream of the tensor's device."""
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(t.get_device())
+
+
+def _matrix(t: torch.Tensor, name: str):
+    """(dtype code, rows, cols, row stride) of a 2-D bf16 or fp32 CUDA tensor with unit
+    last stride.  A single row has any stride (its own says nothing)."""
     code = _DTYPES.get(t.dtype)
     if code is None or t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D bfloat16 or float32 CUDA tensor")
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its last axis")
-    return code
+    return code, rows, cols, (ld if rows > 1 else max(ld, cols))
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row stride in elements; a single row has any (its stride says nothing)."""
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
-
-
-def _dense(t: torch.Tensor, name: str, dtype, shape):
-    """A contiguous CUDA tensor of this dtype and shape."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
+def _dense(t: torch.Tensor, name: str, dtype, *shape) -> int:
+    """The address of a contiguous CUDA tensor of this dtype and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor {list(shape)}")
-    return t
+    return t.data_ptr()
 
 
-def _out_like(out, name, shape, like):
-    """`out` checked against what the call writes, or a new tensor."""
+def _result(out, name, like, code, rows, cols):
+    """(tensor, row stride): `out` checked against what the call writes, or a new tensor
+    of the dtype of `like`."""
     if out is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-    _matrix(out, name)
-    if out.dtype != like.dtype or tuple(out.shape) != shape:
-        raise ValueError(f"{name} must be {str(like.dtype)[6:]} {list(shape)}")
-    return out
+        return like.new_empty((rows, cols)), cols
+    c, r, n, ld = _matrix(out, name)
+    if c != code or r != rows or n != cols:
+        raise ValueError(f"{name} must be {str(like.dtype)[6:]} {[rows, cols]}")
+    return out, ld
 
 
 def _of(table, key, what):
-    if key not in table:
+    got = table.get(key)
+    if got is None:
         raise ValueError(f"unknown {what} {key!r} ({' or '.join(table)})")
-    return table[key]
+    return got
 
 
 def route(logits: torch.Tensor, topk: int, score="softmax", bias=None, n_group: int = 1, topk_group: int = 1,
@@ -543,41 +557,48 @@ def route(logits: torch.Tensor, topk: int, score="softmax", bias=None, n_group: 
     logits: bf16 or fp32 [T, E]; bias: fp32 [E], added for the choice only; token_mask:
     bool or uint8 [T], 0 for padding tokens.  Returns (ids int32 [T, topk], weights
     fp32 [T, topk]); ids is -1 (weight 0) where no expert is left."""
-    code = _matrix(logits, "logits")
-    T, E = logits.shape
-    if bias is not None:
-        _dense(bias, "bias", torch.float32, (E,))
+    code, T, E, ld = _matrix(logits, "logits")
+    b = None if bias is None else _dense(bias, "bias", torch.float32, E)
+    m = None
     if token_mask is not None:
-        _dense(token_mask, "token_mask", torch.bool if token_mask.dtype == torch.bool else torch.uint8, (T,))
+        m = _dense(token_mask, "token_mask", torch.bool if token_mask.dtype is torch.bool else torch.uint8, T)
     if out is None:
-        ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+        if topk < 1:
+            raise ValueError("topk must be at least 1")
+        ids = logits.new_empty((T, topk), dtype=torch.int32)
+        weights = logits.new_empty((T, topk), dtype=torch.float32)
+        i, w = ids.data_ptr(), weights.data_ptr()
     else:
         ids, weights = out
-        _dense(ids, "ids", torch.int32, (T, topk))
-        _dense(weights, "weights", torch.float32, (T, topk))
-    _check(lib().mxq_route(_ptr(logits), code, T, E, _ld(logits), _ptr(bias), _ptr(token_mask),
-                           _of(_SCORES, score, "score"), n_group, topk_group,
-                           _of(_GROUP_SCORES, group_score, "group score"), topk, 1 if renorm else 0, scale, _ptr(ids),
-                           _ptr(weights), _stream()), "mxq_route")
+        i = _dense(ids, "ids", torch.int32, T, topk)
+        w = _dense(weights, "weights", torch.float32, T, topk)
+    _check(lib().mxq_route(logits.data_ptr(), code, T, E, ld, b, m, _of(_SCORES, score, "score"), n_group, topk_group,
+                           _of(_GROUP_SCORES, group_score, "group score"), topk, 1 if renorm else 0, scale, i, w,
+                           _stream_of(logits)), "mxq_route")
     return ids, weights
+
+
+def _slots(t: torch.Tensor, name: str):
+    """(address, T, k) of an int32 matrix of slots."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    T, k = t.shape
+    return _dense(t, name, torch.int32, T, k), T, k
 
 
 def route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score="softmax",
                    renorm: bool = True, scale: float = 1.0, out=None):
     """Gradient of route's weights by its logits (see mxq_route_backward), in the
     logits' dtype; score, renorm and scale as in the forward call."""
-    code = _matrix(logits, "logits")
-    T, E = logits.shape
-    if ids.dim() != 2:
-        raise ValueError("ids must be 2-D")
-    topk = ids.shape[1]
-    _dense(ids, "ids", torch.int32, (T, topk))
-    _dense(dweights, "dweights", torch.float32, (T, topk))
-    out = _out_like(out, "out", (T, E), logits)
-    _check(lib().mxq_route_backward(_ptr(dweights), _ptr(ids), _ptr(logits), code, T, E, _ld(logits),
-                                    _of(_SCORES, score, "score"), topk, 1 if renorm else 0, scale, _ptr(out), _ld(out),
-                                    _stream()), "mxq_route_backward")
+    code, T, E, ld = _matrix(logits, "logits")
+    i, n, k = _slots(ids, "ids")
+    if n != T:
+        raise ValueError("ids and logits must have the same number of tokens")
+    d = _dense(dweights, "dweights", torch.float32, T, k)
+    out, ldo = _result(out, "out", logits, code, T, E)
+    _check(lib().mxq_route_backward(d, i, logits.data_ptr(), code, T, E, ld, _of(_SCORES, score, "score"), k,
+                                    1 if renorm else 0, scale, out.data_ptr(), ldo, _stream_of(logits)),
+           "mxq_route_backward")
     return out
 
 
@@ -586,39 +607,28 @@ def moe_plan(ids: torch.Tensor, experts: int, out=None):
     route.  Returns (offsets int64 [experts + 1], rows int32 [T, k]): offsets are the
     group offsets of the grouped calls, rows[t, j] the row of slot (t, j), -1 - row
     for a dropped slot."""
-    if ids.dim() != 2:
-        raise ValueError("ids must be 2-D")
-    T, k = ids.shape
-    _dense(ids, "ids", torch.int32, (T, k))
+    i, T, k = _slots(ids, "ids")
     if out is None:
-        offsets = torch.empty(experts + 1 if experts > 0 else 1, dtype=torch.int64, device=ids.device)
-        rows = torch.empty((T, k), dtype=torch.int32, device=ids.device)
+        offsets = ids.new_empty(max(experts, 0) + 1, dtype=torch.int64)
+        rows = ids.new_empty((T, k))
+        o, r = offsets.data_ptr(), rows.data_ptr()
     else:
         offsets, rows = out
-        _dense(offsets, "offsets", torch.int64, (experts + 1,))
-        _dense(rows, "rows", torch.int32, (T, k))
-    _check(lib().mxq_moe_plan(_ptr(ids), T, k, experts, _ptr(offsets), _ptr(rows), _stream()), "mxq_moe_plan")
+        o = _dense(offsets, "offsets", torch.int64, experts + 1)
+        r = _dense(rows, "rows", torch.int32, T, k)
+    _check(lib().mxq_moe_plan(i, T, k, experts, o, r, _stream_of(ids)), "mxq_moe_plan")
     return offsets, rows
-
-
-def _rows_shape(rows: torch.Tensor):
-    if rows.dim() != 2:
-        raise ValueError("rows must be 2-D")
-    T, k = rows.shape
-    _dense(rows, "rows", torch.int32, (T, k))
-    return T, k
 
 
 def moe_dispatch(x: torch.Tensor, rows: torch.Tensor, out=None) -> torch.Tensor:
     """The tokens' rows in expert order (see mxq_moe_dispatch): x [T, H], rows from
     moe_plan.  Returns [T * k, H], zeros in the rows of dropped slots."""
-    code = _matrix(x, "x")
-    T, k = _rows_shape(rows)
-    if x.shape[0] != T:
+    code, n, H, ld = _matrix(x, "x")
+    r, T, k = _slots(rows, "rows")
+    if n != T:
         raise ValueError("x and rows must have the same number of tokens")
-    H = x.shape[1]
-    out = _out_like(out, "out", (T * k, H), x)
-    _check(lib().mxq_moe_dispatch(_ptr(x), code, T, k, H, _ld(x), _ptr(rows), _ptr(out), _ld(out), _stream()),
+    out, ldo = _result(out, "out", x, code, T * k, H)
+    _check(lib().mxq_moe_dispatch(x.data_ptr(), code, T, k, H, ld, r, out.data_ptr(), ldo, _stream_of(x)),
            "mxq_moe_dispatch")
     return out
 
@@ -627,94 +637,89 @@ def moe_combine(y: torch.Tensor, rows: torch.Tensor, weights=None, out=None) -> 
     """out[t] = sum over a token's slots of weight * y[row] (see mxq_moe_combine):
     y [T * k, H] in expert order, weights fp32 [T, k] from route.  Without weights it
     is the plain sum, the gradient of moe_dispatch.  Returns [T, H]."""
-    code = _matrix(y, "y")
-    T, k = _rows_shape(rows)
-    if y.shape[0] != T * k:
+    code, n, H, ld = _matrix(y, "y")
+    r, T, k = _slots(rows, "rows")
+    if n != T * k:
         raise ValueError("y must have a row for every slot")
-    if weights is not None:
-        _dense(weights, "weights", torch.float32, (T, k))
-    H = y.shape[1]
-    out = _out_like(out, "out", (T, H), y)
-    _check(lib().mxq_moe_combine(_ptr(y), code, T, k, H, _ld(y), _ptr(rows), _ptr(weights), _ptr(out), _ld(out),
-                                 _stream()), "mxq_moe_combine")
+    w = None if weights is None else _dense(weights, "weights", torch.float32, T, k)
+    out, ldo = _result(out, "out", y, code, T, H)
+    _check(lib().mxq_moe_combine(y.data_ptr(), code, T, k, H, ld, r, w, out.data_ptr(), ldo, _stream_of(y)),
+           "mxq_moe_combine")
     return out
 
 
 def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor, out=None):
     """Gradients of moe_combine (see mxq_moe_combine_backward): returns
-    (dy [T * k, H], dweights fp32 [T, k]); `out` may supply both."""
-    code = _matrix(y, "y")
-    T, k = _rows_shape(rows)
-    H = y.shape[1]
-    if y.shape[0] != T * k:
+    (dy [T * k, H], dweights fp32 [T, k]); `out` may supply either or both."""
+    code, n, H, ldy = _matrix(y, "y")
+    r, T, k = _slots(rows, "rows")
+    if n != T * k:
         raise ValueError("y must have a row for every slot")
-    if _matrix(dout, "dout") != code or tuple(dout.shape) != (T, H):
+    c, n, h, ldd = _matrix(dout, "dout")
+    if c != code or n != T or h != H:
         raise ValueError(f"dout must be {str(y.dtype)[6:]} {[T, H]}")
-    _dense(weights, "weights", torch.float32, (T, k))
+    w = _dense(weights, "weights", torch.float32, T, k)
     dy, dweights = (None, None) if out is None else out
-    dy = _out_like(dy, "dy", (T * k, H), y)
+    dy, lddy = _result(dy, "dy", y, code, T * k, H)
     if dweights is None:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
+        dweights = torch.empty_like(weights)
+        d = dweights.data_ptr()
     else:
-        _dense(dweights, "dweights", torch.float32, (T, k))
-    _check(lib().mxq_moe_combine_backward(_ptr(dout), _ptr(y), code, T, k, H, _ld(dout), _ld(y), _ptr(rows),
-                                          _ptr(weights), _ptr(dy), _ld(dy), _ptr(dweights), _stream()),
-           "mxq_moe_combine_backward")
+        d = _dense(dweights, "dweights", torch.float32, T, k)
+    _check(lib().mxq_moe_combine_backward(dout.data_ptr(), y.data_ptr(), code, T, k, H, ldd, ldy, r, w, dy.data_ptr(),
+                                          lddy, d, _stream_of(y)), "mxq_moe_combine_backward")
     return dy, dweights
 
 
 def _param(t, name, cols):
-    """dtype code of a weight or shift [cols]."""
+    """(address, dtype code) of a weight or shift [cols]."""
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be bfloat16 or float32")
-    _dense(t, name, t.dtype, (cols,))
-    return code
+    return _dense(t, name, t.dtype, cols), code
 
 
 def layer_norm(x: torch.Tensor, weight=None, shift=None, eps: float = 1e-5, out=None):
     """Layer norm of every row of x [M, C] (see mxq_layer_norm); weight and shift [C],
     bf16 or fp32 (both alike), optional.  Returns (y [M, C], mean fp32 [M], rstd fp32
-    [M]); `out` may supply the three (y may be x)."""
-    code = _matrix(x, "x")
-    M, C = x.shape
-    pcode = _param(weight, "weight", C) if weight is not None else None
-    if shift is not None:
-        scode = _param(shift, "shift", C)
-        if pcode is not None and scode != pcode:
-            raise ValueError("weight and shift must have the same dtype")
-        pcode = scode
+    [M]); `out` may supply the three (y may be x; None for a new tensor)."""
+    code, M, C, ld = _matrix(x, "x")
+    w, wcode = (None, None) if weight is None else _param(weight, "weight", C)
+    s, scode = (None, wcode) if shift is None else _param(shift, "shift", C)
+    if wcode is not None and scode != wcode:
+        raise ValueError("weight and shift must have the same dtype")
     y, mean, rstd = (None, None, None) if out is None else out
-    y = _out_like(y, "y", (M, C), x)
-    if mean is None:
-        mean = torch.empty(M, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    y, ldy = _result(y, "y", x, code, M, C)
+    if mean is None or rstd is None:
+        mean, rstd = x.new_empty(M, dtype=torch.float32), x.new_empty(M, dtype=torch.float32)
+        m, r = mean.data_ptr(), rstd.data_ptr()
     else:
-        _dense(mean, "mean", torch.float32, (M,))
-        _dense(rstd, "rstd", torch.float32, (M,))
-    _check(lib().mxq_layer_norm(_ptr(x), code, M, C, _ld(x), _ptr(weight), _ptr(shift), pcode or 0, eps, _ptr(y), _ld(y),
-                                _ptr(mean), _ptr(rstd), _stream()), "mxq_layer_norm")
+        m = _dense(mean, "mean", torch.float32, M)
+        r = _dense(rstd, "rstd", torch.float32, M)
+    _check(lib().mxq_layer_norm(x.data_ptr(), code, M, C, ld, w, s, scode or 0, eps, y.data_ptr(), ldy, m, r,
+                                _stream_of(x)), "mxq_layer_norm")
     return y, mean, rstd
 
 
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight, mean: torch.Tensor, rstd: torch.Tensor, out=None):
     """Gradients of layer_norm (see mxq_layer_norm_backward): returns (dx [M, C],
     dweight fp32 [C], dshift fp32 [C]); `out` may supply dx (which may be dy)."""
-    code = _matrix(x, "x")
-    M, C = x.shape
-    if _matrix(dy, "dy") != code or tuple(dy.shape) != (M, C):
+    code, M, C, ldx = _matrix(x, "x")
+    c, m, n, ldg = _matrix(dy, "dy")
+    if c != code or m != M or n != C:
         raise ValueError(f"dy must be {str(x.dtype)[6:]} {[M, C]}")
-    pcode = _param(weight, "weight", C) if weight is not None else 0
-    _dense(mean, "mean", torch.float32, (M,))
-    _dense(rstd, "rstd", torch.float32, (M,))
-    dx = _out_like(out, "out", (M, C), x)
-    sums = torch.empty((2, C), dtype=torch.float32, device=x.device)
-    size = int(lib().mxq_layer_norm_backward_workspace_size(M, C))
-    workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
-    _check(lib().mxq_layer_norm_backward(_ptr(dy), _ptr(x), code, M, C, _ld(dy), _ld(x), _ptr(weight), pcode, _ptr(mean),
-                                         _ptr(rstd), _ptr(dx), _ld(dx), _ptr(sums[0]), _ptr(sums[1]), _ptr(workspace),
-                                         size, _stream()), "mxq_layer_norm_backward")
-    return dx, sums[0], sums[1]
+    w, wcode = (None, 0) if weight is None else _param(weight, "weight", C)
+    mu = _dense(mean, "mean", torch.float32, M)
+    r = _dense(rstd, "rstd", torch.float32, M)
+    dx, lddx = _result(out, "out", x, code, M, C)
+    L = lib()
+    dweight, dshift = x.new_empty(C, dtype=torch.float32), x.new_empty(C, dtype=torch.float32)
+    size = L.mxq_layer_norm_backward_workspace_size(M, C)
+    workspace = x.new_empty(size, dtype=torch.uint8)
+    _check(L.mxq_layer_norm_backward(dy.data_ptr(), x.data_ptr(), code, M, C, ldg, ldx, w, wcode, mu, r, dx.data_ptr(),
+                                     lddx, dweight.data_ptr(), dshift.data_ptr(), workspace.data_ptr(), size,
+                                     _stream_of(x)), "mxq_layer_norm_backward")
+    return dx, dweight, dshift
 
 
 class GradDesc(ctypes.Structure):
@@ -723,21 +728,29 @@ class GradDesc(ctypes.Structure):
 
 
 def _grad_descs(grads, outs):
-    descs = (GradDesc * max(1, len(grads)))()
-    for d, g, o in zip(descs, grads, outs):
-        code = _DTYPES.get(g.dtype)
-        if code is None or not g.is_cuda or not g.is_contiguous():
-            raise ValueError("gradients must be contiguous bfloat16 or float32 CUDA tensors")
-        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous()):
-            raise ValueError("every output must be contiguous and match its gradient")
-        d.grad, d.out, d.numel, d.dtype = g.data_ptr(), o.data_ptr(), g.numel(), code
-    return descs
+    """The descriptors of a list of gradients as (array of 64-bit words, its address):
+    four words for each, the last one the dtype in its low half."""
+    if len(grads) > MAX_GRADS:
+        raise ValueError(f"at most {MAX_GRADS} gradients")
+    T = torch.Tensor
+    codes = [_DTYPES.get(g.dtype) for g in grads]
+    if None in codes or not all(map(T.is_contiguous, grads)) or not all([g.is_cuda for g in grads]):
+        raise ValueError("gradients must be contiguous bfloat16 or float32 CUDA tensors")
+    sizes = list(map(T.numel, grads))
+    ptrs = list(map(T.data_ptr, grads))
+    to = ptrs
+    if outs is not grads:
+        if (len(outs) != len(grads) or [_DTYPES.get(o.dtype) for o in outs] != codes or list(map(T.numel, outs)) != sizes
+                or not all(map(T.is_contiguous, outs)) or not all([o.is_cuda for o in outs])):
+            raise ValueError("out must have a contiguous tensor like every gradient")
+        to = list(map(T.data_ptr, outs))
+    words = array.array("q", [v for four in zip(ptrs, to, sizes, codes) for v in four])
+    return words, words.buffer_info()[0]
 
 
 def _norm_buffers(grads):
-    if len(grads) > MAX_GRADS:
-        raise ValueError(f"at most {MAX_GRADS} gradients")
-    size = int(lib().mxq_grad_norm_workspace_size(len(grads)))
+    """(norm, workspace, its bytes)."""
+    size = lib().mxq_grad_norm_workspace_size(len(grads))
     device = grads[0].device if grads else torch.device("cuda")
     return (torch.empty((), dtype=torch.float32, device=device), torch.empty(size, dtype=torch.uint8, device=device),
             size)
@@ -747,9 +760,10 @@ def grad_norm(grads) -> torch.Tensor:
     """The 2-norm over all of a list of gradients (bf16 and fp32 mixed), an fp32
     scalar on the device (see mxq_grad_norm)."""
     grads = list(grads)
-    descs = _grad_descs(grads, grads)
+    words, descs = _grad_descs(grads, grads)
     norm, workspace, size = _norm_buffers(grads)
-    _check(lib().mxq_grad_norm(descs, len(grads), _ptr(norm), _ptr(workspace), size, _stream()), "mxq_grad_norm")
+    _check(lib().mxq_grad_norm(descs, len(grads), norm.data_ptr(), workspace.data_ptr(), size, _stream_of(norm)),
+           "mxq_grad_norm")
     return norm
 
 
@@ -760,12 +774,10 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None):
     scalar on the device, the list of outputs)."""
     grads = list(grads)
     out = [torch.empty_like(g) for g in grads] if out is None else list(out)
-    if len(out) != len(grads):
-        raise ValueError("out must have a tensor for every gradient")
-    descs = _grad_descs(grads, out)
+    words, descs = _grad_descs(grads, out)
     norm, workspace, size = _norm_buffers(grads)
-    _check(lib().mxq_clip_grad_norm(descs, len(grads), max_norm, eps, _ptr(norm), _ptr(workspace), size, _stream()),
-           "mxq_clip_grad_norm")
+    _check(lib().mxq_clip_grad_norm(descs, len(grads), max_norm, eps, norm.data_ptr(), workspace.data_ptr(), size,
+                                    _stream_of(norm)), "mxq_clip_grad_norm")
     return norm, out
 
 

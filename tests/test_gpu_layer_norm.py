@@ -97,6 +97,22 @@ def test_layer_norm_and_gradients(M, C, dtype, wdtype):
     _check_backward(dy, x, w, mean, rstd, dx, dw, db)
 
 
+@pytest.mark.parametrize("dtype,wdtype", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32),
+                                          (torch.bfloat16, torch.float32)])
+@pytest.mark.parametrize("M,C", [(4000, 520), (3000, 640), (2001, 2048), (1300, 7168), (1111, 1111), (2500, 515),
+                                 (1531, 4097), (900, 8999), (700, 16384), (9000, 130), (6001, 257), (500, 12345)])
+def test_many_rows(M, C, dtype, wdtype):
+    """Every block walks over many rows: more than the shared memory holds at a time."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    x, w, b, dy = _problem(M, C, dtype, wdtype, M + C)
+    y, mean, rstd = mxq.layer_norm(x, w, b, eps=1e-5)
+    _check_forward(x, w, b, 1e-5, y, mean, rstd)
+    one = mxq.layer_norm_backward(dy, x, w, mean, rstd)
+    _check_backward(dy, x, w, mean, rstd, *one)
+    assert all(torch.equal(p, q) for p, q in zip(one, mxq.layer_norm_backward(dy, x, w, mean, rstd)))
+    assert mxq.get_device_status() == 0
+
+
 def test_without_weight_or_shift():
     from mxfp8_microscaled_precision_gb300 import mxq
     for C in (96, 97):
