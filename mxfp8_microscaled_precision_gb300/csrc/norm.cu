@@ -344,10 +344,20 @@ constexpr int64_t kRingBytes = 204 * 1024;
 
 struct RingBars {
     uint64_t full[kMaxStages];
-    int copies[kMaxStages];    // into each stage, by now
     int abort_flag;            // a wait ran out
     int stop[kMaxGroups][2];   // it as a group's first thread saw it before the barrier of a row (by parity):
                                // the whole group acts on that
+};
+
+// Place of a group in the ring and in the rows.
+struct RingPlace {
+    int64_t row;
+    int stage, phase;
+    __device__ __forceinline__ void move(int by, int stages) {   // to the block's row that many further
+        row += static_cast<int64_t>(by) * gridDim.x;
+        stage += by;
+        while (stage >= stages) stage -= stages, phase ^= 1;
+    }
 };
 
 template <typename T, bool kAny>
@@ -376,15 +386,12 @@ struct RowRing {
         full = smem_u32(bars->full);
         row_bytes = (cols * static_cast<int>(sizeof(T)) + 15) / 16 * 16 + (kAny ? 16 : 0);
         stages = stage_count;
-        if (threadIdx.x == 0) {
-            bars->abort_flag = 0;
-            for (int s = 0; s < stages; ++s) {
-                bars->copies[s] = 0;
-                mbar_init(full + 8 * s, 1);
-            }
+        if (threadIdx.x == 0) bars->abort_flag = 0;
+        if (threadIdx.x < stages) {   // stages <= 32: a lane of the first warp each
+            mbar_init(full + 8 * threadIdx.x, 1);
             fence_mbar_init();
-            int64_t row = blockIdx.x;
-            for (int s = 0; s < stages && row < rows; ++s, row += gridDim.x) fetch(row, s);
+            const int64_t row = blockIdx.x + static_cast<int64_t>(threadIdx.x) * gridDim.x;
+            if (row < rows) fetch(row, threadIdx.x);
         }
     }
 
@@ -414,33 +421,31 @@ struct RowRing {
             bytes[k] = hi - lo;
         }
         const uint32_t bar = full + 8 * stage;
-        ++bars->copies[stage];
         mbar_arrive_expect_tx(bar, bytes[0] + bytes[1]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) bulk_load(smem_u32(dst + k * row_bytes + skip[k]), from[k], bytes[k], bar);
     }
 
-    // All threads of its group have read a row: its stage takes the row `stages` further.
+    // All threads of its group have read a row (the values are in use): its stage takes the row
+    // `stages` further.
     __device__ __forceinline__ void refill(int64_t row, int stage) {
         const int64_t next = row + static_cast<int64_t>(stages) * gridDim.x;
-        if (next >= rows) return;
-        fence_proxy_async_smem();   // the group's reads of the stage before the copy's writes
-        fetch(next, stage);
+        if (next < rows) fetch(next, stage);
     }
 
-    // After a wait that ran out, by all threads that have not ended: one of each group that
-    // gave up waits (bounded) for the copies in flight before the block ends.
-    __device__ __noinline__ void drain(const WaitGuard& guard, bool first_of_group) {
-        __syncthreads();
-        if (!first_of_group) return;
+    // After a wait that ran out, by the first thread of a group that gave up: waits (bounded) for
+    // the copies in flight into the group's stages (from p on, every groups-th row; groups = stages: for
+    // the row at p alone), as the block must not end before them.
+    __device__ __noinline__ void drain(RingPlace p, int groups, const WaitGuard& guard) {
         int again = 0;
         const WaitGuard last{&again, guard.status, guard.limit_ns};
-        for (int s = 0; s < stages; ++s)
-            if (bars->copies[s] > 0) mbar_wait(full + 8 * s, (bars->copies[s] - 1) & 1, last);
+        for (int i = 0; i < stages / groups && p.row < rows; ++i, p.move(groups, stages))
+            mbar_wait(full + 8 * p.stage, p.phase, last);
     }
 
-    __device__ __forceinline__ void wait(int stage, int phase, const WaitGuard& guard) const {
-        if (!mbar_try_wait(full + 8 * stage, phase)) mbar_wait(full + 8 * stage, phase, guard);
+    // False, with abort_flag set, if the row did not arrive in time.
+    __device__ __forceinline__ bool wait(const RingPlace& p, const WaitGuard& guard) const {
+        return mbar_try_wait(full + 8 * p.stage, p.phase) || mbar_wait(full + 8 * p.stage, p.phase, guard);
     }
 
     // Vector q of x's row (k = 0) in `stage`, elements [i, i + V), or the same elements of dy's,
@@ -455,23 +460,9 @@ struct RowRing {
     }
 };
 
-// Place of a group in the ring and in the rows.
-struct RingPlace {
-    int64_t row;
-    int stage, phase;
-    __device__ __forceinline__ void move(int by, int stages) {   // to the block's row that many further
-        row += static_cast<int64_t>(by) * gridDim.x;
-        stage += by;
-        while (stage >= stages) stage -= stages, phase ^= 1;
-    }
-};
-
-// The group's barrier for a row; true if the group has to give up (the same for all its threads).
-__device__ __forceinline__ bool group_barrier(RingBars& bars, int group, int at, int tpr, int parity) {
-    if (at == 0) bars.stop[group][parity] = *static_cast<volatile int*>(&bars.abort_flag);
+__device__ __forceinline__ void group_barrier(int group, int tpr) {
     if (tpr == 32) __syncwarp();
     else named_bar_sync(1 + group, tpr);
-    return bars.stop[group][parity] != 0;
 }
 
 // A thread of 16 elements a row (kKeep) keeps h and u of the row between the two passes; a
@@ -523,7 +514,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_backward_kernel(const No
     while (place.row < a.rows) {
         const float2 st = stats[group][odd];
         const f32x2 rr = pair(st.y, st.y), off = pair(-st.x * st.y, -st.x * st.y);
-        ring.wait(place.stage, place.phase, guard);   // if it runs out, abort_flag is set: seen after the barrier
+        if (at == 0) {
+            bars.stop[group][odd] = *static_cast<volatile int*>(&bars.abort_flag);
+            stats[group][odd ^ 1] = later;
+            later = statistics(place.row + 2 * stride);
+        }
+        const bool arrived = ring.wait(place, guard);   // if not, abort_flag is set: the group stops at its next row
         f32x2 h[kKeep ? kN : 1][H], u[kKeep ? kN : 1][H];
         f32x2 s1 = 0, s2 = 0;
 #pragma unroll
@@ -538,13 +534,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_backward_kernel(const No
         }
         const f32x2 both = warp_sum2(pair(lo_of(s1) + hi_of(s1), lo_of(s2) + hi_of(s2)));
         if (lane == 0) sums[group][odd][warp] = both;
-        if (at == 0) {
-            stats[group][odd ^ 1] = later;
-            later = statistics(place.row + 2 * stride);
-        }
-        stop = group_barrier(bars, group, at, tpr, odd);
+        group_barrier(group, tpr);
+        stop = bars.stop[group][odd] != 0;   // the same for the whole group
         if (stop) break;
-        if (kKeep && at == 0) ring.refill(place.row, place.stage);
+        if (kKeep && at == 0 && arrived) ring.refill(place.row, place.stage);   // never into a copy on its way
         f32x2 total = sums[group][odd][lane & 15];
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) total = add2(total, __shfl_xor_sync(0xFFFFFFFFu, total, d));
@@ -570,10 +563,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_backward_kernel(const No
             store16<S, kAny>(dx, i, cols, pack2<T>(u[m]), !kAny || lead_of<S>(dx) == lead_x);
         }
         if constexpr (!kKeep) {   // the row has been read a second time
-            stop = group_barrier(bars, group, at, tpr, odd);
-            if (stop) break;
-            if (at == 0) ring.refill(place.row, place.stage);
+            group_barrier(group, tpr);
+            if (at == 0 && arrived) ring.refill(place.row, place.stage);
         }
+        if (at == 0 && !arrived) ring.drain(place, stages, guard);
         place.move(groups, stages);
         odd ^= 1;
     }
@@ -590,7 +583,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_backward_kernel(const No
         named_bar_sync(15, groups * tpr);
         for (int i = threadIdx.x; i < 2 * cols; i += groups * tpr) part[i] = meet[i];
     }
-    if (stop) ring.drain(guard, at == 0);   // a group that gave up
+    if (stop && at == 0) ring.drain(place, groups, guard);   // the group gave up
 }
 
 // The longest rows: element by element.  dw and db by columns, one thread each, over the block's rows (their shares in the workspace),
@@ -634,26 +627,25 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormBack
     }
 }
 
-// Columns of dw (and of db): 32 columns a block, 8 threads a column that take
-// the blocks' shares in turn; their 8 sums are added in order.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* partial, int parts, int64_t cols, float* dw,
-                                                          float* db) {
-    __shared__ float sh[8][33];
+// Columns of dw (and of db): 32 columns a block, 32 threads a column that take the
+// blocks' shares in turn; a warp adds up the 32 sums of a column.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* partial, int parts, int cols, float* dw,
+                                                           float* db) {
+    __shared__ float sh[32][33];
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    int i = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (i < 2 * cols) {
-#pragma unroll 8
-        for (int p = y; p < parts; p += 8) s += partial[static_cast<int64_t>(p) * 2 * cols + i];
+#pragma unroll 5
+        for (int p = y; p < parts; p += 32) s += partial[static_cast<int64_t>(p) * 2 * cols + i];
     }
     sh[y][lane] = s;
     __syncthreads();
-    if (y == 0 && i < 2 * cols) {
-        float t = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) t += sh[k][lane];
+    s = warp_sum(sh[lane][y]);
+    i = blockIdx.x * 32 + y;
+    if (lane == 0 && i < 2 * cols) {
         float* out = i < cols ? dw : db;
-        if (out != nullptr) out[i < cols ? i : i - cols] = t;
+        if (out != nullptr) out[i < cols ? i : i - cols] = s;
     }
 }
 
@@ -772,8 +764,8 @@ cudaError_t norm_backward_launch(const NormBackwardArgs& a, cudaStream_t stream)
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || (a.dweight == nullptr && a.dshift == nullptr)) return e;
-    norm_reduce_kernel<<<static_cast<unsigned>((2 * a.cols + 31) / 32), 256, 0, stream>>>(
-        a.partial, static_cast<int>(parts), a.cols, a.dweight, a.dshift);
+    norm_reduce_kernel<<<static_cast<unsigned>((2 * a.cols + 31) / 32), 1024, 0, stream>>>(
+        a.partial, static_cast<int>(parts), static_cast<int>(a.cols), a.dweight, a.dshift);
     return cudaGetLastError();
 }
 
