@@ -23,12 +23,19 @@ namespace cg = cooperative_groups;
 namespace mxq {
 namespace {
 
+constexpr int64_t kPlanWords = 50 * 1024;   // shared memory of a block of the plan, in words
+
 // ---- plan ------------------------------------------------------------------------
 
 // One cluster counts and places all slots: warp w of the cluster's warps owns
-// the slots [w * chunk, (w + 1) * chunk).  Bucket E takes the dropped slots.
-// Shared memory: hist[warps][E + 1] slots per warp and bucket (then: where the
-// warp's next slot of the bucket goes), count[E + 1] of the block, base[E + 1].
+// the slots [w * chunk, (w + 1) * chunk).  Bucket E takes the dropped slots.  Counting
+// goes by integer atomics in shared memory; the places keep the slots' order by the set of a warp's
+// lanes in each bucket, which the lanes write as bits into a word of the bucket (a
+// warp-wide match instruction did the same five times slower).
+//
+// Shared memory, B = E + 1 words each: hist[warps][B] slots of a warp in a bucket, then
+// where its next one goes; lanes[warps][B], zero between steps; count[B] of the
+// block; base[B]; 32 for the scan.
 __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* ids, int64_t slots, int E, int64_t chunk,
                                                     int64_t* offsets, int32_t* rows) {
     extern __shared__ int sh[];
@@ -36,29 +43,28 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* ids, int64_t 
     const int B = E + 1;
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int* hist = sh;
-    int* count = hist + warps * B;
+    int* lanes = hist + warps * B;
+    int* count = lanes + warps * B;
     int* base = count + B;
+    int* scan = base + B;
     const unsigned rank = cluster.block_rank(), blocks = cluster.num_blocks();
 
-    for (int i = threadIdx.x; i < warps * B; i += blockDim.x) hist[i] = 0;
+    for (int i = threadIdx.x; i < 2 * warps * B; i += blockDim.x) sh[i] = 0;
     __syncthreads();
     const int64_t lo = (static_cast<int64_t>(rank) * warps + warp) * chunk;
     const int64_t hi = min(slots, lo + chunk);
     int* mine = hist + warp * B;
-    for (int64_t s0 = lo; s0 < hi; s0 += 32) {
-        const int64_t s = s0 + lane;
-        int e = -1;
-        if (s < hi) {
-            e = ids[s];
-            if (e < 0 || e >= E) e = E;
-        }
-        const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
-        if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-        __syncwarp();
-    }
+    int* bits = lanes + warp * B;
+    auto bucket = [&](int64_t s) {
+        const int e = ids[s];
+        return e < 0 || e >= E ? E : e;
+    };
+#pragma unroll 4
+    for (int64_t s = lo + lane; s < hi; s += 32) atomicAdd(mine + bucket(s), 1);
     __syncthreads();
     for (int e = threadIdx.x; e < B; e += blockDim.x) {   // exclusive over the block's warps
         int sum = 0;
+#pragma unroll 8
         for (int w = 0; w < warps; ++w) {
             const int n = hist[w * B + e];
             hist[w * B + e] = sum;
@@ -67,49 +73,61 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* ids, int64_t 
         count[e] = sum;
     }
     cluster.sync();
-    // base[e] = slots of the cluster's earlier blocks in bucket e; total in count's place is
-    // kept apart (count is read by the other blocks until the next cluster barrier).
-    if (warp == 0) {
-        int carry = 0;
-        for (int e0 = 0; e0 < B; e0 += 32) {
-            const int e = e0 + lane;
-            int before = 0, total = 0;
-            if (e < B) {
-                for (unsigned b = 0; b < blocks; ++b) {
-                    const int n = cluster.map_shared_rank(count, b)[e];
-                    total += n;
-                    if (b < rank) before += n;
-                }
+    // First row of each bucket (a scan over the buckets' totals) plus the slots of the
+    // cluster's earlier blocks in it.
+    int carry = 0;
+    for (int e0 = 0; e0 < B; e0 += blockDim.x) {
+        const int e = e0 + threadIdx.x;
+        int before = 0, total = 0;
+        if (e < B) {
+            for (unsigned b = 0; b < blocks; ++b) {
+                const int n = cluster.map_shared_rank(count, b)[e];
+                total += n;
+                if (b < rank) before += n;
             }
-            int scan = total;
+        }
+        int sum = total;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, scan, d);
-                if (lane >= d) scan += v;
-            }
-            if (e < B) {
-                const int first = carry + scan - total;
-                base[e] = first + before;
-                if (rank == 0) offsets[e] = first;   // bucket E starts where the experts' rows end
-            }
-            carry += __shfl_sync(0xFFFFFFFFu, scan, 31);
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+            if (lane >= d) sum += v;
+        }
+        if (lane == 31) scan[warp] = sum;
+        __syncthreads();
+        int earlier = carry, all = carry;   // the warps before this one, and all
+        for (int w = 0; w < warps; ++w) {
+            all += scan[w];
+            if (w < warp) earlier += scan[w];
+        }
+        __syncthreads();
+        carry = all;
+        if (e < B) {
+            const int first = earlier + sum - total;
+            base[e] = first + before;
+            if (rank == 0) offsets[e] = first;   // bucket E starts where the experts' rows end
         }
     }
-    cluster.sync();
+    cluster.sync();   // base is written, and nobody reads another block's count any more
+    int next = lo + lane < hi ? bucket(lo + lane) : -1;
     for (int64_t s0 = lo; s0 < hi; s0 += 32) {
         const int64_t s = s0 + lane;
-        int e = -1;
-        if (s < hi) {
-            e = ids[s];
-            if (e < 0 || e >= E) e = E;
-        }
-        const unsigned peers = __match_any_sync(0xFFFFFFFFu, e);
+        const int e = next;
+        next = s + 32 < hi ? bucket(s + 32) : -1;
+        if (e >= 0) atomicOr(bits + e, 1 << lane);
+        __syncwarp();
+        unsigned peers = 0;
+        int at = 0;
         if (e >= 0) {
-            const int row = base[e] + mine[e] + __popc(peers & ((1u << lane) - 1u));
+            peers = static_cast<unsigned>(bits[e]);
+            at = mine[e];
+            const int row = base[e] + at + __popc(peers & ((1u << lane) - 1u));
             rows[s] = e == E ? -1 - row : row;
         }
         __syncwarp();
-        if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+        if (e >= 0 && lane == __ffs(peers) - 1) {
+            mine[e] = at + __popc(peers);
+            bits[e] = 0;
+        }
         __syncwarp();
     }
 }
@@ -288,20 +306,30 @@ cudaError_t combine_backward_launch(const PermuteArgs& a, const void* dout, cons
 
 cudaError_t launch_moe_plan(const int32_t* ids, int64_t slots, int experts, int64_t* offsets, int32_t* rows,
                             cudaStream_t stream) {
-    const int B = experts + 1;
-    int blocks = 1, warps = 32;
-    if (slots > 4096) blocks = 8;
-    if (slots <= 32 * 32) warps = static_cast<int>((slots + 31) / 32);
-    if (warps < 4) warps = 4;
-    const int64_t all = static_cast<int64_t>(blocks) * warps;
+    // A warp takes 32 slots at least; one block up to 1024 slots, else a cluster of up to 16 (the most
+    // that an SM group of this GPU holds).
+    const int64_t B = experts + 1;
+    int64_t warps = 32, blocks = 16;
+    if (warps > kPlanWords / (2 * B)) warps = kPlanWords / (2 * B);
+    if (slots <= 32 * warps) {
+        blocks = 1;
+        warps = (slots + 31) / 32 > 8 ? (slots + 31) / 32 : 8;
+    } else {
+        while (blocks > 2 && slots <= blocks / 2 * warps * 32) blocks /= 2;
+    }
+    const int64_t all = blocks * warps;
     const int64_t chunk = ((slots + all - 1) / all + 31) / 32 * 32;
-    const size_t smem = sizeof(int) * (static_cast<size_t>(warps) * B + 2 * static_cast<size_t>(B));
+    const size_t smem = sizeof(int) * static_cast<size_t>(2 * warps * B + 2 * B + 32);
     cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
+    if (blocks > 8) {
+        e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(32 * warps);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
