@@ -83,7 +83,7 @@ mxq_status clip(const mxq_grad_desc* grads, int32_t count, bool scale, float max
     }
     const mxq_status st = device_ok();
     if (st != MXQ_OK) return st;
-    return from_cuda(mxq::launch_clip(list.get(), count, scale, max_norm, eps, norm, static_cast<double*>(workspace),
+    return from_cuda(mxq::launch_clip(list.get(), count, scale, max_norm, eps, norm, static_cast<float*>(workspace),
                                       cu(stream)));
 }
 
@@ -245,7 +245,7 @@ mxq_status mxq_layer_norm_backward(const void* dy, const void* x, mxq_dtype dtyp
 
 size_t mxq_grad_norm_workspace_size(int32_t count) {
     if (count < 0 || count > MXQ_MAX_GRADS) return 0;
-    return static_cast<size_t>(mxq::clip_partials(count)) * sizeof(double);
+    return static_cast<size_t>(mxq::clip_partials(count)) * sizeof(float);
 }
 
 mxq_status mxq_grad_norm(const mxq_grad_desc* grads, int32_t count, float* norm, void* workspace, size_t workspace_bytes,

@@ -188,9 +188,9 @@ struct ClipTensor {
     int64_t n;
     bool f32;
 };
-constexpr int kClipBlocks = 608;   // partial sums of one launch
+constexpr int kClipBlocks = 1216;   // partial sums of one launch
 int clip_partials(int count);
 cudaError_t launch_clip(const ClipTensor* tensors, int count, bool scale_too, float max_norm, float eps, float* norm,
-                        double* partial, cudaStream_t stream);
+                        float* partial, cudaStream_t stream);
 
 }  // namespace mxq
