@@ -1,4 +1,5 @@
-"""Build libmxq.so (the CUDA library) in-tree with nvcc for sm_103a.
+"""Build libmxq.so (the CUDA library) in-tree with nvcc for sm_103a, and the
+extension module that calls it from Python (csrc/calls.c) with gcc.
 
 The translation units are compiled in parallel, then linked into
 ``mxfp8_microscaled_precision_gb300/_build/libmxq.so`` (the CUDA runtime is
@@ -12,6 +13,7 @@ import fcntl
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libmxq.so")
+CALLS = os.path.join(OUT, "_mxqcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "tensor_map.cu", "fsdp.cu", "noalloc.cu",
            "api_block.cu", "route.cu", "permute.cu", "norm.cu", "clip.cu"]
 HEADERS = ["mxq_device.cuh", "mxq_internal.h", "mxq_quant_math.cuh", "mxq_elem.cuh"]
@@ -35,10 +38,10 @@ def _nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "mxq.h")]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + ["calls.c"]] + [os.path.join(INCLUDE, "mxq.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -80,6 +83,14 @@ def _build(verbose: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I" + INCLUDE,
+           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "calls.c"), "-o", tmp, "-L" + OUT, "-l:libmxq.so",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for calls.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
     return LIB
 
 

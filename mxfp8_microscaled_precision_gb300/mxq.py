@@ -15,8 +15,8 @@ block-scaled FP8 matmuls with BF16 output.
 """
 from __future__ import annotations
 
-import array
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -125,7 +125,7 @@ def status_string(status: int) -> str:
 
 
 def _check(status: int, what: str):
-    if status != 0:
+    if status:
         raise MXQError(what, status, status_string(status))
 
 
@@ -501,8 +501,26 @@ MAX_GRADS = 65536
 
 
 # These calls are made for single tokens too, where the host's share is most of the
-# time: addresses go to ctypes as integers, the stream comes without building a Stream object, and a
-# check looks only at what the library cannot see.
+# time: they go through an extension module instead of ctypes (csrc/calls.c), the stream comes without
+# building a Stream object, and a check looks only at what the library cannot see.
+_calls_module = None
+
+
+def _calls():
+    """The extension module that calls the library, loaded once.  Raises if it has not
+    been built."""
+    global _calls_module
+    if _calls_module is None:
+        lib()   # raises the same way if nothing has been built
+        spec = importlib.util.spec_from_file_location("_mxqcall", _build.CALLS)
+        if spec is None or not os.path.exists(_build.CALLS):
+            raise RuntimeError(f"the extension module is not built ({_build.CALLS}); run __graft_entry__.build()")
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _calls_module = module
+    return _calls_module
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -572,7 +590,7 @@ def route(logits: torch.Tensor, topk: int, score="softmax", bias=None, n_group: 
         ids, weights = out
         i = _dense(ids, "ids", torch.int32, T, topk)
         w = _dense(weights, "weights", torch.float32, T, topk)
-    _check(lib().mxq_route(logits.data_ptr(), code, T, E, ld, b, m, _of(_SCORES, score, "score"), n_group, topk_group,
+    _check(_calls().route(logits.data_ptr(), code, T, E, ld, b, m, _of(_SCORES, score, "score"), n_group, topk_group,
                            _of(_GROUP_SCORES, group_score, "group score"), topk, 1 if renorm else 0, scale, i, w,
                            _stream_of(logits)), "mxq_route")
     return ids, weights
@@ -596,7 +614,7 @@ def route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tens
         raise ValueError("ids and logits must have the same number of tokens")
     d = _dense(dweights, "dweights", torch.float32, T, k)
     out, ldo = _result(out, "out", logits, code, T, E)
-    _check(lib().mxq_route_backward(d, i, logits.data_ptr(), code, T, E, ld, _of(_SCORES, score, "score"), k,
+    _check(_calls().route_backward(d, i, logits.data_ptr(), code, T, E, ld, _of(_SCORES, score, "score"), k,
                                     1 if renorm else 0, scale, out.data_ptr(), ldo, _stream_of(logits)),
            "mxq_route_backward")
     return out
@@ -616,7 +634,7 @@ def moe_plan(ids: torch.Tensor, experts: int, out=None):
         offsets, rows = out
         o = _dense(offsets, "offsets", torch.int64, experts + 1)
         r = _dense(rows, "rows", torch.int32, T, k)
-    _check(lib().mxq_moe_plan(i, T, k, experts, o, r, _stream_of(ids)), "mxq_moe_plan")
+    _check(_calls().moe_plan(i, T, k, experts, o, r, _stream_of(ids)), "mxq_moe_plan")
     return offsets, rows
 
 
@@ -628,7 +646,7 @@ def moe_dispatch(x: torch.Tensor, rows: torch.Tensor, out=None) -> torch.Tensor:
     if n != T:
         raise ValueError("x and rows must have the same number of tokens")
     out, ldo = _result(out, "out", x, code, T * k, H)
-    _check(lib().mxq_moe_dispatch(x.data_ptr(), code, T, k, H, ld, r, out.data_ptr(), ldo, _stream_of(x)),
+    _check(_calls().moe_dispatch(x.data_ptr(), code, T, k, H, ld, r, out.data_ptr(), ldo, _stream_of(x)),
            "mxq_moe_dispatch")
     return out
 
@@ -643,7 +661,7 @@ def moe_combine(y: torch.Tensor, rows: torch.Tensor, weights=None, out=None) -> 
         raise ValueError("y must have a row for every slot")
     w = None if weights is None else _dense(weights, "weights", torch.float32, T, k)
     out, ldo = _result(out, "out", y, code, T, H)
-    _check(lib().mxq_moe_combine(y.data_ptr(), code, T, k, H, ld, r, w, out.data_ptr(), ldo, _stream_of(y)),
+    _check(_calls().moe_combine(y.data_ptr(), code, T, k, H, ld, r, w, out.data_ptr(), ldo, _stream_of(y)),
            "mxq_moe_combine")
     return out
 
@@ -666,7 +684,7 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, rows: torch.Tensor
         d = dweights.data_ptr()
     else:
         d = _dense(dweights, "dweights", torch.float32, T, k)
-    _check(lib().mxq_moe_combine_backward(dout.data_ptr(), y.data_ptr(), code, T, k, H, ldd, ldy, r, w, dy.data_ptr(),
+    _check(_calls().moe_combine_backward(dout.data_ptr(), y.data_ptr(), code, T, k, H, ldd, ldy, r, w, dy.data_ptr(),
                                           lddy, d, _stream_of(y)), "mxq_moe_combine_backward")
     return dy, dweights
 
@@ -696,7 +714,7 @@ def layer_norm(x: torch.Tensor, weight=None, shift=None, eps: float = 1e-5, out=
     else:
         m = _dense(mean, "mean", torch.float32, M)
         r = _dense(rstd, "rstd", torch.float32, M)
-    _check(lib().mxq_layer_norm(x.data_ptr(), code, M, C, ld, w, s, scode or 0, eps, y.data_ptr(), ldy, m, r,
+    _check(_calls().layer_norm(x.data_ptr(), code, M, C, ld, w, s, scode or 0, eps, y.data_ptr(), ldy, m, r,
                                 _stream_of(x)), "mxq_layer_norm")
     return y, mean, rstd
 
@@ -712,11 +730,10 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight, mean: torch.T
     mu = _dense(mean, "mean", torch.float32, M)
     r = _dense(rstd, "rstd", torch.float32, M)
     dx, lddx = _result(out, "out", x, code, M, C)
-    L = lib()
     dweight, dshift = x.new_empty(C, dtype=torch.float32), x.new_empty(C, dtype=torch.float32)
-    size = L.mxq_layer_norm_backward_workspace_size(M, C)
+    size = _calls().layer_norm_backward_workspace_size(M, C)
     workspace = x.new_empty(size, dtype=torch.uint8)
-    _check(L.mxq_layer_norm_backward(dy.data_ptr(), x.data_ptr(), code, M, C, ldg, ldx, w, wcode, mu, r, dx.data_ptr(),
+    _check(_calls().layer_norm_backward(dy.data_ptr(), x.data_ptr(), code, M, C, ldg, ldx, w, wcode, mu, r, dx.data_ptr(),
                                      lddx, dweight.data_ptr(), dshift.data_ptr(), workspace.data_ptr(), size,
                                      _stream_of(x)), "mxq_layer_norm_backward")
     return dx, dweight, dshift
@@ -728,29 +745,15 @@ class GradDesc(ctypes.Structure):
 
 
 def _grad_descs(grads, outs):
-    """The descriptors of a list of gradients as (array of 64-bit words, its address):
-    four words for each, the last one the dtype in its low half."""
+    """The mxq_grad_desc array of two lists of tensors, as bytes."""
     if len(grads) > MAX_GRADS:
         raise ValueError(f"at most {MAX_GRADS} gradients")
-    T = torch.Tensor
-    codes = [_DTYPES.get(g.dtype) for g in grads]
-    if None in codes or not all(map(T.is_contiguous, grads)) or not all([g.is_cuda for g in grads]):
-        raise ValueError("gradients must be contiguous bfloat16 or float32 CUDA tensors")
-    sizes = list(map(T.numel, grads))
-    ptrs = list(map(T.data_ptr, grads))
-    to = ptrs
-    if outs is not grads:
-        if (len(outs) != len(grads) or [_DTYPES.get(o.dtype) for o in outs] != codes or list(map(T.numel, outs)) != sizes
-                or not all(map(T.is_contiguous, outs)) or not all([o.is_cuda for o in outs])):
-            raise ValueError("out must have a contiguous tensor like every gradient")
-        to = list(map(T.data_ptr, outs))
-    words = array.array("q", [v for four in zip(ptrs, to, sizes, codes) for v in four])
-    return words, words.buffer_info()[0]
+    return _calls().grad_descs(grads, outs, torch.bfloat16, torch.float32)
 
 
 def _norm_buffers(grads):
     """(norm, workspace, its bytes)."""
-    size = lib().mxq_grad_norm_workspace_size(len(grads))
+    size = _calls().grad_norm_workspace_size(len(grads))
     device = grads[0].device if grads else torch.device("cuda")
     return (torch.empty((), dtype=torch.float32, device=device), torch.empty(size, dtype=torch.uint8, device=device),
             size)
@@ -760,9 +763,9 @@ def grad_norm(grads) -> torch.Tensor:
     """The 2-norm over all of a list of gradients (bf16 and fp32 mixed), an fp32
     scalar on the device (see mxq_grad_norm)."""
     grads = list(grads)
-    words, descs = _grad_descs(grads, grads)
+    descs = _grad_descs(grads, grads)
     norm, workspace, size = _norm_buffers(grads)
-    _check(lib().mxq_grad_norm(descs, len(grads), norm.data_ptr(), workspace.data_ptr(), size, _stream_of(norm)),
+    _check(_calls().grad_norm(descs, len(grads), norm.data_ptr(), workspace.data_ptr(), size, _stream_of(norm)),
            "mxq_grad_norm")
     return norm
 
@@ -774,9 +777,9 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None):
     scalar on the device, the list of outputs)."""
     grads = list(grads)
     out = [torch.empty_like(g) for g in grads] if out is None else list(out)
-    words, descs = _grad_descs(grads, out)
+    descs = _grad_descs(grads, out)
     norm, workspace, size = _norm_buffers(grads)
-    _check(lib().mxq_clip_grad_norm(descs, len(grads), max_norm, eps, norm.data_ptr(), workspace.data_ptr(), size,
+    _check(_calls().clip_grad_norm(descs, len(grads), max_norm, eps, norm.data_ptr(), workspace.data_ptr(), size,
                                     _stream_of(norm)), "mxq_clip_grad_norm")
     return norm, out
 
