@@ -7,14 +7,16 @@
 //   ids = the k largest c, largest first, ties to the lowest expert,
 //   w_j = scale * s_j  [ / (sum_i s_i + 1e-20) ].
 //
-// One warp per token: expert e sits in lane e % 32, register e / 32, so loads
-// are coalesced for any number of experts, and a round of the selection is a
-// scan of the lane's registers and two warp-wide integer reductions (the
-// largest key, then the lowest expert that has it).
+// One warp per token: lane l holds the experts [l N, (l + 1) N), N = the next power of
+// two of experts / 32, so a lane's logits are one vector, of equal values the
+// lowest lane has the lowest expert, and a group of experts is mostly a few neighbouring lanes.  A round of
+// the selection is a scan of the lane's registers, the largest key of the warp and a vote
+// on who has it.  Bound by instructions (some 500 a token of 128 experts).
 
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 #include <type_traits>
 
 #include "mxq_elem.cuh"
@@ -24,35 +26,94 @@ namespace mxq {
 namespace {
 
 constexpr float kRenormEps = 1e-20f;   // keeps a token whose chosen scores are all 0 finite
-constexpr int kWarps = 4;              // tokens per block
+constexpr int kWarps = 8;              // tokens per block
 
 // Order of choice values as unsigned keys: 0 = out (-inf), 1 = NaN (below every
 // number, so that the chosen experts are always distinct and exist), then the
 // numbers in ascending order.
-constexpr uint32_t kOut = 0u;
+constexpr uint32_t kOut = 0u, kNaN = 1u;
 __device__ __forceinline__ uint32_t choice_key(float c) {
-    if (c != c) return 1u;
+    if (c != c) return kNaN;
+    if (c == -INFINITY) return kOut;
     const uint32_t u = __float_as_uint(c + 0.0f);   // -0 and +0 are equal
-    const uint32_t key = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return c == -INFINITY ? kOut : key;
+    return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t key) {   // of a key that is not kOut
+    return key == kNaN ? __uint_as_float(0x7FC00000u) : __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// Score of a group from the keys of its two best values (k1 >= k2).
+__device__ __forceinline__ uint32_t group_key(uint32_t k1, uint32_t k2, bool sums) {
+    if (!sums || k2 == kOut) return k1;
+    const uint32_t key = choice_key(value_of(k1) + value_of(k2));
+    return key == kOut ? kNaN : key;   // a sum that overflowed to -inf: the group still has experts
+}
+
+__device__ __forceinline__ void keep_two(uint32_t k, uint32_t& k1, uint32_t& k2) {
+    const uint32_t low = k < k1 ? k : k1;
+    k1 = k < k1 ? k1 : k;
+    k2 = low < k2 ? k2 : low;
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // Largest logit of the token as the softmax subtracts it: 0 if every logit is
 // -inf (no expert is eligible then, and exp(-inf) stays 0 instead of NaN).
-template <int kPer>
-__device__ __forceinline__ float softmax_max(const float (&x)[kPer]) {
+template <int kN>
+__device__ __forceinline__ float softmax_max(const float (&x)[kN]) {
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) m = fmaxf(m, x[i]);
+    for (int i = 0; i < kN; ++i) m = fmaxf(m, x[i]);
     m = warp_max(m);
     return m == -INFINITY ? 0.0f : m;
 }
 
-template <typename T, int kPer, bool kSoftmax>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const T* logits, RouteArgs a) {
-    extern __shared__ float smem[];
+// The lane's kN elements of a row of n from `first` on; `otherwise` past the row.  kVec: whole
+// vectors of up to 16 bytes (n a multiple of kN, rows aligned to them).
+template <typename T, int kN, bool kVec>
+__device__ __forceinline__ void load_lane(const T* row, int first, int n, float otherwise, float (&x)[kN]) {
+    if constexpr (!kVec) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) x[i] = first + i < n ? to_float(row[first + i]) : otherwise;
+    } else {
+        constexpr int kPer = kN * sizeof(T) >= 16 ? kVec16<T> : kN;   // elements of a load
+        struct alignas(kPer * sizeof(T)) Vec {
+            T v[kPer];
+        };
+#pragma unroll
+        for (int i = 0; i < kN; i += kPer) {
+            Vec v;
+            if (first < n) v = *reinterpret_cast<const Vec*>(row + first + i);
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) x[i + c] = first < n ? to_float(v.v[c]) : otherwise;
+        }
+    }
+}
+
+template <typename T, int kN, bool kVec>
+__device__ __forceinline__ void store_lane(T* row, int first, int n, const float (&x)[kN]) {
+    if constexpr (!kVec) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            if (first + i < n) row[first + i] = from_float<T>(x[i]);
+    } else if (first < n) {
+        constexpr int kPer = kN * sizeof(T) >= 16 ? kVec16<T> : kN;
+        struct alignas(kPer * sizeof(T)) Vec {
+            T v[kPer];
+        };
+#pragma unroll
+        for (int i = 0; i < kN; i += kPer) {
+            Vec v;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) v.v[c] = from_float<T>(x[i + c]);
+            *reinterpret_cast<Vec*>(row + first + i) = v;
+        }
+    }
+}
+
+template <typename T, int kN, bool kSoftmax, bool kVec>
+__global__ void __launch_bounds__(32 * kWarps) route_kernel(const T* logits, const RouteArgs a) {
+    extern __shared__ uint32_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     if (t >= a.tokens) return;
@@ -66,68 +127,62 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T* logits, Rou
         return;
     }
     const T* row = logits + t * a.ld;
-    const int E = a.experts;
-    float x[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
-        x[i] = e < E ? to_float(row[e]) : -INFINITY;
-    }
-    float m = 0.0f, z = 1.0f;
+    const int E = a.experts, first = lane * kN;
+    float x[kN];
+    load_lane<T, kN, kVec>(row, first, E, -INFINITY, x);
+    float m = 0.0f, over_z = 1.0f;
     if constexpr (kSoftmax) {
         m = softmax_max(x);
-        z = 0.0f;
+        float z = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) z += expf(x[i] - m);   // -inf adds 0
-        z = warp_sum(z);
+        for (int i = 0; i < kN; ++i) z += expf(x[i] - m);   // -inf adds 0
+        over_z = 1.0f / warp_sum(z);
     }
     // Score of a logit; a logit of -inf is out whatever its score.
-    auto score = [&](float v) { return kSoftmax ? expf(v - m) / z : sigmoid(v); };
+    auto score = [&](float v) { return kSoftmax ? expf(v - m) * over_z : sigmoid(v); };
 
-    uint32_t key[kPer];
+    // The choice's keys, and the keys that groups are scored by (they differ where sums are formed without a bias).
+    const bool sums = a.top2sum != 0, biased = a.bias != nullptr;
+    uint32_t key[kN];
+    if (biased) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = lane + 32 * i;
-        float c = x[i];
-        if (a.bias != nullptr && e < E && x[i] != -INFINITY) c = score(x[i]) + a.bias[e];
-        key[i] = choice_key(c);
+        for (int i = 0; i < kN; ++i)
+            key[i] = first + i < E && x[i] != -INFINITY ? choice_key(score(x[i]) + a.bias[first + i]) : kOut;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) key[i] = choice_key(x[i]);
     }
 
     if (a.n_group > 1) {
-        // Every expert's value to shared memory; lane g scans group g.
-        float* sh = smem + warp * E;
-        const bool sums = a.top2sum != 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = lane + 32 * i;
-            if (e >= E) continue;
-            float c = x[i];
-            if (c != -INFINITY && (a.bias != nullptr || sums)) {
-                c = score(x[i]);
-                if (a.bias != nullptr) c += a.bias[e];
-            }
-            sh[e] = c;
-        }
-        __syncwarp();
         const int per = E / a.n_group;
-        uint32_t gkey = kOut;
-        if (lane < a.n_group) {
-            const float* g = sh + lane * per;
+        auto by = [&](int i) {
+            return sums && !biased && key[i] != kOut ? choice_key(score(x[i])) : key[i];
+        };
+        const int span = per / kN;   // lanes of a group
+        uint32_t gkey = kOut;        // of group `lane`
+        if (span * kN == per && (span & (span - 1)) == 0) {
             uint32_t k1 = kOut, k2 = kOut;
-            float v1 = 0.0f, v2 = 0.0f;
-            for (int i = 0; i < per; ++i) {
-                const float v = g[i];
-                const uint32_t kk = choice_key(v);
-                if (kk > k1) {
-                    k2 = k1, v2 = v1;
-                    k1 = kk, v1 = v;
-                } else if (kk > k2) {
-                    k2 = kk, v2 = v;
-                }
+#pragma unroll
+            for (int i = 0; i < kN; ++i) keep_two(by(i), k1, k2);
+            for (int d = 1; d < span; d <<= 1) {   // both lists are this lane's and its partner's: the two best of four
+                const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, k1, d), o2 = __shfl_xor_sync(0xFFFFFFFFu, k2, d);
+                keep_two(o1, k1, k2);
+                keep_two(o2, k1, k2);
             }
-            gkey = k1;
-            if (sums && k2 != kOut) gkey = choice_key(v1 + v2);
-            if (k1 != kOut && gkey == kOut) gkey = 1u;   // a sum that overflowed to -inf: still has experts
+            gkey = group_key(k1, k2, sums);
+            gkey = __shfl_sync(0xFFFFFFFFu, gkey, (lane * span) & 31);
+            if (lane >= a.n_group) gkey = kOut;
+        } else {   // through shared memory: lane g scans group g
+            uint32_t* sh = smem + warp * E;
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                if (first + i < E) sh[first + i] = by(i);
+            __syncwarp();
+            if (lane < a.n_group) {
+                uint32_t k1 = kOut, k2 = kOut;
+                for (int i = 0; i < per; ++i) keep_two(sh[lane * per + i], k1, k2);
+                gkey = group_key(k1, k2, sums);
+            }
         }
         int before = 0;   // groups that stand before this lane's
         for (int h = 0; h < a.n_group; ++h) {
@@ -138,8 +193,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T* logits, Rou
         // e / per for e < 1024 by a 20-bit reciprocal (exact: e * (error < per) < 2^20)
         const uint32_t inv = ((1u << 20) + per - 1) / per;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const uint32_t e = lane + 32 * i;
+        for (int i = 0; i < kN; ++i) {
+            const uint32_t e = first + i;
             if (((stays >> ((e * inv >> 20) & 31u)) & 1u) == 0u) key[i] = kOut;
         }
     }
@@ -149,17 +204,16 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T* logits, Rou
         uint32_t best = kOut;
         int at = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
+        for (int i = 0; i < kN; ++i)
             if (key[i] > best) best = key[i], at = i;   // the lowest of equal ones
         const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
         if (top == kOut) break;   // nothing left: the remaining slots stay -1
-        const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == top ? lane + 32u * at : 0xFFFFFFFFu);
-        if (lane == j) chosen = static_cast<int>(e);
-        if ((e & 31u) == static_cast<uint32_t>(lane)) {
+        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, best == top)) - 1;   // the lowest lane: the lowest expert
+        const int e = __shfl_sync(0xFFFFFFFFu, first + at, from);
+        if (lane == j) chosen = e;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (i == static_cast<int>(e >> 5)) key[i] = kOut;
-        }
+        for (int i = 0; i < kN; ++i)
+            if (first + i == e) key[i] = kOut;
     }
     float s = chosen >= 0 ? score(to_float(row[chosen])) : 0.0f;
     float w = a.scale * s;
@@ -174,14 +228,14 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T* logits, Rou
 //   ds_j = (scale dw_j - sum_i dw_i w_i) / S   (renorm)   or   scale dw_j,
 //   sigmoid: dx_j = ds_j s_j (1 - s_j), 0 at experts not chosen;
 //   softmax: dx_e = s_e (ds_e [chosen] - sum_j ds_j s_j).
-template <typename T, int kPer, bool kSoftmax>
-__global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const T* logits, T* dlogits, RouteBackwardArgs a) {
+template <typename T, int kN, bool kSoftmax, bool kVec>
+__global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const T* logits, T* dlogits, const RouteBackwardArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     if (t >= a.tokens) return;
     const T* row = logits + t * a.ld;
     T* out = dlogits + t * a.ld_out;
-    const int E = a.experts;
+    const int E = a.experts, first = lane * kN;
     int id = -1;
     float dw = 0.0f;
     if (lane < a.topk) {
@@ -191,27 +245,23 @@ __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const T* lo
     }
     const bool any = __any_sync(0xFFFFFFFFu, id >= 0);   // no expert (a padding token): zeros, logits not read
     const float xc = id >= 0 ? to_float(row[id]) : 0.0f;
-    float m = 0.0f, z = 1.0f;
-    float x[kPer];
+    float m = 0.0f, over_z = 1.0f;
+    float x[kN] = {};
     if (kSoftmax && any) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = lane + 32 * i;
-            x[i] = e < E ? to_float(row[e]) : -INFINITY;
-        }
+        load_lane<T, kN, kVec>(row, first, E, -INFINITY, x);
         m = softmax_max(x);
-        z = 0.0f;
+        float z = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = 0; i < kN; ++i) {
             x[i] = expf(x[i] - m);
             z += x[i];
         }
-        z = warp_sum(z);
+        over_z = 1.0f / warp_sum(z);
     }
     float s = 0.0f, slope = 0.0f;   // slope: ds/dx of a sigmoid score
     if (id >= 0) {
         if (kSoftmax) {
-            s = expf(xc - m) / z;
+            s = expf(xc - m) * over_z;
         } else {
             // s (1 - s) = q / (1 + q)^2 with q = exp(-|x|): no cancellation near s = 1
             const float q = expf(-fabsf(xc));
@@ -221,82 +271,76 @@ __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const T* lo
     }
     float ds = a.scale * dw;
     if (a.renorm) {
-        const float total = warp_sum(s) + kRenormEps;
-        const float dot = warp_sum(dw * (a.scale * s / total));
-        ds = (a.scale * dw - dot) / total;
+        const float over = 1.0f / (warp_sum(s) + kRenormEps);
+        const float dot = warp_sum(dw * (a.scale * s * over));
+        ds = (a.scale * dw - dot) * over;
     }
     if (id < 0) ds = 0.0f;
-    if constexpr (kSoftmax) {
-        const float d = warp_sum(ds * s);
+    const float d = kSoftmax ? warp_sum(ds * s) : 0.0f;
+    if (kSoftmax && any) {
+        const float scale = -over_z * d;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = lane + 32 * i;
-            if (e < E) out[e] = from_float<T>(any ? -(x[i] / z) * d : 0.0f);
-        }
-        __syncwarp();   // the chosen experts' values replace what the row's pass wrote
-        if (id >= 0) out[id] = from_float<T>(s * (ds - d));
-    } else {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = lane + 32 * i;
-            if (e < E) out[e] = from_float<T>(0.0f);
-        }
-        __syncwarp();
-        if (id >= 0) out[id] = from_float<T>(ds * slope);
+        for (int i = 0; i < kN; ++i) x[i] *= scale;
     }
+    store_lane<T, kN, kVec>(out, first, E, x);
+    __syncwarp();   // the chosen experts' values replace what the row's pass wrote
+    if (id >= 0) out[id] = from_float<T>(kSoftmax ? s * (ds - d) : ds * slope);
 }
 
-template <typename T, int kPer>
+// f(kN, kVec) for the experts and the alignment of the rows.
+template <typename T, typename F>
+cudaError_t by_experts(int experts, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds, F f) {
+    auto go = [&](auto count) {
+        constexpr int kN = count.value;
+        constexpr size_t kBytes = kN * sizeof(T) < 16 ? kN * sizeof(T) : 16;
+        bool vec = experts % kN == 0;
+        for (const void* p : ptrs) vec = vec && reinterpret_cast<uintptr_t>(p) % kBytes == 0;
+        for (int64_t ld : lds) vec = vec && ld * sizeof(T) % kBytes == 0;
+        return vec ? f(count, std::true_type{}) : f(count, std::false_type{});
+    };
+    if (experts <= 32) return go(std::integral_constant<int, 1>{});
+    if (experts <= 64) return go(std::integral_constant<int, 2>{});
+    if (experts <= 128) return go(std::integral_constant<int, 4>{});
+    if (experts <= 256) return go(std::integral_constant<int, 8>{});
+    if (experts <= 512) return go(std::integral_constant<int, 16>{});
+    return go(std::integral_constant<int, 32>{});
+}
+
+template <typename T>
 cudaError_t route_launch(const void* logits, const RouteArgs& a, bool softmax, cudaStream_t stream) {
-    const int64_t blocks = (a.tokens + kWarps - 1) / kWarps;
-    const size_t smem = a.n_group > 1 ? sizeof(float) * kWarps * a.experts : 0;
+    const unsigned blocks = static_cast<unsigned>((a.tokens + kWarps - 1) / kWarps);
+    const size_t smem = a.n_group > 1 ? sizeof(uint32_t) * kWarps * a.experts : 0;
     const T* x = static_cast<const T*>(logits);
-    if (softmax)
-        route_kernel<T, kPer, true><<<static_cast<unsigned>(blocks), 32 * kWarps, smem, stream>>>(x, a);
-    else
-        route_kernel<T, kPer, false><<<static_cast<unsigned>(blocks), 32 * kWarps, smem, stream>>>(x, a);
-    return cudaGetLastError();
+    return by_experts<T>(a.experts, {logits}, {a.ld}, [&](auto n, auto vec) {
+        if (softmax) route_kernel<T, n.value, true, vec.value><<<blocks, 32 * kWarps, smem, stream>>>(x, a);
+        else route_kernel<T, n.value, false, vec.value><<<blocks, 32 * kWarps, smem, stream>>>(x, a);
+        return cudaGetLastError();
+    });
 }
 
-template <typename T, int kPer>
+template <typename T>
 cudaError_t route_backward_launch(const void* logits, void* dlogits, const RouteBackwardArgs& a, bool softmax,
                                   cudaStream_t stream) {
-    const int64_t blocks = (a.tokens + kWarps - 1) / kWarps;
+    const unsigned blocks = static_cast<unsigned>((a.tokens + kWarps - 1) / kWarps);
     const T* x = static_cast<const T*>(logits);
     T* dx = static_cast<T*>(dlogits);
-    if (softmax)
-        route_backward_kernel<T, kPer, true><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, stream>>>(x, dx, a);
-    else
-        route_backward_kernel<T, kPer, false><<<static_cast<unsigned>(blocks), 32 * kWarps, 0, stream>>>(x, dx, a);
-    return cudaGetLastError();
-}
-
-// The registers of a lane that hold a token's experts: the next power of two.
-template <typename F>
-cudaError_t by_experts(int experts, F f) {
-    if (experts <= 32) return f(std::integral_constant<int, 1>{});
-    if (experts <= 64) return f(std::integral_constant<int, 2>{});
-    if (experts <= 128) return f(std::integral_constant<int, 4>{});
-    if (experts <= 256) return f(std::integral_constant<int, 8>{});
-    if (experts <= 512) return f(std::integral_constant<int, 16>{});
-    return f(std::integral_constant<int, 32>{});
+    return by_experts<T>(a.experts, {logits, dlogits}, {a.ld, a.ld_out}, [&](auto n, auto vec) {
+        if (softmax) route_backward_kernel<T, n.value, true, vec.value><<<blocks, 32 * kWarps, 0, stream>>>(x, dx, a);
+        else route_backward_kernel<T, n.value, false, vec.value><<<blocks, 32 * kWarps, 0, stream>>>(x, dx, a);
+        return cudaGetLastError();
+    });
 }
 
 }  // namespace
 
 cudaError_t launch_route(const void* logits, bool f32, const RouteArgs& a, bool softmax, cudaStream_t stream) {
-    return by_experts(a.experts, [&](auto per) {
-        return f32 ? route_launch<float, per.value>(logits, a, softmax, stream)
-                   : route_launch<bf16_bits, per.value>(logits, a, softmax, stream);
-    });
+    return f32 ? route_launch<float>(logits, a, softmax, stream) : route_launch<bf16_bits>(logits, a, softmax, stream);
 }
 
 cudaError_t launch_route_backward(const void* logits, void* dlogits, bool f32, const RouteBackwardArgs& a,
                                   bool softmax, cudaStream_t stream) {
-    return by_experts(a.experts, [&](auto per) {
-        return f32 ? route_backward_launch<float, per.value>(logits, dlogits, a, softmax, stream)
-                   : route_backward_launch<bf16_bits, per.value>(logits, dlogits, a, softmax, stream);
-    });
+    return f32 ? route_backward_launch<float>(logits, dlogits, a, softmax, stream)
+               : route_backward_launch<bf16_bits>(logits, dlogits, a, softmax, stream);
 }
 
 }  // namespace mxq
