@@ -92,9 +92,12 @@ __global__ void __launch_bounds__(kN == 8 ? 512 : 1024) norm_kernel(const NormAr
     constexpr int V = kVec16<T>, H = V / 2, S = sizeof(T);
     constexpr bool kHeld = kAny && kN <= 2;
     __shared__ float sh[2][32];
-    const int group = threadIdx.x / tpr, at = threadIdx.x % tpr;
-    const int64_t row_first = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + group;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (blockDim.x / tpr);
+    // rows of lanes (a power of two of them) share a block, longer ones have it alone
+    const int shift = tpr <= 32 ? 31 - __clz(tpr) : 31;
+    const int group = threadIdx.x >> shift, at = threadIdx.x - (group << shift);
+    const int groups = tpr <= 32 ? blockDim.x >> shift : 1;
+    const int64_t row_first = static_cast<int64_t>(blockIdx.x) * groups + group;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     const int first = at * V - (kAny ? lead_of<S>(static_cast<const T*>(a.x) + row_first * a.ldx) : 0);
     const float inv = 1.0f / static_cast<float>(a.cols);
     const W* w = static_cast<const W*>(a.weight);
@@ -250,8 +253,9 @@ template <typename T, typename W, int kN, bool kAny>
 __global__ void __launch_bounds__(kShortThreads, 2) norm_backward_short_kernel(const NormBackwardArgs a, int tpr) {
     constexpr int V = kVec16<T>, H = V / 2, S = sizeof(T);
     extern __shared__ float cols_sh[];   // [2][cols]: column sums of the block
-    const int groups = kShortThreads / tpr;
-    const int group = threadIdx.x / tpr, at = threadIdx.x % tpr, lane = threadIdx.x & 31;
+    const int shift = 31 - __clz(tpr);   // tpr is a power of two
+    const int groups = kShortThreads >> shift;
+    const int group = threadIdx.x >> shift, at = threadIdx.x & (tpr - 1), lane = threadIdx.x & 31;
     const int64_t row_first = static_cast<int64_t>(blockIdx.x) * groups + group;
     const int all = static_cast<int>(a.cols);
     const int first = at * V - (kAny ? lead_of<S>(static_cast<const T*>(a.x) + row_first * a.ldx) : 0);
@@ -757,7 +761,7 @@ cudaError_t norm_backward_launch(const NormBackwardArgs& a, cudaStream_t stream)
     } else if (vectors <= kRingThreads * (16 / V)) {
         if (parts > kSMs) parts = kSMs;
         e = backward_ring<T, W, 16 / V, kAny>(a, vectors, parts, stream);
-    } else if (vectors <= kRingThreads * (32 / V) && 4 * RowRing<T, kAny>::bytes_of(a.cols) <= kRingBytes) {
+    } else if (vectors <= kRingThreads * (32 / V) && 2 * RowRing<T, kAny>::bytes_of(a.cols) <= kRingBytes) {
         e = backward_ring<T, W, 32 / V, kAny>(a, vectors, parts, stream);
     } else {
         norm_backward_long_kernel<T, W><<<static_cast<unsigned>(parts), 1024, 0, stream>>>(a);
@@ -779,9 +783,11 @@ cudaError_t by_types(bool f32, bool params_f32, F f) {
 }  // namespace
 
 // Blocks of the backward pass at most, each with 2 x cols column sums: one an SM, three for
-// the short rows that need no ring.
+// the short rows that need no ring, fewer where the sums would take more than 80 MB.
 int64_t norm_partials(int64_t rows, int64_t cols) {
-    const int64_t most = cols <= kShortCols ? 3 * kSMs : kSMs;
+    int64_t most = cols <= kShortCols ? 3 * kSMs : kSMs;
+    if (cols > 65536) most = most * 65536 / cols;
+    if (most < 8) most = 8;
     return rows < most ? rows : most;
 }
 
