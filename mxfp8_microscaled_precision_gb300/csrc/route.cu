@@ -69,12 +69,25 @@ __device__ __forceinline__ float softmax_max(const float (&x)[kN]) {
 }
 
 // The lane's kN elements of a row of n from `first` on; `otherwise` past the row.  kVec: whole
-// vectors of up to 16 bytes (n a multiple of kN, rows aligned to them).
+// vectors of up to 16 bytes (n a multiple of kN, rows aligned to them); else the row goes
+// through the warp's kStage words of shared memory, so that neighbouring lanes read neighbouring
+// elements (element e at e + e / kN: no two lanes of a step in one bank).
+template <int kN>
+constexpr int kStage = 32 * (kN + 1);
+
 template <typename T, int kN, bool kVec>
-__device__ __forceinline__ void load_lane(const T* row, int first, int n, float otherwise, float (&x)[kN]) {
+__device__ __forceinline__ void load_lane(const T* row, int first, int n, float otherwise, float* sh, float (&x)[kN]) {
     if constexpr (!kVec) {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] = first + i < n ? to_float(row[first + i]) : otherwise;
+        for (int i = 0; i < kN; ++i) {
+            const int e = 32 * i + lane;
+            sh[e + e / kN] = e < n ? to_float(row[e]) : otherwise;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kN; ++i) x[i] = sh[lane * (kN + 1) + i];
+        __syncwarp();
     } else {
         constexpr int kPer = kN * sizeof(T) >= 16 ? kVec16<T> : kN;   // elements of a load
         struct alignas(kPer * sizeof(T)) Vec {
@@ -91,11 +104,17 @@ __device__ __forceinline__ void load_lane(const T* row, int first, int n, float 
 }
 
 template <typename T, int kN, bool kVec>
-__device__ __forceinline__ void store_lane(T* row, int first, int n, const float (&x)[kN]) {
+__device__ __forceinline__ void store_lane(T* row, int first, int n, float* sh, const float (&x)[kN]) {
     if constexpr (!kVec) {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-            if (first + i < n) row[first + i] = from_float<T>(x[i]);
+        for (int i = 0; i < kN; ++i) sh[lane * (kN + 1) + i] = x[i];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int e = 32 * i + lane;
+            if (e < n) row[e] = from_float<T>(sh[e + e / kN]);
+        }
     } else if (first < n) {
         constexpr int kPer = kN * sizeof(T) >= 16 ? kVec16<T> : kN;
         struct alignas(kPer * sizeof(T)) Vec {
@@ -129,7 +148,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T* logits, con
     const T* row = logits + t * a.ld;
     const int E = a.experts, first = lane * kN;
     float x[kN];
-    load_lane<T, kN, kVec>(row, first, E, -INFINITY, x);
+    load_lane<T, kN, kVec>(row, first, E, -INFINITY, reinterpret_cast<float*>(smem) + warp * kStage<kN>, x);
     float m = 0.0f, over_z = 1.0f;
     if constexpr (kSoftmax) {
         m = softmax_max(x);
@@ -173,7 +192,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T* logits, con
             gkey = __shfl_sync(0xFFFFFFFFu, gkey, (lane * span) & 31);
             if (lane >= a.n_group) gkey = kOut;
         } else {   // through shared memory: lane g scans group g
-            uint32_t* sh = smem + warp * E;
+            uint32_t* sh = smem + warp * kStage<kN>;
 #pragma unroll
             for (int i = 0; i < kN; ++i)
                 if (first + i < E) sh[first + i] = by(i);
@@ -199,21 +218,42 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T* logits, con
         }
     }
 
+    // The lane's best, by blocks of up to 4 registers: the place of a chosen expert is the same number
+    // of registers into every lane, so one block is scanned again, in all lanes, and the
+    // blocks' bests are compared.
+    constexpr int kBlock = kN < 4 ? kN : 4, kBlocks = kN / kBlock;
+    uint32_t best[kBlocks];
+    int at[kBlocks];
+    auto scan = [&](int b) {
+        best[b] = key[b * kBlock];
+        at[b] = b * kBlock;
+#pragma unroll
+        for (int i = b * kBlock + 1; i < (b + 1) * kBlock; ++i)
+            if (key[i] > best[b]) best[b] = key[i], at[b] = i;   // the lowest of equal ones
+    };
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) scan(b);
     int chosen = -1;   // of slot `lane`
     for (int j = 0; j < a.topk; ++j) {
-        uint32_t best = kOut;
-        int at = 0;
+        uint32_t mine = best[0];
+        int place = at[0];
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-            if (key[i] > best) best = key[i], at = i;   // the lowest of equal ones
-        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+        for (int b = 1; b < kBlocks; ++b)
+            if (best[b] > mine) mine = best[b], place = at[b];
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, mine);
         if (top == kOut) break;   // nothing left: the remaining slots stay -1
-        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, best == top)) - 1;   // the lowest lane: the lowest expert
-        const int e = __shfl_sync(0xFFFFFFFFu, first + at, from);
+        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, mine == top)) - 1;   // the lowest lane: the lowest expert
+        const int e = __shfl_sync(0xFFFFFFFFu, first + place, from);
         if (lane == j) chosen = e;
+        const int block = (e & (kN - 1)) / kBlock;
 #pragma unroll
-        for (int i = 0; i < kN; ++i)
-            if (first + i == e) key[i] = kOut;
+        for (int b = 0; b < kBlocks; ++b) {
+            if (block != b) continue;
+#pragma unroll
+            for (int i = b * kBlock; i < (b + 1) * kBlock; ++i)
+                if (first + i == e) key[i] = kOut;
+            scan(b);
+        }
     }
     float s = chosen >= 0 ? score(to_float(row[chosen])) : 0.0f;
     float w = a.scale * s;
@@ -230,6 +270,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T* logits, con
 //   softmax: dx_e = s_e (ds_e [chosen] - sum_j ds_j s_j).
 template <typename T, int kN, bool kSoftmax, bool kVec>
 __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const T* logits, T* dlogits, const RouteBackwardArgs a) {
+    extern __shared__ float stage[];   // without kVec
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     if (t >= a.tokens) return;
@@ -248,7 +289,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const T* lo
     float m = 0.0f, over_z = 1.0f;
     float x[kN] = {};
     if (kSoftmax && any) {
-        load_lane<T, kN, kVec>(row, first, E, -INFINITY, x);
+        load_lane<T, kN, kVec>(row, first, E, -INFINITY, stage + warp * kStage<kN>, x);
         m = softmax_max(x);
         float z = 0.0f;
 #pragma unroll
@@ -282,7 +323,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const T* lo
 #pragma unroll
         for (int i = 0; i < kN; ++i) x[i] *= scale;
     }
-    store_lane<T, kN, kVec>(out, first, E, x);
+    store_lane<T, kN, kVec>(out, first, E, stage + warp * kStage<kN>, x);
     __syncwarp();   // the chosen experts' values replace what the row's pass wrote
     if (id >= 0) out[id] = from_float<T>(kSoftmax ? s * (ds - d) : ds * slope);
 }
@@ -309,9 +350,9 @@ cudaError_t by_experts(int experts, std::initializer_list<const void*> ptrs, std
 template <typename T>
 cudaError_t route_launch(const void* logits, const RouteArgs& a, bool softmax, cudaStream_t stream) {
     const unsigned blocks = static_cast<unsigned>((a.tokens + kWarps - 1) / kWarps);
-    const size_t smem = a.n_group > 1 ? sizeof(uint32_t) * kWarps * a.experts : 0;
     const T* x = static_cast<const T*>(logits);
     return by_experts<T>(a.experts, {logits}, {a.ld}, [&](auto n, auto vec) {
+        const size_t smem = vec.value && a.n_group == 1 ? 0 : sizeof(uint32_t) * kWarps * kStage<n.value>;
         if (softmax) route_kernel<T, n.value, true, vec.value><<<blocks, 32 * kWarps, smem, stream>>>(x, a);
         else route_kernel<T, n.value, false, vec.value><<<blocks, 32 * kWarps, smem, stream>>>(x, a);
         return cudaGetLastError();
@@ -325,8 +366,9 @@ cudaError_t route_backward_launch(const void* logits, void* dlogits, const Route
     const T* x = static_cast<const T*>(logits);
     T* dx = static_cast<T*>(dlogits);
     return by_experts<T>(a.experts, {logits, dlogits}, {a.ld, a.ld_out}, [&](auto n, auto vec) {
-        if (softmax) route_backward_kernel<T, n.value, true, vec.value><<<blocks, 32 * kWarps, 0, stream>>>(x, dx, a);
-        else route_backward_kernel<T, n.value, false, vec.value><<<blocks, 32 * kWarps, 0, stream>>>(x, dx, a);
+        const size_t smem = vec.value ? 0 : sizeof(float) * kWarps * kStage<n.value>;
+        if (softmax) route_backward_kernel<T, n.value, true, vec.value><<<blocks, 32 * kWarps, smem, stream>>>(x, dx, a);
+        else route_backward_kernel<T, n.value, false, vec.value><<<blocks, 32 * kWarps, smem, stream>>>(x, dx, a);
         return cudaGetLastError();
     });
 }
