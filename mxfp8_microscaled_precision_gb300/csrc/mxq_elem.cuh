@@ -134,25 +134,18 @@ __device__ __forceinline__ uint4 shift16(const uint4 a, const uint4 b, unsigned 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Elements [i, i + V) (V = 16 / kSize) of a row of n, one by one; 0 outside the row.  The
-// loads do not depend on the bounds (an index outside becomes the nearest one inside), so they are all
-// in flight together.
+// Elements [i, i + V) (V = 16 / kSize) of a row of n, one by one; 0 outside the row.
 template <int kSize>
 __device__ __noinline__ uint4 load_ends(const void* row, int i, int n) {
     uint32_t w[4] = {};
-    if (n <= 0) return make_uint4(0u, 0u, 0u, 0u);
-    uint32_t e[16 / kSize];
 #pragma unroll
     for (int c = 0; c < 16 / kSize; ++c) {
-        const int at = min(max(i + c, 0), n - 1);
-        if constexpr (kSize == 2) e[c] = static_cast<const unsigned short*>(row)[at];
-        else e[c] = static_cast<const uint32_t*>(row)[at];
-    }
-#pragma unroll
-    for (int c = 0; c < 16 / kSize; ++c) {
-        if (i + c < 0 || i + c >= n) e[c] = 0u;
-        if constexpr (kSize == 2) w[c / 2] |= e[c] << (16 * (c & 1));
-        else w[c] = e[c];
+        if (i + c >= 0 && i + c < n) {
+            if constexpr (kSize == 2)
+                w[c / 2] |= static_cast<uint32_t>(static_cast<const unsigned short*>(row)[i + c]) << (16 * (c & 1));
+            else
+                w[c] = static_cast<const uint32_t*>(row)[i + c];
+        }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }

@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int32_t* ids, int64_t 
 // ---- rows ------------------------------------------------------------------------
 
 constexpr int kThreads = 256;
+constexpr int kRowThreads = 320;   // of dispatch and combine at most
 
 // Where a slot's entry of `rows` points: the row and whether the slot is kept.
 // Entries that mxq_moe_plan does not give (a row that does not exist) point nowhere.
@@ -153,11 +154,11 @@ __device__ __forceinline__ Place place_of(int entry, int64_t slots) {
 // the row per thread, blockIdx.y over the row: x is read once, whatever k.  With kAny
 // the vectors are those of the row that is written.
 template <int kSize, bool kAny>
-__global__ void __launch_bounds__(kThreads) dispatch_kernel(const unsigned char* x, int64_t ldx, unsigned char* a,
+__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const unsigned char* x, int64_t ldx, unsigned char* a,
                                                             int64_t lda, int H, const int32_t* rows, int k) {
     constexpr int V = 16 / kSize;
     const int64_t t = blockIdx.x;
-    const int at = (blockIdx.y * kThreads + threadIdx.x) * V;
+    const int at = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     const int32_t* r = rows + t * k;
     const int64_t slots = static_cast<int64_t>(gridDim.x) * k;
     const unsigned char* from = x + t * ldx * kSize;
@@ -187,11 +188,11 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const unsigned char*
 // out[t] = sum_j w_j y[rows[t, j]] (w_j = 1 without weights), summed in FP32 in
 // the order of j and rounded once.  With kAny the vectors are those of out's row.
 template <typename T, bool kAny>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const T* y, int64_t ldy, const int32_t* rows,
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* y, int64_t ldy, const int32_t* rows,
                                                            const float* weights, int k, T* out, int64_t ldo, int H) {
     constexpr int V = kVec16<T>, S = sizeof(T);
     const int64_t t = blockIdx.x;
-    const int at = (blockIdx.y * kThreads + threadIdx.x) * V;
+    const int at = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     T* to = out + t * ldo;
     const int i = kAny ? at - lead_of<S>(to) : at;
     if (i >= H) return;
@@ -294,15 +295,27 @@ bool on_grid(int64_t H, size_t size, std::initializer_list<const void*> ptrs, st
     return true;
 }
 
-// kAny: a row off the grid lies in one vector more.
-dim3 row_grid(int64_t tokens, int64_t H, int64_t size, bool any) {
+// One block per token and per part of its row of 256 vectors; a rest of less than 64
+// vectors joins the parts before it (4097 BF16: two parts of 288 threads).  kAny: a row
+// off the grid lies in one vector more.
+struct RowGrid {
+    dim3 grid;
+    unsigned threads;
+};
+RowGrid row_grid(int64_t tokens, int64_t H, int64_t size, bool any) {
     const int64_t vectors = (H * size + 15) / 16 + (any ? 1 : 0);
-    return dim3(static_cast<unsigned>(tokens), static_cast<unsigned>((vectors + kThreads - 1) / kThreads));
+    int64_t parts = (vectors + 191) / 256;
+    if (parts < 1) parts = 1;
+    int64_t threads = ((vectors + parts - 1) / parts + 31) / 32 * 32;
+    if (parts > 1 && threads < 256) threads = 256;
+    return {dim3(static_cast<unsigned>(tokens), static_cast<unsigned>((vectors + threads - 1) / threads)),
+            static_cast<unsigned>(threads)};
 }
 
 template <int kSize, bool kAny>
 cudaError_t dispatch_launch(const PermuteArgs& a, const void* x, void* out, cudaStream_t stream) {
-    dispatch_kernel<kSize, kAny><<<row_grid(a.tokens, a.H, kSize, kAny), kThreads, 0, stream>>>(
+    const RowGrid g = row_grid(a.tokens, a.H, kSize, kAny);
+    dispatch_kernel<kSize, kAny><<<g.grid, g.threads, 0, stream>>>(
         static_cast<const unsigned char*>(x), a.ld_tokens, static_cast<unsigned char*>(out), a.ld_rows, static_cast<int>(a.H),
         a.rows, a.k);
     return cudaGetLastError();
@@ -310,7 +323,8 @@ cudaError_t dispatch_launch(const PermuteArgs& a, const void* x, void* out, cuda
 
 template <typename T, bool kAny>
 cudaError_t combine_launch(const PermuteArgs& a, const void* y, const float* weights, void* out, cudaStream_t stream) {
-    combine_kernel<T, kAny><<<row_grid(a.tokens, a.H, sizeof(T), kAny), kThreads, 0, stream>>>(
+    const RowGrid g = row_grid(a.tokens, a.H, sizeof(T), kAny);
+    combine_kernel<T, kAny><<<g.grid, g.threads, 0, stream>>>(
         static_cast<const T*>(y), a.ld_rows, a.rows, weights, a.k, static_cast<T*>(out), a.ld_tokens,
         static_cast<int>(a.H));
     return cudaGetLastError();
