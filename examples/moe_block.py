@@ -117,7 +117,8 @@ def main():
         began = time.perf_counter()
         loss, norm = block.step(x, target, lr=a.lr)
         torch.cuda.synchronize()
-        print(f"step {i}: loss {float(loss):.5f}  gradient norm {float(norm):.4g}  {(time.perf_counter() - began) * 1e3:.2f} ms")
+        took = (time.perf_counter() - began) * 1e3
+        print(f"step {i}: loss {float(loss):.5f}  gradient norm {float(norm):.4g}  {took:.2f} ms")
     for t in range(3):   # one token at a time
         torch.cuda.synchronize()
         began = time.perf_counter()

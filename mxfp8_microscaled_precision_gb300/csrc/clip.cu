@@ -11,6 +11,8 @@
 // timing.  (Sums in FP64 cost more than the whole rest of a small call: this GPU adds two doubles
 // a clock and SM.)  The scaling blocks take the chunks backwards: what the other pass read last
 // still lies in the L2.  Bound by memory: one read for the norm, one read and one write.
+// Measured: 36 gradients of 671 MB: the norm 101 us (98% of a copy's 6787 GB/s), scaled too 323 us
+// (3 x 671 MB: 92%); 300 ragged ones of 56 MB 16 us and 31 us; 6 of 2.6 MB 6 us and 9 us.
 
 #include <cuda_runtime.h>
 

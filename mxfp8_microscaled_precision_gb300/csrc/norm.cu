@@ -11,6 +11,11 @@
 // share of dw and db in FP32 registers, the shares meet in a workspace and are
 // added in a fixed order.
 //
+// Bound by memory for long rows and many.  Measured, of the 6787 GB/s a copy reaches:
+// forward 16384 x 7168 BF16 80 us (87%), 16384 x 4096 45 us (87%), 32767 x 1000 FP32 42 us
+// (93%), 8 x 4096 2.3 us; backward 141 us (74%), 76 us (78%), 78 us (74%).  Rows off the
+// 16-byte grid: 8191 x 4097 BF16 forward 56 us (36%), backward 93 us (32%).
+//
 // kAny: rows that start at any element (mxq_elem.cuh), in vectors of x's rows.  dy and the
 // result mostly start like x, as rows of the same length in buffers of their own do; where
 // one does not, it goes element by element.  The sums are formed in the same order either way.
@@ -82,7 +87,8 @@ __device__ __forceinline__ uint4 inside(const uint4 v, int i, int cols) {
 // ---- forward ----------------------------------------------------------------------------
 
 // Thread i of a row holds the vectors i, i + tpr, ... (kN of 16 bytes), packed as they
-// came: unpacking them in each pass costs less than the registers of 32-bit copies.  On
+// came: unpacking them in each pass costs less than the registers of 32-bit copies (a ring of
+// bulk copies, as in the backward pass, took 96 us where this takes 80).  On
 // the grid a block has one row (or one for each group of lanes), and the parameters come from the
 // L1; with kAny they would have to be shifted for every row, so the blocks are fewer, each
 // keeps its threads' parameters and walks over rows that are a multiple of 8
@@ -290,7 +296,8 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_backward_short_kernel(c
             unpack2<T>(qg[n], u[n]);
             add_vector<H>(h[n], u[n], w[n], rr, off, dw[n], db[n], s1, s2);
         }
-        const float m1 = lanes_sum(lo_of(s1) + hi_of(s1), tpr) * inv, m2 = lanes_sum(lo_of(s2) + hi_of(s2), tpr) * inv;
+        const float m1 = lanes_sum(lo_of(s1) + hi_of(s1), tpr) * inv;
+        const float m2 = lanes_sum(lo_of(s2) + hi_of(s2), tpr) * inv;
         const f32x2 c1 = pair(-m1 * r, -m1 * r), c2 = pair(-m2 * r, -m2 * r);
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
@@ -378,7 +385,8 @@ struct RowRing {
     }
 
     // By all threads; a __syncthreads must follow.  Starts the first copies.
-    __device__ __forceinline__ void init(const NormBackwardArgs& a, RingBars* all, unsigned char* memory, int stage_count) {
+    __device__ __forceinline__ void init(const NormBackwardArgs& a, RingBars* all, unsigned char* memory,
+                                         int stage_count) {
         src[0] = static_cast<const T*>(a.x);
         src[1] = static_cast<const T*>(a.dy);
         ld[0] = a.ldx;
@@ -434,7 +442,9 @@ struct RowRing {
     // `stages` further.
     __device__ __forceinline__ void refill(int64_t row, int stage) {
         const int64_t next = row + static_cast<int64_t>(stages) * gridDim.x;
-        if (next < rows) fetch(next, stage);
+        if (next >= rows) return;
+        fence_proxy_async_smem();   // the group's accesses to the stage before the copy's writes
+        fetch(next, stage);
     }
 
     // After a wait that ran out, by the first thread of a group that gave up: waits (bounded) for
@@ -470,12 +480,18 @@ __device__ __forceinline__ void group_barrier(int group, int tpr) {
 }
 
 // A thread of 16 elements a row (kKeep) keeps h and u of the row between the two passes; a
-// longer row is read a second time from the ring: registers hold the column sums.
+// longer row is read a second time from the ring: registers hold the column sums.  What
+// bounds it: the chain of a row's sums (wait, shuffles, barrier, shuffles), some 2300
+// clocks, which 16 warps of 128 registers do not quite hide (issue slots 46% used, DRAM 63%,
+// at 16384 x 7168).  Twice the threads with half the registers spill and are slower
+// (211 us), as are 8 elements a thread (194 us); a warp of its own for the copies changes nothing.
 template <typename T, typename W, int kN, bool kAny>
-__global__ void __launch_bounds__(kRingThreads, 1) norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
+__global__ void __launch_bounds__(kRingThreads, 1)
+norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
     constexpr int V = kVec16<T>, H = V / 2, S = sizeof(T);
     constexpr bool kKeep = kN * V <= 16;
-    constexpr bool kHeld = kN * V * sizeof(W) <= (kAny ? 64 : 32);   // weights in 8 registers (16 where each use would shift them)
+    // weights kept in 8 registers, or in 16 where each use would have to shift them
+    constexpr bool kHeld = kN * V * sizeof(W) <= (kAny ? 64 : 32);
     extern __shared__ __align__(128) unsigned char buf[];
     __shared__ f32x2 sums[kMaxGroups][2][16];    // [group][row parity][warp]: of u and of u h
     __shared__ float2 stats[kMaxGroups][2];      // mean and rstd of the group's row
@@ -590,8 +606,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_backward_kernel(const No
     if (stop && at == 0) ring.drain(place, groups, guard);   // the group gave up
 }
 
-// The longest rows: element by element.  dw and db by columns, one thread each, over the block's rows (their shares in the workspace),
-// then dx from two passes over each row.
+// The longest rows: element by element.  dw and db by columns, one thread each, over the
+// block's rows (their shares in the workspace), then dx from two passes over each row.
 template <typename T, typename W>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormBackwardArgs a) {
     __shared__ float sh[2][32];
@@ -656,7 +672,8 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* partial,
 // ---- launches ---------------------------------------------------------------------------
 
 // Whether the rows of several tensors all lie on the 16-byte grid in whole vectors.
-bool on_grid(int64_t cols, size_t size, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
+bool on_grid(int64_t cols, size_t size, std::initializer_list<const void*> ptrs,
+             std::initializer_list<int64_t> lds) {
     if (cols * size % 16 != 0) return false;
     for (const void* p : ptrs)
         if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;

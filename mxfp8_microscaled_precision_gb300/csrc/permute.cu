@@ -6,8 +6,13 @@
 // A slot (t, j) is the j-th expert of token t; rows[t, j] is its row in expert
 // order.  A dropped slot (no expert) has a row too, behind all experts' rows:
 // it is given as -1 - row, so that every row is written by exactly one slot and
-// nothing needs clearing beforehand.  No atomics: results do not depend on the
-// order in which blocks run.
+// nothing needs clearing beforehand.  No floating-point atomics: results do not depend on
+// the order in which blocks run.
+//
+// The row kernels are bound by memory, which they move once.  Measured, of the 6787 GB/s a
+// copy reaches: 16384 tokens x 8 slots of 4096 BF16: dispatch 181 us (98%), combine 181 us
+// (98%), its backward pass 361 us (93%); 8191 x 4 of 4097 BF16, off the 16-byte grid: 66 us
+// (75%), 82 us (61%), 122 us (73%), where elements one by one took 148, 164 and 206 us.
 
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -31,8 +36,9 @@ constexpr int64_t kPlanWords = 50 * 1024;   // shared memory of a block of the p
 // One cluster counts and places all slots: warp w of the cluster's warps owns
 // the slots [w * chunk, (w + 1) * chunk).  Bucket E takes the dropped slots.  Counting
 // goes by integer atomics in shared memory; the places keep the slots' order by the set of a warp's
-// lanes in each bucket, which the lanes write as bits into a word of the bucket (a
-// warp-wide match instruction did the same five times slower).
+// lanes in each bucket, which the lanes write as bits into a word of the bucket.  Bound by
+// the latency of shared memory and of the cluster's barriers: 16384 x 8 slots to 128 experts 9.7 us
+// (37 us with a warp-wide match instruction and 8 blocks), 8 x 8 slots 3.3 us.
 //
 // Shared memory, B = E + 1 words each: hist[warps][B] slots of a warp in a bucket, then
 // where its next one goes; lanes[warps][B], zero between steps; count[B] of the
@@ -286,7 +292,8 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const T* dou
 }
 
 // Whether every row lies on the 16-byte grid in whole vectors.
-bool on_grid(int64_t H, size_t size, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
+bool on_grid(int64_t H, size_t size, std::initializer_list<const void*> ptrs,
+             std::initializer_list<int64_t> lds) {
     if (H * size % 16 != 0) return false;
     for (const void* p : ptrs)
         if (reinterpret_cast<uintptr_t>(p) % 16 != 0) return false;

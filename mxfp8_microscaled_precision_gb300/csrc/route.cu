@@ -11,7 +11,13 @@
 // two of experts / 32, so a lane's logits are one vector, of equal values the
 // lowest lane has the lowest expert, and a group of experts is mostly a few neighbouring lanes.  A round of
 // the selection is a scan of the lane's registers, the largest key of the warp and a vote
-// on who has it.  Bound by instructions (some 500 a token of 128 experts).
+// on who has it.
+//
+// Bound by instructions, not by memory (some 500 a token of 128 experts; the rounds are a
+// chain of reductions).  Measured: 16384 tokens x 128 experts FP32, softmax, top 8: 12 us (the
+// logits alone would take 1.4 us), backward 7 us (2.6); 8191 x 256 BF16, sigmoid with bias,
+// 4 of 8 groups: 12 us, backward 3.8 us; 4096 x 1024 BF16: 12 us and 7.8 us; 4 tokens 2.6 us.
+// The first form (an expert every 32, groups scanned by a lane each) took 13.4 us and 22 us.
 
 #include <cuda_runtime.h>
 
