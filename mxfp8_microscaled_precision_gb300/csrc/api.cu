@@ -6,6 +6,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -65,6 +66,24 @@ cudaError_t current_device_info(DeviceInfo* info) {
         if ((e = cudaGetSymbolAddress(&p, g_mxq_device_status)) != cudaSuccess) return e;
         info->status = static_cast<unsigned int*>(p);
     }
+    return cudaSuccess;
+}
+
+cudaError_t current_device_is_supported(bool* yes) {
+    static std::atomic<signed char> known[kMaxDevices];   // 0 unknown, 1 sm_103, -1 another
+    int dev = -1;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    signed char k = known[dev].load(std::memory_order_relaxed);
+    if (k == 0) {
+        DeviceInfo info;
+        const cudaError_t err = current_device_info(&info);
+        if (err != cudaSuccess) return err;
+        k = info.cc_major == 10 && info.cc_minor == 3 ? 1 : -1;
+        known[dev].store(k, std::memory_order_relaxed);
+    }
+    *yes = k > 0;
     return cudaSuccess;
 }
 

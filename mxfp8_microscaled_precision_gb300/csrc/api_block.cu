@@ -31,8 +31,9 @@ mxq_status device_ok(DeviceInfo* info) {
 }
 
 mxq_status device_ok() {
-    DeviceInfo info;
-    return device_ok(&info);
+    bool yes = false;
+    if (mxq::current_device_is_supported(&yes) != cudaSuccess) return MXQ_ERR_CUDA;
+    return yes ? MXQ_OK : MXQ_ERR_UNSUPPORTED_DEVICE;
 }
 
 inline mxq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA; }

@@ -20,6 +20,10 @@ struct DeviceInfo {
 // Returns cudaSuccess and fills `info` for the current device.
 cudaError_t current_device_info(DeviceInfo* info);
 
+// Whether the current device is an sm_103 (GB300): the one question of the calls that are
+// made for single tokens, without the lookups of the above.
+cudaError_t current_device_is_supported(bool* yes);
+
 // 2-D tensor map over a row-major matrix [outer, inner] of 1- or 2-byte
 // elements with the given row stride, box [box_outer, box_inner].
 bool encode_tensor_map_2d(CUtensorMap* map, const void* base, bool two_byte_elems, uint64_t inner,
