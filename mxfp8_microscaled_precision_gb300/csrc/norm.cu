@@ -143,14 +143,17 @@ __global__ void __launch_bounds__(kN == 8 ? 512 : 1024) norm_kernel(const NormAr
             f32x2 f[H], part = 0;
             unpack2<T>(q[n], f);
 #pragma unroll
-            for (int c = 0; c < H; ++c) {
-                f32x2 d = add2(f[c], minus);
-                if (kAny && (i < 0 || i + V > cols)) {   // a vector that the row has a part of
+            for (int c = 0; c < H; ++c) f[c] = add2(f[c], minus);
+            if (kAny && (i < 0 || i + V > cols)) {   // a vector that the row has a part of
+#pragma unroll
+                for (int c = 0; c < H; ++c) {
                     const int e = i + 2 * c;
-                    d = pair(e >= 0 && e < cols ? lo_of(d) : 0.0f, e + 1 >= 0 && e + 1 < cols ? hi_of(d) : 0.0f);
+                    f[c] = pair(e >= 0 && e < cols ? lo_of(f[c]) : 0.0f,
+                                e + 1 >= 0 && e + 1 < cols ? hi_of(f[c]) : 0.0f);
                 }
-                part = fma2(d, d, part);
             }
+#pragma unroll
+            for (int c = 0; c < H; ++c) part = fma2(f[c], f[c], part);
             sq = add2(sq, part);
         }
         const float r = inverse_root(row_sum(lo_of(sq) + hi_of(sq), tpr, sh[1]) * inv + a.eps);
