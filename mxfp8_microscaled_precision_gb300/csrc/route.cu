@@ -15,8 +15,8 @@
 //
 // Bound by instructions, not by memory (some 500 a token of 128 experts; the rounds are a
 // chain of reductions).  Measured: 16384 tokens x 128 experts FP32, softmax, top 8: 12 us (the
-// logits alone would take 1.4 us), backward 7 us (2.6); 8191 x 256 BF16, sigmoid with bias,
-// 4 of 8 groups: 12 us, backward 3.8 us; 4096 x 1024 BF16: 12 us and 7.8 us; 4 tokens 2.6 us.
+// logits alone would take 1.4 us), backward 7.5 us (2.6); 8191 x 256 BF16, sigmoid with bias,
+// 4 of 8 groups: 12 us, backward 4.1 us; 4096 x 1024 BF16: 12 us and 8.0 us; 4 tokens 2.6 us.
 // The first form (an expert every 32, groups scanned by a lane each) took 13.4 us and 22 us.
 
 #include <cuda_runtime.h>
@@ -318,9 +318,11 @@ __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const T* lo
     }
     float ds = a.scale * dw;
     if (a.renorm) {
-        const float over = 1.0f / (warp_sum(s) + kRenormEps);
-        const float dot = warp_sum(dw * (a.scale * s * over));
-        ds = (a.scale * dw - dot) * over;
+        // the weights as the forward pass rounds them, both products rounded: where one expert is all
+        // there is and its weight is the scale, the difference is 0 and not the products' rounding
+        const float total = warp_sum(s) + kRenormEps;
+        const float dot = warp_sum(__fmul_rn(dw, a.scale * s / total));
+        ds = (__fmul_rn(a.scale, dw) - dot) / total;
     }
     if (id < 0) ds = 0.0f;
     const float d = kSoftmax ? warp_sum(ds * s) : 0.0f;

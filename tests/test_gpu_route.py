@@ -195,6 +195,20 @@ def test_route_backward_against_differences(score, renorm):
             assert abs((f[0] - f[1]) / (2 * h) - dx[t, e]) <= 1e-8 + 1e-4 * np.abs(D[t]).max() * scale
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("scale", [1.0, 2.0])
+def test_one_expert_with_all_the_weight_has_no_gradient(score, scale):
+    """top 1, renormalised: the weight is the scale whatever the logits are.  With a power of two every step is
+    exact (s / s = 1, two equal products), so the gradient is 0 and not a rounding of it."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x = 3.0 * torch.randn(1000, 72, generator=gen, device="cuda")
+    dw = torch.randn(1000, 1, generator=gen, device="cuda")
+    ids, w = mxq.route(x, 1, score=score, renorm=True, scale=scale)
+    assert (w == scale).all()
+    assert (mxq.route_backward(dw, x, ids, score=score, renorm=True, scale=scale) == 0).all()
+
+
 def test_ties_go_to_the_lowest_expert():
     from mxfp8_microscaled_precision_gb300 import mxq
     for E in (40, 128, 700):
