@@ -262,6 +262,40 @@ struct Params {
     }
 };
 
+// The same in shared memory, n vectors of V a thread, each thread's its own (nobody else reads
+// them): [n][16-byte parts of V parameters][threads].
+template <typename W, int V>
+struct ParamSlots {
+    static constexpr int kWords = V * static_cast<int>(sizeof(W)) / 4;   // 2, 4 or 8
+    static constexpr int kPart = kWords < 4 ? kWords : 4;
+    uint32_t* mine;
+    int threads;
+    static constexpr int64_t bytes_of(int64_t n, int64_t threads) { return n * threads * V * sizeof(W); }
+    __device__ __forceinline__ ParamSlots(void* memory, int thread, int threads)
+        : mine(static_cast<uint32_t*>(memory) + thread * kPart), threads(threads) {}
+    __device__ __forceinline__ uint32_t* part(int n, int k) const {
+        return mine + (n * (kWords / kPart) + k) * threads * kPart;
+    }
+    __device__ __forceinline__ void put(int n, const Params<W, V>& p) const {
+#pragma unroll
+        for (int c = 0; c < kWords; ++c) part(n, c / kPart)[c % kPart] = p.u[c];
+    }
+    __device__ __forceinline__ void get(int n, f32x2 (&f)[V / 2]) const {
+        Params<W, V> p;
+#pragma unroll
+        for (int k = 0; k < kWords / kPart; ++k) {
+            if constexpr (kPart == 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(part(n, k));
+                p.u[4 * k] = v.x, p.u[4 * k + 1] = v.y, p.u[4 * k + 2] = v.z, p.u[4 * k + 3] = v.w;
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(part(n, k));
+                p.u[0] = v.x, p.u[1] = v.y;
+            }
+        }
+        p.get(f);
+    }
+};
+
 // Sum over the warp, the same order on every call, the result in all lanes.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

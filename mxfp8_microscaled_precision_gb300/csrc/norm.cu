@@ -13,8 +13,8 @@
 //
 // Bound by memory for long rows and many.  Measured, of the 6787 GB/s a copy reaches:
 // forward 16384 x 7168 BF16 80 us (87%), 16384 x 4096 45 us (87%), 32767 x 1000 FP32 42 us
-// (93%), 8 x 4096 2.3 us; backward 141 us (74%), 76 us (78%), 78 us (74%).  Rows off the
-// 16-byte grid: 8191 x 4097 BF16 forward 56 us (36%), backward 93 us (32%).
+// (93%), 8 x 4096 2.3 us; backward 134 us (78%), 72 us (82%), 81 us (71%).  Rows off the
+// 16-byte grid: 8191 x 4097 BF16 forward 55 us (36%), backward 73 us (41%).
 //
 // kAny: rows that start at any element (mxq_elem.cuh), in vectors of x's rows.  dy and the
 // result mostly start like x, as rows of the same length in buffers of their own do; where
@@ -354,12 +354,13 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_backward_short_kernel(c
 constexpr int kMaxStages = 32;
 constexpr int kMaxGroups = 14;               // named barriers: one each, and one for all
 constexpr int kRingThreads = 512;
+constexpr int kManyThreads = 640;
 constexpr int64_t kRingBytes = 204 * 1024;
 
 struct RingBars {
     uint64_t full[kMaxStages];
     int abort_flag;            // a wait ran out
-    int stop[kMaxGroups][2];   // it as a group's first thread saw it before the barrier of a row (by parity):
+    int stop[kMaxGroups][2];   // it as one thread of a group saw it before the barrier of a row (by parity):
                                // the whole group acts on that
 };
 
@@ -484,40 +485,43 @@ __device__ __forceinline__ void group_barrier(int group, int tpr) {
 
 // A thread of 16 elements a row (kKeep) keeps h and u of the row between the two passes; a
 // longer row is read a second time from the ring: registers hold the column sums.  What
-// bounds it: the chain of a row's sums (wait, shuffles, barrier, shuffles), some 2300
-// clocks, which 16 warps of 128 registers do not quite hide (issue slots 46% used, DRAM 63%,
-// at 16384 x 7168).  Twice the threads with half the registers spill and are slower
-// (211 us), as are 8 elements a thread (194 us); a warp of its own for the copies changes nothing.
-template <typename T, typename W, int kN, bool kAny>
-__global__ void __launch_bounds__(kRingThreads, 1)
+// bounds it: the chain of a row's sums (wait, shuffles, barrier, shuffles) and its arithmetic, some 2200
+// clocks, of which 14 to 16 warps of 128 registers fill less than half (issue slots 46% used, DRAM 63%,
+// at 16384 x 7168; figures below are for that size).  Twice the threads with half the registers spill and are slower
+// (211 us), as are 8 elements a thread (194 us) and the sums of the next row before the results of this
+// one (170 us: two rows' values leave the scheduler no registers); a warp of its own for the
+// copies changes nothing.  Without any loads and stores 118 us of 138 remain.
+// The weights wait in shared memory: in registers they took 146 us, and from the L1, of which the ring
+// leaves little, 206 us (FP32).
+template <typename T, typename W, int kN, bool kAny, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1)
 norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
     constexpr int V = kVec16<T>, H = V / 2, S = sizeof(T);
     constexpr bool kKeep = kN * V <= 16;
-    // weights kept in 8 registers, or in 16 where each use would have to shift them
-    constexpr bool kHeld = kN * V * sizeof(W) <= (kAny ? 64 : 32);
-    extern __shared__ __align__(128) unsigned char buf[];
+    extern __shared__ __align__(128) unsigned char buf[];   // the weights, then the ring
     __shared__ f32x2 sums[kMaxGroups][2][16];    // [group][row parity][warp]: of u and of u h
     __shared__ float2 stats[kMaxGroups][2];      // mean and rstd of the group's row
     __shared__ __align__(8) RingBars bars;
     const int groups = blockDim.x / tpr, group = threadIdx.x / tpr, at = threadIdx.x - group * tpr;
     const int warp = at >> 5, lane = threadIdx.x & 31;
     RowRing<T, kAny> ring;
-    ring.init(a, &bars, buf, stages);
+    ring.init(a, &bars, buf + ParamSlots<W, V>::bytes_of(kN, tpr), stages);
     for (int i = threadIdx.x; i < kMaxGroups * 2 * 16; i += blockDim.x)
         (&sums[0][0][0])[i] = 0;   // warps that a group does not have
     RingPlace place{blockIdx.x, 0, 0};
     place.move(group, stages);
     const int64_t stride = static_cast<int64_t>(groups) * gridDim.x;
-    // The group's first thread loads mean and rstd two rows ahead.
+    // A thread of the group's last warp, as the first one has the copies to start, loads mean
+    // and rstd two rows ahead.
+    const bool ahead = at == tpr - 32;
     auto statistics = [&](int64_t row) {
         return row < a.rows ? make_float2(a.mean[row], a.rstd[row]) : make_float2(0.0f, 0.0f);
     };
     float2 later = make_float2(0.0f, 0.0f);
-    if (at == 0) {
+    if (ahead) {
         stats[group][0] = statistics(place.row);
         later = statistics(place.row + stride);
     }
-    __syncthreads();
     const WaitGuard guard{&bars.abort_flag, a.status, kDefaultWaitLimitNs};
     const int cols = static_cast<int>(a.cols);
     const float inv = 1.0f / static_cast<float>(cols);
@@ -525,19 +529,21 @@ norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
     const int lead_g = kAny ? lead_of<S>(static_cast<const T*>(a.dy) + blockIdx.x * a.lddy) : 0;
     const int first = at * V - lead_x;
     const bool alike = lead_g == lead_x;
-    const W* wp = static_cast<const W*>(a.weight);
-    Params<W, V> w[kHeld ? kN : 1];
-    if constexpr (kHeld) {
+    const ParamSlots<W, V> w(buf, at, tpr);
 #pragma unroll
-        for (int n = 0; n < kN; ++n) w[n].template load<kAny>(wp, first + n * tpr * V, cols, 1.0f);
+    for (int n = 0; n < kN; ++n) {   // the same from every group: their rows start alike
+        Params<W, V> p;
+        p.template load<kAny>(static_cast<const W*>(a.weight), first + n * tpr * V, cols, 1.0f);
+        w.put(n, p);
     }
+    __syncthreads();
     f32x2 dw[kN][H] = {}, db[kN][H] = {};
     bool stop = false;
     int odd = 0;
     while (place.row < a.rows) {
         const float2 st = stats[group][odd];
         const f32x2 rr = pair(st.y, st.y), off = pair(-st.x * st.y, -st.x * st.y);
-        if (at == 0) {
+        if (ahead) {
             bars.stop[group][odd] = *static_cast<volatile int*>(&bars.abort_flag);
             stats[group][odd ^ 1] = later;
             later = statistics(place.row + 2 * stride);
@@ -551,8 +557,7 @@ norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
             f32x2 fw[H];
             unpack2<T>(ring.read(0, place.stage, q, i), h[m]);
             unpack2<T>(ring.read(1, place.stage, q, i, lead_g, alike), u[m]);
-            if constexpr (kHeld) w[n].get(fw);
-            else load_params2<W, V, kAny>(wp, i, cols, 1.0f, fw);
+            w.get(n, fw);
             add_vector<H>(h[m], u[m], fw, rr, off, dw[n], db[n], s1, s2);
         }
         const f32x2 both = warp_sum2(pair(lo_of(s1) + hi_of(s1), lo_of(s2) + hi_of(s2)));
@@ -574,8 +579,7 @@ norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
                 f32x2 fw[H];
                 unpack2<T>(ring.read(0, place.stage, q, i), h[m]);
                 unpack2<T>(ring.read(1, place.stage, q, i, lead_g, alike), u[m]);
-                if constexpr (kHeld) w[n].get(fw);
-                else load_params2<W, V, kAny>(wp, i, cols, 1.0f, fw);
+                w.get(n, fw);
 #pragma unroll
                 for (int c = 0; c < H; ++c) {
                     h[m][c] = fma2(h[m][c], rr, off);
@@ -736,25 +740,36 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t stream) {
 
 template <typename T, typename W, int kN, bool kAny>
 cudaError_t backward_ring(const NormBackwardArgs& a, int64_t vectors, int64_t grid, cudaStream_t stream) {
+    constexpr int V = kVec16<T>;
     const int64_t stage = 2 * RowRing<T, kAny>::bytes_of(a.cols);
     const int tpr = static_cast<int>((vectors + 32 * kN - 1) / (32 * kN)) * 32;
-    int64_t stages = kRingBytes / stage;
+    const int64_t weights = ParamSlots<W, V>::bytes_of(kN, tpr);
+    int64_t stages = (kRingBytes - weights) / stage;
     if (stages > kMaxStages) stages = kMaxStages;
-    // as many groups as there are threads for, with two stages each, and none without a row
-    int64_t groups = kRingThreads / tpr;
     const int64_t rows = (a.rows + grid - 1) / grid;
-    if (groups > kMaxGroups) groups = kMaxGroups;
-    if (groups > stages / 2) groups = stages / 2;
-    if (groups > rows) groups = rows;
-    if (groups < 1) groups = 1;
-    stages -= stages % groups;
-    auto kernel = norm_backward_kernel<T, W, kN, kAny>;
-    const int smem = static_cast<int>(stages * stage);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(grid), static_cast<unsigned>(tpr * groups), smem, stream>>>(
-        a, static_cast<int>(stages), tpr);
-    return cudaGetLastError();
+    // as many groups as there are threads for, with two stages each, and none without a row
+    auto go = [&](auto kernel, int64_t threads) {
+        int64_t groups = threads / tpr;
+        if (groups > kMaxGroups) groups = kMaxGroups;
+        if (groups > stages / 2) groups = stages / 2;
+        if (groups > rows) groups = rows;
+        if (groups < 1) groups = 1;
+        stages -= stages % groups;
+        const int smem = static_cast<int>(weights + stages * stage);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kernel<<<static_cast<unsigned>(grid), static_cast<unsigned>(tpr * groups), smem, stream>>>(
+            a, static_cast<int>(stages), tpr);
+        return cudaGetLastError();
+    };
+    if constexpr (kN * V <= 16) {
+        // Rows that leave a block of 512 threads half empty: two groups of 320 threads, with 96 registers
+        // (8192 x 5120 BF16: 57 us, one group of 128 registers 71 us; where 512 threads hold as many groups
+        // more registers are faster: 16384 x 4096 80 us against 82).
+        if (tpr > kRingThreads / 2 && tpr <= kManyThreads / 2)
+            return go(norm_backward_kernel<T, W, kN, kAny, kManyThreads>, kManyThreads);
+    }
+    return go(norm_backward_kernel<T, W, kN, kAny, kRingThreads>, kRingThreads);
 }
 
 template <typename T, typename W, bool kAny>
@@ -781,7 +796,7 @@ cudaError_t norm_backward_launch(const NormBackwardArgs& a, cudaStream_t stream)
     } else if (vectors <= kRingThreads * (16 / V)) {
         if (parts > kSMs) parts = kSMs;
         e = backward_ring<T, W, 16 / V, kAny>(a, vectors, parts, stream);
-    } else if (vectors <= kRingThreads * (32 / V) && 2 * RowRing<T, kAny>::bytes_of(a.cols) <= kRingBytes) {
+    } else if (vectors <= kRingThreads * (32 / V)) {   // 16384 columns: one stage at least beside the weights
         e = backward_ring<T, W, 32 / V, kAny>(a, vectors, parts, stream);
     } else {
         norm_backward_long_kernel<T, W><<<static_cast<unsigned>(parts), 1024, 0, stream>>>(a);
