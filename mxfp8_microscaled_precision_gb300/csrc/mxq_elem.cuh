@@ -164,11 +164,41 @@ __device__ __noinline__ void store_ends(void* row, int i, int n, const uint4 v) 
     }
 }
 
+// v with the elements outside [0, n) set to 0; i: index of its first element.
+template <int kSize>
+__device__ __forceinline__ uint4 inside(const uint4 v, int i, int n) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if constexpr (kSize == 2) {
+            const int e = i + 2 * c;
+            w[c] &= (e >= 0 && e < n ? 0xFFFFu : 0u) | (e + 1 >= 0 && e + 1 < n ? 0xFFFF0000u : 0u);
+        } else {
+            w[c] = i + c >= 0 && i + c < n ? w[c] : 0u;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Whether rows of n, of which this is one, lie before and after it in memory, so that a
+// vector (or two) that it has a part of can be loaded whole.  Element by element the ends of a row cost
+// its threads a second latency.
+template <int kSize>
+__device__ __forceinline__ bool is_between(int64_t row, int64_t rows, int n) {
+    return row > 0 && row < rows - 1 && n >= 2 * (16 / kSize);
+}
+
 // Elements [i, i + V) of a row of n, where element i lies on the 16-byte grid; 0 outside the
 // row.  Without kAny the row holds whole vectors, from its first element on.
 template <int kSize, bool kAny>
-__device__ __forceinline__ uint4 load16(const void* row, int i, int n) {
+__device__ __forceinline__ uint4 load16(const void* row, int i, int n, bool between = false) {
     const void* p = static_cast<const unsigned char*>(row) + static_cast<int64_t>(i) * kSize;
+    if (kAny && between) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (i < n) v = *static_cast<const uint4*>(p);
+        if (i < 0 || i + 16 / kSize > n) v = inside<kSize>(v, i, n);
+        return v;
+    }
     if (kAny ? i >= 0 && i + 16 / kSize <= n : i < n) return *static_cast<const uint4*>(p);
     if (kAny && i < n) return load_ends<kSize>(row, i, n);
     return make_uint4(0u, 0u, 0u, 0u);
@@ -197,6 +227,15 @@ __device__ __forceinline__ uint4 load_inner(const void* row, int i) {
     const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 15u);
     const uint4* q = reinterpret_cast<const uint4*>(p - off);
     return shift16(q[0], q[1], off);
+}
+
+// The same of any row, i < n; 0 outside it.
+template <int kSize>
+__device__ __forceinline__ uint4 load_shifted(const void* row, int i, int n, bool between) {
+    if (!between && !is_inner<kSize>(i, n)) return load_ends<kSize>(row, i, n);
+    uint4 v = load_inner<kSize>(row, i);
+    if (i < 0 || i + 16 / kSize > n) v = inside<kSize>(v, i, n);
+    return v;
 }
 
 // V parameters [i, i + V) of W (weights and the like, n of them, read by many rows) as

@@ -12,9 +12,9 @@
 // added in a fixed order.
 //
 // Bound by memory for long rows and many.  Measured, of the 6787 GB/s a copy reaches:
-// forward 16384 x 7168 BF16 80 us (87%), 16384 x 4096 45 us (87%), 32767 x 1000 FP32 42 us
-// (93%), 8 x 4096 2.3 us; backward 134 us (78%), 72 us (82%), 81 us (71%).  Rows off the
-// 16-byte grid: 8191 x 4097 BF16 forward 55 us (36%), backward 73 us (41%).
+// forward 16384 x 7168 BF16 79 us (87%), 16384 x 4096 45 us (87%), 32767 x 1000 FP32 41 us
+// (94%), 8 x 4096 2.3 us; backward 134 us (78%), 72 us (82%), 81 us (71%).  Rows off the
+// 16-byte grid: 8191 x 4097 BF16 forward 48 us (41%), backward 73 us (41%).
 //
 // kAny: rows that start at any element (mxq_elem.cuh), in vectors of x's rows.  dy and the
 // result mostly start like x, as rows of the same length in buffers of their own do; where
@@ -33,6 +33,8 @@ namespace mxq {
 namespace {
 
 constexpr int kSMs = 152;
+constexpr int kHeldGroups = 16;       // of more than a warp (forward, held parameters): named barriers
+constexpr int64_t kHeldBytes = 200 * 1024;
 constexpr int64_t kShortCols = 512;   // rows up to this long need no ring (backward)
 
 // ---- sums over the threads of a row ---------------------------------------------------
@@ -68,63 +70,130 @@ __device__ __forceinline__ float inverse_root(float v) {
     return v > 0.0f && v < INFINITY ? better : r;   // 0 and infinity: r is exact, the step would be NaN
 }
 
-// v with the elements outside [0, cols) set to 0; i: index of its first element.
-template <typename T>
-__device__ __forceinline__ uint4 inside(const uint4 v, int i, int cols) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if constexpr (sizeof(T) == 2) {
-            const int e = i + 2 * c;
-            w[c] &= (e >= 0 && e < cols ? 0xFFFFu : 0u) | (e + 1 >= 0 && e + 1 < cols ? 0xFFFF0000u : 0u);
-        } else {
-            w[c] = i + c >= 0 && i + c < cols ? w[c] : 0u;
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // ---- forward ----------------------------------------------------------------------------
+
+template <int H>
+__device__ __forceinline__ f32x2 squares_of(const f32x2 (&f)[H]) {
+    f32x2 s = 0;
+#pragma unroll
+    for (int c = 0; c < H; ++c) s = fma2(f[c], f[c], s);
+    return s;
+}
 
 // Thread i of a row holds the vectors i, i + tpr, ... (kN of 16 bytes), packed as they
 // came: unpacking them in each pass costs less than the registers of 32-bit copies (a ring of
-// bulk copies, as in the backward pass, took 96 us where this takes 80).  On
-// the grid a block has one row (or one for each group of lanes), and the parameters come from the
-// L1; with kAny they would have to be shifted for every row, so the blocks are fewer, each
-// keeps its threads' parameters and walks over rows that are a multiple of 8
-// apart and so all start alike.
-template <typename T, typename W, int kN, bool kAny>
+// bulk copies, as in the backward pass, took 96 us where this takes 80).  A block has one row
+// (or one for each group of lanes), and the parameters come from the L1.
+template <typename T, typename W, int kN>
 __global__ void __launch_bounds__(kN == 8 ? 512 : 1024) norm_kernel(const NormArgs a, int tpr) {
     constexpr int V = kVec16<T>, H = V / 2, S = sizeof(T);
-    constexpr bool kHeld = kAny && kN <= 2;
     __shared__ float sh[2][32];
     // rows of lanes (a power of two of them) share a block, longer ones have it alone
     const int shift = tpr <= 32 ? 31 - __clz(tpr) : 31;
     const int group = threadIdx.x >> shift, at = threadIdx.x - (group << shift);
-    const int groups = tpr <= 32 ? blockDim.x >> shift : 1;
-    const int64_t row_first = static_cast<int64_t>(blockIdx.x) * groups + group;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-    const int first = at * V - (kAny ? lead_of<S>(static_cast<const T*>(a.x) + row_first * a.ldx) : 0);
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (tpr <= 32 ? blockDim.x >> shift : 1) + group;
+    const bool live = row < a.rows;
+    // Never so, with a block a row; but 8 vectors' loads come out better ordered behind it (3000 x 12288
+    // FP32: 55 us, without 61; fewer vectors are 1.5% faster without).
+    if (kN == 8 && row - group >= a.rows) return;
+    const int first = at * V, cols = live ? static_cast<int>(a.cols) : 0;   // a row past the end loads and stores nothing
     const float inv = 1.0f / static_cast<float>(a.cols);
-    const W* w = static_cast<const W*>(a.weight);
-    const W* b = static_cast<const W*>(a.shift);
-    Params<W, V> held_w[kHeld ? kN : 1], held_b[kHeld ? kN : 1];
-    if constexpr (kHeld) {
+    const T* x = static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx;
+    T* y = static_cast<T*>(a.y) + (live ? row : 0) * a.ldy;
+    uint4 q[kN];
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
-            held_w[n].template load<true>(w, first + n * tpr * V, static_cast<int>(a.cols), 1.0f);
-            held_b[n].template load<true>(b, first + n * tpr * V, static_cast<int>(a.cols), 0.0f);
-        }
+    for (int n = 0; n < kN; ++n) q[n] = load16<S, false>(x, first + n * tpr * V, cols);
+    f32x2 sum = 0;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+        f32x2 f[H];
+        unpack2<T>(q[n], f);
+#pragma unroll
+        for (int c = 0; c < H; ++c) sum = add2(sum, f[c]);   // elements outside the row are 0
     }
-    for (int64_t row0 = row_first - group; row0 < a.rows; row0 += step) {   // one turn without kAny
-        const int64_t row = row0 + group;
+    const float mu = row_sum(lo_of(sum) + hi_of(sum), tpr, sh[0]) * inv;
+    const f32x2 minus = pair(-mu, -mu);
+    f32x2 sq = 0;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+        if (first + n * tpr * V >= cols) continue;
+        f32x2 f[H];
+        unpack2<T>(q[n], f);
+#pragma unroll
+        for (int c = 0; c < H; ++c) f[c] = add2(f[c], minus);
+        sq = add2(sq, squares_of<H>(f));
+    }
+    const float r = inverse_root(row_sum(lo_of(sq) + hi_of(sq), tpr, sh[1]) * inv + a.eps);
+    if (live && at == 0) {
+        a.mean[row] = mu;
+        a.rstd[row] = r;
+    }
+    const f32x2 rr = pair(r, r);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+        const int i = first + n * tpr * V;
+        if (i >= cols) continue;
+        f32x2 f[H], fw[H], fb[H];
+        unpack2<T>(q[n], f);
+        load_params2<W, V, false>(static_cast<const W*>(a.weight), i, cols, 1.0f, fw);
+        load_params2<W, V, false>(static_cast<const W*>(a.shift), i, cols, 0.0f, fb);
+#pragma unroll
+        for (int c = 0; c < H; ++c) f[c] = fma2(mul2(add2(f[c], minus), rr), fw[c], fb[c]);
+        store16<S, false>(y, i, cols, pack2<T>(f));
+    }
+}
+
+// The same where the parameters cost more than the row: off the grid, where they would have to be
+// shifted for every row, and in FP32 beside BF16 rows.  One block an SM keeps them in shared memory (in
+// registers they left room for two vectors a thread: 8191 x 513 18.6 us, so 14.6) and walks over its
+// rows blockIdx.x, + gridDim.x, ... with groups of tpr threads, a row each.  gridDim.x
+// is a multiple of 8 (or a block has one row), so a block's rows all start alike.  FP32 parameters of
+// 16384 x 7168 BF16: 150 us from the L1, so 105.  BF16 ones on the grid are faster from the L1 (81 us, so
+// 88), where fewer registers and no loop leave the SM more rows.  Bound by instructions (issue slots 63%
+// used at 4097 columns) and by the warps of a row that wait for those with its ends; the next row's loads
+// before this row's sums change nothing.
+template <typename T, typename W, int kN, bool kAny>
+__global__ void __launch_bounds__(kN == 8 ? 512 : 1024) norm_held_kernel(const NormArgs a, int tpr) {
+    constexpr int V = kVec16<T>, H = V / 2, S = sizeof(T);
+    extern __shared__ __align__(16) unsigned char params[];
+    __shared__ float sh[kHeldGroups][2][32];
+    const int group = threadIdx.x / tpr, at = threadIdx.x - group * tpr, groups = blockDim.x / tpr;
+    const int all = static_cast<int>(a.cols);
+    const int first = at * V - (kAny ? lead_of<S>(static_cast<const T*>(a.x) + blockIdx.x * a.ldx) : 0);
+    const float inv = 1.0f / static_cast<float>(all);
+    const ParamSlots<W, V> w(params, at, tpr), b(params + ParamSlots<W, V>::bytes_of(kN, tpr), at, tpr);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+        const int i = first + n * tpr * V;
+        if (group != 0) break;
+        Params<W, V> p;
+        p.template load<kAny>(static_cast<const W*>(a.weight), i, all, 1.0f);
+        w.put(n, p);
+        p.template load<kAny>(static_cast<const W*>(a.shift), i, all, 0.0f);
+        b.put(n, p);
+    }
+    __syncthreads();
+    auto sum_of_row = [&](float v, int place) {   // as row_sum, over the group's threads
+        if (tpr <= 32) return lanes_sum(v, tpr);
+        v = warp_sum(v);
+        float* s = sh[group][place];
+        if ((at & 31) == 0) s[at >> 5] = v;
+        named_bar_sync(group, tpr);
+        return warp_sum((at & 31) < (tpr >> 5) ? s[at & 31] : 0.0f);
+    };
+    // The groups of a warp walk together: the last turn may find rows for some of them only.
+    const int in_warp = tpr < 32 ? group & (32 / tpr - 1) : 0;
+    for (int64_t row0 = blockIdx.x + static_cast<int64_t>(group - in_warp) * gridDim.x; row0 < a.rows;
+         row0 += static_cast<int64_t>(groups) * gridDim.x) {
+        const int64_t row = row0 + static_cast<int64_t>(in_warp) * gridDim.x;
         const bool live = row < a.rows;
-        const int cols = live ? static_cast<int>(a.cols) : -V;   // a row past the end loads and stores nothing
+        const int cols = live ? all : -V;   // a row past the end loads and stores nothing
         const T* x = static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx;
         T* y = static_cast<T*>(a.y) + (live ? row : 0) * a.ldy;
         uint4 q[kN];
+        const bool between = kAny && is_between<S>(row, a.rows, cols);
 #pragma unroll
-        for (int n = 0; n < kN; ++n) q[n] = load16<S, kAny>(x, first + n * tpr * V, cols);
+        for (int n = 0; n < kN; ++n) q[n] = load16<S, kAny>(x, first + n * tpr * V, cols, between);
         f32x2 sum = 0;
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
@@ -133,18 +202,18 @@ __global__ void __launch_bounds__(kN == 8 ? 512 : 1024) norm_kernel(const NormAr
 #pragma unroll
             for (int c = 0; c < H; ++c) sum = add2(sum, f[c]);   // elements outside the row are 0
         }
-        const float mu = row_sum(lo_of(sum) + hi_of(sum), tpr, sh[0]) * inv;
+        const float mu = sum_of_row(lo_of(sum) + hi_of(sum), 0) * inv;
         const f32x2 minus = pair(-mu, -mu);
         f32x2 sq = 0;
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
             const int i = first + n * tpr * V;
             if (i >= cols) continue;
-            f32x2 f[H], part = 0;
+            f32x2 f[H];
             unpack2<T>(q[n], f);
 #pragma unroll
             for (int c = 0; c < H; ++c) f[c] = add2(f[c], minus);
-            if (kAny && (i < 0 || i + V > cols)) {   // a vector that the row has a part of
+            if (kAny && (i < 0 || i + V > cols)) {   // 0 outside the row
 #pragma unroll
                 for (int c = 0; c < H; ++c) {
                     const int e = i + 2 * c;
@@ -152,35 +221,27 @@ __global__ void __launch_bounds__(kN == 8 ? 512 : 1024) norm_kernel(const NormAr
                                 e + 1 >= 0 && e + 1 < cols ? hi_of(f[c]) : 0.0f);
                 }
             }
-#pragma unroll
-            for (int c = 0; c < H; ++c) part = fma2(f[c], f[c], part);
-            sq = add2(sq, part);
+            sq = add2(sq, squares_of<H>(f));
         }
-        const float r = inverse_root(row_sum(lo_of(sq) + hi_of(sq), tpr, sh[1]) * inv + a.eps);
+        const float r = inverse_root(sum_of_row(lo_of(sq) + hi_of(sq), 1) * inv + a.eps);
         if (live && at == 0) {
             a.mean[row] = mu;
             a.rstd[row] = r;
         }
         const f32x2 rr = pair(r, r);
-        const bool alike = kAny && lead_of<S>(y) == lead_of<S>(x);
+        const bool alike = !kAny || lead_of<S>(y) == lead_of<S>(x);
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
             const int i = first + n * tpr * V;
             if (i >= cols) continue;
             f32x2 f[H], fw[H], fb[H];
             unpack2<T>(q[n], f);
-            if constexpr (kHeld) {
-                held_w[n].get(fw);
-                held_b[n].get(fb);
-            } else {
-                load_params2<W, V, kAny>(w, i, cols, 1.0f, fw);
-                load_params2<W, V, kAny>(b, i, cols, 0.0f, fb);
-            }
+            w.get(n, fw);
+            b.get(n, fb);
 #pragma unroll
             for (int c = 0; c < H; ++c) f[c] = fma2(mul2(add2(f[c], minus), rr), fw[c], fb[c]);
             store16<S, kAny>(y, i, cols, pack2<T>(f), alike);
         }
-        if (!kAny) return;
     }
 }
 
@@ -283,11 +344,12 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_backward_short_kernel(c
         const T* x = static_cast<const T*>(a.x) + at_row * a.ldx;
         const T* dy = static_cast<const T*>(a.dy) + at_row * a.lddy;
         T* dx = static_cast<T*>(a.dx) + at_row * a.lddx;
+        const bool between = kAny && is_between<S>(row, a.rows, cols);
         uint4 qx[kN], qg[kN];
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-            qx[n] = load16<S, kAny>(x, first + n * tpr * V, cols);
-            if (!kAny || lead_of<S>(dy) == lead_of<S>(x)) qg[n] = load16<S, kAny>(dy, first + n * tpr * V, cols);
+            qx[n] = load16<S, kAny>(x, first + n * tpr * V, cols, between);
+            if (!kAny || lead_of<S>(dy) == lead_of<S>(x)) qg[n] = load16<S, kAny>(dy, first + n * tpr * V, cols, between);
             else qg[n] = load_ends<S>(dy, first + n * tpr * V, cols);
         }
         const float mu = live ? a.mean[at_row] : 0.0f, r = live ? a.rstd[at_row] : 0.0f;
@@ -473,7 +535,7 @@ struct RowRing {
         if (kAny && !alike) return load_ends<sizeof(T)>(row + lead * sizeof(T), i, cols);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (i < cols) v = *reinterpret_cast<const uint4*>(row + 16 * q);
-        if (kAny && (i < 0 || i + kVec16<T> > cols)) v = inside<T>(v, i, cols);
+        if (kAny && (i < 0 || i + kVec16<T> > cols)) v = inside<sizeof(T)>(v, i, cols);
         return v;
     }
 };
@@ -712,13 +774,19 @@ int64_t vectors_of(const void* x, int64_t ldx, int64_t cols) {
 template <typename T, typename W, bool kAny>
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t stream) {
     const int64_t vectors = vectors_of<T>(a.x, a.ldx, a.cols);
-    if (vectors > 8 * 512) {
+    constexpr int V = kVec16<T>;
+    const bool few = a.rows <= 2 * kSMs;
+    const bool hold = kAny || (sizeof(W) > sizeof(T) && !few);
+    auto longest = [&] {
         norm_long_kernel<T, W><<<static_cast<unsigned>(a.rows), 1024, 0, stream>>>(a);
         return cudaGetLastError();
-    }
+    };
+    if (vectors > 8 * 512) return longest();
     // Few rows: 2 vectors a thread (latency).  Many: 4, and 8 for the longest rows, so that
-    // several blocks with a row each share an SM (16384 x 4096 BF16: 52 us with 4, 61 with 8, 72 with 2).
-    const int64_t most = kAny || a.rows <= 2 * kSMs ? 2 : 4;
+    // several rows share an SM (16384 x 4096 BF16: 52 us with 4, 61 with 8, 72 with 2), but 2 off the grid where 4
+    // leave a third more places empty (8191 x 1025: 21 us, with 4 23; 8191 x 4097: 48 with 4, 58 with 2).
+    auto places = [&](int64_t k) { return (vectors + 32 * k - 1) / (32 * k) * 32 * k; };
+    const int64_t most = few || (kAny && 3 * places(4) >= 4 * places(2)) ? 2 : 4;
     int64_t n = (vectors + 31) / 32;   // vectors of a thread if a warp has the row
     if (n > most) n = most;
     while (n < 8 && vectors > n * 512) n *= 2;
@@ -726,15 +794,30 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t stream) {
         constexpr int kN = count.value;
         int tpr = lanes_of(vectors);
         if (vectors > 32 * kN) tpr = static_cast<int>((vectors + 32 * kN - 1) / (32 * kN)) * 32;
-        const int threads = tpr <= 32 ? 128 : tpr;
-        const int64_t per = threads / tpr;
-        int64_t grid = (a.rows + per - 1) / per;
-        if (kAny) {   // what the SMs hold at a time, by registers
-            const int64_t most = kSMs * (65536 / (threads * (kN == 8 ? 128 : 64)));
-            if (grid > most) grid = most;
+        const int64_t held = 2 * ParamSlots<W, V>::bytes_of(kN, tpr);
+        if constexpr (kAny || sizeof(W) > sizeof(T)) {
+            if (hold && held <= kHeldBytes) {
+                const int64_t grid = a.rows < kSMs ? a.rows : kSMs, rows = (a.rows + grid - 1) / grid;
+                int64_t groups = (kN == 8 ? 512 : 1024) / tpr;
+                if (tpr > 32 && groups > kHeldGroups) groups = kHeldGroups;
+                if (groups > rows) groups = rows;
+                const unsigned threads = static_cast<unsigned>((groups * tpr + 31) / 32 * 32);
+                auto kernel = norm_held_kernel<T, W, kN, kAny>;
+                const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                           static_cast<int>(held));
+                if (e != cudaSuccess) return e;
+                kernel<<<static_cast<unsigned>(grid), threads, held, stream>>>(a, tpr);
+                return cudaGetLastError();
+            }
         }
-        norm_kernel<T, W, kN, kAny><<<static_cast<unsigned>(grid), threads, 0, stream>>>(a, tpr);
-        return cudaGetLastError();
+        if constexpr (kAny) {
+            return longest();   // FP32 parameters of BF16 rows over 25000 columns
+        } else {
+            const int threads = tpr <= 32 ? 128 : tpr;
+            const int64_t per = threads / tpr;
+            norm_kernel<T, W, kN><<<static_cast<unsigned>((a.rows + per - 1) / per), threads, 0, stream>>>(a, tpr);
+            return cudaGetLastError();
+        }
     });
 }
 

@@ -113,6 +113,17 @@ def test_many_rows(M, C, dtype, wdtype):
     assert mxq.get_device_status() == 0
 
 
+@pytest.mark.parametrize("M,C,dtype,wdtype", [
+    (700, 5120, torch.bfloat16, torch.bfloat16), (613, 4999, torch.bfloat16, torch.float32),
+    (500, 4616, torch.float32, torch.float32), (457, 5121, torch.bfloat16, torch.bfloat16),
+    (3000, 40, torch.bfloat16, torch.float32), (2999, 33, torch.bfloat16, torch.float32), (5000, 9, torch.float32, torch.bfloat16),
+    (306, 24000, torch.bfloat16, torch.float32), (310, 25999, torch.bfloat16, torch.float32)])
+def test_rows_of_every_grouping(M, C, dtype, wdtype):
+    """Two groups of 320 threads; parameters kept in shared memory for parts of a warp, for a whole block, and
+    too long for it."""
+    test_many_rows(M, C, dtype, wdtype)
+
+
 def test_without_weight_or_shift():
     from mxfp8_microscaled_precision_gb300 import mxq
     for C in (96, 97):
