@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* y, int64_
     const int64_t slots = static_cast<int64_t>(gridDim.x) * k;
     f32x2 acc[V / 2] = {};
     // kB rows' loads in flight at a time: 4 on the grid (16384 tokens x 8 rows of 4096 BF16: 180 us, one at a
-    // time 203), one off it, where a load is two already (8191 x 4 rows of 4097: 81 us, with 4 113).
+    // time 203), one off it, where a load is two already (8191 x 4 rows of 4097: 74 us, with 2 82, with 4 124).
     auto add = [&](auto batch, auto load) {
         constexpr int kB = batch.value;
         for (int j0 = 0; j0 < k; j0 += kB) {
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* y, int64_
                 const Place p = place_of(r[j0 + j], slots);
                 if (!p.kept || !p.exists) continue;
                 w[j] = weights != nullptr ? weights[t * k + j0 + j] : 1.0f;
-                v[j] = load(y + p.row * ldy);
+                v[j] = load(p.row);
             }
 #pragma unroll
             for (int j = 0; j < kB; ++j) {
@@ -233,9 +233,10 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* y, int64_
         }
     };
     using std::integral_constant;
-    if constexpr (!kAny) add(integral_constant<int, 4>{}, [&](const T* row) { return load16<S, false>(row, i, H); });
-    else if (is_inner<S>(i, H)) add(integral_constant<int, 1>{}, [&](const T* row) { return load_inner<S>(row, i); });
-    else add(integral_constant<int, 1>{}, [&](const T* row) { return load_ends<S>(row, i, H); });
+    if constexpr (!kAny) add(integral_constant<int, 4>{}, [&](int64_t row) { return load16<S, false>(y + row * ldy, i, H); });
+    else add(integral_constant<int, 1>{}, [&](int64_t row) {
+        return load_shifted<S>(y + row * ldy, i, H, is_between<S>(row, slots, H));
+    });
     store16<S, kAny>(to, i, H, pack2<T>(acc));
 }
 
