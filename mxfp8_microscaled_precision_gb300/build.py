@@ -1,5 +1,5 @@
 """Build libmxq.so (the CUDA library) in-tree with nvcc for sm_103a, and the
-extension module that calls it from Python (csrc/calls.c) with gcc.
+extension module that calls it from Python (csrc/calls.cpp) with g++.
 
 The translation units are compiled in parallel, then linked into
 ``mxfp8_microscaled_precision_gb300/_build/libmxq.so`` (the CUDA runtime is
@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import fcntl
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -41,7 +42,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + ["calls.c"]] + [os.path.join(INCLUDE, "mxq.h")]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + ["calls.cpp"]] + [os.path.join(INCLUDE, "mxq.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -61,6 +62,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
             fcntl.flock(lock, fcntl.LOCK_UN)
 
 
+def _gxx() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _compile_calls() -> str:
+    obj = os.path.join(OUT, "calls.o")
+    include = os.path.join(_torch_dir(), "include")
+    r = subprocess.run([_gxx(), "-O2", "-std=c++17", "-Wall", "-fPIC", "-I" + INCLUDE,
+                        "-I" + sysconfig.get_paths()["include"], "-isystem", include, "-isystem",
+                        os.path.join(include, "torch", "csrc", "api", "include"), "-c", os.path.join(CSRC, "calls.cpp"),
+                        "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for calls.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
 def _build(verbose: bool) -> str:
     nvcc = _nvcc()
     objs = []
@@ -75,21 +96,23 @@ def _build(verbose: bool) -> str:
             print(r.stdout, r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(compile_one, SOURCES))
+        calls_obj = calls.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    # torch's libraries are in the process before the module is: no path to them is needed
     tmp = CALLS + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I" + INCLUDE,
-           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "calls.c"), "-o", tmp, "-L" + OUT, "-l:libmxq.so",
-           "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    r = subprocess.run([_gxx(), "-shared", "-o", tmp, calls_obj, "-L" + OUT, "-l:libmxq.so", "-Wl,-rpath,$ORIGIN",
+                        "-L" + os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"],
+                       capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed for calls.c:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"link failed for calls.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
     return LIB
 

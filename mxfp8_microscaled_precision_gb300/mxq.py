@@ -1,7 +1,8 @@
 """Python binding of libmxq (the C ABI in include/mxq.h).
 
 Argument marshalling only: tensors are allocated by PyTorch on the current
-CUDA device, their pointers and sizes go through ctypes to the C ABI, and
+CUDA device, their pointers and sizes go through ctypes (the calls of the last
+section: through an extension module) to the C ABI, and
 every step of the computation runs in the library's CUDA kernels on the
 current stream.  There is no fallback: if the library is missing or the
 device is not a GB300 the calls raise.
@@ -494,15 +495,14 @@ def grouped_gemm_group_tiled(a_q, a_s_grouped, b_q, b_s, offsets: torch.Tensor, 
 # ---- operators around the experts' products (see the same section of mxq.h) ----
 
 BF16, F32 = 0, 1
-_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORES = {"max": 0, "top2sum": 1}
 MAX_GRADS = 65536
 
 
 # These calls are made for single tokens too, where the host's share is most of the
-# time: they go through an extension module instead of ctypes (csrc/calls.c), the stream comes without
-# building a Stream object, and a check looks only at what the library cannot see.
+# time: their tensors are checked, their results allocated and the library is called by an
+# extension module instead of ctypes (csrc/calls.cpp).
 _calls_module = None
 
 
@@ -517,49 +517,13 @@ def _calls():
             raise RuntimeError(f"the extension module is not built ({_build.CALLS}); run __graft_entry__.build()")
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
+
+        def failed(what, status):
+            _check(status, what)
+
+        module.set_error(failed)
         _calls_module = module
     return _calls_module
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_of(t: torch.Tensor) -> int:
-    """The current stream of the tensor's device."""
-    if _raw_stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(t.get_device())
-
-
-def _matrix(t: torch.Tensor, name: str):
-    """(dtype code, rows, cols, row stride) of a 2-D bf16 or fp32 CUDA tensor with unit
-    last stride.  A single row has any stride (its own says nothing)."""
-    code = _DTYPES.get(t.dtype)
-    if code is None or t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D bfloat16 or float32 CUDA tensor")
-    rows, cols = t.shape
-    ld, unit = t.stride()
-    if unit != 1 and cols > 1:
-        raise ValueError(f"{name} must have unit stride along its last axis")
-    return code, rows, cols, (ld if rows > 1 else max(ld, cols))
-
-
-def _dense(t: torch.Tensor, name: str, dtype, *shape) -> int:
-    """The address of a contiguous CUDA tensor of this dtype and shape."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} CUDA tensor {list(shape)}")
-    return t.data_ptr()
-
-
-def _result(out, name, like, code, rows, cols):
-    """(tensor, row stride): `out` checked against what the call writes, or a new tensor
-    of the dtype of `like`."""
-    if out is None:
-        return like.new_empty((rows, cols)), cols
-    c, r, n, ld = _matrix(out, name)
-    if c != code or r != rows or n != cols:
-        raise ValueError(f"{name} must be {str(like.dtype)[6:]} {[rows, cols]}")
-    return out, ld
 
 
 def _of(table, key, what):
@@ -575,49 +539,15 @@ def route(logits: torch.Tensor, topk: int, score="softmax", bias=None, n_group: 
     logits: bf16 or fp32 [T, E]; bias: fp32 [E], added for the choice only; token_mask:
     bool or uint8 [T], 0 for padding tokens.  Returns (ids int32 [T, topk], weights
     fp32 [T, topk]); ids is -1 (weight 0) where no expert is left."""
-    code, T, E, ld = _matrix(logits, "logits")
-    b = None if bias is None else _dense(bias, "bias", torch.float32, E)
-    m = None
-    if token_mask is not None:
-        m = _dense(token_mask, "token_mask", torch.bool if token_mask.dtype is torch.bool else torch.uint8, T)
-    if out is None:
-        if topk < 1:
-            raise ValueError("topk must be at least 1")
-        ids = logits.new_empty((T, topk), dtype=torch.int32)
-        weights = logits.new_empty((T, topk), dtype=torch.float32)
-        i, w = ids.data_ptr(), weights.data_ptr()
-    else:
-        ids, weights = out
-        i = _dense(ids, "ids", torch.int32, T, topk)
-        w = _dense(weights, "weights", torch.float32, T, topk)
-    _check(_calls().route(logits.data_ptr(), code, T, E, ld, b, m, _of(_SCORES, score, "score"), n_group, topk_group,
-                           _of(_GROUP_SCORES, group_score, "group score"), topk, 1 if renorm else 0, scale, i, w,
-                           _stream_of(logits)), "mxq_route")
-    return ids, weights
-
-
-def _slots(t: torch.Tensor, name: str):
-    """(address, T, k) of an int32 matrix of slots."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    T, k = t.shape
-    return _dense(t, name, torch.int32, T, k), T, k
+    return _calls().route(logits, topk, _of(_SCORES, score, "score"), bias, n_group, topk_group,
+                          _of(_GROUP_SCORES, group_score, "group score"), 1 if renorm else 0, scale, token_mask, out)
 
 
 def route_backward(dweights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score="softmax",
                    renorm: bool = True, scale: float = 1.0, out=None):
     """Gradient of route's weights by its logits (see mxq_route_backward), in the
     logits' dtype; score, renorm and scale as in the forward call."""
-    code, T, E, ld = _matrix(logits, "logits")
-    i, n, k = _slots(ids, "ids")
-    if n != T:
-        raise ValueError("ids and logits must have the same number of tokens")
-    d = _dense(dweights, "dweights", torch.float32, T, k)
-    out, ldo = _result(out, "out", logits, code, T, E)
-    _check(_calls().route_backward(d, i, logits.data_ptr(), code, T, E, ld, _of(_SCORES, score, "score"), k,
-                                    1 if renorm else 0, scale, out.data_ptr(), ldo, _stream_of(logits)),
-           "mxq_route_backward")
-    return out
+    return _calls().route_backward(dweights, logits, ids, _of(_SCORES, score, "score"), 1 if renorm else 0, scale, out)
 
 
 def moe_plan(ids: torch.Tensor, experts: int, out=None):
@@ -625,118 +555,39 @@ def moe_plan(ids: torch.Tensor, experts: int, out=None):
     route.  Returns (offsets int64 [experts + 1], rows int32 [T, k]): offsets are the
     group offsets of the grouped calls, rows[t, j] the row of slot (t, j), -1 - row
     for a dropped slot."""
-    i, T, k = _slots(ids, "ids")
-    if out is None:
-        offsets = ids.new_empty(max(experts, 0) + 1, dtype=torch.int64)
-        rows = ids.new_empty((T, k))
-        o, r = offsets.data_ptr(), rows.data_ptr()
-    else:
-        offsets, rows = out
-        o = _dense(offsets, "offsets", torch.int64, experts + 1)
-        r = _dense(rows, "rows", torch.int32, T, k)
-    _check(_calls().moe_plan(i, T, k, experts, o, r, _stream_of(ids)), "mxq_moe_plan")
-    return offsets, rows
+    return _calls().moe_plan(ids, experts, out)
 
 
 def moe_dispatch(x: torch.Tensor, rows: torch.Tensor, out=None) -> torch.Tensor:
     """The tokens' rows in expert order (see mxq_moe_dispatch): x [T, H], rows from
     moe_plan.  Returns [T * k, H], zeros in the rows of dropped slots."""
-    code, n, H, ld = _matrix(x, "x")
-    r, T, k = _slots(rows, "rows")
-    if n != T:
-        raise ValueError("x and rows must have the same number of tokens")
-    out, ldo = _result(out, "out", x, code, T * k, H)
-    _check(_calls().moe_dispatch(x.data_ptr(), code, T, k, H, ld, r, out.data_ptr(), ldo, _stream_of(x)),
-           "mxq_moe_dispatch")
-    return out
+    return _calls().moe_dispatch(x, rows, out)
 
 
 def moe_combine(y: torch.Tensor, rows: torch.Tensor, weights=None, out=None) -> torch.Tensor:
     """out[t] = sum over a token's slots of weight * y[row] (see mxq_moe_combine):
     y [T * k, H] in expert order, weights fp32 [T, k] from route.  Without weights it
     is the plain sum, the gradient of moe_dispatch.  Returns [T, H]."""
-    code, n, H, ld = _matrix(y, "y")
-    r, T, k = _slots(rows, "rows")
-    if n != T * k:
-        raise ValueError("y must have a row for every slot")
-    w = None if weights is None else _dense(weights, "weights", torch.float32, T, k)
-    out, ldo = _result(out, "out", y, code, T, H)
-    _check(_calls().moe_combine(y.data_ptr(), code, T, k, H, ld, r, w, out.data_ptr(), ldo, _stream_of(y)),
-           "mxq_moe_combine")
-    return out
+    return _calls().moe_combine(y, rows, weights, out)
 
 
 def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor, out=None):
     """Gradients of moe_combine (see mxq_moe_combine_backward): returns
     (dy [T * k, H], dweights fp32 [T, k]); `out` may supply either or both."""
-    code, n, H, ldy = _matrix(y, "y")
-    r, T, k = _slots(rows, "rows")
-    if n != T * k:
-        raise ValueError("y must have a row for every slot")
-    c, n, h, ldd = _matrix(dout, "dout")
-    if c != code or n != T or h != H:
-        raise ValueError(f"dout must be {str(y.dtype)[6:]} {[T, H]}")
-    w = _dense(weights, "weights", torch.float32, T, k)
-    dy, dweights = (None, None) if out is None else out
-    dy, lddy = _result(dy, "dy", y, code, T * k, H)
-    if dweights is None:
-        dweights = torch.empty_like(weights)
-        d = dweights.data_ptr()
-    else:
-        d = _dense(dweights, "dweights", torch.float32, T, k)
-    _check(_calls().moe_combine_backward(dout.data_ptr(), y.data_ptr(), code, T, k, H, ldd, ldy, r, w, dy.data_ptr(),
-                                          lddy, d, _stream_of(y)), "mxq_moe_combine_backward")
-    return dy, dweights
-
-
-def _param(t, name, cols):
-    """(address, dtype code) of a weight or shift [cols]."""
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be bfloat16 or float32")
-    return _dense(t, name, t.dtype, cols), code
+    return _calls().moe_combine_backward(dout, y, rows, weights, out)
 
 
 def layer_norm(x: torch.Tensor, weight=None, shift=None, eps: float = 1e-5, out=None):
     """Layer norm of every row of x [M, C] (see mxq_layer_norm); weight and shift [C],
     bf16 or fp32 (both alike), optional.  Returns (y [M, C], mean fp32 [M], rstd fp32
     [M]); `out` may supply the three (y may be x; None for a new tensor)."""
-    code, M, C, ld = _matrix(x, "x")
-    w, wcode = (None, None) if weight is None else _param(weight, "weight", C)
-    s, scode = (None, wcode) if shift is None else _param(shift, "shift", C)
-    if wcode is not None and scode != wcode:
-        raise ValueError("weight and shift must have the same dtype")
-    y, mean, rstd = (None, None, None) if out is None else out
-    y, ldy = _result(y, "y", x, code, M, C)
-    if mean is None or rstd is None:
-        mean, rstd = x.new_empty(M, dtype=torch.float32), x.new_empty(M, dtype=torch.float32)
-        m, r = mean.data_ptr(), rstd.data_ptr()
-    else:
-        m = _dense(mean, "mean", torch.float32, M)
-        r = _dense(rstd, "rstd", torch.float32, M)
-    _check(_calls().layer_norm(x.data_ptr(), code, M, C, ld, w, s, scode or 0, eps, y.data_ptr(), ldy, m, r,
-                                _stream_of(x)), "mxq_layer_norm")
-    return y, mean, rstd
+    return _calls().layer_norm(x, weight, shift, eps, out)
 
 
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight, mean: torch.Tensor, rstd: torch.Tensor, out=None):
     """Gradients of layer_norm (see mxq_layer_norm_backward): returns (dx [M, C],
     dweight fp32 [C], dshift fp32 [C]); `out` may supply dx (which may be dy)."""
-    code, M, C, ldx = _matrix(x, "x")
-    c, m, n, ldg = _matrix(dy, "dy")
-    if c != code or m != M or n != C:
-        raise ValueError(f"dy must be {str(x.dtype)[6:]} {[M, C]}")
-    w, wcode = (None, 0) if weight is None else _param(weight, "weight", C)
-    mu = _dense(mean, "mean", torch.float32, M)
-    r = _dense(rstd, "rstd", torch.float32, M)
-    dx, lddx = _result(out, "out", x, code, M, C)
-    dweight, dshift = x.new_empty(C, dtype=torch.float32), x.new_empty(C, dtype=torch.float32)
-    size = _calls().layer_norm_backward_workspace_size(M, C)
-    workspace = x.new_empty(size, dtype=torch.uint8)
-    _check(_calls().layer_norm_backward(dy.data_ptr(), x.data_ptr(), code, M, C, ldg, ldx, w, wcode, mu, r, dx.data_ptr(),
-                                     lddx, dweight.data_ptr(), dshift.data_ptr(), workspace.data_ptr(), size,
-                                     _stream_of(x)), "mxq_layer_norm_backward")
-    return dx, dweight, dshift
+    return _calls().layer_norm_backward(dy, x, weight, mean, rstd, out)
 
 
 class GradDesc(ctypes.Structure):
@@ -744,30 +595,17 @@ class GradDesc(ctypes.Structure):
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int)]
 
 
-def _grad_descs(grads, outs):
-    """The mxq_grad_desc array of two lists of tensors, as bytes."""
+def _list_of(grads):
+    grads = list(grads)
     if len(grads) > MAX_GRADS:
         raise ValueError(f"at most {MAX_GRADS} gradients")
-    return _calls().grad_descs(grads, outs, torch.bfloat16, torch.float32)
-
-
-def _norm_buffers(grads):
-    """(norm, workspace, its bytes)."""
-    size = _calls().grad_norm_workspace_size(len(grads))
-    device = grads[0].device if grads else torch.device("cuda")
-    return (torch.empty((), dtype=torch.float32, device=device), torch.empty(size, dtype=torch.uint8, device=device),
-            size)
+    return grads
 
 
 def grad_norm(grads) -> torch.Tensor:
     """The 2-norm over all of a list of gradients (bf16 and fp32 mixed), an fp32
     scalar on the device (see mxq_grad_norm)."""
-    grads = list(grads)
-    descs = _grad_descs(grads, grads)
-    norm, workspace, size = _norm_buffers(grads)
-    _check(_calls().grad_norm(descs, len(grads), norm.data_ptr(), workspace.data_ptr(), size, _stream_of(norm)),
-           "mxq_grad_norm")
-    return norm
+    return _calls().grad_norm(_list_of(grads))
 
 
 def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None):
@@ -775,13 +613,7 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None):
     of them (see mxq_clip_grad_norm).  out: a list of tensors like the gradients, the
     gradients themselves to scale in place, or None for new ones.  Returns (norm fp32
     scalar on the device, the list of outputs)."""
-    grads = list(grads)
-    out = [torch.empty_like(g) for g in grads] if out is None else list(out)
-    descs = _grad_descs(grads, out)
-    norm, workspace, size = _norm_buffers(grads)
-    _check(_calls().clip_grad_norm(descs, len(grads), max_norm, eps, norm.data_ptr(), workspace.data_ptr(), size,
-                                    _stream_of(norm)), "mxq_clip_grad_norm")
-    return norm, out
+    return _calls().clip_grad_norm(_list_of(grads), max_norm, eps, None if out is None else list(out))
 
 
 def get_device_status() -> int:

@@ -105,3 +105,22 @@ def test_clip_argument_errors(L):
     assert call("clip", grads=((0x10000, None, 8, 0), (0x30000, 0x40000, 8, 1))) == 1
     for args in ((-1.0, 1e-6), (NAN, 1e-6), (1.0, -1.0), (1.0, NAN), (1.0, INF)):
         assert call("clip", args=args) == 1
+
+
+def test_python_calls_refuse_what_is_no_cuda_tensor(L):
+    """The extension module checks its tensors before it allocates or calls anything."""
+    import torch
+    from mxfp8_microscaled_precision_gb300 import mxq
+    x, ids = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    for call in (lambda: mxq.route(x, 2), lambda: mxq.route(x, 2, score="relu"), lambda: mxq.route(x, 2, group_score="mean"),
+                 lambda: mxq.route_backward(x, x, ids), lambda: mxq.moe_plan(ids, 4), lambda: mxq.moe_plan(ids[0], 4),
+                 lambda: mxq.moe_dispatch(x, ids), lambda: mxq.moe_combine(x, ids), lambda: mxq.layer_norm(x),
+                 lambda: mxq.moe_combine_backward(x, x, ids, x), lambda: mxq.layer_norm_backward(x, x, None, x[0], x[0]),
+                 lambda: mxq.grad_norm([x]), lambda: mxq.clip_grad_norm([x], 1.0), lambda: mxq.clip_grad_norm([x], 1.0, out=[]),
+                 lambda: mxq.grad_norm([x] * (mxq.MAX_GRADS + 1))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: mxq.route(None, 2), lambda: mxq.moe_plan([[1, 2]], 4), lambda: mxq.layer_norm("x"),
+                 lambda: mxq.grad_norm([None]), lambda: mxq.clip_grad_norm([3], 1.0)):
+        with pytest.raises(TypeError):
+            call()
