@@ -12,7 +12,7 @@
 // a clock and SM.)  The scaling blocks take the chunks backwards: what the other pass read last
 // still lies in the L2.  Bound by memory: one read for the norm, one read and one write.
 // Measured: 36 gradients of 671 MB: the norm 101 us (98% of a copy's 6787 GB/s), scaled too 323 us
-// (3 x 671 MB: 92%); 300 ragged ones of 56 MB 16 us and 31 us; 6 of 2.6 MB 6 us and 9 us.
+// (3 x 671 MB: 92%); 300 ragged ones of 56 MB 16 us and 31 us; 6 of 2.6 MB 5.5 us and 8.2 us.
 
 #include <cuda_runtime.h>
 
@@ -139,6 +139,7 @@ __device__ __forceinline__ float norm_of(const float* partial, int parts, float*
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const float* partial, int parts, float* norm) {
     __shared__ float sh[kThreads / 32];
+    wait_for_previous();
     const float n = norm_of(partial, parts, sh);
     if (threadIdx.x == 0) *norm = n;
 }
@@ -174,6 +175,7 @@ template <int kTable>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<kTable> t, const float* partial,
                                                          int parts, float max_norm, float eps, float* norm) {
     __shared__ float sh[kThreads / 32];
+    wait_for_previous();
     const float n = norm_of(partial, parts, sh);
     if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
     float c = max_norm / (n + eps);
@@ -223,15 +225,16 @@ cudaError_t clip_launch(const ClipTensor* tensors, int count, int chunk_bytes, b
         parts += kClipBlocks;
     }
     if (!scale_too) {
-        norm_kernel<<<1, kThreads, 0, stream>>>(partial, parts, norm);
-        return cudaGetLastError();
+        return launch_behind(norm_kernel, 1, kThreads, stream, partial, parts, norm);
     }
     bool first = true;
     for (int at = 0; at < count || first; first = false) {
         at = whole ? count : fill(&t, tensors, count, at, chunk_bytes);
-        scale_kernel<kTable><<<kClipBlocks, kThreads, 0, stream>>>(t, partial, parts, max_norm, eps, first ? norm : nullptr);
+        const cudaError_t e = launch_behind(scale_kernel<kTable>, kClipBlocks, kThreads, stream, t, partial, parts,
+                                            max_norm, eps, first ? norm : nullptr);
+        if (e != cudaSuccess) return e;
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace

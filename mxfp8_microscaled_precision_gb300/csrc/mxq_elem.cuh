@@ -335,6 +335,10 @@ struct ParamSlots {
     }
 };
 
+// In a kernel launched by launch_behind: returns when the kernel before it has ended and its
+// results are visible.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Sum over the warp, the same order on every call, the result in all lanes.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

@@ -724,6 +724,7 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* partial,
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     int i = blockIdx.x * 32 + lane;
     float s = 0.0f;
+    wait_for_previous();
     if (i < 2 * cols) {
 #pragma unroll 5
         for (int p = y; p < parts; p += 32) s += partial[static_cast<int64_t>(p) * 2 * cols + i];
@@ -886,9 +887,8 @@ cudaError_t norm_backward_launch(const NormBackwardArgs& a, cudaStream_t stream)
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || (a.dweight == nullptr && a.dshift == nullptr)) return e;
-    norm_reduce_kernel<<<static_cast<unsigned>((2 * a.cols + 31) / 32), 1024, 0, stream>>>(
-        a.partial, static_cast<int>(parts), static_cast<int>(a.cols), a.dweight, a.dshift);
-    return cudaGetLastError();
+    return launch_behind(norm_reduce_kernel, static_cast<unsigned>((2 * a.cols + 31) / 32), 1024, stream, a.partial,
+                         static_cast<int>(parts), static_cast<int>(a.cols), a.dweight, a.dshift);
 }
 
 // f(T, W) of the tensors' and the parameters' types.
