@@ -13,8 +13,8 @@
 //
 // Bound by memory for long rows and many.  Measured, of the 6787 GB/s a copy reaches:
 // forward 16384 x 7168 BF16 79 us (87%), 16384 x 4096 45 us (87%), 32767 x 1000 FP32 41 us
-// (94%), 8 x 4096 2.3 us; backward 134 us (78%), 72 us (82%), 81 us (71%).  Rows off the
-// 16-byte grid: 8191 x 4097 BF16 forward 48 us (41%), backward 73 us (41%).
+// (94%), 8 x 4096 2.3 us; backward 129 us (80%), 71 us (84%), 73 us (80%).  Rows off the
+// 16-byte grid: 8191 x 4097 BF16 forward 48 us (41%), backward 72 us (41%).
 //
 // kAny: rows that start at any element (mxq_elem.cuh), in vectors of x's rows.  dy and the
 // result mostly start like x, as rows of the same length in buffers of their own do; where
@@ -301,17 +301,36 @@ __device__ __forceinline__ void dx_vector(const f32x2 (&h)[H], f32x2 (&u)[H], f3
     for (int c = 0; c < H; ++c) u[c] = fma2(u[c], rr, fma2(h[c], c2, c1));
 }
 
-// One thread's column sums of one vector into (or onto) those of the block.
-template <int H>
-__device__ __forceinline__ void put_columns(float* sums, int i, int cols, bool add, const f32x2 (&dw)[H],
-                                            const f32x2 (&db)[H]) {
+// The column sums of a block: each group of tpr threads leaves its own in shared memory
+// ([group][dw, db][kN tpr V], where element e of a row lies at e + lead), and after a
+// barrier the block's threads add up the groups' in their order and write them out side by side.  (One group
+// after the other onto the same sums took a barrier and 32 dependent additions each: 8191 x 513 32 us, so 23;
+// 32767 x 1000 FP32 80 us, so 73; straight to the workspace from one group 2047 x 16384 68 us, so 61.)
+template <int kN, int H>
+__device__ __forceinline__ void leave_columns(float* meet, int group, int tpr, int at, const f32x2 (&dw)[kN][H],
+                                              const f32x2 (&db)[kN][H]) {
+    const int all = kN * tpr * 2 * H;
+    float* mine = meet + group * 2 * all;
 #pragma unroll
-    for (int c = 0; c < 2 * H; ++c) {
-        if (i + c < 0 || i + c >= cols) continue;
-        const float fw = c & 1 ? hi_of(dw[c / 2]) : lo_of(dw[c / 2]);
-        const float fb = c & 1 ? hi_of(db[c / 2]) : lo_of(db[c / 2]);
-        sums[i + c] = (add ? sums[i + c] : 0.0f) + fw;
-        sums[cols + i + c] = (add ? sums[cols + i + c] : 0.0f) + fb;
+    for (int n = 0; n < kN; ++n) {
+#pragma unroll
+        for (int c = 0; c < H; c += 2) {
+            const int place = (n * tpr + at) * 2 * H + 2 * c;
+            *reinterpret_cast<ulonglong2*>(mine + place) = make_ulonglong2(dw[n][c], dw[n][c + 1]);
+            *reinterpret_cast<ulonglong2*>(mine + all + place) = make_ulonglong2(db[n][c], db[n][c + 1]);
+        }
+    }
+}
+
+// lead(group): of the group's rows.
+template <typename F>
+__device__ __forceinline__ void add_columns(const float* meet, int groups, int all, int cols, float* part, F lead) {
+    for (int i = threadIdx.x; i < 2 * cols; i += blockDim.x) {
+        const bool second = i >= cols;
+        const float* of = meet + (second ? all - cols : 0) + i;
+        float s = 0.0f;
+        for (int g = 0; g < groups; ++g) s += of[g * 2 * all + lead(g)];
+        part[i] = s;
     }
 }
 
@@ -322,10 +341,11 @@ constexpr int kShortThreads = 256;
 template <typename T, typename W, int kN, bool kAny>
 __global__ void __launch_bounds__(kShortThreads, 2) norm_backward_short_kernel(const NormBackwardArgs a, int tpr) {
     constexpr int V = kVec16<T>, H = V / 2, S = sizeof(T);
-    extern __shared__ float cols_sh[];   // [2][cols]: column sums of the block
+    extern __shared__ __align__(16) float cols_sh[];
+    __shared__ int leads[kShortThreads / 4];   // of the groups' rows
     const int shift = 31 - __clz(tpr);   // tpr is a power of two
     const int groups = kShortThreads >> shift;
-    const int group = threadIdx.x >> shift, at = threadIdx.x & (tpr - 1), lane = threadIdx.x & 31;
+    const int group = threadIdx.x >> shift, at = threadIdx.x & (tpr - 1);
     const int64_t row_first = static_cast<int64_t>(blockIdx.x) * groups + group;
     const int all = static_cast<int>(a.cols);
     const int first = at * V - (kAny ? lead_of<S>(static_cast<const T*>(a.x) + row_first * a.ldx) : 0);
@@ -370,30 +390,11 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_backward_short_kernel(c
             store16<S, kAny>(dx, first + n * tpr * V, cols, pack2<T>(u[n]), !kAny || lead_of<S>(dx) == lead_of<S>(x));
         }
     }
-    // The groups' sums one after the other; those of a warp, which start alike on the grid, meet by shuffles.
-    const int turns = kAny ? groups : kShortThreads / 32;
-    const int turn = kAny ? group : static_cast<int>(threadIdx.x >> 5);
-    if (!kAny) {
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-#pragma unroll
-            for (int c = 0; c < H; ++c) {
-                for (int d = tpr; d < 32; d <<= 1) {
-                    dw[n][c] = add2(dw[n][c], __shfl_xor_sync(0xFFFFFFFFu, dw[n][c], d));
-                    db[n][c] = add2(db[n][c], __shfl_xor_sync(0xFFFFFFFFu, db[n][c], d));
-                }
-            }
-        }
-    }
-    for (int i = 0; i < turns; ++i) {
-        if (turn == i && (kAny || lane < tpr)) {
-#pragma unroll
-            for (int n = 0; n < kN; ++n) put_columns<H>(cols_sh, first + n * tpr * V, all, i > 0, dw[n], db[n]);
-        }
-        __syncthreads();
-    }
-    float* part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * all;
-    for (int i = threadIdx.x; i < 2 * all; i += kShortThreads) part[i] = cols_sh[i];
+    leave_columns<kN, H>(cols_sh, group, tpr, at, dw, db);
+    if (kAny && at == 0) leads[group] = -first;
+    __syncthreads();
+    add_columns(cols_sh, groups, kN * tpr * V, all, a.partial + static_cast<int64_t>(blockIdx.x) * 2 * all,
+                [&](int g) { return kAny ? leads[g] : 0; });
 }
 
 // ---- a ring of rows in shared memory (longer rows) ---------------------------------------
@@ -552,7 +553,7 @@ __device__ __forceinline__ void group_barrier(int group, int tpr) {
 // at 16384 x 7168; figures below are for that size).  Twice the threads with half the registers spill and are slower
 // (211 us), as are 8 elements a thread (194 us) and the sums of the next row before the results of this
 // one (170 us: two rows' values leave the scheduler no registers); a warp of its own for the
-// copies changes nothing.  Without any loads and stores 118 us of 138 remain.
+// copies changes nothing.  Without any loads and stores 118 us of 138 remained.
 // The weights wait in shared memory: in registers they took 146 us, and from the L1, of which the ring
 // leaves little, 206 us (FP32).
 template <typename T, typename W, int kN, bool kAny, int kThreads>
@@ -659,19 +660,11 @@ norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
         place.move(groups, stages);
         odd ^= 1;
     }
-    // The groups' column sums one after the other, in the ring (all rows have been read).
     float* part = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * cols;
-    float* meet = groups == 1 ? part : reinterpret_cast<float*>(buf);
-    for (int g = 0; g < groups; ++g) {
-        if (groups > 1) named_bar_sync(15, groups * tpr);
-        if (g != group) continue;
-#pragma unroll
-        for (int n = 0; n < kN; ++n) put_columns<H>(meet, first + n * tpr * V, cols, g > 0, dw[n], db[n]);
-    }
-    if (groups > 1) {
-        named_bar_sync(15, groups * tpr);
-        for (int i = threadIdx.x; i < 2 * cols; i += groups * tpr) part[i] = meet[i];
-    }
+    named_bar_sync(15, groups * tpr);   // in the ring, when all rows have been read
+    leave_columns<kN, H>(reinterpret_cast<float*>(buf), group, tpr, at, dw, db);
+    named_bar_sync(15, groups * tpr);
+    add_columns(reinterpret_cast<const float*>(buf), groups, kN * tpr * V, cols, part, [&](int) { return lead_x; });
     if (stop && at == 0) ring.drain(place, groups, guard);   // the group gave up
 }
 
@@ -839,7 +832,10 @@ cudaError_t backward_ring(const NormBackwardArgs& a, int64_t vectors, int64_t gr
         if (groups > rows) groups = rows;
         if (groups < 1) groups = 1;
         stages -= stages % groups;
-        const int smem = static_cast<int>(weights + stages * stage);
+        int64_t bytes = weights + stages * stage;
+        const int64_t meet = groups * 2 * kN * tpr * V * static_cast<int64_t>(sizeof(float));   // at most 128 KB
+        if (bytes < meet) bytes = meet;
+        const int smem = static_cast<int>(bytes);
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         kernel<<<static_cast<unsigned>(grid), static_cast<unsigned>(tpr * groups), smem, stream>>>(
@@ -870,9 +866,13 @@ cudaError_t norm_backward_launch(const NormBackwardArgs& a, cudaStream_t stream)
             const int64_t per = kShortThreads / tpr;
             if (parts > (a.rows + per - 1) / per) parts = (a.rows + per - 1) / per;
             if (count.value * V > 8 && parts > 2 * kSMs) parts = 2 * kSMs;   // what the registers leave room for
-            const size_t smem = static_cast<size_t>(2 * a.cols) * sizeof(float);
-            norm_backward_short_kernel<T, W, count.value, kAny>
-                <<<static_cast<unsigned>(parts), kShortThreads, smem, stream>>>(a, tpr);
+            const int smem = 2 * count.value * kShortThreads * V * static_cast<int>(sizeof(float));   // at most 48 KB
+            auto kernel = norm_backward_short_kernel<T, W, count.value, kAny>;
+            if (smem > 40 * 1024) {
+                const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                if (err != cudaSuccess) return err;
+            }
+            kernel<<<static_cast<unsigned>(parts), kShortThreads, smem, stream>>>(a, tpr);
             return cudaGetLastError();
         };
         e = n <= 1 ? go(std::integral_constant<int, 1>{}) : n <= 2 ? go(std::integral_constant<int, 2>{})
