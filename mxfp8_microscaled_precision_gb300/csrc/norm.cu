@@ -797,9 +797,11 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t stream) {
                 if (groups > rows) groups = rows;
                 const unsigned threads = static_cast<unsigned>((groups * tpr + 31) / 32 * 32);
                 auto kernel = norm_held_kernel<T, W, kN, kAny>;
-                const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                           static_cast<int>(held));
-                if (e != cudaSuccess) return e;
+                if (held > 40 * 1024) {   // beside the kernel's own 4 KB more than a launch has unasked
+                    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                               static_cast<int>(held));
+                    if (e != cudaSuccess) return e;
+                }
                 kernel<<<static_cast<unsigned>(grid), threads, held, stream>>>(a, tpr);
                 return cudaGetLastError();
             }

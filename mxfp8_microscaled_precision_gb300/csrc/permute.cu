@@ -11,8 +11,8 @@
 //
 // The row kernels are bound by memory, which they move once.  Measured, of the 6787 GB/s a
 // copy reaches: 16384 tokens x 8 slots of 4096 BF16: dispatch 181 us (98%), combine 181 us
-// (98%), its backward pass 361 us (93%); 8191 x 4 of 4097 BF16, off the 16-byte grid: 66 us
-// (75%), 82 us (61%), 122 us (73%), where elements one by one took 148, 164 and 206 us.
+// (98%), its backward pass 361 us (93%); 8191 x 4 of 4097 BF16, off the 16-byte grid: 59 us
+// (84%), 74 us (67%), 122 us (73%), where elements one by one took 148, 164 and 206 us.
 
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -158,7 +158,7 @@ __device__ __forceinline__ Place place_of(int entry, int64_t slots) {
 
 // a[rows[t, j]] = x[t], zeros for a dropped slot.  Token blockIdx.x; 16 bytes of
 // the row per thread, blockIdx.y over the row: x is read once, whatever k.  With kAny
-// the vectors are those of the row that is written.
+// the vectors are those of the row that is written, shifted out of x's.
 template <int kSize, bool kAny>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const unsigned char* x, int64_t ldx, unsigned char* a,
                                                             int64_t lda, int H, const int32_t* rows, int k) {
@@ -178,15 +178,26 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const unsigned ch
         }
     } else {
         if (at >= H + V) return;
-#pragma unroll 2
+        // The three blocks of x's row that the vectors of any lead lie in, loaded once (two for every row of a: 66 us
+        // instead of 59); what is outside the row is never stored.
+        const int lead = lead_of<kSize>(from);
+        const bool between = is_between<kSize>(t, gridDim.x, H);
+        uint4 part[3];
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+            const int i = at - lead + (c - 1) * V;
+            part[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < H && i + V > 0) part[c] = load16<kSize, true>(from, i, H, between);
+        }
         for (int j = 0; j < k; ++j) {
             const Place p = place_of(r[j], slots);
             if (!p.exists) continue;
             unsigned char* to = a + p.row * lda * kSize;
-            const int i = at - lead_of<kSize>(to);
+            const int lead_to = lead_of<kSize>(to);
+            const unsigned off = static_cast<unsigned>((V + lead - lead_to) * kSize);   // 1 to 2 V - 1 elements
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (p.kept) v = is_inner<kSize>(i, H) ? load_inner<kSize>(from, i) : load_ends<kSize>(from, i, H);
-            store16<kSize, true>(to, i, H, v);
+            if (p.kept) v = off < 16 ? shift16(part[0], part[1], off) : shift16(part[1], part[2], off - 16);
+            store16<kSize, true>(to, at - lead_to, H, v);
         }
     }
 }
