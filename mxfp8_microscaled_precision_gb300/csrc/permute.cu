@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const T* dou
         for (int c = 0; c < V / 2; ++c) g[c] = mul2(g[c], ww);
         store16<S, kAny>(to, i, H, pack2<T>(g));
     };
+    const bool alike = kAny && lead_of<S>(from) == lead_of<S>(to);   // as rows of the same length in buffers of their own do
     int i = first;
     if constexpr (!kAny) {   // two vectors of each row in flight
         for (; i + 32 * V < H; i += 64 * V) {
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const T* dou
     }
     for (; i < H; i += 32 * V) {
         if constexpr (!kAny) step(i, load16<S, false>(d, i, H), load16<S, false>(from, i, H));
-        else if (is_inner<S>(i, H)) step(i, load_inner<S>(d, i), load_inner<S>(from, i));
+        else if (is_inner<S>(i, H)) step(i, load_inner<S>(d, i), alike ? *reinterpret_cast<const uint4*>(from + i) : load_inner<S>(from, i));
         else step(i, load_ends<S>(d, i, H), load_ends<S>(from, i, H));
     }
     const float total = warp_sum(lo_of(dot) + hi_of(dot));
