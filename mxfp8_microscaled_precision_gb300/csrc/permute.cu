@@ -12,7 +12,7 @@
 // The row kernels are bound by memory, which they move once.  Measured, of the 6787 GB/s a
 // copy reaches: 16384 tokens x 8 slots of 4096 BF16: dispatch 181 us (98%), combine 181 us
 // (98%), its backward pass 361 us (93%); 8191 x 4 of 4097 BF16, off the 16-byte grid: 59 us
-// (84%), 74 us (67%), 122 us (73%), where elements one by one took 148, 164 and 206 us.
+// (84%), 74 us (67%), 107 us (83%), where elements one by one took 148, 164 and 206 us.
 
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -285,7 +285,9 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const T* dou
         for (int c = 0; c < V / 2; ++c) g[c] = mul2(g[c], ww);
         store16<S, kAny>(to, i, H, pack2<T>(g));
     };
-    const bool alike = kAny && lead_of<S>(from) == lead_of<S>(to);   // as rows of the same length in buffers of their own do
+    // Rows of the same length in buffers of their own start alike: no shift of y's then (8191 x 4 rows of 4097: 107 us,
+    // shifting both 122; two vectors in flight, as on the grid, 120).
+    const bool alike = kAny && lead_of<S>(from) == lead_of<S>(to);
     int i = first;
     if constexpr (!kAny) {   // two vectors of each row in flight
         for (; i + 32 * V < H; i += 64 * V) {
@@ -297,7 +299,8 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const T* dou
     }
     for (; i < H; i += 32 * V) {
         if constexpr (!kAny) step(i, load16<S, false>(d, i, H), load16<S, false>(from, i, H));
-        else if (is_inner<S>(i, H)) step(i, load_inner<S>(d, i), alike ? *reinterpret_cast<const uint4*>(from + i) : load_inner<S>(from, i));
+        else if (is_inner<S>(i, H))
+            step(i, load_inner<S>(d, i), alike ? *reinterpret_cast<const uint4*>(from + i) : load_inner<S>(from, i));
         else step(i, load_ends<S>(d, i, H), load_ends<S>(from, i, H));
     }
     const float total = warp_sum(lo_of(dot) + hi_of(dot));
