@@ -11,7 +11,7 @@
 //
 // The row kernels are bound by memory, which they move once.  Measured, of the 6787 GB/s a
 // copy reaches: 16384 tokens x 8 slots of 4096 BF16: dispatch 181 us (98%), combine 181 us
-// (98%), its backward pass 361 us (93%); 8191 x 4 of 4097 BF16, off the 16-byte grid: 59 us
+// (98%), its backward pass 331 us (the copy's rate); 8191 x 4 of 4097 BF16, off the 16-byte grid: 59 us
 // (84%), 74 us (67%), 107 us (83%), where elements one by one took 148, 164 and 206 us.
 
 #include <cooperative_groups.h>
@@ -156,17 +156,19 @@ __device__ __forceinline__ Place place_of(int entry, int64_t slots) {
     return {row, kept, row < slots};
 }
 
-// a[rows[t, j]] = x[t], zeros for a dropped slot.  Token blockIdx.x; 16 bytes of
+// a[rows[t, j]] = x[t], zeros for a dropped slot.  Threads of one threadIdx.y have a token; 16 bytes of
 // the row per thread, blockIdx.y over the row: x is read once, whatever k.  With kAny
 // the vectors are those of the row that is written, shifted out of x's.
 template <int kSize, bool kAny>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const unsigned char* x, int64_t ldx, unsigned char* a,
-                                                            int64_t lda, int H, const int32_t* rows, int k) {
+                                                            int64_t lda, int H, const int32_t* rows, int64_t tokens,
+                                                            int k) {
     constexpr int V = 16 / kSize;
-    const int64_t t = blockIdx.x;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (t >= tokens) return;
     const int at = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     const int32_t* r = rows + t * k;
-    const int64_t slots = static_cast<int64_t>(gridDim.x) * k;
+    const int64_t slots = tokens * k;
     const unsigned char* from = x + t * ldx * kSize;
     if constexpr (!kAny) {
         if (at >= H) return;
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const unsigned ch
         // The three blocks of x's row that the vectors of any lead lie in, loaded once (two for every row of a: 66 us
         // instead of 59); what is outside the row is never stored.
         const int lead = lead_of<kSize>(from);
-        const bool between = is_between<kSize>(t, gridDim.x, H);
+        const bool between = is_between<kSize>(t, tokens, H);
         uint4 part[3];
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
@@ -206,15 +208,17 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const unsigned ch
 // the order of j and rounded once.  With kAny the vectors are those of out's row.
 template <typename T, bool kAny>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* y, int64_t ldy, const int32_t* rows,
-                                                           const float* weights, int k, T* out, int64_t ldo, int H) {
+                                                           const float* weights, int64_t tokens, int k, T* out,
+                                                           int64_t ldo, int H) {
     constexpr int V = kVec16<T>, S = sizeof(T);
-    const int64_t t = blockIdx.x;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (t >= tokens) return;
     const int at = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     T* to = out + t * ldo;
     const int i = kAny ? at - lead_of<S>(to) : at;
     if (i >= H) return;
     const int32_t* r = rows + t * k;
-    const int64_t slots = static_cast<int64_t>(gridDim.x) * k;
+    const int64_t slots = tokens * k;
     f32x2 acc[V / 2] = {};
     // kB rows' loads in flight at a time: 4 on the grid (16384 tokens x 8 rows of 4096 BF16: 180 us, one at a
     // time 203), one off it, where a load is two already (8191 x 4 rows of 4097: 74 us, with 2 82, with 4 124).
@@ -251,60 +255,64 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const T* y, int64_
     store16<S, kAny>(to, i, H, pack2<T>(acc));
 }
 
-// dy[rows[t, j]] = w_j dout[t], dw_j = <dout[t], y[rows[t, j]]>: one warp per slot.
+// dy[rows[t, j]] = w_j dout[t], dw_j = <dout[t], y[rows[t, j]]>: one warp per slot, or 1 << shift lanes of it
+// for rows of up to 16 vectors (kShort; 16384 tokens x 7 rows of 120 BF16: 20 us, a warp each 28).
 // With kAny the vectors are those of dy's row.
-template <typename T, bool kAny>
+template <typename T, bool kAny, bool kShort>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const T* dout, int64_t ldd, const T* y, int64_t ldy,
                                                                     const int32_t* rows, const float* weights, int k,
-                                                                    int64_t slots, T* dy, int64_t lddy,
+                                                                    int64_t slots, int shift, T* dy, int64_t lddy,
                                                                     float* dweights, int H) {
     constexpr int V = kVec16<T>, S = sizeof(T);
-    const int64_t s = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (s >= slots) return;
-    const Place p = place_of(rows[s], slots);
+    if (!kShort) shift = 5;
+    const int64_t s = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> shift;
+    const int lanes = 1 << shift, lane = threadIdx.x & (lanes - 1), step_by = lanes * V;
+    const Place p = s < slots ? place_of(rows[s], slots) : Place{0, false, false};
     T* to = dy + (p.exists ? p.row : 0) * lddy;
     const int first = lane * V - (kAny ? lead_of<S>(to) : 0);
-    if (!p.kept || !p.exists) {
-        for (int i = first; p.exists && i < H; i += 32 * V) store16<S, kAny>(to, i, H, make_uint4(0u, 0u, 0u, 0u));
-        if (lane == 0) dweights[s] = 0.0f;
-        return;
-    }
-    const T* d = dout + (s / k) * ldd;
-    const T* from = y + p.row * ldy;
-    const float w = weights[s];
-    const f32x2 ww = pair(w, w);
     f32x2 dot = 0;
-    auto step = [&](int i, const uint4 vg, const uint4 vf) {
-        f32x2 g[V / 2], f[V / 2];
-        unpack2<T>(vg, g);
-        unpack2<T>(vf, f);
+    if (!p.kept || !p.exists) {
+        for (int i = first; p.exists && i < H; i += step_by) store16<S, kAny>(to, i, H, make_uint4(0u, 0u, 0u, 0u));
+    } else {
+        const T* d = dout + (s / k) * ldd;
+        const T* from = y + p.row * ldy;
+        const float w = weights[s];
+        const f32x2 ww = pair(w, w);
+        auto step = [&](int i, const uint4 vg, const uint4 vf) {
+            f32x2 g[V / 2], f[V / 2];
+            unpack2<T>(vg, g);
+            unpack2<T>(vf, f);
 #pragma unroll
-        for (int c = 0; c < V / 2; ++c) dot = fma2(g[c], f[c], dot);
+            for (int c = 0; c < V / 2; ++c) dot = fma2(g[c], f[c], dot);
 #pragma unroll
-        for (int c = 0; c < V / 2; ++c) g[c] = mul2(g[c], ww);
-        store16<S, kAny>(to, i, H, pack2<T>(g));
-    };
-    // Rows of the same length in buffers of their own start alike: no shift of y's then (8191 x 4 rows of 4097: 107 us,
-    // shifting both 122; two vectors in flight, as on the grid, 120).
-    const bool alike = kAny && lead_of<S>(from) == lead_of<S>(to);
-    int i = first;
-    if constexpr (!kAny) {   // two vectors of each row in flight
-        for (; i + 32 * V < H; i += 64 * V) {
-            const uint4 g0 = load16<S, false>(d, i, H), f0 = load16<S, false>(from, i, H);
-            const uint4 g1 = load16<S, false>(d, i + 32 * V, H), f1 = load16<S, false>(from, i + 32 * V, H);
-            step(i, g0, f0);
-            step(i + 32 * V, g1, f1);
+            for (int c = 0; c < V / 2; ++c) g[c] = mul2(g[c], ww);
+            store16<S, kAny>(to, i, H, pack2<T>(g));
+        };
+        // Rows of the same length in buffers of their own start alike: no shift of y's then (8191 x 4 rows of 4097: 107 us,
+        // shifting both 122; two vectors in flight, as on the grid, 120).
+        const bool alike = kAny && lead_of<S>(from) == lead_of<S>(to);
+        int i = first;
+        if constexpr (!kAny) {   // two vectors of each row in flight; more, as unrolled loops have them, are slower
+                                 // (16384 tokens x 8 rows of 4096: 331 us, unrolled 361)
+#pragma unroll 1
+            for (; i + step_by < H; i += 2 * step_by) {
+                const uint4 g0 = load16<S, false>(d, i, H), f0 = load16<S, false>(from, i, H);
+                const uint4 g1 = load16<S, false>(d, i + step_by, H), f1 = load16<S, false>(from, i + step_by, H);
+                step(i, g0, f0);
+                step(i + step_by, g1, f1);
+            }
+        }
+#pragma unroll 1
+        for (; i < H; i += step_by) {
+            if constexpr (!kAny) step(i, load16<S, false>(d, i, H), load16<S, false>(from, i, H));
+            else if (is_inner<S>(i, H))
+                step(i, load_inner<S>(d, i), alike ? *reinterpret_cast<const uint4*>(from + i) : load_inner<S>(from, i));
+            else step(i, load_ends<S>(d, i, H), load_ends<S>(from, i, H));
         }
     }
-    for (; i < H; i += 32 * V) {
-        if constexpr (!kAny) step(i, load16<S, false>(d, i, H), load16<S, false>(from, i, H));
-        else if (is_inner<S>(i, H))
-            step(i, load_inner<S>(d, i), alike ? *reinterpret_cast<const uint4*>(from + i) : load_inner<S>(from, i));
-        else step(i, load_ends<S>(d, i, H), load_ends<S>(from, i, H));
-    }
-    const float total = warp_sum(lo_of(dot) + hi_of(dot));
-    if (lane == 0) dweights[s] = total;
+    float total = lo_of(dot) + hi_of(dot);
+    for (int half = lanes >> 1; half > 0; half >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, half);
+    if (lane == 0 && s < slots) dweights[s] = total;   // 0 for a dropped slot
 }
 
 // Whether every row lies on the 16-byte grid in whole vectors.
@@ -319,20 +327,26 @@ bool on_grid(int64_t H, size_t size, std::initializer_list<const void*> ptrs,
 }
 
 // One block per token and per part of its row of 256 vectors; a rest of less than 64
-// vectors joins the parts before it (4097 BF16: two parts of 288 threads).  kAny: a row
-// off the grid lies in one vector more.
+// vectors joins the parts before it (4097 BF16: two parts of 288 threads).  Rows of up to 32 vectors share a
+// block of 256 threads, a power of two of them each (16384 tokens x 7 rows of 120 BF16 dispatched: 6.5 us, a warp
+// and block each 10.1).  kAny: a row off the grid lies in one vector more.
 struct RowGrid {
-    dim3 grid;
-    unsigned threads;
+    dim3 grid, threads;
 };
 RowGrid row_grid(int64_t tokens, int64_t H, int64_t size, bool any) {
     const int64_t vectors = (H * size + 15) / 16 + (any ? 1 : 0);
+    if (vectors <= 32) {
+        unsigned threads = 1;
+        while (threads < vectors) threads *= 2;
+        const unsigned together = 256 / threads;
+        return {dim3(static_cast<unsigned>((tokens + together - 1) / together)), dim3(threads, together)};
+    }
     int64_t parts = (vectors + 191) / 256;
     if (parts < 1) parts = 1;
     int64_t threads = ((vectors + parts - 1) / parts + 31) / 32 * 32;
     if (parts > 1 && threads < 256) threads = 256;
     return {dim3(static_cast<unsigned>(tokens), static_cast<unsigned>((vectors + threads - 1) / threads)),
-            static_cast<unsigned>(threads)};
+            dim3(static_cast<unsigned>(threads))};
 }
 
 template <int kSize, bool kAny>
@@ -340,7 +354,7 @@ cudaError_t dispatch_launch(const PermuteArgs& a, const void* x, void* out, cuda
     const RowGrid g = row_grid(a.tokens, a.H, kSize, kAny);
     dispatch_kernel<kSize, kAny><<<g.grid, g.threads, 0, stream>>>(
         static_cast<const unsigned char*>(x), a.ld_tokens, static_cast<unsigned char*>(out), a.ld_rows, static_cast<int>(a.H),
-        a.rows, a.k);
+        a.rows, a.tokens, a.k);
     return cudaGetLastError();
 }
 
@@ -348,7 +362,7 @@ template <typename T, bool kAny>
 cudaError_t combine_launch(const PermuteArgs& a, const void* y, const float* weights, void* out, cudaStream_t stream) {
     const RowGrid g = row_grid(a.tokens, a.H, sizeof(T), kAny);
     combine_kernel<T, kAny><<<g.grid, g.threads, 0, stream>>>(
-        static_cast<const T*>(y), a.ld_rows, a.rows, weights, a.k, static_cast<T*>(out), a.ld_tokens,
+        static_cast<const T*>(y), a.ld_rows, a.rows, weights, a.tokens, a.k, static_cast<T*>(out), a.ld_tokens,
         static_cast<int>(a.H));
     return cudaGetLastError();
 }
@@ -357,9 +371,13 @@ template <typename T, bool kAny>
 cudaError_t combine_backward_launch(const PermuteArgs& a, const void* dout, const void* y, int64_t ldy,
                                     const float* weights, void* dy, float* dweights, cudaStream_t stream) {
     const int64_t slots = a.tokens * a.k;
-    const int64_t blocks = (slots + kThreads / 32 - 1) / (kThreads / 32);
-    combine_backward_kernel<T, kAny><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
-        static_cast<const T*>(dout), a.ld_tokens, static_cast<const T*>(y), ldy, a.rows, weights, a.k, slots,
+    const int64_t vectors = (a.H * static_cast<int64_t>(sizeof(T)) + 15) / 16 + (kAny ? 1 : 0);
+    int shift = 0;   // lanes of a slot: a power of two up to a warp
+    while (shift < 5 && (1 << shift) < vectors) ++shift;
+    const int64_t per = kThreads >> shift, blocks = (slots + per - 1) / per;
+    auto kernel = shift < 5 ? combine_backward_kernel<T, kAny, true> : combine_backward_kernel<T, kAny, false>;
+    kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(
+        static_cast<const T*>(dout), a.ld_tokens, static_cast<const T*>(y), ldy, a.rows, weights, a.k, slots, shift,
         static_cast<T*>(dy), a.ld_rows, dweights, static_cast<int>(a.H));
     return cudaGetLastError();
 }
