@@ -383,12 +383,11 @@ PyObject* layer_norm(Args a) {
         type = shift_type;
     }
     const Given out(a[4], 3);
-    const bool fresh_stats = out[1] == Py_None || out[2] == Py_None;
     Results got;
     int64_t ld;
     void* y = got.matrix(out[0], "y", like, x.type, x.rows, x.cols, &ld);
-    void* mean = got.dense(fresh_stats ? Py_None : out[1], "mean", like, at::kFloat, {x.rows});
-    void* rstd = got.dense(fresh_stats ? Py_None : out[2], "rstd", like, at::kFloat, {x.rows});
+    void* mean = got.dense(out[1], "mean", like, at::kFloat, {x.rows});
+    void* rstd = got.dense(out[2], "rstd", like, at::kFloat, {x.rows});
     check(mxq_layer_norm(x.data, x.type, x.rows, x.cols, x.ld, weight, shift, static_cast<mxq_dtype>(type), number(a[3]),
                          y, ld, static_cast<float*>(mean), static_cast<float*>(rstd), stream_of(like)),
           "mxq_layer_norm");
