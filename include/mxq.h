@@ -615,7 +615,7 @@ mxq_status mxq_moe_combine_backward(const void* dout, const void* y, mxq_dtype d
  *   y = (x - mean) rstd weight + shift.
  * weight, shift  [cols] of param_dtype, either may be NULL (1 and 0).
  * y              [rows, cols] of dtype; may be x itself.
- * mean, rstd     FP32 [rows], for the backward pass.
+ * mean, rstd     FP32 [rows], for the backward pass; NaN (0 / 0) with cols == 0.
  * eps            finite, >= 0.
  */
 mxq_status mxq_layer_norm(const void* x, mxq_dtype dtype, int64_t rows, int64_t cols, int64_t ldx, const void* weight,

@@ -195,14 +195,20 @@ mxq_status mxq_layer_norm(const void* x, mxq_dtype dtype, int64_t rows, int64_t 
     mxq_status st = check_norm(dtype, param_dtype, rows, cols);
     if (st != MXQ_OK) return st;
     if (ldx < cols || ldy < cols || !(eps >= 0.0f) || std::isinf(eps)) return MXQ_ERR_INVALID_ARG;
-    if (rows == 0 || cols == 0) return MXQ_OK;
-    if (!x || !y || !mean || !rstd) return MXQ_ERR_INVALID_ARG;
+    if (rows == 0) return MXQ_OK;
+    if (cols > 0 && (!x || !y || !mean || !rstd)) return MXQ_ERR_INVALID_ARG;
     const size_t s = size_of(dtype), p = size_of(param_dtype);
     if (!aligned(x, s) || !aligned(y, s) || !aligned(weight, p) || !aligned(shift, p) || !aligned(mean, 4) ||
         !aligned(rstd, 4))
         return MXQ_ERR_INVALID_ARG;
     st = device_ok();
     if (st != MXQ_OK) return st;
+    if (cols == 0) {   // 0 / 0 in every row: all bits set are a NaN
+        cudaError_t e = cudaSuccess;
+        if (mean) e = cudaMemsetAsync(mean, 0xFF, static_cast<size_t>(rows) * 4, cu(stream));
+        if (e == cudaSuccess && rstd) e = cudaMemsetAsync(rstd, 0xFF, static_cast<size_t>(rows) * 4, cu(stream));
+        return from_cuda(e);
+    }
     return from_cuda(mxq::launch_layer_norm({rows, cols, ldx, ldy, x, weight, shift, eps, y, mean, rstd},
                                             dtype == MXQ_F32, param_dtype == MXQ_F32, cu(stream)));
 }

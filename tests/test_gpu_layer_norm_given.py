@@ -1,4 +1,4 @@
-"""Buffers that a caller gives to mxq.layer_norm."""
+"""Buffers that a caller gives to mxq.layer_norm, and rows without a column."""
 import pytest
 import torch
 
@@ -34,3 +34,16 @@ def test_a_statistic_that_does_not_fit_is_refused():
         for out in ((None, bad, None), (None, None, bad), (None, good, bad), (None, bad, good)):
             with pytest.raises(ValueError):
                 mxq.layer_norm(x, out=out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_statistics_of_rows_without_a_column(dtype):
+    """0 / 0: NaN in every row, and not what the memory held."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    x = torch.empty(5, 0, dtype=dtype, device="cuda")
+    mean, rstd = (torch.full((5,), 7.0, device="cuda") for _ in range(2))
+    y, m, r = mxq.layer_norm(x, out=(None, mean, rstd))
+    assert y.shape == (5, 0) and m is mean and r is rstd
+    assert torch.isnan(mean).all() and torch.isnan(rstd).all()
+    dx, dw, db = mxq.layer_norm_backward(x, x, None, mean, rstd)
+    assert dx.shape == (5, 0) and dw.shape == db.shape == (0,)
