@@ -13,7 +13,7 @@
 //
 // Bound by memory for long rows and many.  Measured, of the 6787 GB/s a copy reaches:
 // forward 16384 x 7168 BF16 79 us (87%), 16384 x 4096 45 us (87%), 32767 x 1000 FP32 41 us
-// (94%), 8 x 4096 2.3 us; backward 129 us (80%), 71 us (84%), 73 us (80%).  Rows off the
+// (94%), 8 x 4096 2.3 us; backward 132 us (79%), 71 us (83%), 73 us (80%).  Rows off the
 // 16-byte grid: 8191 x 4097 BF16 forward 48 us (41%), backward 72 us (41%).
 //
 // kAny: rows that start at any element (mxq_elem.cuh), in vectors of x's rows.  dy and the
@@ -278,14 +278,16 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
 // ---- backward ---------------------------------------------------------------------------
 
 // One vector of x and dy: adds to the column sums, and to sum(u), sum(u h) of the row;
-// leaves h = x r - mu r in x and u in g.  rr = (r, r), off = (-mu r, -mu r).  Elements outside the
-// row are 0 in both and add nothing.
+// leaves h = (x - mu) r in x and u in g.  rr = (r, r), minus = (-mu, -mu).  The difference comes first: in
+// x r - mu r the rounding of mu r stays when the rest cancels (with a mean of 4096 spreads h was off by 1e-4; the
+// instruction that it saved is 2% at 16384 x 7168, nothing at other sizes).  Elements outside the row are 0 in dy
+// and add nothing.
 template <int H>
-__device__ __forceinline__ void add_vector(f32x2 (&x)[H], f32x2 (&g)[H], const f32x2 (&w)[H], f32x2 rr, f32x2 off,
+__device__ __forceinline__ void add_vector(f32x2 (&x)[H], f32x2 (&g)[H], const f32x2 (&w)[H], f32x2 rr, f32x2 minus,
                                            f32x2 (&dw)[H], f32x2 (&db)[H], f32x2& s1, f32x2& s2) {
 #pragma unroll
     for (int c = 0; c < H; ++c) {
-        x[c] = fma2(x[c], rr, off);
+        x[c] = mul2(add2(x[c], minus), rr);
         dw[c] = fma2(g[c], x[c], dw[c]);
         db[c] = add2(db[c], g[c]);
         g[c] = mul2(g[c], w[c]);
@@ -373,13 +375,13 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_backward_short_kernel(c
             else qg[n] = load_ends<S>(dy, first + n * tpr * V, cols);
         }
         const float mu = live ? a.mean[at_row] : 0.0f, r = live ? a.rstd[at_row] : 0.0f;
-        const f32x2 rr = pair(r, r), off = pair(-mu * r, -mu * r);
+        const f32x2 rr = pair(r, r), minus = pair(-mu, -mu);
         f32x2 h[kN][H], u[kN][H], s1 = 0, s2 = 0;
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
             unpack2<T>(qx[n], h[n]);
             unpack2<T>(qg[n], u[n]);
-            add_vector<H>(h[n], u[n], w[n], rr, off, dw[n], db[n], s1, s2);
+            add_vector<H>(h[n], u[n], w[n], rr, minus, dw[n], db[n], s1, s2);
         }
         const float m1 = lanes_sum(lo_of(s1) + hi_of(s1), tpr) * inv;
         const float m2 = lanes_sum(lo_of(s2) + hi_of(s2), tpr) * inv;
@@ -605,7 +607,7 @@ norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
     int odd = 0;
     while (place.row < a.rows) {
         const float2 st = stats[group][odd];
-        const f32x2 rr = pair(st.y, st.y), off = pair(-st.x * st.y, -st.x * st.y);
+        const f32x2 rr = pair(st.y, st.y), minus = pair(-st.x, -st.x);
         if (ahead) {
             bars.stop[group][odd] = *static_cast<volatile int*>(&bars.abort_flag);
             stats[group][odd ^ 1] = later;
@@ -621,7 +623,7 @@ norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
             unpack2<T>(ring.read(0, place.stage, q, i), h[m]);
             unpack2<T>(ring.read(1, place.stage, q, i, lead_g, alike), u[m]);
             w.get(n, fw);
-            add_vector<H>(h[m], u[m], fw, rr, off, dw[n], db[n], s1, s2);
+            add_vector<H>(h[m], u[m], fw, rr, minus, dw[n], db[n], s1, s2);
         }
         const f32x2 both = warp_sum2(pair(lo_of(s1) + hi_of(s1), lo_of(s2) + hi_of(s2)));
         if (lane == 0) sums[group][odd][warp] = both;
@@ -645,7 +647,7 @@ norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
                 w.get(n, fw);
 #pragma unroll
                 for (int c = 0; c < H; ++c) {
-                    h[m][c] = fma2(h[m][c], rr, off);
+                    h[m][c] = mul2(add2(h[m][c], minus), rr);
                     u[m][c] = mul2(u[m][c], fw[c]);
                 }
             }
