@@ -222,6 +222,8 @@ cudaError_t clip_launch(const ClipTensor* tensors, int count, int chunk_bytes, b
         whole = at == 0;
         at = fill(&t, tensors, count, at, chunk_bytes);
         squares_kernel<kTable><<<kClipBlocks, kThreads, 0, stream>>>(t, partial + parts);
+        const cudaError_t e = cudaGetLastError();   // without its sums nothing may be scaled
+        if (e != cudaSuccess) return e;
         parts += kClipBlocks;
     }
     if (!scale_too) {
