@@ -36,7 +36,13 @@ mxq_status device_ok() {
     return yes ? MXQ_OK : MXQ_ERR_UNSUPPORTED_DEVICE;
 }
 
-inline mxq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MXQ_OK : MXQ_ERR_CUDA; }
+// The runtime keeps an error for the next cudaGetLastError: it is taken here, or it would be read as that
+// of a later call's launch.
+inline mxq_status from_cuda(cudaError_t e) {
+    if (e == cudaSuccess) return MXQ_OK;
+    (void)cudaGetLastError();
+    return MXQ_ERR_CUDA;
+}
 
 inline cudaStream_t cu(mxq_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 

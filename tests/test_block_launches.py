@@ -23,3 +23,16 @@ def test_a_refused_launch_is_reported_and_nothing_follows_it(record, count, scal
         assert done == launches[:n - 1]
         assert record.L.rec_launches() == n
     assert record("clip", count, 1000, scale)[0] == 0
+
+
+@pytest.mark.parametrize("call,args", [("route", (100, 64, 4)), ("plan", (4096, 8, 128)), ("clip", (40, 1000, 0)),
+                                       ("clip", (40, 1000, 1)), ("norm", (0, 0, 100, 1024)),
+                                       ("norm_backward", (0, 0, 100, 64)), ("norm_backward", (0, 0, 100, 1024)),
+                                       ("norm_backward", (0, 0, 100, 20001))])
+def test_a_refused_launch_leaves_no_error_for_the_next_call(record, call, args):
+    """The runtime keeps the error of a launch for whoever asks next: a good call after a bad one must not
+    find it."""
+    launches = record(call, *args)[1]
+    for n in range(1, len(launches) + 1):
+        assert record(call, *args, refuse=n)[0] != 0
+        assert record("route", 100, 64, 4, forget=False)[0] == 0, f"the error of launch {n} of {len(launches)} was still there"
