@@ -514,7 +514,8 @@ mxq_status mxq_grouped_gemm_noalloc(const void* a_q, const void* a_s, const void
  * stride (ld) in elements; rows may start at any multiple of the element
  * size (16-byte aligned rows of a multiple of 16 bytes run fastest).  Outputs
  * must not overlap inputs unless a call says so.  Results are the same on
- * every call (no floating-point atomics).  Errors: MXQ_ERR_INVALID_ARG,
+ * every call (no floating-point atomics).  Host threads may make the calls at
+ * the same time, on outputs and workspaces of their own.  Errors: MXQ_ERR_INVALID_ARG,
  * MXQ_ERR_UNSUPPORTED_SHAPE (a size past the stated limit; rows and slots are
  * limited to 2^31 - 4096, elements of a row to 2^23), MXQ_ERR_UNSUPPORTED_DEVICE,
  * MXQ_ERR_CUDA.

@@ -34,7 +34,10 @@ namespace {
 
 constexpr int kSMs = 152;
 constexpr int kHeldGroups = 16;       // of more than a warp (forward, held parameters): named barriers
-constexpr int64_t kHeldBytes = 200 * 1024;
+// Shared memory at most.  The limits of the kernels are set to these sizes whatever a call needs: a limit
+// belongs to the kernel, and host threads with other shapes launch it too.
+constexpr int kHeldBytes = 200 * 1024;
+constexpr int kRingBytes = 204 * 1024;
 constexpr int64_t kShortCols = 512;   // rows up to this long need no ring (backward)
 
 // ---- sums over the threads of a row ---------------------------------------------------
@@ -420,7 +423,6 @@ constexpr int kMaxStages = 32;
 constexpr int kMaxGroups = 14;               // named barriers: one each, and one for all
 constexpr int kRingThreads = 512;
 constexpr int kManyThreads = 640;
-constexpr int64_t kRingBytes = 204 * 1024;
 
 struct RingBars {
     uint64_t full[kMaxStages];
@@ -800,8 +802,7 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t stream) {
                 const unsigned threads = static_cast<unsigned>((groups * tpr + 31) / 32 * 32);
                 auto kernel = norm_held_kernel<T, W, kN, kAny>;
                 if (held > 40 * 1024) {   // beside the kernel's own 4 KB more than a launch has unasked
-                    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                               static_cast<int>(held));
+                    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldBytes);
                     if (e != cudaSuccess) return e;
                 }
                 kernel<<<static_cast<unsigned>(grid), threads, held, stream>>>(a, tpr);
@@ -839,10 +840,9 @@ cudaError_t backward_ring(const NormBackwardArgs& a, int64_t vectors, int64_t gr
         int64_t bytes = weights + stages * stage;
         const int64_t meet = groups * 2 * kN * tpr * V * static_cast<int64_t>(sizeof(float));   // at most 128 KB
         if (bytes < meet) bytes = meet;
-        const int smem = static_cast<int>(bytes);
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
         if (e != cudaSuccess) return e;
-        kernel<<<static_cast<unsigned>(grid), static_cast<unsigned>(tpr * groups), smem, stream>>>(
+        kernel<<<static_cast<unsigned>(grid), static_cast<unsigned>(tpr * groups), bytes, stream>>>(
             a, static_cast<int>(stages), tpr);
         return cudaGetLastError();
     };

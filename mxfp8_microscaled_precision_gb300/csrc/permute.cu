@@ -29,7 +29,10 @@ namespace cg = cooperative_groups;
 namespace mxq {
 namespace {
 
-constexpr int64_t kPlanWords = 50 * 1024;   // shared memory of a block of the plan, in words
+constexpr int64_t kPlanWords = 50 * 1024;   // of the plan's counts by warp, in words
+// Shared memory of a block of the plan at most (1024 experts and the dropped slots).  It is what the kernel's limit
+// is set to, whatever a call needs: the limit is the kernel's, and host threads with other shapes launch it too.
+constexpr int kPlanBytes = 4 * (kPlanWords + 2 * 1025 + 32);
 
 // ---- plan ------------------------------------------------------------------------
 
@@ -400,11 +403,12 @@ cudaError_t launch_moe_plan(const int32_t* ids, int64_t slots, int experts, int6
     const int64_t all = blocks * warps;
     const int64_t chunk = ((slots + all - 1) / all + 31) / 32 * 32;
     const size_t smem = sizeof(int) * static_cast<size_t>(2 * warps * B + 2 * B + 32);
-    cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {   // more than a launch has unasked
+        const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanBytes);
+        if (e != cudaSuccess) return e;
+    }
     if (blocks > 8) {
-        e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
