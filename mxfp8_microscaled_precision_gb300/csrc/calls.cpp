@@ -9,6 +9,8 @@
 // with results given), routing 9.5 us to 5.2 us, plan 9.6 us to 4.9 us, dispatch 7.9 us to 3.6 us; clipping 300
 // gradients 155 us of host time to less than the kernels' 31 us.
 //
+// The library launches on the current device: a call's tensors all have to be there.
+//
 // Errors: ValueError for a tensor that a call cannot take, TypeError for an object that is none,
 // the package's error class for a status of the library; a C++ exception (memory) becomes
 // torch's own Python error.  Nothing leaves as an exception of C++.
@@ -19,6 +21,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -118,6 +121,30 @@ int code_of(const at::Tensor& t) {
     return type == at::kBFloat16 ? MXQ_BF16 : type == at::kFloat ? MXQ_F32 : -1;
 }
 
+// The device of the call's tensors, the first one's; -1 before it.
+thread_local int call_device = -1;
+
+// A call may run inside another one (a destructor that the interpreter runs meanwhile).
+class OnDevice {
+public:
+    OnDevice() : outer_(call_device) { call_device = -1; }
+    OnDevice(const OnDevice&) = delete;
+    OnDevice& operator=(const OnDevice&) = delete;
+    ~OnDevice() { call_device = outer_; }
+
+private:
+    int outer_;
+};
+
+// Every tensor passes here, a CUDA tensor as its type has been checked.
+void same_device(const at::Tensor& t, const char* name) {
+    const int device = t.get_device();
+    if (call_device < 0) call_device = device;
+    if (device != call_device)
+        throw Refused{std::string(name) + " is on cuda:" + std::to_string(device) + ", another tensor of the call on cuda:" +
+                      std::to_string(call_device)};
+}
+
 // A 2-D bf16 or fp32 CUDA tensor with unit last stride.  A single row has any stride (its own says nothing).
 struct Matrix {
     void* data;
@@ -128,6 +155,7 @@ Matrix matrix(const at::Tensor& t, const char* name) {
     const int code = code_of(t);
     if (code < 0 || t.dim() != 2 || !t.is_cuda())
         throw Refused{std::string(name) + " must be a 2-D bfloat16 or float32 CUDA tensor"};
+    same_device(t, name);
     const int64_t rows = t.size(0), cols = t.size(1), ld = t.stride(0);
     if (t.stride(1) != 1 && cols > 1) throw Refused{std::string(name) + " must have unit stride along its last axis"};
     return {t.data_ptr(), static_cast<mxq_dtype>(code), rows, cols, rows > 1 || ld > cols ? ld : cols};
@@ -137,6 +165,7 @@ Matrix matrix(const at::Tensor& t, const char* name) {
 void* dense(const at::Tensor& t, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) {
     if (t.scalar_type() != type || t.sizes() != at::IntArrayRef(shape) || !t.is_cuda() || !t.is_contiguous())
         throw Refused{std::string(name) + " must be a contiguous " + name_of(type) + " CUDA tensor " + shape_of(shape)};
+    same_device(t, name);
     return t.data_ptr();
 }
 void* dense(PyObject* o, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) {
@@ -157,8 +186,13 @@ Slots slots(PyObject* o, const char* name) {
     return {static_cast<int32_t*>(dense(t, name, at::kInt, {t.size(0), t.size(1)})), t.size(0), t.size(1)};
 }
 
+// The current stream, of the current device, on which all tensors of the call have to be: t is one of them.
 mxq_stream_t stream_of(const at::Tensor& t) {
-    const Owned index(PyLong_FromLong(t.get_device()));
+    const int current = c10::impl::VirtualGuardImpl(at::kCUDA).getDevice().index();
+    if (t.get_device() != current)
+        throw Refused{"the tensors are on cuda:" + std::to_string(t.get_device()) + ", the current device is cuda:" +
+                      std::to_string(current)};
+    const Owned index(PyLong_FromLong(current));
     const Owned stream(PyObject_CallOneArg(raw_stream, index.get()));
     return reinterpret_cast<mxq_stream_t>(static_cast<intptr_t>(integer(stream.get())));
 }
@@ -425,6 +459,7 @@ mxq_grad_desc grad_desc(const at::Tensor& g) {
     const int code = code_of(g);
     if (code < 0 || !g.is_cuda() || !g.is_contiguous())
         throw Refused{"gradients must be contiguous bfloat16 or float32 CUDA tensors"};
+    same_device(g, "a gradient");
     mxq_grad_desc d{};
     d.grad = d.out = g.data_ptr();
     d.numel = g.numel();
@@ -486,6 +521,7 @@ PyObject* clip_grad_norm(Args a) {
         const at::Tensor& t = tensor(o, "an output");
         if (t.scalar_type() != g.scalar_type() || t.numel() != descs[i].numel || !t.is_cuda() || !t.is_contiguous())
             throw Refused{"every output must be a contiguous tensor like its gradient"};
+        same_device(t, "an output");
         descs[i].out = t.data_ptr();
     }
     const NormBuffers b(a[0]);
@@ -502,6 +538,7 @@ PyObject* clip_grad_norm(Args a) {
 template <PyObject* (*kCall)(Args), int kArgs>
 PyObject* entry(PyObject*, Args args, Py_ssize_t given) {
     HANDLE_TH_ERRORS
+    const OnDevice device;
     try {
         if (given != kArgs) {
             PyErr_Format(PyExc_TypeError, "%d arguments are wanted, not %zd", kArgs, given);

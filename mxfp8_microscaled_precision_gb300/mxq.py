@@ -502,7 +502,8 @@ MAX_GRADS = 65536
 
 # These calls are made for single tokens too, where the host's share is most of the
 # time: their tensors are checked, their results allocated and the library is called by an
-# extension module instead of ctypes (csrc/calls.cpp).
+# extension module instead of ctypes (csrc/calls.cpp).  All tensors of a call are on the current
+# device; one that is not is refused (ValueError).
 _calls_module = None
 
 
