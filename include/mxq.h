@@ -556,9 +556,12 @@ typedef enum {
  * weights     FP32 [tokens, topk]; 0 where ids is -1.
  * A NaN choice value ranks below every number and stays eligible: the ids are
  * always distinct and in range, and a chosen NaN shows in the weights.
- * Limits: experts <= 1024, topk <= 32 and <= the experts of topk_group groups,
- * n_group <= 32 and a divisor of experts.
+ * Limits: experts <= MXQ_MAX_EXPERTS, topk <= MXQ_MAX_TOPK and <= the experts of
+ * topk_group groups, n_group <= 32 and a divisor of experts.
  */
+#define MXQ_MAX_EXPERTS 1024
+#define MXQ_MAX_TOPK 32
+
 mxq_status mxq_route(const void* logits, mxq_dtype dtype, int64_t tokens, int32_t experts, int64_t ld,
                      const float* bias, const uint8_t* token_mask, mxq_route_score score, int32_t n_group,
                      int32_t topk_group, mxq_group_score group_score, int32_t topk, int32_t renorm, float scale,
@@ -585,7 +588,7 @@ mxq_status mxq_route_backward(const float* dweights, const int32_t* ids, const v
  *          mxq_grouped_gemm and mxq_quant_1x32_cols_grouped.
  * rows     int32 [tokens, k]: the row of every slot.  Dropped slots have the rows
  *          from offsets[experts] on, each given as -1 - row.
- * experts <= 1024.  With dropped slots offsets[experts] < tokens * k: the grouped
+ * experts <= MXQ_MAX_EXPERTS.  With dropped slots offsets[experts] < tokens * k: the grouped
  * calls, given M_total = tokens * k, leave the rows behind it alone, and the calls
  * below never read them.  tokens == 0 writes zero offsets.
  */

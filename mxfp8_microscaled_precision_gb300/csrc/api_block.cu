@@ -55,7 +55,7 @@ mxq_status check_route(mxq_dtype dtype, int64_t tokens, int32_t experts, int64_t
     if (bad_dtype(dtype) || (score != MXQ_SCORE_SOFTMAX && score != MXQ_SCORE_SIGMOID)) return MXQ_ERR_INVALID_ARG;
     if (tokens < 0 || experts < 1 || topk < 1 || ld < experts || !std::isfinite(scale)) return MXQ_ERR_INVALID_ARG;
     if (topk > experts) return MXQ_ERR_INVALID_ARG;
-    if (experts > 1024 || topk > 32 || tokens > kMaxRows) return MXQ_ERR_UNSUPPORTED_SHAPE;
+    if (experts > MXQ_MAX_EXPERTS || topk > MXQ_MAX_TOPK || tokens > kMaxRows) return MXQ_ERR_UNSUPPORTED_SHAPE;
     return MXQ_OK;
 }
 
@@ -141,7 +141,7 @@ mxq_status mxq_route_backward(const float* dweights, const int32_t* ids, const v
 mxq_status mxq_moe_plan(const int32_t* ids, int64_t tokens, int32_t k, int32_t experts, int64_t* offsets, int32_t* rows,
                         mxq_stream_t stream) {
     if (tokens < 0 || k < 1 || experts < 1) return MXQ_ERR_INVALID_ARG;
-    if (experts > 1024 || tokens > kMaxRows / k) return MXQ_ERR_UNSUPPORTED_SHAPE;
+    if (experts > MXQ_MAX_EXPERTS || tokens > kMaxRows / k) return MXQ_ERR_UNSUPPORTED_SHAPE;
     if (!offsets || !aligned(offsets, 8)) return MXQ_ERR_INVALID_ARG;
     if (tokens > 0 && (!ids || !rows || !aligned(ids, 4) || !aligned(rows, 4))) return MXQ_ERR_INVALID_ARG;
     const mxq_status st = device_ok();

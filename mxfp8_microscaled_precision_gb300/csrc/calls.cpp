@@ -297,7 +297,9 @@ PyObject* route(Args a) {
         const at::Tensor& m = tensor(a[9], "token_mask");
         mask = dense(m, "token_mask", m.scalar_type() == at::kBool ? at::kBool : at::kByte, {x.rows});
     }
-    if (a[10] == Py_None && topk < 1) throw Refused{"topk must be at least 1"};
+    // before anything of that size is allocated
+    if (topk < 1) throw Refused{"topk must be at least 1"};
+    if (topk > MXQ_MAX_TOPK) check(topk > x.cols ? MXQ_ERR_INVALID_ARG : MXQ_ERR_UNSUPPORTED_SHAPE, "mxq_route");
     const Given out(a[10], 2);
     Results got;
     void* ids = got.dense(out[0], "ids", logits, at::kInt, {x.rows, topk});
@@ -333,7 +335,8 @@ PyObject* moe_plan(Args a) {
     const at::Tensor& like = tensor(a[0], "ids");
     const Slots ids = slots(a[0], "ids");
     const int64_t experts = integer(a[1]);
-    if (experts < 1 || experts > INT32_MAX) check(MXQ_ERR_INVALID_ARG, "mxq_moe_plan");
+    if (experts < 1) check(MXQ_ERR_INVALID_ARG, "mxq_moe_plan");
+    if (experts > MXQ_MAX_EXPERTS) check(MXQ_ERR_UNSUPPORTED_SHAPE, "mxq_moe_plan");   // before it is allocated
     const Given out(a[2], 2);
     Results got;
     void* offsets = got.dense(out[0], "offsets", like, at::kLong, {experts + 1});
