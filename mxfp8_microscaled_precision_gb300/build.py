@@ -10,8 +10,10 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import fcntl
+import functools
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -22,7 +24,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libmxq.so")
-CALLS = os.path.join(OUT, "_mxqcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "tensor_map.cu", "fsdp.cu", "noalloc.cu",
            "api_block.cu", "route.cu", "permute.cu", "norm.cu", "clip.cu"]
 HEADERS = ["mxq_device.cuh", "mxq_internal.h", "mxq_quant_math.cuh", "mxq_elem.cuh"]
@@ -38,10 +39,27 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: set NVCC or put the CUDA toolkit on PATH")
 
 
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+@functools.lru_cache(maxsize=None)
+def _torch_version() -> str:
+    """Of the torch that would be imported, without importing it."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return re.search(r"""^__version__\s*=\s*['"]([^'"]+)""", f.read(), re.MULTILINE).group(1)
+
+
+def calls_path() -> str:
+    """The extension module, by the Python and the torch that it is built for: torch's C++
+    interface is not the same from one version to the next."""
+    return os.path.join(OUT, f"_mxqcall-torch-{_torch_version()}" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+    if not os.path.exists(LIB) or not os.path.exists(calls_path()):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(calls_path()))
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + ["calls.cpp"]] + [os.path.join(INCLUDE, "mxq.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -64,10 +82,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 def _gxx() -> str:
     return os.environ.get("CXX", "g++")
-
-
-def _torch_dir() -> str:
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
 
 
 def _compile_calls() -> str:
@@ -107,13 +121,14 @@ def _build(verbose: bool) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     # torch's libraries are in the process before the module is: no path to them is needed
-    tmp = CALLS + f".tmp{os.getpid()}"
+    calls_so = calls_path()
+    tmp = calls_so + f".tmp{os.getpid()}"
     r = subprocess.run([_gxx(), "-shared", "-o", tmp, calls_obj, "-L" + OUT, "-l:libmxq.so", "-Wl,-rpath,$ORIGIN",
                         "-L" + os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed for calls.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    os.replace(tmp, calls_so)
     return LIB
 
 

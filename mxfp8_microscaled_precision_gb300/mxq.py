@@ -513,9 +513,10 @@ def _calls():
     global _calls_module
     if _calls_module is None:
         lib()   # raises the same way if nothing has been built
-        spec = importlib.util.spec_from_file_location("_mxqcall", _build.CALLS)
-        if spec is None or not os.path.exists(_build.CALLS):
-            raise RuntimeError(f"the extension module is not built ({_build.CALLS}); run __graft_entry__.build()")
+        path = _build.calls_path()
+        spec = importlib.util.spec_from_file_location("_mxqcall", path)
+        if spec is None or not os.path.exists(path):
+            raise RuntimeError(f"the extension module is not built ({path}); run __graft_entry__.build()")
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
 
