@@ -24,8 +24,9 @@ MXFP8 GEMM timed in the same run), `roofline_quant` the quantizers.
 `cpu_baseline` times the oracle on a bounded sample.  `--impl reference`
 times the oracle alone (CPU).
 
-Multi-GPU: the path has no exchange step, so N ranks run N independent
-replicas (weak scaling); the timing is the max over ranks.
+One GPU: ranks of a larger job are refused before they touch the GPU.  The
+GEMMs share operand tiles by TMA loads with cluster multicast, which are for
+runs on a single GPU alone.  The reference arm (CPU) runs on rank 0.
 """
 from __future__ import annotations
 
@@ -80,7 +81,7 @@ def load_peaks():
         return dict(FALLBACK_PEAKS, source="fallback")
 
 
-# ---- distributed plumbing (replicas; only timing crosses ranks) ------------------------
+# ---- ranks (only timing would cross them) -----------------------------------------------
 
 def dist_env():
     return (int(os.environ.get("RANK", "0")), int(os.environ.get("WORLD_SIZE", "1")),
@@ -1042,13 +1043,20 @@ def gemm_peak_of(peaks, vendor):
                          f"vendor MXFP8 in this run {vendor}")
 
 
+def refuse_ranks():
+    """Ends a process that is one rank of several: the GPU arm runs on one GPU (see the module's text)."""
+    rank, world, _ = dist_env()
+    if world == 1:
+        return
+    why = f"the benchmark runs on one GPU: {world} ranks are refused (GEMMs with multicast loads are for single-GPU runs)"
+    if rank == 0:
+        print(json.dumps({"metric": METRIC, "n_gpus": world, "impl": "mxq", "unavailable": why}), flush=True)
+    raise SystemExit(why)
+
+
 def run_gpu(args):
     import torch
-    rank, world, local = dist_env()
-    if world > 1:
-        import torch.distributed as dist
-        torch.cuda.set_device(local)
-        dist.init_process_group("nccl")
+    _, world, local = dist_env()   # world is 1
     dev = torch.device("cuda", local)
     torch.cuda.set_device(dev)
     from mxfp8_microscaled_precision_gb300 import build as mbuild, mxq
@@ -1069,7 +1077,7 @@ def run_gpu(args):
     nk = len(kern)
     total_s = sum(t["step_ms"]) / 1e3
     step_median_ms = statistics.median(t["step_ms"])
-    max_total_s = max_over_ranks(total_s, dev if world > 1 else None)
+    max_total_s = max_over_ranks(total_s)
     value = aggregate_value(w.gemm_flops, args.steps, world, max_total_s)
     r = rates(t, args.steps, peaks, gemm_peak)
     roofline = {"bound": "tensor", "kernel": "gemm_mxf8_pair_kernel", "achieved": round(r["gemm_tflops"], 1),
@@ -1137,7 +1145,7 @@ def run_gpu(args):
         barrier(dev)
         run_pipeline(n_e2e, tev)
         e2e_total = tev[0].elapsed_time(tev[1]) / 1e3
-        e2e_total = max_over_ranks(e2e_total, dev if world > 1 else None)
+        e2e_total = max_over_ranks(e2e_total)
         e2e = {"value": round(aggregate_value(w.gemm_flops, n_e2e, world, e2e_total), 2), "unit": "TFLOP/s",
                "h2d_bytes_per_step": h2d, "d2h_bytes_per_step": d2h,
                "ms_per_step": round(e2e_total / n_e2e * 1e3, 4),
@@ -1210,7 +1218,7 @@ def run_gpu(args):
         wx = make_workload(name, dev)
         tx = time_device(wx, args, dev, world)
         rx = rates(tx, args.steps, peaks, gemm_peak)
-        tot_x = max_over_ranks(sum(tx["step_ms"]) / 1e3, dev if world > 1 else None)
+        tot_x = max_over_ranks(sum(tx["step_ms"]) / 1e3)
         extra[name] = {"config": workload_config(wx),
                        "value": round(aggregate_value(wx.gemm_flops, args.steps, world, tot_x), 2),
                        "unit": "TFLOP/s", "ms_per_step": round(tot_x / args.steps * 1e3, 4),
@@ -1224,37 +1232,33 @@ def run_gpu(args):
         del wx, tx
 
     cpu = None
-    if rank == 0 and world == 1 and not args.no_cpu_baseline:
+    if not args.no_cpu_baseline:
         cpu = cpu_baseline(w, args.cpu_budget)
 
-    if rank == 0:
-        line = {"metric": METRIC, "value": round(value, 2), "unit": "TFLOP/s", "n_gpus": world,
-                "steps": args.steps, "warmup": args.warmup,
-                "ms_per_step": round(max_total_s / args.steps * 1e3, 4),
-                "ms_per_step_median": round(step_median_ms, 4), "higher_is_better": True,
-                "scaling": "weak", "vs_baseline": None, "dtype": "fp8_e4m3 (E8M0 block scales, fp32 accumulate)",
-                "data": "synthetic (seeded generators; shapes of the linear / MoE-expert workloads)",
-                "config": workload_config(w),
-                "gemm_tflops": round(r["gemm_tflops"], 1), "gemm_frac_peak": round(r["gemm_frac"], 4),
-                "quant_tbs": round(r["quant_gbs"] / 1e3, 3), "quant_frac_hbm": round(r["quant_frac"], 4),
-                "kernels_ms": r["kernels_ms"], "kernels_ms_median": r["kernels_ms_median"],
-                "roofline": roofline, "roofline_quant": roofline_quant, "roofline_quant_alone": quant_alone,
-                "cpu_baseline": cpu, "e2e": e2e,
-                "gpu_launches": own_launches * args.steps + extra_launches + quant_alone_launches,
-                "gpu_launches_split": {w.name: own_launches * args.steps, "extra_workloads": extra_launches,
-                                       "quant_alone": quant_alone_launches},
-                "clocks": main_clocks, "vendor_mxfp8_tflops": vendor,
-                "vendor_mxfp8_sustained": vendor_sustained, "impl": "mxq"}
-        if r["other_hbm"]:
-            line["hbm_kernels"] = r["other_hbm"]
-        if hasattr(w, "extra"):
-            line.update(w.extra())
-        for name, block in extra.items():
-            line["moe_block" if name == "moe_grouped" else "extra_" + name] = block
-        print(json.dumps(line), flush=True)
-    if world > 1:
-        import torch.distributed as dist
-        dist.destroy_process_group()
+    line = {"metric": METRIC, "value": round(value, 2), "unit": "TFLOP/s", "n_gpus": world,
+            "steps": args.steps, "warmup": args.warmup,
+            "ms_per_step": round(max_total_s / args.steps * 1e3, 4),
+            "ms_per_step_median": round(step_median_ms, 4), "higher_is_better": True,
+            "scaling": "weak", "vs_baseline": None, "dtype": "fp8_e4m3 (E8M0 block scales, fp32 accumulate)",
+            "data": "synthetic (seeded generators; shapes of the linear / MoE-expert workloads)",
+            "config": workload_config(w),
+            "gemm_tflops": round(r["gemm_tflops"], 1), "gemm_frac_peak": round(r["gemm_frac"], 4),
+            "quant_tbs": round(r["quant_gbs"] / 1e3, 3), "quant_frac_hbm": round(r["quant_frac"], 4),
+            "kernels_ms": r["kernels_ms"], "kernels_ms_median": r["kernels_ms_median"],
+            "roofline": roofline, "roofline_quant": roofline_quant, "roofline_quant_alone": quant_alone,
+            "cpu_baseline": cpu, "e2e": e2e,
+            "gpu_launches": own_launches * args.steps + extra_launches + quant_alone_launches,
+            "gpu_launches_split": {w.name: own_launches * args.steps, "extra_workloads": extra_launches,
+                                   "quant_alone": quant_alone_launches},
+            "clocks": main_clocks, "vendor_mxfp8_tflops": vendor,
+            "vendor_mxfp8_sustained": vendor_sustained, "impl": "mxq"}
+    if r["other_hbm"]:
+        line["hbm_kernels"] = r["other_hbm"]
+    if hasattr(w, "extra"):
+        line.update(w.extra())
+    for name, block in extra.items():
+        line["moe_block" if name == "moe_grouped" else "extra_" + name] = block
+    print(json.dumps(line), flush=True)
 
 
 def cpu_baseline(w, budget_s):
@@ -1363,6 +1367,8 @@ def main(argv=None):
     ap.add_argument("--profile-gemm", metavar="MxNxK",
                     help="launch this library's GEMM and the vendor's once each at this shape (for ncu) and exit")
     args = ap.parse_args(argv)
+    if args.impl != "reference" or args.profile_gemm:
+        refuse_ranks()
     if args.profile_gemm:
         return run_profile_gemm(args.profile_gemm)
     if args.warmup < 3:
