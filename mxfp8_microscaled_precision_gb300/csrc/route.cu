@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T* logits, con
 }
 
 // dlogits from dweights.  With S = sum_i s_i + 1e-20 over the chosen experts:
-//   ds_j = (scale dw_j - sum_i dw_i w_i) / S   (renorm)   or   scale dw_j,
+//   ds_j = scale (dw_j - sum_i dw_i s_i / S) / S   (renorm)   or   scale dw_j,
 //   sigmoid: dx_j = ds_j s_j (1 - s_j), 0 at experts not chosen;
 //   softmax: dx_e = s_e (ds_e [chosen] - sum_j ds_j s_j).
 template <typename T, int kN, bool kSoftmax, bool kVec>
@@ -318,11 +318,11 @@ __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const T* lo
     }
     float ds = a.scale * dw;
     if (a.renorm) {
-        // the weights as the forward pass rounds them, both products rounded: where one expert is all
-        // there is and its weight is the scale, the difference is 0 and not the products' rounding
+        // the scale comes last and the products are rounded: where one expert is all there is, its share is
+        // 1 and the difference 0, whatever a scale that is no power of two would have rounded
         const float total = warp_sum(s) + kRenormEps;
-        const float dot = warp_sum(__fmul_rn(dw, a.scale * s / total));
-        ds = (__fmul_rn(a.scale, dw) - dot) / total;
+        const float dot = warp_sum(__fmul_rn(dw, s / total));
+        ds = a.scale * (dw - dot) / total;
     }
     if (id < 0) ds = 0.0f;
     const float d = kSoftmax ? warp_sum(ds * s) : 0.0f;
