@@ -494,7 +494,6 @@ def grouped_gemm_group_tiled(a_q, a_s_grouped, b_q, b_s, offsets: torch.Tensor, 
 
 # ---- operators around the experts' products (see the same section of mxq.h) ----
 
-BF16, F32 = 0, 1
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORES = {"max": 0, "top2sum": 1}
 MAX_GRADS = 65536
