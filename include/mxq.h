@@ -655,7 +655,8 @@ typedef struct {
 
 /* norm (DEVICE FP32) = sqrt(sum over all gradients of the sum of squares).  Squares
  * are summed in FP32, in parts and then the parts, so a gradient beyond about 1e19
- * gives inf.  grads: host array, read during the call.
+ * gives inf, one below about 1e-19 loses bits of its square and one below 2.6e-23
+ * adds nothing.  grads: host array, read during the call.
  * workspace: DEVICE scratch, 16-byte aligned, of at least
  * mxq_grad_norm_workspace_size(count) bytes.  count <= MXQ_MAX_GRADS; 0 gives 0. */
 mxq_status mxq_grad_norm(const mxq_grad_desc* grads, int32_t count, float* norm, void* workspace, size_t workspace_bytes,

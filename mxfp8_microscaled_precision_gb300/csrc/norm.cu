@@ -248,8 +248,9 @@ __global__ void __launch_bounds__(kN == 8 ? 512 : 1024) norm_held_kernel(const N
     }
 }
 
-// Rows longer than the registers of a block hold: element by element, read again in
-// each pass, one block per row.
+// Rows longer than the registers of a block hold (over 32768 BF16 or 16384 FP32; off the grid also those whose FP32
+// parameters beside BF16 rows do not fit the shared memory): element by element, read again in each pass, one block
+// per row (2048 x 32767 FP32 212 us, 37% of a copy's rate; 2048 x 25999 BF16 with FP32 parameters 157 us, 20%).
 template <typename T, typename W>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
     __shared__ float sh[2][32];
@@ -553,13 +554,12 @@ __device__ __forceinline__ void group_barrier(int group, int tpr) {
 // A thread of 16 elements a row (kKeep) keeps h and u of the row between the two passes; a
 // longer row is read a second time from the ring: registers hold the column sums.  What
 // bounds it: the chain of a row's sums (wait, shuffles, barrier, shuffles) and its arithmetic, some 2200
-// clocks, of which 14 to 16 warps of 128 registers fill less than half (issue slots 46% used, DRAM 63%,
-// at 16384 x 7168; figures below are for that size).  Twice the threads with half the registers spill and are slower
-// (211 us), as are 8 elements a thread (194 us) and the sums of the next row before the results of this
-// one (170 us: two rows' values leave the scheduler no registers); a warp of its own for the
-// copies changes nothing.  Without any loads and stores 118 us of 138 remained.
-// The weights wait in shared memory: in registers they took 146 us, and from the L1, of which the ring
-// leaves little, 206 us (FP32).
+// clocks, of which 14 to 16 warps of 128 registers fill less than half (issue slots 44% used, DRAM 59%,
+// at 8192 x 7168).  Tried at 16384 x 7168 on the form that took 138 us there (132 now): twice the threads with half the
+// registers spill and are slower (211 us), as are 8 elements a thread (194 us) and the sums of the next row before the
+// results of this one (170 us: two rows' values leave the scheduler no registers); a warp of its own for the
+// copies changed nothing; without any loads and stores 118 us remained.  The weights wait in shared memory: in
+// registers they took 146 us when that took 142, and from the L1, of which the ring leaves little, 206 us (FP32).
 template <typename T, typename W, int kN, bool kAny, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1)
 norm_backward_kernel(const NormBackwardArgs a, int stages, int tpr) {
@@ -848,8 +848,8 @@ cudaError_t backward_ring(const NormBackwardArgs& a, int64_t vectors, int64_t gr
     };
     if constexpr (kN * V <= 16) {
         // Rows that leave a block of 512 threads half empty: two groups of 320 threads, with 96 registers
-        // (8192 x 5120 BF16: 57 us, one group of 128 registers 71 us; where 512 threads hold as many groups
-        // more registers are faster: 16384 x 4096 80 us against 82).
+        // (8192 x 5120 BF16: 51 us, one group of 128 registers 63 us; where 512 threads hold as many groups
+        // more registers are faster: 16384 x 4096 71 us against 76).
         if (tpr > kRingThreads / 2 && tpr <= kManyThreads / 2)
             return go(norm_backward_kernel<T, W, kN, kAny, kManyThreads>, kManyThreads);
     }
@@ -886,7 +886,8 @@ cudaError_t norm_backward_launch(const NormBackwardArgs& a, cudaStream_t stream)
         e = backward_ring<T, W, 16 / V, kAny>(a, vectors, parts, stream);
     } else if (vectors <= kRingThreads * (32 / V)) {   // 16384 columns: one stage at least beside the weights
         e = backward_ring<T, W, 32 / V, kAny>(a, vectors, parts, stream);
-    } else {
+    } else {   // off the grid from 16384 less a vector's elements on, as such a row lies in one vector more
+               // (2048 x 16373 BF16 73 us in the ring, 2048 x 16381 so 288 us, 2048 x 32768 600 us)
         norm_backward_long_kernel<T, W><<<static_cast<unsigned>(parts), 1024, 0, stream>>>(a);
         e = cudaGetLastError();
     }
@@ -905,7 +906,8 @@ cudaError_t by_types(bool f32, bool params_f32, F f) {
 }  // namespace
 
 // Blocks of the backward pass at most, each with 2 x cols column sums: one an SM, three for
-// the short rows that need no ring, fewer where the sums would take more than 80 MB.
+// the short rows that need no ring, fewer where the sums would take more than 80 MB, but 8 at least
+// (512 MB of sums at 2^23 columns).
 int64_t norm_partials(int64_t rows, int64_t cols) {
     int64_t most = cols <= kShortCols ? 3 * kSMs : kSMs;
     if (cols > 65536) most = most * 65536 / cols;
