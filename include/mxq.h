@@ -672,6 +672,133 @@ mxq_status mxq_clip_grad_norm(const mxq_grad_desc* grads, int32_t count, float m
 /* Host only; 0 for a bad count. */
 size_t mxq_grad_norm_workspace_size(int32_t count);
 
+/*
+ * ---- MXFP4, and activations kept in 8 bits ----------------------------------
+ *
+ * The same microscaling with 4-bit elements: quantization along either axis, dense products and
+ * the experts' products on the tensor cores, the values that a payload stands for; and the activation
+ * between two products, its input kept in E4M3 for the backward pass.  Conventions are those
+ * of the operators around the experts' products (inputs of mxq_dtype that may start at any element,
+ * arithmetic in FP32, results rounded once, the same on every call), except that
+ * payloads and scales are 16-byte aligned.
+ *
+ *   element  E2M1: 1 sign, 2 exponent, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; two a
+ *            byte, the first in the low half.
+ *   rule     e = ceil(log2(amax/6)), -127 at least; amax 0 -> -127.  q = E2M1 of x * 2^-e, to nearest even.
+ *            A group holding NaN or Inf gets scale 0xFF (NaN) and codes 7 | sign(x).
+ *   payload  of a matrix [R, C] quantized along C: R rows of 16 * ceil(C/32) bytes.  The last group of a
+ *            row is filled up with zeros where 32 does not divide C.
+ *   scales   as for 8-bit payloads, ceil(C/32) a row (mxq_scale_bytes(R, 32 * ceil(C/32), layout) bytes).
+ */
+
+/* Elements of a payload. */
+typedef enum {
+    MXQ_ELEM_E4M3 = 0,
+    MXQ_ELEM_E5M2 = 1,
+    MXQ_ELEM_E2M1 = 2
+} mxq_element;
+
+/*
+ * MXFP4 quantization of `batch` matrices [rows, cols] (row stride ld >= cols, matrix b at x + b *
+ * batch_stride, which is ignored for one matrix) along their columns (row copy) and along their rows (column
+ * copy), the two operand forms that a layer's three products read.
+ *
+ * q_row, s_row  payload [rows, .] and scales of the row copy;
+ * q_col, s_col  of the transposed matrix [cols, rows].
+ * Either pair may be NULL, not both.  The outputs of matrix b follow those of matrix b - 1.
+ * Scales in `layout`; tiled padding is written as zero.  batch <= 65535; rows and cols up to
+ * 2^31 - 4096, batch * ceil(rows/128) * ceil(cols/128) below 2^31.  An empty matrix writes nothing.
+ */
+mxq_status mxq_quant_mxfp4(const void* x, mxq_dtype dtype, int64_t batch, int64_t rows, int64_t cols, int64_t ld,
+                           int64_t batch_stride, void* q_row, void* s_row, void* q_col, void* s_col,
+                           mxq_scale_layout layout, mxq_stream_t stream);
+
+/*
+ * The row copy of rows sorted by expert, with the scales tiled per expert for
+ * mxq_grouped_gemm_mxfp4: the rows of expert g, [off[g], off[g+1]), are rows 0, 1, .. of their own
+ * MMA-tiled layout, which starts at 128-row band floor(off[g] / 128) + g of s (ceil(n_g / 128) bands for n_g rows
+ * always fit before the next expert's; band b at b * ceil(cols/128) * 512 bytes).
+ *
+ * group_offsets  DEVICE int64 [G+1], as mxq_moe_plan gives them: 0 = off[0] <= ... <= off[G] <= rows.
+ *                Offsets that break the rule give unspecified results, never an access out of bounds.
+ * bands_cap      bands of s, at least ceil(rows/128) + G.
+ * Rows behind off[G] and the padding of a band are not written.  1 <= G <= 1024.
+ */
+mxq_status mxq_quant_mxfp4_grouped(const void* x, mxq_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                                   const int64_t* group_offsets, int32_t G, int64_t bands_cap, void* q, void* s,
+                                   mxq_stream_t stream);
+
+/*
+ * The values that a payload [rows, cols] and its scales (one per 32 elements of a row) stand for:
+ * out = q * 2^(s - 127), NaN where the scale is 0xFF.  E2M1, E4M3 and E5M2 payloads, those of
+ * this library's quantizers and of mxq_activation among them.
+ *
+ * ldq   row stride of q in bytes (E2M1: at least 16 * ceil(cols/32), q 4-byte aligned and ldq a multiple of 4).
+ * lds   row stride of plain scales (at least ceil(cols/32)); ignored for tiled ones.
+ * out   [rows, cols] of dtype, row stride ldo.  E4M3 and E2M1 values are exact in either type
+ *       (below 2^-133 BF16 rounds).
+ */
+mxq_status mxq_dequant_1x32(const void* q, const void* s, mxq_element element, int64_t rows, int64_t cols, int64_t ldq,
+                            int64_t lds, mxq_scale_layout layout, void* out, mxq_dtype dtype, int64_t ldo,
+                            mxq_stream_t stream);
+
+/*
+ * Product of MXFP4 operands: y[m, n] = sum_k deq(A)[m, k] * deq(B)[n, k], FP32 accumulation on the tensor
+ * cores, rounded once to BF16.
+ *
+ * a_q, a_s  payload [M, .] and MMA-tiled scales of A [M, K]; b_q, b_s of B [N, K].
+ * y         BF16 [M, N], row stride ldy >= N.  16-byte aligned rows run fastest.
+ * Any M, N, K (up to 2^31 - 4096 each); K == 0 writes zeros.  The operands of a layer's training step are
+ * those of mxq_gemm_bf16out: forward X and W row copies, dX the row copy of dY and the column copy of W, dW
+ * the column copies of dY and X.
+ */
+mxq_status mxq_gemm_mxfp4(const void* a_q, const void* a_s, const void* b_q, const void* b_s, int64_t M, int64_t N,
+                          int64_t K, void* y, int64_t ldy, mxq_stream_t stream);
+
+/*
+ * The experts' products: y[r, n] = sum_k deq(A)[r, k] * deq(B_g)[n, k] for the rows r of expert g.
+ *
+ * a_q, a_s       payload [M_total, .] and scales of mxq_quant_mxfp4_grouped with the same group_offsets and
+ *                bands_cap (a_bands_cap, at least ceil(M_total/128) + G).
+ * b_q, b_s       payloads [G, N, .] and MMA-tiled scales of each expert's [N, K] one after the other: the row
+ *                (forward) or column (input gradient) copies of mxq_quant_mxfp4 on the stacked weights.
+ * group_offsets  DEVICE int64 [G+1], read on the device: 0 = off[0] <= ... <= off[G] <= M_total.  Offsets that
+ *                break the rule give unspecified rows, never an access out of bounds.
+ * y              BF16 [M_total, N], row stride ldy >= N; rows behind off[G] are left as they are.
+ * 1 <= G <= 1024, K >= 1, G * N up to 2^31 - 4096.
+ */
+mxq_status mxq_grouped_gemm_mxfp4(const void* a_q, const void* a_s, int64_t a_bands_cap, const void* b_q,
+                                  const void* b_s, const int64_t* group_offsets, int32_t G, int64_t M_total, int64_t N,
+                                  int64_t K, void* y, int64_t ldy, mxq_stream_t stream);
+
+typedef enum {
+    MXQ_ACT_SILU = 0,   /* f(g) = g / (1 + exp(-g)) */
+    MXQ_ACT_GELU = 1    /* f(g) = g (1 + erf(g / sqrt 2)) / 2 */
+} mxq_act;
+
+/*
+ * The activation between two products: y = f(g) u with z = [g | u] (gated = 1), or y = f(z) (gated = 0).
+ *
+ * z     [rows, 2 inter] or [rows, inter] of dtype, row stride ldz.
+ * y     [rows, inter] of dtype, row stride ldy.
+ * q, s  optional (both or neither): z in E4M3 for the backward pass, payload bytes [rows, 2 inter] or [rows, inter]
+ *       and plain E8M0 scales [rows, 2 ceil(inter/32)] or [rows, ceil(inter/32)], dense; g and u in groups of
+ *       32 of their own.  8.25 bits instead of the input's 16 or 32.  A group with a NaN or an infinity
+ *       comes back as NaN.
+ */
+mxq_status mxq_activation(const void* z, mxq_dtype dtype, int64_t rows, int64_t inter, int64_t ldz, mxq_act kind,
+                          int32_t gated, void* y, int64_t ldy, void* q, void* s, mxq_stream_t stream);
+
+/*
+ * Its gradients from dy [rows, inter] and the checkpoint, whose values g', u' take the place of z:
+ *   dz = [dy u' f'(g') | dy f(g')], or dy f'(z');   y = f(g') u' or f(z') (optional: the next
+ * product's weight gradient needs it, and it need not be kept).
+ * dz [rows, 2 inter] or [rows, inter] of dtype, row stride lddz; y may be NULL (ldy is then ignored).
+ */
+mxq_status mxq_activation_backward(const void* dy, mxq_dtype dtype, int64_t lddy, const void* q, const void* s,
+                                   int64_t rows, int64_t inter, mxq_act kind, int32_t gated, void* dz, int64_t lddz,
+                                   void* y, int64_t ldy, mxq_stream_t stream);
+
 /* Waits for the work queued on `stream` (synchronizes the host with it), then
  * returns MXQ_ERR_TIMEOUT if any kernel of this library on the current device
  * recorded a bounded wait that ran out since the last call, MXQ_ERR_CUDA if

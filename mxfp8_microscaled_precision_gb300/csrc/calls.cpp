@@ -1,5 +1,5 @@
 // calls.cpp -- the calls of libmxq that run in every decoding step (mxq.h, operators
-// around the experts' products) as a CPython extension module: the checks of the
+// around the experts' products; MXFP4, and activations kept in 8 bits) as a CPython extension module: the checks of the
 // tensors, the allocation of results and workspaces, the current stream and the call.
 //
 // For a single token the host's share is most of the time.  Through ctypes a call of 13 to 18
@@ -535,6 +535,245 @@ PyObject* clip_grad_norm(Args a) {
     return PyTuple_Pack(2, norm.get(), out.get());
 }
 
+// ---- MXFP4, and activations kept in 8 bits ---------------------------------------------------
+
+int64_t groups_of(int64_t cols) { return (cols + 31) / 32; }
+
+int64_t scale_bytes(int64_t rows, int64_t cols, mxq_scale_layout layout) {
+    return static_cast<int64_t>(mxq_scale_bytes(rows, 32 * groups_of(cols), layout));
+}
+
+// A contiguous uint8 CUDA tensor of this many bytes, whatever its shape.
+void* bytes_of(PyObject* o, const char* name, int64_t size) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.scalar_type() != at::kByte || !t.is_cuda() || !t.is_contiguous() || t.numel() != size)
+        throw Refused{std::string(name) + " must be a contiguous uint8 CUDA tensor of " + std::to_string(size) + " bytes"};
+    same_device(t, name);
+    return t.data_ptr();
+}
+
+// A given matrix of this type and shape, or a new one.
+void* matrix_out(Results& got, PyObject* given, const char* name, const at::Tensor& like, mxq_dtype type, int64_t rows,
+                 int64_t cols, int64_t* ld) {
+    const at::ScalarType scalar = type == MXQ_F32 ? at::kFloat : at::kBFloat16;
+    if (given == Py_None) {
+        *ld = cols;
+        return got.add(fresh(like, {rows, cols}, scalar));
+    }
+    const Matrix m = matrix(tensor(given, name), name);
+    if (m.type != type || m.rows != rows || m.cols != cols)
+        throw Refused{std::string(name) + " must be " + name_of(scalar) + " " + shape_of({rows, cols})};
+    *ld = m.ld;
+    got.add(given);
+    return m.data;
+}
+
+// A size that is an argument: what the library refuses is refused before memory is asked for.
+int64_t size_arg(PyObject* o, const char* name) {
+    const int64_t v = integer(o);
+    if (v < 0) throw Refused{std::string(name) + " must not be negative"};
+    if (v > (int64_t(1) << 31) - 4096) check(MXQ_ERR_UNSUPPORTED_SHAPE, name);
+    return v;
+}
+
+mxq_scale_layout layout_of(PyObject* o) { return static_cast<mxq_scale_layout>(integer32(o)); }
+
+// Payload and scales of one copy of `batch` matrices [rows, cols], as results.
+struct Copy4 {
+    void *q = nullptr, *s = nullptr;
+    Copy4(Results& got, PyObject* q_out, PyObject* s_out, bool wanted, const char* q_name, const char* s_name,
+          const at::Tensor& like, bool batched, int64_t batch, int64_t rows, int64_t cols, mxq_scale_layout layout) {
+        if (!wanted) {
+            if (q_out != Py_None || s_out != Py_None) throw Refused{std::string(q_name) + " is given and not asked for"};
+            got.add(Py_None);
+            got.add(Py_None);
+            return;
+        }
+        const int64_t groups = groups_of(cols), size = scale_bytes(rows, cols, layout);
+        if (batched) {
+            q = got.dense(q_out, q_name, like, at::kByte, {batch, rows, 16 * groups});
+            s = layout == MXQ_SCALE_ROWMAJOR ? got.dense(s_out, s_name, like, at::kByte, {batch, rows, groups})
+                                             : got.dense(s_out, s_name, like, at::kByte, {batch, size});
+        } else {
+            q = got.dense(q_out, q_name, like, at::kByte, {rows, 16 * groups});
+            s = layout == MXQ_SCALE_ROWMAJOR ? got.dense(s_out, s_name, like, at::kByte, {rows, groups})
+                                             : got.dense(s_out, s_name, like, at::kByte, {size});
+        }
+    }
+};
+
+// (x, row, col, layout, out)
+PyObject* quant_mxfp4(Args a) {
+    const at::Tensor& x = tensor(a[0], "x");
+    const int code = code_of(x);
+    const bool batched = x.dim() == 3;
+    if (code < 0 || (x.dim() != 2 && !batched) || !x.is_cuda())
+        throw Refused{"x must be a 2-D or 3-D bfloat16 or float32 CUDA tensor"};
+    same_device(x, "x");
+    const int at0 = batched ? 1 : 0;
+    const int64_t batch = batched ? x.size(0) : 1, rows = x.size(at0), cols = x.size(at0 + 1);
+    if (x.stride(at0 + 1) != 1 && cols > 1) throw Refused{"x must have unit stride along its last axis"};
+    const int64_t ld = rows > 1 || x.stride(at0) > cols ? x.stride(at0) : cols;
+    const bool row = integer(a[1]) != 0, col = integer(a[2]) != 0;
+    if (!row && !col) throw Refused{"neither copy is asked for"};
+    const mxq_scale_layout layout = layout_of(a[3]);
+    const Given out(a[4], 4);
+    Results got;
+    const Copy4 r(got, out[0], out[1], row, "q_row", "s_row", x, batched, batch, rows, cols, layout);
+    const Copy4 c(got, out[2], out[3], col, "q_col", "s_col", x, batched, batch, cols, rows, layout);
+    check(mxq_quant_mxfp4(x.data_ptr(), static_cast<mxq_dtype>(code), batch, rows, cols, ld, batched ? x.stride(0) : 0, r.q,
+                          r.s, c.q, c.s, layout, stream_of(x)),
+          "mxq_quant_mxfp4");
+    return got.tuple();
+}
+
+// The experts' offsets [G + 1]; more experts than the library takes are refused before memory is asked for.
+int32_t offsets_of(PyObject* o, const int64_t** data, const char* call) {
+    const at::Tensor& t = tensor(o, "offsets");
+    if (t.dim() != 1 || t.size(0) < 2) throw Refused{"offsets must be int64 [experts + 1]"};
+    if (t.size(0) > 1025) check(MXQ_ERR_UNSUPPORTED_SHAPE, call);
+    *data = static_cast<const int64_t*>(dense(t, "offsets", at::kLong, {t.size(0)}));
+    return narrow(t.size(0) - 1);
+}
+
+// (x, offsets, out)
+PyObject* quant_mxfp4_grouped(Args a) {
+    const at::Tensor& like = tensor(a[0], "x");
+    const Matrix x = matrix(like, "x");
+    const int64_t* offsets;
+    const int32_t G = offsets_of(a[1], &offsets, "mxq_quant_mxfp4_grouped");
+    const int64_t bands = (x.rows + 127) / 128 + G;
+    const Given out(a[2], 2);
+    Results got;
+    void* q = got.dense(out[0], "q", like, at::kByte, {x.rows, 16 * groups_of(x.cols)});
+    void* s = got.dense(out[1], "s", like, at::kByte, {bands * ((x.cols + 127) / 128) * 512});
+    check(mxq_quant_mxfp4_grouped(x.data, x.type, x.rows, x.cols, x.ld, offsets, G, bands, q, s, stream_of(like)),
+          "mxq_quant_mxfp4_grouped");
+    return got.tuple();
+}
+
+// (q, s, cols, element, layout, dtype, out)
+PyObject* dequant_1x32(Args a) {
+    const at::Tensor& q = tensor(a[0], "q");
+    const at::Tensor& s = tensor(a[1], "s");
+    if (q.scalar_type() != at::kByte || q.dim() != 2 || !q.is_cuda() || (q.stride(1) != 1 && q.size(1) > 1))
+        throw Refused{"q must be a 2-D uint8 CUDA tensor with unit stride along its last axis"};
+    same_device(q, "q");
+    const int64_t rows = q.size(0), cols = size_arg(a[2], "cols"), groups = groups_of(cols);
+    const mxq_element element = static_cast<mxq_element>(integer32(a[3]));
+    const mxq_scale_layout layout = layout_of(a[4]);
+    const mxq_dtype type = static_cast<mxq_dtype>(integer32(a[5]));
+    const int64_t width = element == MXQ_ELEM_E2M1 ? 16 * groups : cols;
+    if (q.size(1) != width) throw Refused{"q must have " + std::to_string(width) + " bytes a row"};
+    int64_t lds = groups;
+    const void* scales;
+    if (layout == MXQ_SCALE_MMA_TILED) {
+        scales = bytes_of(a[1], "s", scale_bytes(rows, cols, layout));
+    } else {
+        if (s.scalar_type() != at::kByte || s.dim() != 2 || !s.is_cuda() || s.size(0) != rows || s.size(1) != groups ||
+            (s.stride(1) != 1 && groups > 1))
+            throw Refused{"s must be a uint8 CUDA tensor " + shape_of({rows, groups}) + " with unit stride along its last axis"};
+        same_device(s, "s");
+        if (rows > 1) lds = s.stride(0);
+        scales = s.data_ptr();
+    }
+    Results got;
+    int64_t ld;
+    void* out = matrix_out(got, a[6], "out", q, type, rows, cols, &ld);
+    check(mxq_dequant_1x32(q.data_ptr(), scales, element, rows, cols, rows > 1 || q.stride(0) > width ? q.stride(0) : width,
+                           lds, layout, out, type, ld, stream_of(q)),
+          "mxq_dequant_1x32");
+    return got.one();
+}
+
+// (a_q, a_s, b_q, b_s, M, N, K, out)
+PyObject* gemm_mxfp4(Args a) {
+    const at::Tensor& like = tensor(a[0], "a_q");
+    const int64_t M = size_arg(a[4], "M"), N = size_arg(a[5], "N"), K = size_arg(a[6], "K"), row = 16 * groups_of(K);
+    const void* a_q = bytes_of(a[0], "a_q", M * row);
+    const void* a_s = bytes_of(a[1], "a_s", scale_bytes(M, K, MXQ_SCALE_MMA_TILED));
+    const void* b_q = bytes_of(a[2], "b_q", N * row);
+    const void* b_s = bytes_of(a[3], "b_s", scale_bytes(N, K, MXQ_SCALE_MMA_TILED));
+    Results got;
+    int64_t ld;
+    void* y = matrix_out(got, a[7], "out", like, MXQ_BF16, M, N, &ld);
+    check(mxq_gemm_mxfp4(a_q, a_s, b_q, b_s, M, N, K, y, ld, stream_of(like)), "mxq_gemm_mxfp4");
+    return got.one();
+}
+
+// (a_q, a_s, b_q, b_s, offsets, N, K, out)
+PyObject* grouped_gemm_mxfp4(Args a) {
+    const at::Tensor& like = tensor(a[0], "a_q");
+    if (like.dim() != 2) throw Refused{"a_q must be 2-D"};
+    const int64_t M = like.size(0), N = size_arg(a[5], "N"), K = size_arg(a[6], "K"), row = 16 * groups_of(K);
+    const int64_t* offsets;
+    const int32_t G = offsets_of(a[4], &offsets, "mxq_grouped_gemm_mxfp4");
+    const int64_t bands = (M + 127) / 128 + G;
+    const void* a_q = bytes_of(a[0], "a_q", M * row);
+    const void* a_s = bytes_of(a[1], "a_s", bands * ((K + 127) / 128) * 512);
+    const void* b_q = bytes_of(a[2], "b_q", G * N * row);
+    const void* b_s = bytes_of(a[3], "b_s", G * scale_bytes(N, K, MXQ_SCALE_MMA_TILED));
+    Results got;
+    int64_t ld;
+    void* y = matrix_out(got, a[7], "out", like, MXQ_BF16, M, N, &ld);
+    check(mxq_grouped_gemm_mxfp4(a_q, a_s, bands, b_q, b_s, offsets, G, M, N, K, y, ld, stream_of(like)),
+          "mxq_grouped_gemm_mxfp4");
+    return got.one();
+}
+
+// (z, kind, gated, checkpoint, out)
+PyObject* activation(Args a) {
+    const at::Tensor& like = tensor(a[0], "z");
+    const Matrix z = matrix(like, "z");
+    const int32_t gated = integer32(a[2]);
+    if (gated != 0 && z.cols % 2 != 0) throw Refused{"a gated z must have an even number of columns"};
+    const bool keep = integer(a[3]) != 0;
+    const int64_t parts = gated != 0 ? 2 : 1, inter = z.cols / parts;
+    const Given out(a[4], 3);
+    Results got;
+    int64_t ld;
+    void* y = got.matrix(out[0], "y", like, z.type, z.rows, inter, &ld);
+    void *q = nullptr, *s = nullptr;
+    if (keep) {
+        q = got.dense(out[1], "q", like, at::kByte, {z.rows, z.cols});
+        s = got.dense(out[2], "s", like, at::kByte, {z.rows, parts * groups_of(inter)});
+    } else {
+        if (out[1] != Py_None || out[2] != Py_None) throw Refused{"a checkpoint's tensor is given and none is asked for"};
+        got.add(Py_None);
+        got.add(Py_None);
+    }
+    check(mxq_activation(z.data, z.type, z.rows, inter, z.ld, static_cast<mxq_act>(integer32(a[1])), gated, y, ld, q, s,
+                         stream_of(like)),
+          "mxq_activation");
+    return got.tuple();
+}
+
+// (dy, q, s, kind, gated, output, out)
+PyObject* activation_backward(Args a) {
+    const at::Tensor& like = tensor(a[0], "dy");
+    const Matrix dy = matrix(like, "dy");
+    const int32_t gated = integer32(a[4]);
+    const int64_t parts = gated != 0 ? 2 : 1;
+    const void* q = dense(a[1], "q", at::kByte, {dy.rows, parts * dy.cols});
+    const void* s = dense(a[2], "s", at::kByte, {dy.rows, parts * groups_of(dy.cols)});
+    const bool again = integer(a[5]) != 0;
+    const Given out(a[6], 2);
+    Results got;
+    int64_t lddz, ldy = 0;
+    void* dz = got.matrix(out[0], "dz", like, dy.type, dy.rows, parts * dy.cols, &lddz);
+    void* y = nullptr;
+    if (again) {
+        y = got.matrix(out[1], "y", like, dy.type, dy.rows, dy.cols, &ldy);
+    } else {
+        if (out[1] != Py_None) throw Refused{"y is given and not asked for"};
+        got.add(Py_None);
+    }
+    check(mxq_activation_backward(dy.data, dy.type, dy.ld, q, s, dy.rows, dy.cols, static_cast<mxq_act>(integer32(a[3])), gated,
+                                  dz, lddz, y, ldy, stream_of(like)),
+          "mxq_activation_backward");
+    return got.tuple();
+}
+
 // ---- the module -----------------------------------------------------------------------------
 
 // f(args) with every exception as a Python error.
@@ -569,7 +808,9 @@ PyObject* set_error(Args a) {
 PyMethodDef methods[] = {ENTRY(route, 11), ENTRY(route_backward, 7), ENTRY(moe_plan, 3), ENTRY(moe_dispatch, 3),
                          ENTRY(moe_combine, 4), ENTRY(moe_combine_backward, 5), ENTRY(layer_norm, 5),
                          ENTRY(layer_norm_backward, 6), ENTRY(grad_norm, 1), ENTRY(clip_grad_norm, 4),
-                         ENTRY(set_error, 1), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(quant_mxfp4, 5), ENTRY(quant_mxfp4_grouped, 3), ENTRY(dequant_1x32, 7),
+                         ENTRY(gemm_mxfp4, 8), ENTRY(grouped_gemm_mxfp4, 8), ENTRY(activation, 5),
+                         ENTRY(activation_backward, 7), ENTRY(set_error, 1), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mxqcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

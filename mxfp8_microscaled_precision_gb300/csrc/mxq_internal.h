@@ -217,4 +217,58 @@ int clip_partials(int count);
 cudaError_t launch_clip(const ClipTensor* tensors, int count, bool scale_too, float max_norm, float eps, float* norm,
                         float* partial, cudaStream_t stream);
 
+// ---- MXFP4, and activations kept in 8 bits (fp4.cu, gemm_fp4.cu, act.cu) ----
+
+// MXFP4 quantization of `batch` matrices (see mxq_quant_mxfp4).  offsets (one matrix, row copy only): the
+// scales tiled by expert in bands_cap bands (see mxq_quant_mxfp4_grouped).
+struct Quant4Args {
+    const void* x;
+    int64_t batch, rows, cols, ld, batch_stride;
+    void *q_row, *s_row, *q_col, *s_col;      // either copy may be null
+    int64_t s_row_bytes, s_col_bytes;         // of one matrix
+    bool tiled;
+    const int64_t* offsets;
+    int G;
+    int64_t bands_cap;
+};
+cudaError_t launch_quant_mxfp4(const Quant4Args& a, bool f32, cudaStream_t stream);
+
+// Values of a microscaled payload (see mxq_dequant_1x32); lds: row stride of plain scales.
+struct Dequant4Args {
+    const void *q, *s;
+    int64_t rows, cols, ldq, lds;
+    bool tiled;
+    void* out;
+    int64_t ldo;
+};
+cudaError_t launch_dequant(const Dequant4Args& a, int format, bool f32, cudaStream_t stream);
+
+// Product of MXFP4 operands (see mxq_gemm_mxfp4, mxq_grouped_gemm_mxfp4); offsets null: dense.
+struct Gemm4Args {
+    const void *a_q, *a_s, *b_q, *b_s;
+    int64_t M, N, K;
+    void* y;
+    int64_t ldy;
+    const int64_t* offsets;
+    int G;
+    int64_t bands_cap;
+};
+cudaError_t launch_gemm_mxfp4(const DeviceInfo& dev, const Gemm4Args& a, cudaStream_t stream);
+
+// The activation between two products (see mxq_activation); q and s null: nothing is kept.
+struct ActArgs {
+    int64_t rows, inter, ldz, ldy;
+    const void* z;
+    void *y, *q, *s;
+};
+cudaError_t launch_activation(const ActArgs& a, bool f32, int kind, bool gated, cudaStream_t stream);
+
+// Its backward pass; y may be null.
+struct ActBackwardArgs {
+    int64_t rows, inter, lddy, lddz, ldy;
+    const void *dy, *q, *s;
+    void *dz, *y;
+};
+cudaError_t launch_activation_backward(const ActBackwardArgs& a, bool f32, int kind, bool gated, cudaStream_t stream);
+
 }  // namespace mxq

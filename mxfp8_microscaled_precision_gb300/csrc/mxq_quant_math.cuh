@@ -77,5 +77,75 @@ __device__ __forceinline__ uint32_t nan_bytes4(uint32_t w0, uint32_t w1) {
            (w1 & 0x80000000u);
 }
 
+// ---- from FP32 bits (the operators whose inputs are BF16 or FP32) ------------------------------
+
+// Element formats of a payload.
+constexpr int kE4M3 = 0, kE5M2 = 1, kE2M1 = 2;
+
+// rceil exponent of a finite, non-negative amax given as FP32 bits: ceil(log2(amax / most)), -127 at
+// least, most = 448 = 1.75 2^8, 57344 = 1.75 2^15 or 6 = 1.5 2^2: the ceiling steps up where the
+// 23-bit mantissa exceeds most's.  Zero and subnormal amax lie below -127.
+template <int kFormat>
+__device__ __forceinline__ int rceil_exponent_f32(uint32_t amax_bits) {
+    constexpr int kLog = kFormat == kE4M3 ? 8 : kFormat == kE5M2 ? 15 : 2;
+    constexpr uint32_t kMantissa = kFormat == kE2M1 ? 0x400000u : 0x600000u;
+    const int e = static_cast<int>(amax_bits >> 23) - 127 - kLog + ((amax_bits & 0x7FFFFFu) > kMantissa ? 1 : 0);
+    return e < -127 ? -127 : e;
+}
+
+constexpr uint32_t kInfBits = 0x7F800000u;   // amax bits of a group with a NaN or an infinity are at least this
+
+// 2^e for e in [-127, 127]; NaN for the code 0xFF (e = 128).
+__device__ __forceinline__ float scale_of(uint32_t code) {
+    return __uint_as_float(code == 0u ? 0x00400000u : code == 0xFFu ? 0x7FC00000u : code << 23);
+}
+
+// Eight floats -> eight E2M1 codes, round to nearest even, saturating to +-6; the first one in the lowest half byte.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// Eight E2M1 codes -> four pairs of halves (exact).
+__device__ __forceinline__ void cvt_f16_e2m1x8(uint32_t codes, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+}
+
+// Two FP8 codes -> a pair of halves (exact; NaN stays NaN, an E5M2 infinity infinite).
+template <int kFormat>
+__device__ __forceinline__ uint32_t cvt_f16_fp8x2(uint32_t codes) {
+    uint32_t h;
+    if constexpr (kFormat == kE4M3)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+    else
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+    return h;
+}
+
+__device__ __forceinline__ float f16_lo(uint32_t h) {
+    float f;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(f) : "r"(h));
+    return f;
+}
+__device__ __forceinline__ float f16_hi(uint32_t h) {
+    float f;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, b;\n\t}" : "=f"(f) : "r"(h));
+    return f;
+}
 
 }  // namespace mxq

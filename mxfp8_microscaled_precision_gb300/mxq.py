@@ -2,7 +2,7 @@
 
 Argument marshalling only: tensors are allocated by PyTorch on the current
 CUDA device, their pointers and sizes go through ctypes (the calls of the last
-section: through an extension module) to the C ABI, and
+two sections: through an extension module) to the C ABI, and
 every step of the computation runs in the library's CUDA kernels on the
 current stream.  There is no fallback: if the library is missing or the
 device is not a GB300 the calls raise.
@@ -106,6 +106,13 @@ def lib() -> ctypes.CDLL:
         L.mxq_clip_grad_norm.argtypes = [P, I32, F, F, P, P, SZ, P]
         L.mxq_grad_norm_workspace_size.argtypes = [I32]
         L.mxq_grad_norm_workspace_size.restype = SZ
+        L.mxq_quant_mxfp4.argtypes = [P, S, I64, I64, I64, I64, I64, P, P, P, P, S, P]
+        L.mxq_quant_mxfp4_grouped.argtypes = [P, S, I64, I64, I64, P, I32, I64, P, P, P]
+        L.mxq_dequant_1x32.argtypes = [P, P, S, I64, I64, I64, I64, S, P, S, I64, P]
+        L.mxq_gemm_mxfp4.argtypes = [P, P, P, P, I64, I64, I64, P, I64, P]
+        L.mxq_grouped_gemm_mxfp4.argtypes = [P, P, I64, P, P, P, I32, I64, I64, I64, P, I64, P]
+        L.mxq_activation.argtypes = [P, S, I64, I64, I64, S, I32, P, I64, P, P, P]
+        L.mxq_activation_backward.argtypes = [P, S, I64, P, P, I64, I64, S, I32, P, I64, P, I64, P]
         for f in ("mxq_quant_1x32_dual", "mxq_quant_32x32", "mxq_gemm_bf16out",
                   "mxq_grouped_gemm", "mxq_get_device_status", "mxq_debug_wait_timeout",
                   "mxq_quant_1x32_dual_batched", "mxq_quant_1x32_cols_grouped",
@@ -115,7 +122,8 @@ def lib() -> ctypes.CDLL:
                   "mxq_grouped_gemm_group_tiled", "mxq_scale_regroup_rows", "mxq_quant_32x32_fmt",
                   "mxq_route", "mxq_route_backward", "mxq_moe_plan", "mxq_moe_dispatch", "mxq_moe_combine",
                   "mxq_moe_combine_backward", "mxq_layer_norm", "mxq_layer_norm_backward", "mxq_grad_norm",
-                  "mxq_clip_grad_norm"):
+                  "mxq_clip_grad_norm", "mxq_quant_mxfp4", "mxq_quant_mxfp4_grouped", "mxq_dequant_1x32", "mxq_gemm_mxfp4",
+                  "mxq_grouped_gemm_mxfp4", "mxq_activation", "mxq_activation_backward"):
             getattr(L, f).restype = S
         _lib = L
         return L
@@ -615,6 +623,63 @@ def clip_grad_norm(grads, max_norm: float, eps: float = 1e-6, out=None):
     gradients themselves to scale in place, or None for new ones.  Returns (norm fp32
     scalar on the device, the list of outputs)."""
     return _calls().clip_grad_norm(_list_of(grads), max_norm, eps, None if out is None else list(out))
+
+
+# ---- MXFP4, and activations kept in 8 bits (see the same section of mxq.h) ----
+
+_ELEMENTS = {"e4m3": 0, "e5m2": 1, "e2m1": 2}
+_ACTS = {"silu": 0, "gelu": 1}
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def quant_mxfp4(x: torch.Tensor, row: bool = True, col: bool = True, layout="tiled", out=None):
+    """MXFP4 quantization (see mxq_quant_mxfp4) of x [R, C], or of each matrix of x [B, R, C] (stacked
+    expert weights), bf16 or fp32, any sizes.  Returns (q_row [R, 16 ceil(C/32)], s_row, q_col
+    [C, 16 ceil(R/32)], s_col), uint8, with B in front for a batch; copies not asked for
+    are None.  `out` may supply the tensors (None for a new one)."""
+    return _calls().quant_mxfp4(x, 1 if row else 0, 1 if col else 0, _layout(layout), out)
+
+
+def quant_mxfp4_grouped(x: torch.Tensor, offsets: torch.Tensor, out=None):
+    """The row copy of rows sorted by expert with its scales tiled per expert (see mxq_quant_mxfp4_grouped), the
+    left operand of grouped_gemm_mxfp4: x [M, C], offsets int64 [experts + 1] from moe_plan.  Returns
+    (q [M, 16 ceil(C/32)], s); what belongs to no expert is not written."""
+    return _calls().quant_mxfp4_grouped(x, offsets, out)
+
+
+def dequant_1x32(q: torch.Tensor, s: torch.Tensor, cols: int, fmt="e4m3", layout="tiled", dtype=torch.bfloat16,
+                 out=None) -> torch.Tensor:
+    """The values [R, cols] that a payload q [R, .] with one scale per 32 elements of a row stands for (see
+    mxq_dequant_1x32): fmt "e4m3", "e5m2" or "e2m1", scales tiled or (layout "rowmajor") [R, ceil(cols/32)], as bf16 or
+    fp32.  Restores a checkpoint that one of the quantizers made, or one half of activation's."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be bfloat16 or float32, not {dtype}")
+    return _calls().dequant_1x32(q, s, cols, _of(_ELEMENTS, fmt, "element format"), _layout(layout), _DTYPES[dtype], out)
+
+
+def gemm_mxfp4(a_q, a_s, b_q, b_s, M: int, N: int, K: int, out=None) -> torch.Tensor:
+    """y [M, N] bf16 = deq(A) deq(B)^T of MXFP4 operands with tiled scales (see mxq_gemm_mxfp4), any sizes."""
+    return _calls().gemm_mxfp4(a_q, a_s, b_q, b_s, M, N, K, out)
+
+
+def grouped_gemm_mxfp4(a_q, a_s, b_q, b_s, offsets: torch.Tensor, N: int, K: int, out=None) -> torch.Tensor:
+    """Per-expert y[r] = deq(A)[r] deq(B_g)^T (see mxq_grouped_gemm_mxfp4): a_q, a_s from quant_mxfp4_grouped with
+    the same offsets, b_q, b_s the row copies (of the transposed weights: the column copies) of quant_mxfp4 on
+    stacked weights [experts, N, K].  Returns y [M, N] bf16; rows of no expert are not written."""
+    return _calls().grouped_gemm_mxfp4(a_q, a_s, b_q, b_s, offsets, N, K, out)
+
+
+def activation(z: torch.Tensor, kind="silu", gated: bool = True, checkpoint: bool = True, out=None):
+    """y = f(g) u with z = [g | u], or f(z) without a gate; kind "silu" or "gelu" (see mxq_activation).  Returns
+    (y [M, I], q, s): z in 8 bits for activation_backward, None without a checkpoint (serving)."""
+    return _calls().activation(z, _of(_ACTS, kind, "activation"), 1 if gated else 0, 1 if checkpoint else 0, out)
+
+
+def activation_backward(dy: torch.Tensor, q: torch.Tensor, s: torch.Tensor, kind="silu", gated: bool = True,
+                        output: bool = True, out=None):
+    """Gradient of activation from its checkpoint (see mxq_activation_backward).  Returns (dz, y): y is the
+    activation's output computed again, for the weight gradient of the product behind it (None without `output`)."""
+    return _calls().activation_backward(dy, q, s, _of(_ACTS, kind, "activation"), 1 if gated else 0, 1 if output else 0, out)
 
 
 def get_device_status() -> int:
