@@ -483,20 +483,6 @@ __device__ __forceinline__ void store_quant_staged(const GemmArgs& a, const Prob
         *reinterpret_cast<uint32_t*>(a.ys + tiled_scale_offset(row, g0, ngroups)) = codes;
 }
 
-// Wait for the accumulator hand-off between the MMA warp and the epilogue, on
-// the critical path between tiles: busy polling without suspending the thread
-// (measured 1-4% faster than the suspending probe), bounded, then the timed wait.
-__device__ __forceinline__ bool spin_phase(uint32_t bar, uint32_t parity, const WaitGuard& g) {
-    for (uint32_t i = 0; i < (1u << 20); ++i)
-        if (mbar_test_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity, g);
-}
-
-// Fast path of a bounded wait: one probe inline, the polling loop out of line.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const WaitGuard& g) {
-    return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, g);
-}
-
 template <int BN, int STAGES, bool kMnMajor, int kMode>
 __global__ void __launch_bounds__(Cfg<BN, STAGES, kMode>::kThreads, 1)
     gemm_mxf8_kernel(const __grid_constant__ TensorMaps maps, const GemmArgs p) {

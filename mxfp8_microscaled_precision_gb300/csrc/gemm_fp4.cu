@@ -1,72 +1,821 @@
 // gemm_fp4.cu -- products of MXFP4 operands with BF16 output, dense and grouped by expert.
 //
 //   y[m, n] = sum_k (qa[m, k] 2^ea[m, k/32]) (qb[n, k] 2^eb[n, k/32])
+//
+// tcgen05.mma.kind::mxf4.block_scale: packed E2M1 operands from shared memory, two E8M0 scales a row and
+// instruction from tensor memory, 64 K elements an instruction, FP32 accumulators in tensor memory.  A pipeline stage is
+// 256 K elements: 128 bytes of payload and two 512-byte scale atoms for 128 rows of an operand.
+//
+// Two kernels.  gemm_mxfp4_pair_kernel: 256 x 256 tiles on CTA pairs, for products that fill the device with such
+// tiles.  gemm_mxfp4_rows_kernel: 128 columns of B by up to 128 rows of A on a single CTA, B in the place of the
+// instruction's 128-row operand, so that few rows of A cost few instructions; K split over a cluster where
+// there are few tiles.  Every mbarrier wait is bounded (see mxq_device.cuh).
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "mxq_elem.cuh"
 #include "mxq_internal.h"
-#include "mxq_quant_math.cuh"
 
 namespace mxq {
 namespace {
 
-constexpr int kSide = 16;
+constexpr int kBK = 256;              // K elements of a stage (128 bytes of payload)
+constexpr int kBandBytes = 128 * 128; // payload of 128 rows of a stage
+constexpr int kAtom = 512;            // scales of 128 rows and 4 groups
+constexpr int kMaxExperts = 1024;
 
-// One output a thread, FP32 sums.
-template <bool kGrouped>
-__global__ void __launch_bounds__(kSide* kSide) gemm_mxfp4_kernel(const Gemm4Args a) {
-    const int64_t m = blockIdx.y * static_cast<int64_t>(kSide) + threadIdx.y;
-    const int64_t n = blockIdx.x * static_cast<int64_t>(kSide) + threadIdx.x;
-    if (m >= a.M || n >= a.N) return;
-    const int64_t groups = (a.K + 31) >> 5;
-    int64_t a_row = m, b_row = n, b_scale = n;
-    if constexpr (kGrouped) {
-        int lo = 0, hi = a.G;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.offsets[mid] <= m) lo = mid; else hi = mid;
-        }
-        const int64_t first = a.offsets[lo];
-        if (first < 0 || m < first || m >= a.offsets[lo + 1]) return;
-        a_row = (first / 128 + lo) * 128 + (m - first);
-        if (a_row >= a.bands_cap * 128) return;
-        b_row = lo * a.N + n;
-        b_scale = lo * ((a.N + 127) / 128 * 128) + n;
+struct Args {
+    const uint8_t *a_s, *b_s;
+    uint16_t* y;
+    int64_t M, N, ldy;
+    int64_t k_atoms;           // scale atoms of a 128-row band
+    int64_t k_padded;          // K up to a multiple of 32
+    int64_t m_tiles, n_tiles;  // dense
+    int64_t b_bands;           // 128-row bands of an expert's (of B's) scales
+    const int64_t* offsets;    // grouped: [G + 1] on the device
+    int G;
+    int64_t bands_cap;         // grouped: bands of A's scales
+    int y_tma, y_vec;          // the output has a map; its rows hold whole 16-byte vectors
+    int tok_cap, stages, split;   // rows kernel: rows of A in a slot, slots, CTAs along K
+    unsigned int* status;
+    uint64_t wait_limit_ns;
+};
+
+// Offset g, inside [0, M] whatever it holds.
+__device__ __forceinline__ int64_t offset_at(const Args& p, int g) {
+    const int64_t o = p.offsets[g];
+    return o < 0 ? int64_t(0) : (o > p.M ? p.M : o);
+}
+
+// First 128-row band of expert g's scales; its bands end before the next expert's.
+__device__ __forceinline__ int64_t first_band(int64_t first_row, int g) { return first_row / 128 + g; }
+
+// Grouped: prefix[g] = work items of the experts before g; `rows` rows of A an item.  All threads of the block.
+__device__ __forceinline__ void build_prefix(const Args& p, int rows, int* prefix) {
+    for (int g = threadIdx.x; g < p.G; g += blockDim.x) {
+        const int64_t lo = offset_at(p, g), hi = offset_at(p, g + 1);
+        int64_t n = hi > lo ? (hi - lo + rows - 1) / rows : 0;
+        if (first_band(lo, g) + (hi - lo + 127) / 128 > p.bands_cap) n = 0;   // offsets that break the rule
+        prefix[g + 1] = static_cast<int>(n * p.n_tiles);
     }
-    const uint8_t* qa = static_cast<const uint8_t*>(a.a_q) + m * groups * 16;
-    const uint8_t* qb = static_cast<const uint8_t*>(a.b_q) + b_row * groups * 16;
-    const uint8_t* sa = static_cast<const uint8_t*>(a.a_s);
-    const uint8_t* sb = static_cast<const uint8_t*>(a.b_s);
-    float sum = 0.0f;
-    for (int64_t g = 0; g < groups; ++g) {
-        const uint4 va = reinterpret_cast<const uint4*>(qa)[g], vb = reinterpret_cast<const uint4*>(qb)[g];
-        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-        float part = 0.0f;
+    if (threadIdx.x == 0) prefix[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int carry = 0;
+        for (int base = 0; base < p.G; base += 32) {
+            const int g = base + static_cast<int>(threadIdx.x);
+            int v = g < p.G ? prefix[g + 1] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xFFFFFFFFu, v, d);
+                if (static_cast<int>(threadIdx.x) >= d) v += up;
+            }
+            if (g < p.G) prefix[g + 1] = carry + v;
+            carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
+    }
+    __syncthreads();
+}
+
+// The expert of item t.
+__device__ __forceinline__ int expert_of(const int* prefix, int G, int64_t t) {
+    int lo = 0, hi = G;   // the last g with prefix[g] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= t) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Instructions (64 K elements each) that K block kb of k_padded elements needs.
+__device__ __forceinline__ int mmas_of(int64_t k_padded, int64_t kb) {
+    const int64_t left = k_padded - kb * kBK;
+    return left >= kBK ? 4 : static_cast<int>((left + 63) / 64);
+}
+
+// ---- CTA pairs -------------------------------------------------------------------------------
+//
+// Output tiles of 256 x 256 per pair of SMs (cta_group::2).  CTA r of the pair loads 128 rows of A, its 128-row half
+// of B, its two A scale atoms, and multicasts the two scale atoms of its half of B to both (each tensor
+// core needs the scales of all 256 B rows).  One thread of the even CTA issues, per stage, six scale copies
+// and four 256 x 256 x 64 instructions of 128 cycles each.
+//
+// Tensor memory (512 columns): two accumulators of 256 columns that share 64 of them, at 0 and 192, and two
+// slots of 24 columns of scales.  The epilogue of a tile reads the shared columns first and hands them back,
+// so the next tile's instructions wait for a quarter of it only.  A scale slot is written again when the
+// instructions of two stages before have completed.
+struct PairCfg {
+    static constexpr int kStages = 5;
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kThreads = 64 + 32 * kEpiWarps;
+    static constexpr int kSfaBytes = 2 * kAtom, kSfbBytes = 4 * kAtom;
+    static constexpr int kStageBytes = 2 * kBandBytes + kSfaBytes + kSfbBytes;
+    static constexpr int kOffB = 0;
+    static constexpr int kOffA = kOffB + kStages * kBandBytes;
+    static constexpr int kOffSfa = kOffA + kStages * kBandBytes;
+    static constexpr int kOffSfb = kOffSfa + kStages * kSfaBytes;
+    static constexpr int kOffStage = kOffSfb + kStages * kSfbBytes;   // 1024-byte aligned
+    static constexpr int kStageWarpBytes = 32 * 32 * 2;               // a BF16 chunk of 32 rows, twice a warp
+    static constexpr int kOffBar = kOffStage + 2 * kEpiWarps * kStageWarpBytes;
+    static constexpr int kNumBars = 2 * kStages + 3;   // full, empty, accumulator full / handed back, drain
+    static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
+    static constexpr int kOffAbort = kOffTmemSlot + 4;
+    static constexpr int kOffEpiFlag = kOffAbort + 4;
+    static constexpr int kOffPrefix = kOffEpiFlag + 4;
+    static constexpr int kBytes = kOffPrefix + 4 * (kMaxExperts + 1);
+    static constexpr int kAlloc = kBytes + 1024;
+    static constexpr int kTmemCols = 512;
+    static constexpr int kAcc1 = 192;                 // second accumulator
+    static constexpr int kShared = 256 - kAcc1;       // columns of both
+    static constexpr int kTmemScales = kAcc1 + 256, kScaleCols = 24;
+    static_assert(kTmemScales + 2 * kScaleCols <= kTmemCols, "tensor memory budget");
+    static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+    static_assert(kOffStage % 1024 == 0, "swizzle atoms");
+};
+
+struct PairMaps {
+    CUtensorMap a, b, sfa, sfb, y;
+};
+
+struct PairTile {
+    int64_t m0;              // this CTA's first A row (may lie past the matrix)
+    int64_t a_band;          // its A scale band
+    int64_t row_lo, row_hi;  // rows that are stored (empty: none)
+    int64_t n0;              // first output column
+    int64_t b_row, b_band;   // first B row of the pair's tile and its scale band
+};
+
+template <bool kGrouped>
+__device__ __forceinline__ PairTile pair_tile(const Args& p, const int* prefix, int64_t t, uint32_t rank) {
+    PairTile ti;
+    if constexpr (!kGrouped) {
+        constexpr int kBand = 4;   // raster: bands of 1024 rows, columns inside a band
+        const int64_t per_band = kBand * p.n_tiles, band = t / per_band, within = t - band * per_band;
+        const int64_t height = min(static_cast<int64_t>(kBand), p.m_tiles - band * kBand);
+        ti.m0 = (band * kBand + within % height) * 256 + 128 * rank;
+        ti.n0 = within / height * 256;
+        ti.a_band = ti.m0 / 128;
+        ti.row_lo = ti.m0;
+        ti.row_hi = min(ti.m0 + 128, p.M);
+        ti.b_row = ti.n0;
+        ti.b_band = ti.n0 / 128;
+    } else {
+        const int g = expert_of(prefix, p.G, t);
+        const int64_t local = t - prefix[g], lo = offset_at(p, g), hi = offset_at(p, g + 1);
+        ti.n0 = local % p.n_tiles * 256;
+        const int64_t i = 2 * (local / p.n_tiles) + rank;
+        const bool any = lo + 128 * i < hi;   // an odd number of row tiles leaves the last odd CTA without rows
+        ti.m0 = any ? lo + 128 * i : lo;
+        ti.a_band = first_band(lo, g) + (any ? i : 0);
+        ti.row_lo = ti.m0;
+        ti.row_hi = any ? min(ti.m0 + 128, hi) : ti.m0;
+        ti.b_row = static_cast<int64_t>(g) * p.N + ti.n0;
+        ti.b_band = static_cast<int64_t>(g) * p.b_bands + ti.n0 / 128;
+    }
+    return ti;
+}
+
+// 32 x 32 results of a warp (lane l: output row row0 + l, columns n .. n + 31) through its staging buffer: 16-byte
+// chunk j of row r sits at position j ^ ((r >> 1) & 3), the 64-byte swizzle of a tiled bulk copy.  Rows that are
+// all stored leave with one such copy (the map clips columns past N); otherwise by rows, in vectors or
+// element by element.
+__device__ __forceinline__ void store_chunk(const Args& p, const uint32_t (&v)[32], uint32_t stage, int64_t row0,
+                                            int64_t row_lo, int64_t row_hi, int64_t n, int lane, const CUtensorMap* map) {
+    if (n >= p.N) return;
+    if (lane == 0) bulk_wait_read_but_one();   // the copy before the last one has read this buffer
+    __syncwarp();
+    const uint32_t wrow = stage + 64u * static_cast<uint32_t>(lane), swz = static_cast<uint32_t>((lane >> 1) & 3);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint4 o;
+        o.x = cvt_bf16x2(__uint_as_float(v[8 * j + 0]), __uint_as_float(v[8 * j + 1]));
+        o.y = cvt_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
+        o.z = cvt_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
+        o.w = cvt_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
+        sts128(wrow + 16u * (static_cast<uint32_t>(j) ^ swz), o);
+    }
+    if (p.y_tma && row0 >= row_lo && row0 + 32 <= row_hi) {
+        fence_proxy_async_smem();   // the buffer is read by the bulk copy (async proxy)
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(map, static_cast<int32_t>(n), static_cast<int32_t>(row0), stage);
+            bulk_commit_group();
+        }
+        return;
+    }
+    __syncwarp();
+    if (p.y_vec) {
+        const int jj = lane & 3;
+        const int64_t col = n + 8 * jj;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t ha[4], hb[4];
-            cvt_f16_e2m1x8(wa[i], ha);
-            cvt_f16_e2m1x8(wb[i], hb);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part += f16_lo(ha[j]) * f16_lo(hb[j]) + f16_hi(ha[j]) * f16_hi(hb[j]);
+            const int r = 8 * i + (lane >> 2);
+            const uint4 x = lds128_ordered(stage + 64u * static_cast<uint32_t>(r) +
+                                           16u * (static_cast<uint32_t>(jj) ^ static_cast<uint32_t>((r >> 1) & 3)));
+            if (row0 + r < row_lo || row0 + r >= row_hi) continue;
+            uint16_t* to = p.y + (row0 + r) * p.ldy + col;
+            if (col + 8 <= p.N) {
+                *reinterpret_cast<uint4*>(to) = x;
+            } else {
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                for (int c = 0; c < 8 && col + c < p.N; ++c) to[c] = static_cast<uint16_t>(w[c >> 1] >> (16 * (c & 1)));
+            }
         }
-        sum += part * scale_of(sa[tiled_scale_offset(a_row, g, groups)]) * scale_of(sb[tiled_scale_offset(b_scale, g, groups)]);
+    } else if (n + lane < p.N) {
+        for (int r = 0; r < 32; ++r) {
+            if (row0 + r < row_lo || row0 + r >= row_hi) continue;
+            const uint32_t at = stage + 64u * static_cast<uint32_t>(r) +
+                                16u * (static_cast<uint32_t>(lane >> 3) ^ static_cast<uint32_t>((r >> 1) & 3)) +
+                                4u * static_cast<uint32_t>((lane & 7) >> 1);
+            p.y[(row0 + r) * p.ldy + n + lane] = static_cast<uint16_t>(lds32(at) >> (16 * (lane & 1)));
+        }
     }
-    static_cast<bf16_bits*>(a.y)[m * a.ldy + n] = from_float<bf16_bits>(sum);
+    __syncwarp();
+}
+
+template <bool kGrouped>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1)
+    gemm_mxfp4_pair_kernel(const __grid_constant__ PairMaps maps, const Args p) {
+    using L = PairCfg;
+    constexpr int STAGES = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = blockIdx.x & 1u;
+    const bool leader = rank == 0;
+    const uint32_t bar0 = sbase + L::kOffBar;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    const uint32_t tfull_bar = bar0 + 8u * (2 * STAGES), tempty_bar = tfull_bar + 8u, drain_bar = tfull_bar + 16u;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
+    volatile int* epi_flag = reinterpret_cast<volatile int*>(smem + L::kOffEpiFlag);
+    int* prefix = reinterpret_cast<int*>(smem + L::kOffPrefix);
+    const WaitGuard guard{abort_flag, p.status, p.wait_limit_ns};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);    // the even CTA's producer (with both CTAs' bytes)
+            mbar_init(empty_bar(s), 1);   // the even CTA's commit
+        }
+        mbar_init(tfull_bar, 1);
+        mbar_init(tempty_bar, 2 * L::kEpiWarps);   // every epilogue warp of both CTAs
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&maps.a);
+        prefetch_tensormap(&maps.b);
+        prefetch_tensormap(&maps.sfa);
+        prefetch_tensormap(&maps.sfb);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(sbase + L::kOffTmemSlot, L::kTmemCols);
+        tmem_relinquish_pair();
+    }
+    wait_for_previous();
+    int64_t total = p.m_tiles * p.n_tiles;
+    if constexpr (kGrouped) {
+        build_prefix(p, 256, prefix);
+        total = prefix[p.G];
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();   // both CTAs' barriers initialised and tensor memory allocated
+    tc_fence_after();
+    const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffTmemSlot);
+    const int64_t pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+    const int64_t num_kb = (p.k_padded + kBK - 1) / kBK;
+
+    if (warp == 0) {
+        // ---- producer (both CTAs) --------------------------------------------------
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            const uint32_t full0 = leader ? full_bar(0) : mapa_shared(full_bar(0), 0);
+            bool stop = false;
+            for (int64_t t = pair_id; t < total && !stop && !*abort_flag; t += n_pairs) {
+                const PairTile ti = pair_tile<kGrouped>(p, prefix, t, rank);
+                const int32_t ma = static_cast<int32_t>(ti.m0), nb = static_cast<int32_t>(ti.b_row + 128 * rank);
+                const int32_t sfa_row = static_cast<int32_t>(2 * ti.a_band * p.k_atoms);
+                const int32_t sfb_row = static_cast<int32_t>(2 * (ti.b_band + rank) * p.k_atoms);
+                for (int64_t kb = 0; kb < num_kb; ++kb) {
+                    if (!wait_phase(empty_bar(stage), phase ^ 1u, guard)) { stop = true; break; }
+                    const uint32_t fb = full0 + 8u * stage;
+                    if (leader) mbar_arrive_expect_tx(fb, 2u * L::kStageBytes);
+                    const int32_t kx = static_cast<int32_t>(kb * 128), ks = static_cast<int32_t>(4 * kb);
+                    tma_load_2d_pair(sbase + L::kOffA + stage * kBandBytes, &maps.a, kx, ma, fb);
+                    tma_load_2d_pair(sbase + L::kOffB + stage * kBandBytes, &maps.b, kx, nb, fb);
+                    tma_load_2d_pair(sbase + L::kOffSfa + stage * L::kSfaBytes, &maps.sfa, 0, sfa_row + ks, fb);
+                    tma_load_2d_pair_mc(sbase + L::kOffSfb + stage * L::kSfbBytes + 2 * kAtom * rank, &maps.sfb, 0,
+                                        sfb_row + ks, fb, 0x3);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (*abort_flag) {
+                // Loads in flight complete on the even CTA's barrier, which the odd
+                // CTA cannot wait on: give them a bounded while to land.
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 200000ull) __nanosleep(1000);
+            }
+        }
+    } else if (warp == 1) {
+        // ---- MMA issuer (even CTA; warp-uniform loops, one elected lane issues) -----------
+        if (leader) {
+            const uint64_t a_desc0 = make_smem_desc(sbase + L::kOffA, 16, 1024, 2);
+            const uint64_t b_desc0 = make_smem_desc(sbase + L::kOffB, 16, 1024, 2);
+            const uint64_t sfa_desc0 = make_smem_desc(sbase + L::kOffSfa, 0, 128, 0);
+            const uint64_t sfb_desc0 = make_smem_desc(sbase + L::kOffSfb, 0, 128, 0);
+            int stage = 0, before = STAGES - 2;   // this stage and the one two before
+            uint32_t phase = 0, before_phase = 1, acc = 0, acc_phase = 0, slot = 0;
+            bool ok = true;
+            for (int64_t t = pair_id; t < total && ok; t += n_pairs) {
+                int got = 1;
+                if (lane == 0) got = spin_phase(tempty_bar, acc_phase ^ 1u, guard) ? 1 : 0;
+                if (!__shfl_sync(0xFFFFFFFFu, got, 0)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc * L::kAcc1;
+                for (int64_t kb = 0; kb < num_kb; ++kb) {
+                    // the slot's scales have been read: the stage two before has completed (before the
+                    // first two stages a fresh barrier's odd phase counts as complete)
+                    if (lane == 0)
+                        got = wait_phase(full_bar(stage), phase, guard) && wait_phase(empty_bar(before), before_phase, guard) ? 1 : 0;
+                    if (!__shfl_sync(0xFFFFFFFFu, got, 0)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sfa_t = tmem_base + L::kTmemScales + L::kScaleCols * slot, sfb_t = sfa_t + 8;
+                    const uint64_t a_desc = a_desc0 + static_cast<uint64_t>((stage * kBandBytes) >> 4);
+                    const uint64_t b_desc = b_desc0 + static_cast<uint64_t>((stage * kBandBytes) >> 4);
+                    const uint64_t sfa_d = sfa_desc0 + static_cast<uint64_t>((stage * L::kSfaBytes) >> 4);
+                    const uint64_t sfb_d = sfb_desc0 + static_cast<uint64_t>((stage * L::kSfbBytes) >> 4);
+                    const int mmas = mmas_of(p.k_padded, kb);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {   // atom i: K elements 128 i .. of the stage
+                            tc_cp_32x128b_warpx4_pair(sfa_t + 4 * i, sfa_d + static_cast<uint64_t>((i * kAtom) >> 4));
+                            tc_cp_32x128b_warpx4_pair(sfb_t + 8 * i, sfb_d + static_cast<uint64_t>((i * kAtom) >> 4));
+                            tc_cp_32x128b_warpx4_pair(sfb_t + 8 * i + 4, sfb_d + static_cast<uint64_t>(((i + 2) * kAtom) >> 4));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < mmas)
+                                tc_mma_mxf4_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k,
+                                                 make_idesc_mxf4(256, 256, 2 * (k & 1)), sfa_t + 4 * (k >> 1),
+                                                 sfb_t + 8 * (k >> 1), (kb > 0 || k > 0) ? 1u : 0u);
+                        tc_commit_pair_multicast(empty_bar(stage), 0x3);   // frees the slot in both CTAs
+                    }
+                    __syncwarp();
+                    slot ^= 1u;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (++before == STAGES) { before = 0; before_phase ^= 1u; }
+                }
+                if (!ok) break;
+                if (elect_one()) tc_commit_pair_multicast(tfull_bar, 0x3);
+                __syncwarp();
+                acc ^= 1u;
+                acc_phase ^= 1u;
+            }
+            // Drain: every MMA and copy issued above completes before teardown.
+            if (lane == 0) {
+                tc_commit_pair(drain_bar);
+                WaitGuard g2 = guard;
+                volatile int never = 0;
+                g2.abort_flag = &never;
+                (void)mbar_wait(drain_bar, 0, g2);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---- epilogue (both CTAs; warps 2..9) ----------------------------------------
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t tempty_leader = leader ? tempty_bar : mapa_shared(tempty_bar, 0);
+        const uint32_t buffer = sbase + L::kOffStage + (warp - 2) * 2 * L::kStageWarpBytes;
+        uint32_t acc = 0, acc_phase = 0, turn = 0;
+        for (int64_t t = pair_id; t < total; t += n_pairs) {
+            const PairTile ti = pair_tile<kGrouped>(p, prefix, t, rank);
+            // One thread waits (suspending), the other epilogue warps sleep on a
+            // named barrier; barrier 2 keeps the verdict until every warp read it.
+            if (warp == 2 && lane == 0) *epi_flag = wait_phase(tfull_bar, acc_phase, guard) ? 1 : 0;
+            named_bar_sync(1, 32 * L::kEpiWarps);
+            const int ok = *epi_flag;
+            named_bar_sync(2, 32 * L::kEpiWarps);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + acc * L::kAcc1;
+            const int64_t row0 = ti.m0 + 32 * quad;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                // the columns that the other accumulator shares come first: the last 64 of the first
+                // accumulator, the first 64 of the second
+                const int col = c == 0 ? (acc ? 0 : L::kAcc1) + 32 * half : (acc ? L::kShared : 0) + 96 * half + 32 * (c - 1);
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(taddr + col, v);
+                tmem_ld_wait();
+                if (c == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader) mbar_arrive(tempty_bar);
+                        else mbar_arrive_cluster(tempty_leader);
+                    }
+                }
+                store_chunk(p, v, buffer + (turn & 1u) * L::kStageWarpBytes, row0, ti.row_lo, ti.row_hi, ti.n0 + col, lane, &maps.y);
+                ++turn;
+            }
+            acc ^= 1u;
+            acc_phase ^= 1u;
+        }
+        if (lane == 0) bulk_wait_all();   // this warp's tiled stores complete before the CTA ends
+        __syncwarp();
+    }
+
+    // ---- teardown: nothing may still target the peer when either CTA leaves ----
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc_pair(tmem_base, L::kTmemCols);
+    }
+}
+
+// ---- few rows ----------------------------------------------------------------------------------
+//
+// A tile: 128 columns of y (rows of B) by up to 128 rows of A, transposed in tensor memory: lane n, column m.  The
+// instruction's N is the number of rows of A, rounded up to 16, so few rows cost little beside B's bytes.
+// Slots of B (16 KB), up to tok_cap rows of A in boxes of 16 rows, and two scale atoms of each; as many of them as
+// shared memory holds, since what bounds such a product is the stream of B's bytes.
+//
+// split > 1 (a cluster, one tile): CTA r takes the r-th part of K; the parts' sums are joined through
+// distributed shared memory in the order of the parts.  split == 1: persistent over tiles, two accumulators.
+struct RowsCfg {
+    static constexpr int kThreads = 192;      // producer, MMA issuer, four epilogue warps
+    static constexpr int kMaxStages = 8;
+    static constexpr int kNumBars = 2 * kMaxStages + 5;
+    static constexpr int kTail = 8 * kNumBars + 16 + 4 * (kMaxExperts + 1);   // behind the ring
+    static constexpr int kAlloc = 227 * 1024;
+    static constexpr int kRing = (kAlloc - 1024 - kTail) / 1024 * 1024;
+    static constexpr int kTmemCols = 512;
+    static constexpr int kTmemScales = 256;   // after two accumulators of 128 columns: 16 columns a slot
+    static_assert(kTmemScales + 16 * kMaxStages <= kTmemCols, "tensor memory budget");
+};
+
+struct RowsMaps {
+    CUtensorMap a, b;
+};
+
+struct RowsTile {
+    int64_t m0, a_band, n0, b_row, b_band;
+    int rows;   // of A
+};
+
+template <bool kGrouped>
+__device__ __forceinline__ RowsTile rows_tile(const Args& p, const int* prefix, int64_t t) {
+    RowsTile ti;
+    if constexpr (!kGrouped) {   // the row tiles of a column tile follow each other: B's tile is in L2
+        const int64_t i = t % p.m_tiles;
+        ti.n0 = t / p.m_tiles * 128;
+        ti.m0 = 128 * i;
+        ti.a_band = i;
+        ti.rows = static_cast<int>(min(static_cast<int64_t>(128), p.M - ti.m0));
+        ti.b_row = ti.n0;
+        ti.b_band = ti.n0 / 128;
+    } else {
+        const int g = expert_of(prefix, p.G, t);
+        const int64_t lo = offset_at(p, g), hi = offset_at(p, g + 1), tiles = (hi - lo + 127) / 128, local = t - prefix[g];
+        const int64_t i = local % tiles;
+        ti.n0 = local / tiles * 128;
+        ti.m0 = lo + 128 * i;
+        ti.a_band = first_band(lo, g) + i;
+        ti.rows = static_cast<int>(min(static_cast<int64_t>(128), hi - ti.m0));
+        ti.b_row = static_cast<int64_t>(g) * p.N + ti.n0;
+        ti.b_band = static_cast<int64_t>(g) * p.b_bands + ti.n0 / 128;
+    }
+    return ti;
+}
+
+template <bool kGrouped>
+__global__ void __launch_bounds__(RowsCfg::kThreads, 1)
+    gemm_mxfp4_rows_kernel(const __grid_constant__ RowsMaps maps, const Args p) {
+    using L = RowsCfg;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = p.split, stages = p.stages;
+    const int rank = split > 1 ? static_cast<int>(blockIdx.x % split) : 0;
+    const int tok_bytes = p.tok_cap * 128, stage_bytes = kBandBytes + tok_bytes + 4 * kAtom;
+    const uint32_t bar0 = sbase + L::kRing;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (L::kMaxStages + s); };
+    auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * L::kMaxStages) + 8u * a; };
+    auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * L::kMaxStages + 2) + 8u * a; };
+    const uint32_t drain_bar = bar0 + 8u * (2 * L::kMaxStages + 4);
+    uint8_t* tail = smem + L::kRing + 8 * L::kNumBars;
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(tail);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
+    int* prefix = reinterpret_cast<int*>(tail + 16);
+    const WaitGuard guard{abort_flag, p.status, p.wait_limit_ns};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (uint32_t a = 0; a < 2; ++a) {
+            mbar_init(tfull_bar(a), 1);
+            mbar_init(tempty_bar(a), 4);   // the epilogue warps
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&maps.a);
+        prefetch_tensormap(&maps.b);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tail), L::kTmemCols);
+        tmem_relinquish();
+    }
+    wait_for_previous();
+    int64_t total = p.m_tiles * p.n_tiles;
+    if constexpr (kGrouped) {
+        build_prefix(p, 128, prefix);
+        total = prefix[p.G];
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int64_t num_kb = (p.k_padded + kBK - 1) / kBK;
+    const int64_t kb_lo = num_kb * rank / split, kb_hi = num_kb * (rank + 1) / split;
+    const int64_t first = blockIdx.x / split, step = gridDim.x / split;
+
+    if (warp == 0) {
+        // ---- producer ------------------------------------------------------------------
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t issued = 0;
+            bool stop = false;
+            for (int64_t t = first; t < total && !stop && !*abort_flag; t += step) {
+                const RowsTile ti = rows_tile<kGrouped>(p, prefix, t);
+                const int boxes = (ti.rows + 15) >> 4;
+                const uint8_t* sfa = p.a_s + ti.a_band * p.k_atoms * kAtom;
+                const uint8_t* sfb = p.b_s + ti.b_band * p.k_atoms * kAtom;
+                for (int64_t kb = kb_lo; kb < kb_hi; ++kb) {
+                    if (!wait_phase(empty_bar(stage), phase ^ 1u, guard)) { stop = true; break; }
+                    const uint32_t fb = full_bar(stage), at = sbase + stage * stage_bytes;
+                    const uint32_t scales = kAtom * static_cast<uint32_t>(min(int64_t(2), p.k_atoms - 2 * kb));
+                    mbar_arrive_expect_tx(fb, kBandBytes + 2048u * boxes + 2u * scales);
+                    const int32_t kx = static_cast<int32_t>(kb * 128);
+                    tma_load_2d(at, &maps.b, kx, static_cast<int32_t>(ti.b_row), fb);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_2d(at + kBandBytes + 2048u * i, &maps.a, kx, static_cast<int32_t>(ti.m0 + 16 * i), fb);
+                    bulk_load(at + kBandBytes + tok_bytes, sfb + 2 * kb * kAtom, scales, fb);
+                    bulk_load(at + kBandBytes + tok_bytes + 2 * kAtom, sfa + 2 * kb * kAtom, scales, fb);
+                    ++issued;
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (*abort_flag) {
+                // Let copies already in flight land before the CTA exits.
+                const int64_t n = issued < stages ? issued : stages;
+                int s = stage;
+                uint32_t ph = phase;
+                for (int64_t i = 0; i < n; ++i) {
+                    if (--s < 0) { s = stages - 1; ph ^= 1u; }
+                    WaitGuard g2 = guard;
+                    volatile int never = 0;
+                    g2.abort_flag = &never;
+                    (void)mbar_wait(full_bar(s), ph, g2);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---- MMA issuer ----------------------------------------------------------------
+        int stage = 0;
+        uint32_t phase = 0, acc = 0, acc_phase = 0;
+        bool ok = true;
+        for (int64_t t = first; t < total && ok; t += step) {
+            const int rows = rows_tile<kGrouped>(p, prefix, t).rows;
+            const uint32_t N = static_cast<uint32_t>((rows + 15) & ~15);
+            int got = 1;
+            if (lane == 0) got = spin_phase(tempty_bar(acc), acc_phase ^ 1u, guard) ? 1 : 0;
+            if (!__shfl_sync(0xFFFFFFFFu, got, 0)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + acc * 128;
+            for (int64_t kb = kb_lo; kb < kb_hi; ++kb) {
+                if (lane == 0) got = wait_phase(full_bar(stage), phase, guard) ? 1 : 0;
+                if (!__shfl_sync(0xFFFFFFFFu, got, 0)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t at = sbase + stage * stage_bytes, sc = at + kBandBytes + tok_bytes;
+                const uint32_t sfb_t = tmem_base + L::kTmemScales + 16 * stage, sfa_t = sfb_t + 8;
+                const uint64_t b_desc = make_smem_desc(at, 16, 1024, 2), a_desc = make_smem_desc(at + kBandBytes, 16, 1024, 2);
+                const uint64_t s_desc = make_smem_desc(sc, 0, 128, 0);
+                const int mmas = mmas_of(p.k_padded, kb);
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)   // B's two atoms, then A's
+                        tc_cp_32x128b_warpx4(sfb_t + 4 * i, s_desc + static_cast<uint64_t>((i * kAtom) >> 4));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < mmas)
+                            tc_mma_mxf4(d_tmem, b_desc + 2 * k, a_desc + 2 * k, make_idesc_mxf4(128, N, 2 * (k & 1)),
+                                        sfb_t + 4 * (k >> 1), sfa_t + 4 * (k >> 1), (kb > kb_lo || k > 0) ? 1u : 0u);
+                    tc_commit(empty_bar(stage));
+                }
+                __syncwarp();
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok) break;
+            if (elect_one()) tc_commit(tfull_bar(acc));
+            __syncwarp();
+            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        }
+        // Drain: every MMA and copy issued above completes before teardown.
+        if (lane == 0) {
+            tc_commit(drain_bar);
+            WaitGuard g2 = guard;
+            volatile int never = 0;
+            g2.abort_flag = &never;
+            (void)mbar_wait(drain_bar, 0, g2);
+        }
+        __syncwarp();
+    } else {
+        // ---- epilogue: lane l of the warp on quarter q holds column n0 + 32 q + l of y ----------------
+        const int quad = warp & 3, n = 32 * quad + lane;
+        uint32_t acc = 0, acc_phase = 0;
+        for (int64_t t = first; t < total; t += step) {
+            const RowsTile ti = rows_tile<kGrouped>(p, prefix, t);
+            int got = 1;
+            if (lane == 0) got = wait_phase(tfull_bar(acc), acc_phase, guard) ? 1 : 0;
+            if (!__shfl_sync(0xFFFFFFFFu, got, 0)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + acc * 128;
+            const bool in = ti.n0 + n < p.N;
+            uint16_t* out = p.y + ti.m0 * p.ldy + ti.n0 + n;
+#pragma unroll 1
+            for (int c = 0; c < ti.rows; c += 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(taddr + c, v);
+                tmem_ld_wait();
+                if (split > 1) {   // the ring is free: every copy has been consumed
+                    float* part = reinterpret_cast<float*>(smem) + c * 128 + n;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) part[i * 128] = __uint_as_float(v[i]);
+                } else if (in) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < ti.rows) out[(c + i) * p.ldy] = from_float<bf16_bits>(__uint_as_float(v[i]));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(acc));
+            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (split > 1) {
+        cluster_sync_all();   // every part is written
+        if (first < total && warp >= 2) {
+            const RowsTile ti = rows_tile<kGrouped>(p, prefix, first);
+            const int n = static_cast<int>(threadIdx.x) - 64;
+            if (ti.n0 + n < p.N) {
+                for (int m = rank; m < ti.rows; m += split) {
+                    float sum = 0.0f;
+                    for (int s = 0; s < split; ++s)
+                        sum += ld_cluster(mapa_shared(sbase + 4u * static_cast<uint32_t>(m * 128 + n), static_cast<uint32_t>(s)));
+                    p.y[(ti.m0 + m) * p.ldy + ti.n0 + n] = from_float<bf16_bits>(sum);
+                }
+            }
+        }
+        cluster_sync_all();   // nobody leaves while its part is read
+    }
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem_base, L::kTmemCols);
+    }
+}
+
+// ---- host --------------------------------------------------------------------------------------
+
+// Payload [rows, row_bytes], boxes of box_rows x 128 bytes, 128-byte swizzle.
+bool payload_map(CUtensorMap* map, const void* q, int64_t rows, int64_t row_bytes, uint32_t box_rows) {
+    return encode_tensor_map_2d(map, q, false, static_cast<uint64_t>(row_bytes), static_cast<uint64_t>(rows),
+                                static_cast<uint64_t>(row_bytes), 128u, box_rows, true);
+}
+
+// MMA-tiled scales as rows of 256 bytes, boxes of two atoms.
+bool scale_map(CUtensorMap* map, const void* s, int64_t bands, int64_t k_atoms) {
+    if ((bands + 2) * k_atoms * 2 >= (int64_t(1) << 31)) return false;
+    return encode_tensor_map_2d(map, s, false, 256u, static_cast<uint64_t>(bands * k_atoms * 2), 256u, 256u, 4u, false);
+}
+
+// One launch of `grid` CTAs in clusters of `cluster` (0: as the kernel says), whose start overlaps the end of the
+// kernel before it on the stream.
+template <typename Maps>
+cudaError_t launch(void (*kernel)(const Maps, const Args), int64_t grid, int threads, int smem, int cluster,
+                   cudaStream_t stream, const Maps& maps, const Args& args) {
+    cudaLaunchAttribute attrs[2] = {};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = static_cast<unsigned>(cluster > 0 ? cluster : 1);
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3(static_cast<unsigned>(grid));
+    config.blockDim = dim3(static_cast<unsigned>(threads));
+    config.dynamicSmemBytes = static_cast<size_t>(smem);
+    config.stream = stream;
+    config.attrs = attrs;
+    config.numAttrs = cluster > 0 ? 2 : 1;
+    void* addresses[] = {const_cast<Maps*>(&maps), const_cast<Args*>(&args)};
+    return cudaLaunchKernelExC(&config, reinterpret_cast<const void*>(kernel), addresses);
+}
+
+// The kernel's shared-memory limit, once per device and thread.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel* kernel, int bytes, int device, int* configured) {
+    if (*configured == device) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) *configured = device;
+    return e;
+}
+
+template <bool kGrouped>
+cudaError_t launch_pair(const DeviceInfo& dev, const Gemm4Args& g, Args args, cudaStream_t stream) {
+    using L = PairCfg;
+    static thread_local int configured = -1;
+    const cudaError_t e = allow_smem(gemm_mxfp4_pair_kernel<kGrouped>, L::kAlloc, dev.device, &configured);
+    if (e != cudaSuccess) return e;
+    const int64_t row_bytes = args.k_padded / 2, experts = kGrouped ? g.G : 1;
+    PairMaps maps;
+    if (!payload_map(&maps.a, g.a_q, g.M, row_bytes, 128) || !payload_map(&maps.b, g.b_q, experts * g.N, row_bytes, 128) ||
+        !scale_map(&maps.sfa, g.a_s, kGrouped ? g.bands_cap : (g.M + 127) / 128, args.k_atoms) ||
+        !scale_map(&maps.sfb, g.b_s, experts * args.b_bands, args.k_atoms))
+        return cudaErrorInvalidValue;
+    args.m_tiles = (g.M + 255) / 256;
+    args.n_tiles = (g.N + 255) / 256;
+    args.y_vec = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0;
+    args.y_tma = args.y_vec && encode_tensor_map_bf16_store(&maps.y, g.y, static_cast<uint64_t>(g.N),
+                                                            static_cast<uint64_t>(g.M), static_cast<uint64_t>(g.ldy));
+    int64_t pairs = dev.sm_count / 2;
+    if (!kGrouped && args.m_tiles * args.n_tiles < pairs) pairs = args.m_tiles * args.n_tiles;
+    return launch(gemm_mxfp4_pair_kernel<kGrouped>, 2 * pairs, L::kThreads, L::kAlloc, 0, stream, maps, args);
+}
+
+template <bool kGrouped>
+cudaError_t launch_rows(const DeviceInfo& dev, const Gemm4Args& g, Args args, cudaStream_t stream) {
+    using L = RowsCfg;
+    static thread_local int configured = -1;
+    const cudaError_t e = allow_smem(gemm_mxfp4_rows_kernel<kGrouped>, L::kAlloc, dev.device, &configured);
+    if (e != cudaSuccess) return e;
+    const int64_t row_bytes = args.k_padded / 2, experts = kGrouped ? g.G : 1;
+    RowsMaps maps;
+    if (!payload_map(&maps.a, g.a_q, g.M, row_bytes, 16) || !payload_map(&maps.b, g.b_q, experts * g.N, row_bytes, 128))
+        return cudaErrorInvalidValue;
+    args.m_tiles = (g.M + 127) / 128;
+    args.n_tiles = (g.N + 127) / 128;
+    args.tok_cap = static_cast<int>(g.M < 128 ? (g.M + 15) / 16 * 16 : 128);
+    const int stage_bytes = kBandBytes + args.tok_cap * 128 + 4 * kAtom;
+    args.stages = L::kRing / stage_bytes < L::kMaxStages ? L::kRing / stage_bytes : L::kMaxStages;
+    // tiles, at most: of experts with rows, each with one partly filled tile
+    int64_t tiles = args.m_tiles * args.n_tiles;
+    if (kGrouped) tiles = ((g.M < g.G ? g.M : g.G) + g.M / 128) * args.n_tiles;
+    const int64_t num_kb = (args.k_padded + kBK - 1) / kBK;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= dev.sm_count && num_kb >= split * 4) split *= 2;
+    args.split = split;
+    const int64_t grid = split > 1 ? tiles * split : (tiles < dev.sm_count ? tiles : dev.sm_count);
+    return launch(gemm_mxfp4_rows_kernel<kGrouped>, grid, L::kThreads, L::kAlloc, split > 1 ? split : 0, stream, maps, args);
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_mxfp4(const DeviceInfo&, const Gemm4Args& a, cudaStream_t stream) {
-    const int64_t by = (a.M + kSide - 1) / kSide;
-    if (by > 65535) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>((a.N + kSide - 1) / kSide), static_cast<unsigned>(by)), block(kSide, kSide);
-    if (a.offsets != nullptr) gemm_mxfp4_kernel<true><<<grid, block, 0, stream>>>(a);
-    else gemm_mxfp4_kernel<false><<<grid, block, 0, stream>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_gemm_mxfp4(const DeviceInfo& dev, const Gemm4Args& g, cudaStream_t stream) {
+    Args a{};
+    a.a_s = static_cast<const uint8_t*>(g.a_s);
+    a.b_s = static_cast<const uint8_t*>(g.b_s);
+    a.y = static_cast<uint16_t*>(g.y);
+    a.M = g.M, a.N = g.N, a.ldy = g.ldy;
+    a.k_padded = (g.K + 31) / 32 * 32;
+    a.k_atoms = (a.k_padded + 127) / 128;
+    a.b_bands = (g.N + 127) / 128;
+    a.offsets = g.offsets;
+    a.G = g.G;
+    a.bands_cap = g.bands_cap;
+    a.split = 1;
+    a.status = dev.status;
+    a.wait_limit_ns = kDefaultWaitLimitNs;
+    if (g.offsets != nullptr)
+        return g.M > 64 * static_cast<int64_t>(g.G) ? launch_pair<true>(dev, g, a, stream) : launch_rows<true>(dev, g, a, stream);
+    return ((g.M + 255) / 256) * ((g.N + 255) / 256) >= 64 ? launch_pair<false>(dev, g, a, stream)
+                                                            : launch_rows<false>(dev, g, a, stream);
 }
 
 }  // namespace mxq
