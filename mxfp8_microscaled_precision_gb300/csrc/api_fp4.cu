@@ -85,8 +85,7 @@ mxq_status mxq_dequant_1x32(const void* q, const void* s, mxq_element element, i
     const bool four = element == MXQ_ELEM_E2M1;
     if (ldq < (four ? 16 * groups_of(cols) : cols) || (four && ldq % 4 != 0)) return MXQ_ERR_INVALID_ARG;
     if (layout == MXQ_SCALE_ROWMAJOR && lds < groups_of(cols)) return MXQ_ERR_INVALID_ARG;
-    if (rows > kMaxRows || cols > kMaxRows || rows > 0 && (cols + 7) / 8 > (int64_t(0x7FFFFFFF) * 256 - 255) / rows)
-        return MXQ_ERR_UNSUPPORTED_SHAPE;
+    if (rows > kMaxRows || cols > kMaxCols) return MXQ_ERR_UNSUPPORTED_SHAPE;
     if (rows == 0 || cols == 0) return MXQ_OK;
     if (!q || !s || !out || !aligned(out, size_of(dtype)) || (four && !aligned(q, 4))) return MXQ_ERR_INVALID_ARG;
     const mxq_status st = device_ok();

@@ -227,12 +227,12 @@ cudaError_t clip_launch(const ClipTensor* tensors, int count, int chunk_bytes, b
         parts += kClipBlocks;
     }
     if (!scale_too) {
-        return launch_behind(norm_kernel, 1, kThreads, stream, partial, parts, norm);
+        return launch_behind(norm_kernel, 1, kThreads, 0, stream, partial, parts, norm);
     }
     bool first = true;
     for (int at = 0; at < count || first; first = false) {
         at = whole ? count : fill(&t, tensors, count, at, chunk_bytes);
-        const cudaError_t e = launch_behind(scale_kernel<kTable>, kClipBlocks, kThreads, stream, t, partial, parts,
+        const cudaError_t e = launch_behind(scale_kernel<kTable>, kClipBlocks, kThreads, 0, stream, t, partial, parts,
                                             max_norm, eps, first ? norm : nullptr);
         if (e != cudaSuccess) return e;
     }

@@ -20,221 +20,539 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kThreads = 256;
 
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
 // Eight elements of a row, as they are stored.
 template <typename T>
 struct Eight {
-    uint4 w[sizeof(T) / 2];
+    static constexpr int kWords = sizeof(T) / 2;
+    uint4 w[kWords];
+    // The elements [c, c + 8) of a row whose neighbourhood is all there.  kVec: rows start on 16 bytes.
+    template <bool kVec>
+    __device__ __forceinline__ void load_whole(const T* row, int c) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            const int at = c + i * kVec16<T>;
+            w[i] = kVec ? *reinterpret_cast<const uint4*>(row + at) : load_inner<sizeof(T)>(row, at);
+        }
+    }
+    __device__ __forceinline__ void from_shared(const T* p) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void to_shared(T* p) const {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+    }
     __device__ __forceinline__ void floats(float (&f)[8]) const {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+        for (int i = 0; i < kWords; ++i) {
             float s[kVec16<T>];
             unpack<T>(w[i], s);
 #pragma unroll
             for (int j = 0; j < kVec16<T>; ++j) f[i * kVec16<T> + j] = s[j];
         }
     }
-    // The elements [c, c + 8) of a row of n, 0 behind it.  kVec: rows start on 16 bytes.
-    template <bool kVec>
-    __device__ __forceinline__ void load(const T* row, int64_t c, int64_t n) {
-        if (kVec && c + 8 <= n) {
-#pragma unroll
-            for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(row + c)[i];
-            return;
-        }
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = c + i < n ? to_float(row[c + i]) : 0.0f;
+    // largest |x|, as FP32 bits
+    __device__ __forceinline__ uint32_t amax() const {
         if constexpr (sizeof(T) == 2) {
-            w[0] = pack<T>(f);   // exact
+            return amax8_bits(w[0]) << 16;
         } else {
+            float f[8];
+            floats(f);
+            uint32_t m = abs_bits(f[0]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                w[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
-                                  __float_as_uint(f[4 * i + 3]));
+            for (int i = 1; i < 8; ++i) m = max(m, abs_bits(f[i]));
+            return m;
+        }
+    }
+    // times 2^-e; the BF16 product is exact, or so small that it converts to a signed zero as the exact one does
+    __device__ __forceinline__ void scaled(int e, float (&f)[8]) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t s = pow2_neg_bf16(e) * 0x10001u;
+            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t v = mul_bf16x2(u[i], s);
+                f[2 * i] = bf16_lo(v);
+                f[2 * i + 1] = bf16_hi(v);
+            }
+        } else {
+            floats(f);
+            const float s = pow2_neg(e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= s;
         }
     }
 };
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// Codes of eight elements of a group with a NaN or an infinity: 7 with the sign.
+__device__ __forceinline__ uint32_t bad_codes(const float (&f)[8]) {
+    uint32_t r = 0x77777777u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r |= (__float_as_uint(f[i]) >> 31) << (4 * i + 3);
+    return r;
+}
 
-// Codes of eight elements of a group whose largest |x| has the bits `amax`; *code: its scale.
-__device__ __forceinline__ uint32_t quant8_e2m1(const float (&f)[8], uint32_t amax, uint32_t* code) {
-    if (amax >= kInfBits) {   // NaN or infinity in the group: 7 with the sign
-        uint32_t r = 0x77777777u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r |= (__float_as_uint(f[i]) >> 31) << (4 * i + 3);
+// Codes of a column's 32 rows f, of which the largest |x| has the bits m; *code: the scale.
+__device__ __forceinline__ uint4 column_codes(const float (&f)[32], uint32_t m, uint32_t* code) {
+    uint32_t o[4];
+    if (m >= kInfBits) {
         *code = 0xFFu;
-        return r;
-    }
-    const int e = rceil_exponent_f32<kE2M1>(amax);
-    *code = static_cast<uint32_t>(e + 127);
-    float v[8];
-    const float s = pow2_neg(e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = f[i] * s;
-    return cvt_e2m1x8(v);
+        for (int i = 0; i < 4; ++i) {
+            float part[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) part[n] = f[8 * i + n];
+            o[i] = bad_codes(part);
+        }
+    } else {
+        const int e = rceil_exponent_f32<kE2M1>(m);
+        *code = static_cast<uint32_t>(e + 127);
+        const float s = pow2_neg(e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float part[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) part[n] = f[8 * i + n] * s;
+            o[i] = cvt_e2m1x8(part);
+        }
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 struct Shape {
-    int64_t tiles_c, per_batch;   // 128 x 128 tiles of a row of tiles and of a matrix
+    int tiles_c, per_batch;   // 128 x 128 tiles of a row of tiles and of a matrix
 };
 
-// One 128 x 128 tile.  Thread t holds the elements 8 (t % 16) .. of the tile's rows t / 16 + 16 j; the
-// four threads of a group sit side by side.  The column copy reads the tile back from shared memory: a
-// thread takes a column of 32 rows.
-template <typename T, bool kRow, bool kCol, bool kVec>
-__global__ void __launch_bounds__(kThreads) quant_mxfp4_kernel(const Quant4Args a, const Shape s) {
-    __shared__ __align__(16) T tile[kCol ? kTile * kTile : 1];
-    __shared__ uint32_t s_codes[kTile];   // four scale codes of every row (of every column)
+// Where 16-byte block `block` (32 rows) of a column of the tile waits to be stored: the blocks of a column take
+// turns so that a warp's 32 column pairs do not meet in the same banks.
+__device__ __forceinline__ int place_of(int column, int block) { return 4 * column + (block ^ ((column >> 1) & 3)); }
+
+// The four codes of row r's groups g .. g + 3 in the scales of a matrix [rows, 32 groups].
+__device__ __forceinline__ void store_codes(uint8_t* out, bool tiled, int64_t r, int64_t rows, int64_t g, int64_t groups,
+                                            uint32_t codes) {
+    if (tiled) {   // one word of the tile's 512-byte atom; padding is zero
+        *reinterpret_cast<uint32_t*>(out + tiled_scale_offset(r, g, groups)) = codes;
+    } else if (r < rows) {
+        for (int i = 0; i < 4; ++i)
+            if (g + i < groups) out[r * groups + g + i] = static_cast<uint8_t>(codes >> (8 * i));
+    }
+}
+
+// Eight rows r, r + step, .. of `rows` rows of n elements: their elements [c, c + 8), 0 outside the matrix.  What a vector
+// load may touch comes first, all of it in flight at once; the ends that it may not, element by element, last.
+template <typename T, bool kVec>
+__device__ __forceinline__ void load_rows(Eight<T> (&v)[8], const T* x, int64_t ld, int64_t r, int step, int64_t rows, int c, int n) {
+    bool ends = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t row = r + j * step;
+        const T* p = x + j * step * ld;
+#pragma unroll
+        for (int i = 0; i < Eight<T>::kWords; ++i) {
+            const int at = c + i * kVec16<T>;
+            v[j].w[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row >= rows || at >= n) continue;
+            if (kVec ? at + kVec16<T> <= n : is_between<sizeof(T)>(row, rows, n) || is_inner<sizeof(T)>(at, n)) {
+                v[j].w[i] = kVec ? *reinterpret_cast<const uint4*>(p + at) : load_inner<sizeof(T)>(p, at);
+                if (!kVec && at + kVec16<T> > n) v[j].w[i] = inside<sizeof(T)>(v[j].w[i], at, n);
+            } else {
+                ends = true;
+            }
+        }
+    }
+    if (!ends) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t row = r + j * step;
+#pragma unroll
+        for (int i = 0; i < Eight<T>::kWords; ++i) {
+            const int at = c + i * kVec16<T>;
+            if (row < rows && at < n &&
+                !(kVec ? at + kVec16<T> <= n : is_between<sizeof(T)>(row, rows, n) || is_inner<sizeof(T)>(at, n)))
+                v[j].w[i] = load_ends<sizeof(T)>(x + j * step * ld, at, n);
+        }
+    }
+}
+
+// Codes of a thread's eight elements and the scale code of their group, which four neighbouring threads hold.
+template <typename T>
+__device__ __forceinline__ uint32_t group_codes(const Eight<T>& v, uint32_t* code) {
+    uint32_t m = v.amax();
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    float f[8];
+    if (m >= kInfBits) {
+        *code = 0xFFu;
+        v.floats(f);
+        return bad_codes(f);
+    }
+    const int e = rceil_exponent_f32<kE2M1>(m);
+    *code = static_cast<uint32_t>(e + 127);
+    v.scaled(e, f);
+    return cvt_e2m1x8(f);
+}
+
+// Whether a tile's elements, and of rows that start anywhere the 16 bytes around each row's part, lie in the matrix.
+template <bool kVec>
+__device__ __forceinline__ bool is_whole(const Quant4Args& a, int64_t r0, int rows, int64_t c0, int cols) {
+    return c0 + cols <= a.cols && (kVec ? r0 + rows <= a.rows : r0 > 0 && r0 + rows < a.rows);
+}
+
+// Row copy alone: 64 rows of 256 elements a block.  A warp has a row of it at a time, eight elements a lane, and stores
+// its 128 bytes of payload together; all loads of a thread are issued before the first is used.
+constexpr int kRowTile = 64, kColTile = 256;
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_rows_kernel(const Quant4Args a, const Shape s) {
+    __shared__ uint32_t s_codes[kRowTile][2];   // four scale codes of every row and 128 columns
+    __shared__ int64_t s_at[kRowTile];          // grouped: the row in the scales, -1: none
+    let_next_start();
+    wait_for_previous();
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const int b = static_cast<int>(blockIdx.x) / s.per_batch, local = static_cast<int>(blockIdx.x) - b * s.per_batch;
+    const int tr = local / s.tiles_c, tc = local - tr * s.tiles_c;
+    const int64_t r0 = static_cast<int64_t>(tr) * kRowTile, c0 = static_cast<int64_t>(tc) * kColTile;
+    const int64_t groups = (a.cols + 31) >> 5;
+    const T* x = static_cast<const T*>(a.x) + b * a.batch_stride + (r0 + w) * a.ld;
+    Eight<T> v[8];
+    if (is_whole<kVec>(a, r0, kRowTile, c0, kColTile)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j].template load_whole<kVec>(x + 8 * j * a.ld, static_cast<int>(c0) + 8 * lane);
+    } else {
+        load_rows<T, kVec>(v, x, a.ld, r0 + w, 8, a.rows, static_cast<int>(c0) + 8 * lane, static_cast<int>(a.cols));
+    }
+    if (a.offsets != nullptr && t < kRowTile) {   // tiled by expert: its first row starts a band
+        const int64_t r = r0 + t;
+        int lo = 0, hi = a.G;   // the last expert that starts at or before the row
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.offsets[mid] <= r) lo = mid; else hi = mid;
+        }
+        const int64_t first = a.offsets[lo], end = a.offsets[lo + 1], at = (first / kTile + lo) * kTile + (r - first);
+        s_at[t] = r < a.rows && first >= 0 && r >= first && r < end && at < a.bands_cap * kTile ? at : -1;
+    }
+    const int64_t g = (c0 >> 5) + (lane >> 2);
+    uint8_t* q = static_cast<uint8_t*>(a.q_row) + (b * a.rows + r0 + w) * groups * 16 + c0 / 2 + 4 * lane;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t r = r0 + w + 8 * j;
+        uint32_t code;
+        const uint32_t o = group_codes(v[j], &code);
+        const bool in = r < a.rows && g < groups;
+        if (in) *reinterpret_cast<uint32_t*>(q + 8 * j * groups * 16) = o;
+        if ((lane & 3) == 0)
+            reinterpret_cast<uint8_t*>(s_codes[w + 8 * j])[lane >> 2] = in ? static_cast<uint8_t>(code) : 0;
+    }
+    __syncthreads();
+    if (t < 2 * kRowTile) {
+        const int row = t >> 1, part = t & 1;
+        const int64_t first = (c0 >> 5) + 4 * part;   // of the four groups
+        uint8_t* out = static_cast<uint8_t*>(a.s_row) + b * a.s_row_bytes;
+        if (first >= groups) return;
+        if (a.offsets == nullptr) store_codes(out, a.tiled, r0 + row, a.rows, first, groups, s_codes[row][part]);
+        else if (s_at[row] >= 0) store_codes(out, true, s_at[row], 0, first, groups, s_codes[row][part]);
+    }
+}
+
+// Column copy, alone or with the row copy: a 128 x 128 tile in shared memory, its loads in flight at once (rows that start
+// on 16 bytes: without passing registers), several blocks on an SM.  Rows: thread t takes the elements
+// 8 (t % 16) .. of the rows t / 16 + 16 j.  Columns: a thread takes 32 rows of a column (BF16: of two
+// neighbouring ones, in packed operations), and the payload goes out through shared memory, 64 bytes of a
+// column together.
+template <typename T, bool kRow, bool kVec>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_tile_kernel(const Quant4Args a, const Shape s) {
+    extern __shared__ __align__(16) uint8_t s_memory[];
+    T* tile = reinterpret_cast<T*>(s_memory);
+    uint4* s_out = reinterpret_cast<uint4*>(s_memory + kTile * kTile * sizeof(T));
+    __shared__ uint32_t s_row_codes[kTile], s_col_codes[kTile];   // four scale codes of every row and column
+    let_next_start();
+    wait_for_previous();
     const int t = threadIdx.x;
-    const int64_t b = blockIdx.x / s.per_batch, local = blockIdx.x - b * s.per_batch;
-    const int64_t tr = local / s.tiles_c, tc = local - tr * s.tiles_c;
-    const int64_t r0 = tr * kTile, c0 = tc * kTile;
+    const int b = static_cast<int>(blockIdx.x) / s.per_batch, local = static_cast<int>(blockIdx.x) - b * s.per_batch;
+    const int tr = local / s.tiles_c, tc = local - tr * s.tiles_c;
+    const int64_t r0 = static_cast<int64_t>(tr) * kTile, c0 = static_cast<int64_t>(tc) * kTile;
     const int64_t row_groups = (a.cols + 31) >> 5, col_groups = (a.rows + 31) >> 5;
     const T* x = static_cast<const T*>(a.x) + b * a.batch_stride;
     const int chunk = t & 15;
-    uint8_t* codes8 = reinterpret_cast<uint8_t*>(s_codes);
-    Eight<T> v[8];
+    if (kVec) {   // 16 bytes a copy, neighbouring threads side by side; what lies outside is filled up with zeros
+        constexpr int kPer = kTile / kVec16<T>;   // copies of a row
+        const int at = t % kPer, rows_step = kThreads / kPer;
+        const int64_t c = c0 + at * kVec16<T>, left = (a.cols - c) * static_cast<int64_t>(sizeof(T));
+        const uint32_t bytes = left >= 16 ? 16u : (left > 0 ? static_cast<uint32_t>(left) : 0u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int64_t r = r0 + (t >> 4) + 16 * j;
-        v[j].template load<kVec>(x + r * a.ld, c0 + 8 * chunk, r < a.rows ? a.cols : 0);
+        for (int i = 0; i < kTile / rows_step; ++i) {
+            const int row = t / kPer + rows_step * i;
+            const bool in = r0 + row < a.rows && bytes > 0;
+            cp_async16(smem_u32(tile + row * kTile + at * kVec16<T>), in ? x + (r0 + row) * a.ld + c : x, in ? bytes : 0u);
+        }
+        cp_async_wait_all();
+    } else {
+        Eight<T> v[8];
+        const T* p = x + (r0 + (t >> 4)) * a.ld;
+        if (is_whole<kVec>(a, r0, kTile, c0, kTile)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j].template load_whole<kVec>(p + 16 * j * a.ld, static_cast<int>(c0) + 8 * chunk);
+        } else {
+            load_rows<T, kVec>(v, p, a.ld, r0 + (t >> 4), 16, a.rows, static_cast<int>(c0) + 8 * chunk, static_cast<int>(a.cols));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j].to_shared(tile + ((t >> 4) + 16 * j) * kTile + 8 * chunk);
     }
-    if constexpr (kCol) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-                reinterpret_cast<uint4*>(tile + ((t >> 4) + 16 * j) * kTile + 8 * chunk)[i] = v[j].w[i];
-    }
+    __syncthreads();
     if constexpr (kRow) {
-        uint8_t* q = static_cast<uint8_t*>(a.q_row) + b * a.rows * row_groups * 16;
+        const int64_t g = (c0 >> 5) + (chunk >> 2);
+        uint8_t* q = static_cast<uint8_t*>(a.q_row) + (b * a.rows + r0 + (t >> 4)) * row_groups * 16 + c0 / 2 + 4 * chunk;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int tile_row = (t >> 4) + 16 * j;
-            const int64_t r = r0 + tile_row, g = (c0 >> 5) + (chunk >> 2);
-            float f[8];
-            v[j].floats(f);
-            uint32_t m = 0u;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            Eight<T> v;
+            v.from_shared(tile + tile_row * kTile + 8 * chunk);
             uint32_t code;
-            const uint32_t o = quant8_e2m1(f, m, &code);
-            const bool in = r < a.rows && g < row_groups;
-            if (in) *reinterpret_cast<uint32_t*>(q + (r * row_groups + (c0 >> 5)) * 16 + 4 * chunk) = o;
-            if ((chunk & 3) == 0) codes8[4 * tile_row + (chunk >> 2)] = in ? static_cast<uint8_t>(code) : 0;
-        }
-        __syncthreads();
-        // the four codes of a row: one word of the tile's 512-byte atom, or bytes of a plain row
-        if (t < kTile) {
-            uint8_t* out = static_cast<uint8_t*>(a.s_row) + b * a.s_row_bytes;
-            const int64_t r = r0 + t, g = c0 >> 5;
-            if (a.offsets != nullptr) {   // tiled by expert: its first row starts a band
-                int lo = 0, hi = a.G;   // the last expert that starts at or before the row
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (a.offsets[mid] <= r) lo = mid; else hi = mid;
-                }
-                const int64_t first = a.offsets[lo], end = a.offsets[lo + 1];
-                const int64_t at = (first / kTile + lo) * kTile + (r - first);
-                if (r < a.rows && first >= 0 && r >= first && r < end && at < a.bands_cap * kTile)
-                    *reinterpret_cast<uint32_t*>(out + tiled_scale_offset(at, g, row_groups)) = s_codes[t];
-            } else if (a.tiled) {
-                *reinterpret_cast<uint32_t*>(out + tiled_scale_offset(r, g, row_groups)) = s_codes[t];
-            } else if (r < a.rows) {
-                for (int i = 0; i < 4; ++i)
-                    if (g + i < row_groups) out[r * row_groups + g + i] = codes8[4 * t + i];
-            }
+            const uint32_t o = group_codes(v, &code);
+            const bool in = r0 + tile_row < a.rows && g < row_groups;
+            if (in) *reinterpret_cast<uint32_t*>(q + 16 * j * row_groups * 16) = o;
+            if ((chunk & 3) == 0)
+                reinterpret_cast<uint8_t*>(s_row_codes)[4 * tile_row + (chunk >> 2)] = in ? static_cast<uint8_t>(code) : 0;
         }
     }
-    if constexpr (kCol) {
-        __syncthreads();   // the tile is written, the rows' codes are read
-        uint8_t* q = static_cast<uint8_t*>(a.q_col) + b * a.cols * col_groups * 16;
-#pragma unroll 1
-        for (int k = t; k < 4 * kTile; k += kThreads) {
-            const int c = k & (kTile - 1), block = k >> 7;   // a column, 32 rows of it
-            float f[32];
-            uint32_t m = 0u;
+    {
+        uint8_t* codes8 = reinterpret_cast<uint8_t*>(s_col_codes);
+        if constexpr (sizeof(T) == 2) {
+            const int pair = t & 63, block = t >> 6;
+            const uint32_t* from = reinterpret_cast<const uint32_t*>(tile) + 32 * block * (kTile / 2) + pair;
+            uint32_t w[32], m2 = 0u;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                f[i] = to_float(tile[(32 * block + i) * kTile + c]);
-                m = max(m, abs_bits(f[i]));
+                w[i] = from[i * (kTile / 2)];
+                m2 = max_abs_bf16x2(m2, w[i]);
             }
-            uint32_t o[4], code;
+            m2 &= 0x7FFF7FFFu;
+            const uint32_t m[2] = {m2 << 16, m2 & 0xFFFF0000u};
+            uint32_t code[2];
+            uint4 o[2];
+            if (m[0] < kInfBits && m[1] < kInfBits) {
+                const int e0 = rceil_exponent_f32<kE2M1>(m[0]), e1 = rceil_exponent_f32<kE2M1>(m[1]);
+                const uint32_t s2 = pow2_neg_bf16(e0) | (pow2_neg_bf16(e1) << 16);
+                code[0] = static_cast<uint32_t>(e0 + 127), code[1] = static_cast<uint32_t>(e1 + 127);
+                uint32_t p[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float part[8];
+                for (int i = 0; i < 4; ++i) {
+                    float lo[8], hi[8];
 #pragma unroll
-                for (int n = 0; n < 8; ++n) part[n] = f[8 * i + n];
-                o[i] = quant8_e2m1(part, m, &code);
+                    for (int n = 0; n < 8; ++n) {
+                        const uint32_t u = mul_bf16x2(w[8 * i + n], s2);
+                        lo[n] = bf16_lo(u);
+                        hi[n] = bf16_hi(u);
+                    }
+                    p[0][i] = cvt_e2m1x8(lo);
+                    p[1][i] = cvt_e2m1x8(hi);
+                }
+                o[0] = make_uint4(p[0][0], p[0][1], p[0][2], p[0][3]);
+                o[1] = make_uint4(p[1][0], p[1][1], p[1][2], p[1][3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = k == 0 ? bf16_lo(w[i]) : bf16_hi(w[i]);
+                    o[k] = column_codes(f, m[k], &code[k]);
+                }
             }
-            const int64_t col = c0 + c, g = (r0 >> 5) + block;
-            const bool in = col < a.cols && g < col_groups;
-            if (in) *reinterpret_cast<uint4*>(q + (col * col_groups + g) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-            codes8[4 * c + block] = in ? static_cast<uint8_t>(code) : 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int c = 2 * pair + k;
+                s_out[place_of(c, block)] = o[k];
+                codes8[4 * c + block] = c0 + c < a.cols && (r0 >> 5) + block < col_groups ? static_cast<uint8_t>(code[k]) : 0;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int c = t & (kTile - 1), block = (t >> 7) + 2 * k;
+                float f[32];
+                uint32_t m = 0u, code;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    f[i] = tile[(32 * block + i) * kTile + c];
+                    m = max(m, abs_bits(f[i]));
+                }
+                s_out[place_of(c, block)] = column_codes(f, m, &code);
+                codes8[4 * c + block] = c0 + c < a.cols && (r0 >> 5) + block < col_groups ? static_cast<uint8_t>(code) : 0;
+            }
         }
         __syncthreads();
+        uint8_t* q = static_cast<uint8_t*>(a.q_col) + b * a.cols * col_groups * 16;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = (t >> 2) + 64 * k, block = t & 3;
+            const int64_t g = (r0 >> 5) + block;
+            if (c0 + c < a.cols && g < col_groups)
+                *reinterpret_cast<uint4*>(q + ((c0 + c) * col_groups + g) * 16) = s_out[place_of(c, block)];
+        }
         if (t < kTile) {
-            uint8_t* out = static_cast<uint8_t*>(a.s_col) + b * a.s_col_bytes;
-            const int64_t c = c0 + t, g = r0 >> 5;
-            if (a.tiled) {
-                *reinterpret_cast<uint32_t*>(out + tiled_scale_offset(c, g, col_groups)) = s_codes[t];
-            } else if (c < a.cols) {
-                for (int i = 0; i < 4; ++i)
-                    if (g + i < col_groups) out[c * col_groups + g + i] = codes8[4 * t + i];
-            }
+            store_codes(static_cast<uint8_t*>(a.s_col) + b * a.s_col_bytes, a.tiled, c0 + t, a.cols, r0 >> 5, col_groups,
+                        s_col_codes[t]);
+            if (kRow)
+                store_codes(static_cast<uint8_t*>(a.s_row) + b * a.s_row_bytes, a.tiled, r0 + t, a.rows, c0 >> 5, row_groups,
+                            s_row_codes[t]);
         }
     }
 }
 
 template <typename T, bool kVec>
 cudaError_t launch_quant_t(const Quant4Args& a, cudaStream_t stream) {
-    const Shape s{(a.cols + kTile - 1) / kTile, (a.cols + kTile - 1) / kTile * ((a.rows + kTile - 1) / kTile)};
-    const int64_t blocks = a.batch * s.per_batch;
+    const bool rows_only = a.q_col == nullptr;
+    // tiled scales: whole 512-byte atoms, with their padding
+    const int64_t rows = a.tiled ? (a.rows + kTile - 1) / kTile * kTile : a.rows;
+    const int64_t tiles_c = rows_only ? (a.cols + kColTile - 1) / kColTile : (a.cols + kTile - 1) / kTile;
+    const int64_t per_batch = tiles_c * (rows_only ? (rows + kRowTile - 1) / kRowTile : (a.rows + kTile - 1) / kTile);
+    const int64_t blocks = a.batch * per_batch;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    const unsigned grid = static_cast<unsigned>(blocks);
-    if (a.q_col == nullptr) quant_mxfp4_kernel<T, true, false, kVec><<<grid, kThreads, 0, stream>>>(a, s);
-    else if (a.q_row == nullptr) quant_mxfp4_kernel<T, false, true, kVec><<<grid, kThreads, 0, stream>>>(a, s);
-    else quant_mxfp4_kernel<T, true, true, kVec><<<grid, kThreads, 0, stream>>>(a, s);
-    return cudaGetLastError();
+    const Shape s{static_cast<int>(tiles_c), static_cast<int>(per_batch)};
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if (rows_only) return launch_behind(quant_rows_kernel<T, kVec>, grid, kThreads, 0, stream, a, s);
+    constexpr unsigned kShared = kTile * kTile * sizeof(T) + 4 * kTile * sizeof(uint4);
+    if (a.q_row == nullptr) return launch_behind(quant_tile_kernel<T, false, kVec>, grid, kThreads, kShared, stream, a, s);
+    return launch_behind(quant_tile_kernel<T, true, kVec>, grid, kThreads, kShared, stream, a, s);
 }
 
 // ---- values ----------------------------------------------------------------------------
+//
+// Bound by the values that are written.  Rows that hold whole vectors: 16 elements a thread, one 8- or 16-byte load and
+// 32 or 64 bytes of values.  Any other rows: eight elements a thread on the 16-byte grid of the values, the payload's words
+// shifted to them; element by element at a row's ends only.
 
-// Eight elements a thread.
-template <int kFormat, typename T>
-__global__ void __launch_bounds__(kThreads) dequant_kernel(const Dequant4Args a, int64_t per_row) {
-    const int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
-    const int64_t r = i / per_row, c = (i - r * per_row) * 8;
-    if (r >= a.rows) return;
-    const int64_t groups = (a.cols + 31) >> 5, g = c >> 5;
-    const uint8_t* q = static_cast<const uint8_t*>(a.q) + r * a.ldq;
-    const uint8_t* sc = static_cast<const uint8_t*>(a.s);
-    const float s = scale_of(a.tiled ? sc[tiled_scale_offset(r, g, groups)] : sc[r * a.lds + g]);
-    T* out = static_cast<T*>(a.out) + r * a.ldo;
-    for (int k = 0; k < 8 && c + k < a.cols; k += 2) {
-        uint32_t h;
-        if constexpr (kFormat == kE2M1) {
-            uint32_t all[4];
-            cvt_f16_e2m1x8(q[(c + k) >> 1], all);
-            h = all[0];
-        } else {
-            h = cvt_f16_fp8x2<kFormat>(q[c + k] | (c + k + 1 < a.cols ? q[c + k + 1] << 8 : 0));
-        }
-        out[c + k] = from_float<T>(f16_lo(h) * s);
-        if (c + k + 1 < a.cols) out[c + k + 1] = from_float<T>(f16_hi(h) * s);
+template <int kFormat>
+__device__ __forceinline__ void values8(uint32_t lo, uint32_t hi, float s, float (&f)[8]) {
+    uint32_t h[4];
+    if constexpr (kFormat == kE2M1) {
+        cvt_f16_e2m1x8(lo, h);
+    } else {
+        h[0] = cvt_f16_fp8x2<kFormat>(lo & 0xFFFFu), h[1] = cvt_f16_fp8x2<kFormat>(lo >> 16);
+        h[2] = cvt_f16_fp8x2<kFormat>(hi & 0xFFFFu), h[3] = cvt_f16_fp8x2<kFormat>(hi >> 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = f16_lo(h[i]) * s;
+        f[2 * i + 1] = f16_hi(h[i]) * s;
     }
 }
 
+__device__ __forceinline__ uint32_t scale_code(const Dequant4Args& a, int64_t r, int64_t g, int64_t groups) {
+    const uint8_t* s = static_cast<const uint8_t*>(a.s);
+    return a.tiled ? s[tiled_scale_offset(r, g, groups)] : s[r * a.lds + g];
+}
+
+template <int kFormat, typename T>
+__global__ void __launch_bounds__(kThreads) dequant_kernel(const Dequant4Args a, int log_row) {
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads >> log_row) + (threadIdx.x >> log_row);
+    const int64_t c = ((static_cast<int64_t>(blockIdx.y) << log_row) + (threadIdx.x & ((1 << log_row) - 1))) * 16;
+    if (r >= a.rows || c >= a.cols) return;
+    const uint8_t* q = static_cast<const uint8_t*>(a.q) + r * a.ldq + (kFormat == kE2M1 ? c / 2 : c);
+    uint32_t w[4];
+    if constexpr (kFormat == kE2M1) {
+        const uint2 v = *reinterpret_cast<const uint2*>(q);
+        w[0] = v.x, w[2] = v.y, w[1] = w[3] = 0u;
+    } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(q);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+    const float s = scale_of(scale_code(a, r, c >> 5, (a.cols + 31) >> 5));
+    T* out = static_cast<T*>(a.out) + r * a.ldo + c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float f[8];
+        values8<kFormat>(w[2 * i], w[2 * i + 1], s, f);
+#pragma unroll
+        for (int k = 0; k < 8 / kVec16<T>; ++k) {
+            float part[kVec16<T>];
+#pragma unroll
+            for (int j = 0; j < kVec16<T>; ++j) part[j] = f[k * kVec16<T> + j];
+            __stcs(reinterpret_cast<uint4*>(out + 8 * i) + k, pack<T>(part));
+        }
+    }
+}
+
+// Element i of a row.
 template <int kFormat>
-cudaError_t launch_dequant_t(const Dequant4Args& a, bool f32, cudaStream_t stream) {
-    const int64_t per_row = (a.cols + 7) / 8, blocks = (a.rows * per_row + kThreads - 1) / kThreads;
-    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    if (f32) dequant_kernel<kFormat, float><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a, per_row);
-    else dequant_kernel<kFormat, bf16_bits><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a, per_row);
+__device__ __forceinline__ uint32_t code_at(const uint8_t* q, int64_t i) {
+    return kFormat == kE2M1 ? (q[i >> 1] >> (4 * (i & 1))) & 15u : q[i];
+}
+
+template <int kFormat, typename T>
+__global__ void __launch_bounds__(kThreads) dequant_any_kernel(const Dequant4Args a, int log_row) {
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads >> log_row) + (threadIdx.x >> log_row);
+    if (r >= a.rows) return;
+    T* out = static_cast<T*>(a.out) + r * a.ldo;
+    const uint8_t* q = static_cast<const uint8_t*>(a.q) + r * a.ldq;
+    const int64_t groups = (a.cols + 31) >> 5;
+    // eight elements from i on, which lies on the output's 16-byte grid
+    const int64_t i = ((static_cast<int64_t>(blockIdx.y) << log_row) + (threadIdx.x & ((1 << log_row) - 1))) * 8 -
+                      lead_of<sizeof(T)>(out);
+    if (i >= a.cols) return;
+    if (i < 0 || i + 8 > a.cols) {   // a row's ends, which it shares with its neighbours
+        for (int64_t k = i < 0 ? 0 : i; k < i + 8 && k < a.cols; ++k) {
+            float f[8];
+            values8<kFormat>(code_at<kFormat>(q, k), 0u, scale_of(scale_code(a, r, k >> 5, groups)), f);
+            out[k] = from_float<T>(f[0]);
+        }
+        return;
+    }
+    const int64_t g = i >> 5;
+    const int in_first = static_cast<int>(32 - (i & 31));   // elements that the first of at most two groups has here
+    const float s0 = scale_of(scale_code(a, r, g, groups));
+    const float s1 = in_first < 8 ? scale_of(scale_code(a, r, g + 1, groups)) : s0;
+    uint32_t lo, hi = 0u;
+    if constexpr (kFormat == kE2M1) {   // the payload's rows start on words: two of them, shifted by elements
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(q) + (i >> 3);
+        const int at = static_cast<int>(i & 7);
+        lo = __funnelshift_r(w[0], at != 0 ? w[1] : 0u, 4 * at);
+    } else {
+        const uint8_t* p = q + i;
+        const unsigned at = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 3u);
+        if (at == 0 || (i >= 4 && i + 12 <= a.cols)) {   // whole words around it lie in the row
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(p - at);
+            const uint32_t mid = w[1];
+            lo = __funnelshift_r(w[0], mid, 8 * at);
+            hi = __funnelshift_r(mid, at != 0 ? w[2] : 0u, 8 * at);
+        } else {
+            lo = p[0] | (p[1] << 8) | (p[2] << 16) | (static_cast<uint32_t>(p[3]) << 24);
+            hi = p[4] | (p[5] << 8) | (p[6] << 16) | (static_cast<uint32_t>(p[7]) << 24);
+        }
+    }
+    float f[8];
+    values8<kFormat>(lo, hi, 1.0f, f);   // exact: the scale follows
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] *= k < in_first ? s0 : s1;
+#pragma unroll
+    for (int k = 0; k < 8 / kVec16<T>; ++k) {
+        float part[kVec16<T>];
+#pragma unroll
+        for (int j = 0; j < kVec16<T>; ++j) part[j] = f[k * kVec16<T> + j];
+        __stcs(reinterpret_cast<uint4*>(out + i) + k, pack<T>(part));
+    }
+}
+
+template <int kFormat, typename T>
+cudaError_t launch_dequant_t(const Dequant4Args& a, cudaStream_t stream) {
+    constexpr int64_t kLoad = kFormat == kE2M1 ? 8 : 16;
+    const bool vec = a.cols % 16 == 0 && (reinterpret_cast<uintptr_t>(a.q) | static_cast<uintptr_t>(a.ldq)) % kLoad == 0 &&
+                     (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.ldo * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+    const int64_t units = vec ? a.cols / 16 : (a.cols + 7 + 7) / 8;   // a row that starts off the grid has one more
+    int log_row = 0;   // 1 << log_row threads of a block lie along a row
+    while ((1 << log_row) < kThreads && (1 << log_row) < units) ++log_row;
+    const int64_t down = kThreads >> log_row, x = (a.rows + down - 1) / down, y = (units + (1 << log_row) - 1) >> log_row;
+    if (x > 0x7FFFFFFF || y > 65535) return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y));
+    if (vec) dequant_kernel<kFormat, T><<<grid, kThreads, 0, stream>>>(a, log_row);
+    else dequant_any_kernel<kFormat, T><<<grid, kThreads, 0, stream>>>(a, log_row);
     return cudaGetLastError();
+}
+
+template <int kFormat>
+cudaError_t launch_dequant_of(const Dequant4Args& a, bool f32, cudaStream_t stream) {
+    return f32 ? launch_dequant_t<kFormat, float>(a, stream) : launch_dequant_t<kFormat, bf16_bits>(a, stream);
 }
 
 }  // namespace
@@ -247,9 +565,9 @@ cudaError_t launch_quant_mxfp4(const Quant4Args& a, bool f32, cudaStream_t strea
 }
 
 cudaError_t launch_dequant(const Dequant4Args& a, int format, bool f32, cudaStream_t stream) {
-    if (format == kE2M1) return launch_dequant_t<kE2M1>(a, f32, stream);
-    if (format == kE5M2) return launch_dequant_t<kE5M2>(a, f32, stream);
-    return launch_dequant_t<kE4M3>(a, f32, stream);
+    if (format == kE2M1) return launch_dequant_of<kE2M1>(a, f32, stream);
+    if (format == kE5M2) return launch_dequant_of<kE5M2>(a, f32, stream);
+    return launch_dequant_of<kE4M3>(a, f32, stream);
 }
 
 }  // namespace mxq

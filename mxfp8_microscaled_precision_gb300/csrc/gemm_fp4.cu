@@ -33,13 +33,13 @@ struct Args {
     int64_t M, N, ldy;
     int64_t k_atoms;           // scale atoms of a 128-row band
     int64_t k_padded;          // K up to a multiple of 32
-    int64_t m_tiles, n_tiles;  // dense
+    int m_tiles, n_tiles;      // dense
     int64_t b_bands;           // 128-row bands of an expert's (of B's) scales
     const int64_t* offsets;    // grouped: [G + 1] on the device
     int G;
     int64_t bands_cap;         // grouped: bands of A's scales
-    int y_tma, y_vec;          // the output has a map; its rows hold whole 16-byte vectors
-    int tok_cap, stages, split;   // rows kernel: rows of A in a slot, slots, CTAs along K
+    int y_tma, y_vec;          // the output has a map; its rows hold whole vectors (16 bytes, rows kernel 8)
+    int tok_cap, stages, split, log_split, chunked;   // rows kernel: rows of A in a slot, slots, CTAs along K, see RowsMaps
     unsigned int* status;
     uint64_t wait_limit_ns;
 };
@@ -48,6 +48,14 @@ struct Args {
 __device__ __forceinline__ int64_t offset_at(const Args& p, int g) {
     const int64_t o = p.offsets[g];
     return o < 0 ? int64_t(0) : (o > p.M ? p.M : o);
+}
+
+// A wait by one lane, its verdict as a vote: the compiler sees that a vote is the same in all lanes, so that the loops of
+// the issuing warps keep counters, addresses and descriptors in uniform registers, where the
+// instructions want them.
+template <typename Wait>
+__device__ __forceinline__ bool warp_waits(int lane, Wait wait) {
+    return __all_sync(0xFFFFFFFFu, lane != 0 || wait()) != 0;
 }
 
 // First 128-row band of expert g's scales; its bands end before the next expert's.
@@ -81,7 +89,7 @@ __device__ __forceinline__ void build_prefix(const Args& p, int rows, int* prefi
 }
 
 // The expert of item t.
-__device__ __forceinline__ int expert_of(const int* prefix, int G, int64_t t) {
+__device__ __forceinline__ int expert_of(const int* prefix, int G, int t) {
     int lo = 0, hi = G;   // the last g with prefix[g] <= t
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -90,10 +98,11 @@ __device__ __forceinline__ int expert_of(const int* prefix, int G, int64_t t) {
     return lo;
 }
 
-// Instructions (64 K elements each) that K block kb of k_padded elements needs.
+// Instructions (64 K elements each) that block kb of `block` K elements needs.
+template <int kBlock>
 __device__ __forceinline__ int mmas_of(int64_t k_padded, int64_t kb) {
-    const int64_t left = k_padded - kb * kBK;
-    return left >= kBK ? 4 : static_cast<int>((left + 63) / 64);
+    const int64_t left = k_padded - kb * kBlock;
+    return left >= kBlock ? kBlock / 64 : static_cast<int>((left + 63) / 64);
 }
 
 // ---- CTA pairs -------------------------------------------------------------------------------
@@ -149,14 +158,14 @@ struct PairTile {
 };
 
 template <bool kGrouped>
-__device__ __forceinline__ PairTile pair_tile(const Args& p, const int* prefix, int64_t t, uint32_t rank) {
+__device__ __forceinline__ PairTile pair_tile(const Args& p, const int* prefix, int t, uint32_t rank) {
     PairTile ti;
     if constexpr (!kGrouped) {
         constexpr int kBand = 4;   // raster: bands of 1024 rows, columns inside a band
-        const int64_t per_band = kBand * p.n_tiles, band = t / per_band, within = t - band * per_band;
-        const int64_t height = min(static_cast<int64_t>(kBand), p.m_tiles - band * kBand);
-        ti.m0 = (band * kBand + within % height) * 256 + 128 * rank;
-        ti.n0 = within / height * 256;
+        const int per_band = kBand * p.n_tiles, band = t / per_band, within = t - band * per_band;
+        const int height = min(kBand, p.m_tiles - band * kBand), n = within / height;
+        ti.m0 = static_cast<int64_t>(band * kBand + within - n * height) * 256 + 128 * rank;
+        ti.n0 = static_cast<int64_t>(n) * 256;
         ti.a_band = ti.m0 / 128;
         ti.row_lo = ti.m0;
         ti.row_hi = min(ti.m0 + 128, p.M);
@@ -164,9 +173,10 @@ __device__ __forceinline__ PairTile pair_tile(const Args& p, const int* prefix, 
         ti.b_band = ti.n0 / 128;
     } else {
         const int g = expert_of(prefix, p.G, t);
-        const int64_t local = t - prefix[g], lo = offset_at(p, g), hi = offset_at(p, g + 1);
-        ti.n0 = local % p.n_tiles * 256;
-        const int64_t i = 2 * (local / p.n_tiles) + rank;
+        const int64_t lo = offset_at(p, g), hi = offset_at(p, g + 1);
+        const int local = t - prefix[g], row = local / p.n_tiles;
+        ti.n0 = static_cast<int64_t>(local - row * p.n_tiles) * 256;
+        const int64_t i = 2 * static_cast<int64_t>(row) + rank;
         const bool any = lo + 128 * i < hi;   // an odd number of row tiles leaves the last odd CTA without rows
         ti.m0 = any ? lo + 128 * i : lo;
         ti.a_band = first_band(lo, g) + (any ? i : 0);
@@ -271,12 +281,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
         prefetch_tensormap(&maps.sfa);
         prefetch_tensormap(&maps.sfb);
     }
+    __syncwarp();
     if (warp == 1) {
         tmem_alloc_pair(sbase + L::kOffTmemSlot, L::kTmemCols);
         tmem_relinquish_pair();
     }
     wait_for_previous();
-    int64_t total = p.m_tiles * p.n_tiles;
+    int total = p.m_tiles * p.n_tiles;
     if constexpr (kGrouped) {
         build_prefix(p, 256, prefix);
         total = prefix[p.G];
@@ -286,8 +297,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     cluster_sync_all();   // both CTAs' barriers initialised and tensor memory allocated
     tc_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffTmemSlot);
-    const int64_t pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
-    const int64_t num_kb = (p.k_padded + kBK - 1) / kBK;
+    const int pair_id = static_cast<int>(blockIdx.x >> 1), n_pairs = static_cast<int>(gridDim.x >> 1);
+    const int num_kb = static_cast<int>((p.k_padded + kBK - 1) / kBK);
 
     if (warp == 0) {
         // ---- producer (both CTAs) --------------------------------------------------
@@ -296,16 +307,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
             uint32_t phase = 0;
             const uint32_t full0 = leader ? full_bar(0) : mapa_shared(full_bar(0), 0);
             bool stop = false;
-            for (int64_t t = pair_id; t < total && !stop && !*abort_flag; t += n_pairs) {
+            for (int t = pair_id; t < total && !stop && !*abort_flag; t += n_pairs) {
                 const PairTile ti = pair_tile<kGrouped>(p, prefix, t, rank);
                 const int32_t ma = static_cast<int32_t>(ti.m0), nb = static_cast<int32_t>(ti.b_row + 128 * rank);
                 const int32_t sfa_row = static_cast<int32_t>(2 * ti.a_band * p.k_atoms);
                 const int32_t sfb_row = static_cast<int32_t>(2 * (ti.b_band + rank) * p.k_atoms);
-                for (int64_t kb = 0; kb < num_kb; ++kb) {
+                for (int kb = 0; kb < num_kb; ++kb) {
                     if (!wait_phase(empty_bar(stage), phase ^ 1u, guard)) { stop = true; break; }
                     const uint32_t fb = full0 + 8u * stage;
                     if (leader) mbar_arrive_expect_tx(fb, 2u * L::kStageBytes);
-                    const int32_t kx = static_cast<int32_t>(kb * 128), ks = static_cast<int32_t>(4 * kb);
+                    const int32_t kx = 128 * kb, ks = 4 * kb;
                     tma_load_2d_pair(sbase + L::kOffA + stage * kBandBytes, &maps.a, kx, ma, fb);
                     tma_load_2d_pair(sbase + L::kOffB + stage * kBandBytes, &maps.b, kx, nb, fb);
                     tma_load_2d_pair(sbase + L::kOffSfa + stage * L::kSfaBytes, &maps.sfa, 0, sfa_row + ks, fb);
@@ -331,25 +342,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
             int stage = 0, before = STAGES - 2;   // this stage and the one two before
             uint32_t phase = 0, before_phase = 1, acc = 0, acc_phase = 0, slot = 0;
             bool ok = true;
-            for (int64_t t = pair_id; t < total && ok; t += n_pairs) {
-                int got = 1;
-                if (lane == 0) got = spin_phase(tempty_bar, acc_phase ^ 1u, guard) ? 1 : 0;
-                if (!__shfl_sync(0xFFFFFFFFu, got, 0)) { ok = false; break; }
+            for (int t = pair_id; t < total && ok; t += n_pairs) {
+                if (!warp_waits(lane, [&] { return spin_phase(tempty_bar, acc_phase ^ 1u, guard); })) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * L::kAcc1;
-                for (int64_t kb = 0; kb < num_kb; ++kb) {
+                for (int kb = 0; kb < num_kb; ++kb) {
                     // the slot's scales have been read: the stage two before has completed (before the
                     // first two stages a fresh barrier's odd phase counts as complete)
-                    if (lane == 0)
-                        got = wait_phase(full_bar(stage), phase, guard) && wait_phase(empty_bar(before), before_phase, guard) ? 1 : 0;
-                    if (!__shfl_sync(0xFFFFFFFFu, got, 0)) { ok = false; break; }
+                    if (!warp_waits(lane, [&] {
+                            return wait_phase(full_bar(stage), phase, guard) && wait_phase(empty_bar(before), before_phase, guard);
+                        })) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sfa_t = tmem_base + L::kTmemScales + L::kScaleCols * slot, sfb_t = sfa_t + 8;
                     const uint64_t a_desc = a_desc0 + static_cast<uint64_t>((stage * kBandBytes) >> 4);
                     const uint64_t b_desc = b_desc0 + static_cast<uint64_t>((stage * kBandBytes) >> 4);
                     const uint64_t sfa_d = sfa_desc0 + static_cast<uint64_t>((stage * L::kSfaBytes) >> 4);
                     const uint64_t sfb_d = sfb_desc0 + static_cast<uint64_t>((stage * L::kSfbBytes) >> 4);
-                    const int mmas = mmas_of(p.k_padded, kb);
+                    const int mmas = mmas_of<kBK>(p.k_padded, kb);
                     if (elect_one()) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {   // atom i: K elements 128 i .. of the stage
@@ -392,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
         const uint32_t tempty_leader = leader ? tempty_bar : mapa_shared(tempty_bar, 0);
         const uint32_t buffer = sbase + L::kOffStage + (warp - 2) * 2 * L::kStageWarpBytes;
         uint32_t acc = 0, acc_phase = 0, turn = 0;
-        for (int64_t t = pair_id; t < total; t += n_pairs) {
+        for (int t = pair_id; t < total; t += n_pairs) {
             const PairTile ti = pair_tile<kGrouped>(p, prefix, t, rank);
             // One thread waits (suspending), the other epilogue warps sleep on a
             // named barrier; barrier 2 keeps the verdict until every warp read it.
@@ -445,25 +454,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
 //
 // A tile: 128 columns of y (rows of B) by up to 128 rows of A, transposed in tensor memory: lane n, column m.  The
 // instruction's N is the number of rows of A, rounded up to 16, so few rows cost little beside B's bytes.
-// Slots of B (16 KB), up to tok_cap rows of A in boxes of 16 rows, and two scale atoms of each; as many of them as
-// shared memory holds, since what bounds such a product is the stream of B's bytes.
+// What bounds such a product is the stream of B's bytes, and next to that the single threads that issue it: a copy takes
+// its thread about 90 cycles, a scale copy or an instruction of the tensor core about 50.  So a slot is 512 K elements
+// (of B 32 KB), loaded by four copies where a row's payload is a multiple of 128 bytes: B, A, and the four scale
+// atoms of each; as many slots as shared memory holds.  A comes in boxes of 16 rows or of tok_cap.
 //
 // split > 1 (a cluster, one tile): CTA r takes the r-th part of K; the parts' sums are joined through
 // distributed shared memory in the order of the parts.  split == 1: persistent over tiles, two accumulators.
 struct RowsCfg {
     static constexpr int kThreads = 192;      // producer, MMA issuer, four epilogue warps
-    static constexpr int kMaxStages = 8;
+    static constexpr int kBlockK = 2 * kBK;   // K elements of a slot
+    static constexpr int kMaxStages = 6;
     static constexpr int kNumBars = 2 * kMaxStages + 5;
     static constexpr int kTail = 8 * kNumBars + 16 + 4 * (kMaxExperts + 1);   // behind the ring
-    static constexpr int kAlloc = 227 * 1024;
+    static constexpr int kAlloc = 227 * 1024;   // at most
     static constexpr int kRing = (kAlloc - 1024 - kTail) / 1024 * 1024;
     static constexpr int kTmemCols = 512;
-    static constexpr int kTmemScales = 256;   // after two accumulators of 128 columns: 16 columns a slot
-    static_assert(kTmemScales + 16 * kMaxStages <= kTmemCols, "tensor memory budget");
+    static constexpr int kTmemScales = 256, kScaleCols = 32;   // after two accumulators of 128 columns, of a slot
+    static_assert(kTmemScales + kScaleCols * kMaxStages <= kTmemCols, "tensor memory budget");
 };
 
+// Payloads as [chunk of 128 bytes][row][byte] with boxes of two chunks (Args::chunked), or as [row][byte] with boxes of
+// one; a16: boxes of 16 rows of A, a: of tok_cap.
 struct RowsMaps {
-    CUtensorMap a, b;
+    CUtensorMap a, a16, b;
 };
 
 struct RowsTile {
@@ -472,21 +486,22 @@ struct RowsTile {
 };
 
 template <bool kGrouped>
-__device__ __forceinline__ RowsTile rows_tile(const Args& p, const int* prefix, int64_t t) {
+__device__ __forceinline__ RowsTile rows_tile(const Args& p, const int* prefix, int t) {
     RowsTile ti;
     if constexpr (!kGrouped) {   // the row tiles of a column tile follow each other: B's tile is in L2
-        const int64_t i = t % p.m_tiles;
-        ti.n0 = t / p.m_tiles * 128;
-        ti.m0 = 128 * i;
+        const int n = p.m_tiles == 1 ? t : t / p.m_tiles, i = t - n * p.m_tiles;
+        ti.n0 = static_cast<int64_t>(n) * 128;
+        ti.m0 = static_cast<int64_t>(i) * 128;
         ti.a_band = i;
         ti.rows = static_cast<int>(min(static_cast<int64_t>(128), p.M - ti.m0));
         ti.b_row = ti.n0;
         ti.b_band = ti.n0 / 128;
     } else {
         const int g = expert_of(prefix, p.G, t);
-        const int64_t lo = offset_at(p, g), hi = offset_at(p, g + 1), tiles = (hi - lo + 127) / 128, local = t - prefix[g];
-        const int64_t i = local % tiles;
-        ti.n0 = local / tiles * 128;
+        const int64_t lo = offset_at(p, g), hi = offset_at(p, g + 1);
+        const int tiles = static_cast<int>((hi - lo + 127) / 128), local = t - prefix[g], n = local / tiles;
+        const int64_t i = local - n * tiles;
+        ti.n0 = static_cast<int64_t>(n) * 128;
         ti.m0 = lo + 128 * i;
         ti.a_band = first_band(lo, g) + i;
         ti.rows = static_cast<int>(min(static_cast<int64_t>(128), hi - ti.m0));
@@ -505,15 +520,16 @@ __global__ void __launch_bounds__(RowsCfg::kThreads, 1)
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = p.split, stages = p.stages;
-    const int rank = split > 1 ? static_cast<int>(blockIdx.x % split) : 0;
-    const int tok_bytes = p.tok_cap * 128, stage_bytes = kBandBytes + tok_bytes + 4 * kAtom;
-    const uint32_t bar0 = sbase + L::kRing;
+    const int rank = static_cast<int>(blockIdx.x) & (split - 1);
+    const int tok_bytes = p.tok_cap * 256, stage_bytes = 2 * kBandBytes + tok_bytes + 8 * kAtom;
+    const int ring = stages * stage_bytes;
+    const uint32_t bar0 = sbase + ring;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (L::kMaxStages + s); };
     auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * L::kMaxStages) + 8u * a; };
     auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * L::kMaxStages + 2) + 8u * a; };
     const uint32_t drain_bar = bar0 + 8u * (2 * L::kMaxStages + 4);
-    uint8_t* tail = smem + L::kRing + 8 * L::kNumBars;
+    uint8_t* tail = smem + ring + 8 * L::kNumBars;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(tail);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
     int* prefix = reinterpret_cast<int*>(tail + 16);
@@ -532,97 +548,120 @@ __global__ void __launch_bounds__(RowsCfg::kThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tensormap(&maps.a);
+        prefetch_tensormap(&maps.a16);
         prefetch_tensormap(&maps.b);
     }
+    __syncwarp();
     if (warp == 1) {
         tmem_alloc(smem_u32(tail), L::kTmemCols);
         tmem_relinquish();
     }
-    wait_for_previous();
-    int64_t total = p.m_tiles * p.n_tiles;
+    int total = p.m_tiles * p.n_tiles;
     if constexpr (kGrouped) {
+        wait_for_previous();
         build_prefix(p, 128, prefix);
         total = prefix[p.G];
     }
+    // The producer goes on: it needs the barriers, which are its own, and not the tensor memory.
     tc_fence_before();
-    __syncthreads();
+    if (warp == 0) named_bar_arrive(1, L::kThreads);
+    else named_bar_sync(1, L::kThreads);
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
-    const int64_t num_kb = (p.k_padded + kBK - 1) / kBK;
-    const int64_t kb_lo = num_kb * rank / split, kb_hi = num_kb * (rank + 1) / split;
-    const int64_t first = blockIdx.x / split, step = gridDim.x / split;
+    const uint32_t tmem_base = warp == 0 ? 0u : *tmem_slot;
+    // split is a power of two; 64-bit divisions here would cost more than a slot's load
+    const int num_kb = static_cast<int>((p.k_padded + L::kBlockK - 1) / L::kBlockK);
+    const int kb_lo = static_cast<int>(static_cast<uint64_t>(num_kb) * rank >> p.log_split);
+    const int kb_hi = static_cast<int>(static_cast<uint64_t>(num_kb) * (rank + 1) >> p.log_split);
+    const int first = static_cast<int>(blockIdx.x >> p.log_split), step = static_cast<int>(gridDim.x >> p.log_split);
 
     if (warp == 0) {
-        // ---- producer ------------------------------------------------------------------
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int64_t issued = 0;
-            bool stop = false;
-            for (int64_t t = first; t < total && !stop && !*abort_flag; t += step) {
-                const RowsTile ti = rows_tile<kGrouped>(p, prefix, t);
-                const int boxes = (ti.rows + 15) >> 4;
-                const uint8_t* sfa = p.a_s + ti.a_band * p.k_atoms * kAtom;
-                const uint8_t* sfb = p.b_s + ti.b_band * p.k_atoms * kAtom;
-                for (int64_t kb = kb_lo; kb < kb_hi; ++kb) {
-                    if (!wait_phase(empty_bar(stage), phase ^ 1u, guard)) { stop = true; break; }
-                    const uint32_t fb = full_bar(stage), at = sbase + stage * stage_bytes;
-                    const uint32_t scales = kAtom * static_cast<uint32_t>(min(int64_t(2), p.k_atoms - 2 * kb));
-                    mbar_arrive_expect_tx(fb, kBandBytes + 2048u * boxes + 2u * scales);
-                    const int32_t kx = static_cast<int32_t>(kb * 128);
-                    tma_load_2d(at, &maps.b, kx, static_cast<int32_t>(ti.b_row), fb);
-                    for (int i = 0; i < boxes; ++i)
-                        tma_load_2d(at + kBandBytes + 2048u * i, &maps.a, kx, static_cast<int32_t>(ti.m0 + 16 * i), fb);
-                    bulk_load(at + kBandBytes + tok_bytes, sfb + 2 * kb * kAtom, scales, fb);
-                    bulk_load(at + kBandBytes + tok_bytes + 2 * kAtom, sfa + 2 * kb * kAtom, scales, fb);
-                    ++issued;
-                    if (++stage == stages) { stage = 0; phase ^= 1u; }
+        // ---- producer (warp-uniform loops, one elected lane issues) ------------------------------
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool stop = false, waited = kGrouped;
+        for (int t = first; t < total && !stop; t += step) {
+            const RowsTile ti = rows_tile<kGrouped>(p, prefix, t);
+            const bool few = ti.rows <= 16;
+            const CUtensorMap* map_a = few ? &maps.a16 : &maps.a;
+            const int box = few ? 16 * 128 : p.tok_cap * 128;   // bytes of a chunk of A
+            const int32_t row_a = static_cast<int32_t>(ti.m0), row_b = static_cast<int32_t>(ti.b_row);
+            const uint8_t* sfa = p.a_s + (ti.a_band * p.k_atoms + 4 * kb_lo) * kAtom;
+            const uint8_t* sfb = p.b_s + (ti.b_band * p.k_atoms + 4 * kb_lo) * kAtom;
+            int32_t chunk = 2 * kb_lo;
+            int atoms = static_cast<int>(p.k_atoms) - 4 * kb_lo;   // that are left
+            if (!waited) wait_for_previous();   // nothing above reads what the kernel before wrote
+            waited = true;
+            for (int kb = kb_lo; kb < kb_hi; ++kb) {
+                if (!warp_waits(lane, [&] { return wait_phase(empty_bar(stage), phase ^ 1u, guard); })) { stop = true; break; }
+                const uint32_t fb = full_bar(stage), at = sbase + stage * stage_bytes, at_a = at + 2 * kBandBytes;
+                const uint32_t scales = atoms >= 4 ? 4 * kAtom : kAtom * static_cast<uint32_t>(atoms);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(fb, 2u * (kBandBytes + box + scales));
+                    if (p.chunked) {
+                        tma_load_3d(at, &maps.b, 0, row_b, chunk, fb);
+                        tma_load_3d(at_a, map_a, 0, row_a, chunk, fb);
+                    } else {
+                        tma_load_2d(at, &maps.b, 128 * chunk, row_b, fb);
+                        tma_load_2d(at + kBandBytes, &maps.b, 128 * chunk + 128, row_b, fb);
+                        tma_load_2d(at_a, map_a, 128 * chunk, row_a, fb);
+                        tma_load_2d(at_a + box, map_a, 128 * chunk + 128, row_a, fb);
+                    }
+                    bulk_load(at_a + tok_bytes, sfb, scales, fb);
+                    bulk_load(at_a + tok_bytes + 4 * kAtom, sfa, scales, fb);
                 }
-            }
-            if (*abort_flag) {
-                // Let copies already in flight land before the CTA exits.
-                const int64_t n = issued < stages ? issued : stages;
-                int s = stage;
-                uint32_t ph = phase;
-                for (int64_t i = 0; i < n; ++i) {
-                    if (--s < 0) { s = stages - 1; ph ^= 1u; }
-                    WaitGuard g2 = guard;
-                    volatile int never = 0;
-                    g2.abort_flag = &never;
-                    (void)mbar_wait(full_bar(s), ph, g2);
-                }
+                __syncwarp();
+                sfa += 4 * kAtom, sfb += 4 * kAtom, chunk += 2, atoms -= 4;
+                ++issued;
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
             }
         }
+        if (lane == 0 && *abort_flag) {
+            // Let copies already in flight land before the CTA exits.
+            for (int i = issued < stages ? issued : stages; i > 0; --i) {
+                if (--stage < 0) { stage = stages - 1; phase ^= 1u; }
+                WaitGuard g2 = guard;
+                volatile int never = 0;
+                g2.abort_flag = &never;
+                (void)mbar_wait(full_bar(stage), phase, g2);
+            }
+        }
+        __syncwarp();
     } else if (warp == 1) {
         // ---- MMA issuer ----------------------------------------------------------------
+        if (!kGrouped) wait_for_previous();
         int stage = 0;
         uint32_t phase = 0, acc = 0, acc_phase = 0;
         bool ok = true;
-        for (int64_t t = first; t < total && ok; t += step) {
-            const int rows = rows_tile<kGrouped>(p, prefix, t).rows;
-            const uint32_t N = static_cast<uint32_t>((rows + 15) & ~15);
-            int got = 1;
-            if (lane == 0) got = spin_phase(tempty_bar(acc), acc_phase ^ 1u, guard) ? 1 : 0;
-            if (!__shfl_sync(0xFFFFFFFFu, got, 0)) { ok = false; break; }
+        for (int t = first; t < total && ok; t += step) {
+            const RowsTile ti = rows_tile<kGrouped>(p, prefix, t);
+            const uint32_t N = static_cast<uint32_t>((ti.rows + 15) & ~15);
+            if (!warp_waits(lane, [&] { return spin_phase(tempty_bar(acc), acc_phase ^ 1u, guard); })) { ok = false; break; }
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + acc * 128;
-            for (int64_t kb = kb_lo; kb < kb_hi; ++kb) {
-                if (lane == 0) got = wait_phase(full_bar(stage), phase, guard) ? 1 : 0;
-                if (!__shfl_sync(0xFFFFFFFFu, got, 0)) { ok = false; break; }
+            const uint32_t idesc = make_idesc_mxf4(128, N, 0), idesc2 = make_idesc_mxf4(128, N, 2);
+            const uint64_t a_chunk = static_cast<uint64_t>((ti.rows <= 16 ? 16 * 128 : p.tok_cap * 128) >> 4);
+            for (int kb = kb_lo; kb < kb_hi; ++kb) {
+                if (!warp_waits(lane, [&] { return wait_phase(full_bar(stage), phase, guard); })) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t at = sbase + stage * stage_bytes, sc = at + kBandBytes + tok_bytes;
-                const uint32_t sfb_t = tmem_base + L::kTmemScales + 16 * stage, sfa_t = sfb_t + 8;
-                const uint64_t b_desc = make_smem_desc(at, 16, 1024, 2), a_desc = make_smem_desc(at + kBandBytes, 16, 1024, 2);
+                const uint32_t at = sbase + stage * stage_bytes, sc = at + 2 * kBandBytes + tok_bytes;
+                const uint32_t sfb_t = tmem_base + L::kTmemScales + L::kScaleCols * stage, sfa_t = sfb_t + 16;
+                const uint64_t b_desc = make_smem_desc(at, 16, 1024, 2), a_desc = make_smem_desc(at + 2 * kBandBytes, 16, 1024, 2);
                 const uint64_t s_desc = make_smem_desc(sc, 0, 128, 0);
-                const int mmas = mmas_of(p.k_padded, kb);
+                const int mmas = mmas_of<L::kBlockK>(p.k_padded, kb);
                 if (elect_one()) {
+                    // atom i: K elements 128 i .. of the slot, two instructions; chunk i / 2
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)   // B's two atoms, then A's
-                        tc_cp_32x128b_warpx4(sfb_t + 4 * i, s_desc + static_cast<uint64_t>((i * kAtom) >> 4));
+                    for (int i = 0; i < 4; ++i) {
+                        if (2 * i < mmas) {
+                            tc_cp_32x128b_warpx4(sfb_t + 4 * i, s_desc + static_cast<uint64_t>((i * kAtom) >> 4));
+                            tc_cp_32x128b_warpx4(sfa_t + 4 * i, s_desc + static_cast<uint64_t>(((i + 4) * kAtom) >> 4));
+                        }
+                    }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 8; ++k)
                         if (k < mmas)
-                            tc_mma_mxf4(d_tmem, b_desc + 2 * k, a_desc + 2 * k, make_idesc_mxf4(128, N, 2 * (k & 1)),
+                            tc_mma_mxf4(d_tmem, b_desc + static_cast<uint64_t>(((k >> 2) * kBandBytes) >> 4) + 2 * (k & 3),
+                                        a_desc + (k >= 4 ? a_chunk : 0) + 2 * (k & 3), k & 1 ? idesc2 : idesc,
                                         sfb_t + 4 * (k >> 1), sfa_t + 4 * (k >> 1), (kb > kb_lo || k > 0) ? 1u : 0u);
                     tc_commit(empty_bar(stage));
                 }
@@ -645,13 +684,12 @@ __global__ void __launch_bounds__(RowsCfg::kThreads, 1)
         __syncwarp();
     } else {
         // ---- epilogue: lane l of the warp on quarter q holds column n0 + 32 q + l of y ----------------
+        if (!kGrouped) wait_for_previous();
         const int quad = warp & 3, n = 32 * quad + lane;
         uint32_t acc = 0, acc_phase = 0;
-        for (int64_t t = first; t < total; t += step) {
+        for (int t = first; t < total; t += step) {
             const RowsTile ti = rows_tile<kGrouped>(p, prefix, t);
-            int got = 1;
-            if (lane == 0) got = wait_phase(tfull_bar(acc), acc_phase, guard) ? 1 : 0;
-            if (!__shfl_sync(0xFFFFFFFFu, got, 0)) break;
+            if (!warp_waits(lane, [&] { return wait_phase(tfull_bar(acc), acc_phase, guard); })) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + acc * 128;
             const bool in = ti.n0 + n < p.N;
@@ -681,19 +719,34 @@ __global__ void __launch_bounds__(RowsCfg::kThreads, 1)
     __syncthreads();
     if (split > 1) {
         cluster_sync_all();   // every part is written
-        if (first < total && warp >= 2) {
+        if (first < total) {
+            // a warp joins a row of 128 columns at a time, four a lane
             const RowsTile ti = rows_tile<kGrouped>(p, prefix, first);
-            const int n = static_cast<int>(threadIdx.x) - 64;
-            if (ti.n0 + n < p.N) {
-                for (int m = rank; m < ti.rows; m += split) {
-                    float sum = 0.0f;
-                    for (int s = 0; s < split; ++s)
-                        sum += ld_cluster(mapa_shared(sbase + 4u * static_cast<uint32_t>(m * 128 + n), static_cast<uint32_t>(s)));
-                    p.y[(ti.m0 + m) * p.ldy + ti.n0 + n] = from_float<bf16_bits>(sum);
+            const int64_t n = ti.n0 + 4 * lane;
+#pragma unroll 2
+            for (int m = rank + split * warp; m < ti.rows; m += split * (L::kThreads / 32)) {
+                const uint32_t at = sbase + 16u * static_cast<uint32_t>(m * 32 + lane);
+                float4 part[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s < split) part[s] = ld_cluster(mapa_shared(at, static_cast<uint32_t>(s)));
+                float4 sum = part[0];
+#pragma unroll
+                for (int s = 1; s < 8; ++s)
+                    if (s < split) sum.x += part[s].x, sum.y += part[s].y, sum.z += part[s].z, sum.w += part[s].w;
+                const uint32_t lo = cvt_bf16x2(sum.x, sum.y), hi = cvt_bf16x2(sum.z, sum.w);
+                uint16_t* out = p.y + (ti.m0 + m) * p.ldy + n;
+                if (p.y_vec && n + 4 <= p.N) {
+                    *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+                } else {
+                    if (n < p.N) out[0] = static_cast<uint16_t>(lo);
+                    if (n + 1 < p.N) out[1] = static_cast<uint16_t>(lo >> 16);
+                    if (n + 2 < p.N) out[2] = static_cast<uint16_t>(hi);
+                    if (n + 3 < p.N) out[3] = static_cast<uint16_t>(hi >> 16);
                 }
             }
         }
-        cluster_sync_all();   // nobody leaves while its part is read
+        cluster_sync_relaxed();   // nobody leaves while its part is read
     }
     tc_fence_after();
     if (warp == 1) {
@@ -704,10 +757,17 @@ __global__ void __launch_bounds__(RowsCfg::kThreads, 1)
 
 // ---- host --------------------------------------------------------------------------------------
 
+constexpr int64_t kMostItems = (int64_t(1) << 31) - 4096;   // tiles of a launch: 32-bit counters step past the last one
+
 // Payload [rows, row_bytes], boxes of box_rows x 128 bytes, 128-byte swizzle.
 bool payload_map(CUtensorMap* map, const void* q, int64_t rows, int64_t row_bytes, uint32_t box_rows) {
     return encode_tensor_map_2d(map, q, false, static_cast<uint64_t>(row_bytes), static_cast<uint64_t>(rows),
                                 static_cast<uint64_t>(row_bytes), 128u, box_rows, true);
+}
+
+// The same by chunks of 128 bytes (row_bytes a multiple of it), boxes of box_rows rows of two chunks, chunk by chunk.
+bool chunk_map(CUtensorMap* map, const void* q, int64_t rows, int64_t row_bytes, uint32_t box_rows) {
+    return encode_tensor_map_chunks(map, q, static_cast<uint64_t>(rows), static_cast<uint64_t>(row_bytes), box_rows, 2u);
 }
 
 // MMA-tiled scales as rows of 256 bytes, boxes of two atoms.
@@ -759,14 +819,42 @@ cudaError_t launch_pair(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
         !scale_map(&maps.sfa, g.a_s, kGrouped ? g.bands_cap : (g.M + 127) / 128, args.k_atoms) ||
         !scale_map(&maps.sfb, g.b_s, experts * args.b_bands, args.k_atoms))
         return cudaErrorInvalidValue;
-    args.m_tiles = (g.M + 255) / 256;
-    args.n_tiles = (g.N + 255) / 256;
+    const int64_t m_tiles = (g.M + 255) / 256, n_tiles = (g.N + 255) / 256;
+    if ((kGrouped ? m_tiles + g.G : m_tiles) * n_tiles > kMostItems) return cudaErrorInvalidValue;
+    args.m_tiles = static_cast<int>(m_tiles);
+    args.n_tiles = static_cast<int>(n_tiles);
     args.y_vec = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0;
     args.y_tma = args.y_vec && encode_tensor_map_bf16_store(&maps.y, g.y, static_cast<uint64_t>(g.N),
                                                             static_cast<uint64_t>(g.M), static_cast<uint64_t>(g.ldy));
     int64_t pairs = dev.sm_count / 2;
-    if (!kGrouped && args.m_tiles * args.n_tiles < pairs) pairs = args.m_tiles * args.n_tiles;
+    if (!kGrouped && m_tiles * n_tiles < pairs) pairs = m_tiles * n_tiles;
     return launch(gemm_mxfp4_pair_kernel<kGrouped>, 2 * pairs, L::kThreads, L::kAlloc, 0, stream, maps, args);
+}
+
+// Clusters of 1 << log_split CTAs of the rows kernel that the device holds at once (looked up once per device and thread).
+template <bool kGrouped>
+int64_t clusters_of(const DeviceInfo& dev, int log_split) {
+    static thread_local int known_device = -1;
+    static thread_local int known[4];
+    if (known_device != dev.device) {
+        for (int i = 0; i < 4; ++i) {
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 1u << i;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cudaLaunchConfig_t config{};
+            config.gridDim = dim3(static_cast<unsigned>(dev.sm_count >> i << i));
+            config.blockDim = dim3(RowsCfg::kThreads);
+            config.dynamicSmemBytes = RowsCfg::kAlloc;
+            config.attrs = &attr;
+            config.numAttrs = 1;
+            known[i] = 0;
+            if (cudaOccupancyMaxActiveClusters(&known[i], gemm_mxfp4_rows_kernel<kGrouped>, &config) != cudaSuccess)
+                (void)cudaGetLastError();
+        }
+        known_device = dev.device;
+    }
+    return known[log_split];
 }
 
 template <bool kGrouped>
@@ -777,22 +865,49 @@ cudaError_t launch_rows(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
     if (e != cudaSuccess) return e;
     const int64_t row_bytes = args.k_padded / 2, experts = kGrouped ? g.G : 1;
     RowsMaps maps;
-    if (!payload_map(&maps.a, g.a_q, g.M, row_bytes, 16) || !payload_map(&maps.b, g.b_q, experts * g.N, row_bytes, 128))
-        return cudaErrorInvalidValue;
-    args.m_tiles = (g.M + 127) / 128;
-    args.n_tiles = (g.N + 127) / 128;
+    const int64_t m_tiles = (g.M + 127) / 128, n_tiles = (g.N + 127) / 128;
+    // tiles, at most: grouped, of the experts with rows, each with one partly filled tile
+    const int64_t tiles = (kGrouped ? (g.M < g.G ? g.M : g.G) + g.M / 128 : m_tiles) * n_tiles;
+    if (tiles > kMostItems) return cudaErrorInvalidValue;
+    args.m_tiles = static_cast<int>(m_tiles);
+    args.n_tiles = static_cast<int>(n_tiles);
+    args.y_vec = (reinterpret_cast<uintptr_t>(g.y) & 7u) == 0 && g.ldy % 4 == 0;
     args.tok_cap = static_cast<int>(g.M < 128 ? (g.M + 15) / 16 * 16 : 128);
-    const int stage_bytes = kBandBytes + args.tok_cap * 128 + 4 * kAtom;
+    args.chunked = row_bytes % 128 == 0;
+    const auto map = [&](CUtensorMap* m, const void* q, int64_t rows, int box) {
+        return args.chunked ? chunk_map(m, q, rows, row_bytes, static_cast<uint32_t>(box))
+                            : payload_map(m, q, rows, row_bytes, static_cast<uint32_t>(box));
+    };
+    if (!map(&maps.a, g.a_q, g.M, args.tok_cap) || !map(&maps.a16, g.a_q, g.M, 16) || !map(&maps.b, g.b_q, experts * g.N, 128))
+        return cudaErrorInvalidValue;
+    const int stage_bytes = 2 * kBandBytes + args.tok_cap * 256 + 8 * kAtom;
     args.stages = L::kRing / stage_bytes < L::kMaxStages ? L::kRing / stage_bytes : L::kMaxStages;
-    // tiles, at most: of experts with rows, each with one partly filled tile
-    int64_t tiles = args.m_tiles * args.n_tiles;
-    if (kGrouped) tiles = ((g.M < g.G ? g.M : g.G) + g.M / 128) * args.n_tiles;
-    const int64_t num_kb = (args.k_padded + kBK - 1) / kBK;
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= dev.sm_count && num_kb >= split * 4) split *= 2;
+    const int smem = 1024 + args.stages * stage_bytes + L::kTail;
+    const int64_t num_kb = (args.k_padded + L::kBlockK - 1) / L::kBlockK;
+    int log_split = 0;
+    while (log_split < 3 && tiles << (log_split + 1) <= dev.sm_count && num_kb >> (log_split + 1) >= 1) ++log_split;
+    // as many clusters as the device holds at once: 8 CTAs have to lie in one GPC, whose other SMs stay idle
+    while (log_split > 1 && tiles > clusters_of<kGrouped>(dev, log_split)) --log_split;
+    const int split = 1 << log_split;
     args.split = split;
+    args.log_split = log_split;
     const int64_t grid = split > 1 ? tiles * split : (tiles < dev.sm_count ? tiles : dev.sm_count);
-    return launch(gemm_mxfp4_rows_kernel<kGrouped>, grid, L::kThreads, L::kAlloc, split > 1 ? split : 0, stream, maps, args);
+    return launch(gemm_mxfp4_rows_kernel<kGrouped>, grid, L::kThreads, smem, split > 1 ? split : 0, stream, maps, args);
+}
+
+// Which kernel.  Few rows leave most of a 256-row tile's instructions idle and the device without tiles; many rows make
+// the rows kernel read B once for each 128 of them.  Measured, rows kernel / pairs (us, in a graph, N x K):
+//   M = 16    5.7 / 9.9 (4096 x 4096)    4.8 / 5.9 (4096 x 1024)   26 / 33 (16384 x 16384)
+//   M = 64    6.7 / 9.8                  6.3 / 5.8                 29 / 33
+//   M = 128   8.4 / 10.1                 8.0 / 6.1                 36 / 34
+//   M = 256   10.6 / 10.0                8.4 / 6.1                 53 / 34
+// Grouped, 128 experts of 4096 x 4096: 0.5 rows an expert 53 / 63, 16: 191 / 203, 64: 227 / 224, 256: 411 / 318.
+template <bool kGrouped>
+bool fills_pairs(const Gemm4Args& g) {
+    if (kGrouped) return g.M > 48 * static_cast<int64_t>(g.G);
+    if (g.M <= 32) return false;
+    if (g.M > 128 || g.K < 2048) return true;
+    return g.M > 64 && g.N > 8192;
 }
 
 }  // namespace
@@ -812,10 +927,8 @@ cudaError_t launch_gemm_mxfp4(const DeviceInfo& dev, const Gemm4Args& g, cudaStr
     a.split = 1;
     a.status = dev.status;
     a.wait_limit_ns = kDefaultWaitLimitNs;
-    if (g.offsets != nullptr)
-        return g.M > 64 * static_cast<int64_t>(g.G) ? launch_pair<true>(dev, g, a, stream) : launch_rows<true>(dev, g, a, stream);
-    return ((g.M + 255) / 256) * ((g.N + 255) / 256) >= 64 ? launch_pair<false>(dev, g, a, stream)
-                                                            : launch_rows<false>(dev, g, a, stream);
+    return g.offsets != nullptr ? (fills_pairs<true>(g) ? launch_pair<true>(dev, g, a, stream) : launch_rows<true>(dev, g, a, stream))
+                                : (fills_pairs<false>(g) ? launch_pair<false>(dev, g, a, stream) : launch_rows<false>(dev, g, a, stream));
 }
 
 }  // namespace mxq

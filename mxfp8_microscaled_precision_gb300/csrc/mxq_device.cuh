@@ -72,6 +72,11 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
+// The same without sleeping: this warp counts as arrived and goes on.
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // Orders this thread's view of earlier generic-proxy shared-memory accesses
 // (after a CTA barrier: every thread's) before its later async-proxy ones (TMA).
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -339,16 +344,23 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
     return r;
 }
 
-// The float at a shared::cluster address (possibly in a peer CTA).
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+// Four floats at a shared::cluster address (possibly in a peer CTA), which the caller's barrier has made
+// visible; loads of several CTAs may be in flight together.
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
 
 // Every thread of every CTA of the cluster (release / acquire at cluster scope).
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The same for threads whose earlier loads have been consumed and whose stores nobody in the cluster reads: a release
+// would wait until those stores have reached memory.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // Arrive on an mbarrier given by its shared::cluster address (possibly in the

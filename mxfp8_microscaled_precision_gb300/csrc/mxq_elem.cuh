@@ -335,9 +335,19 @@ struct ParamSlots {
     }
 };
 
+// Asynchronous copy of 16 bytes to shared memory (both sides aligned), of which `bytes` are read and the others set to 0.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // In a kernel launched by launch_behind: returns when the kernel before it has ended and its
 // results are visible.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// In any kernel: a kernel launched behind it by launch_behind may be put on the device from now on, as far as there is
+// room; what it reads still waits for this one's end.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Sum over the warp, the same order on every call, the result in all lanes.
 __device__ __forceinline__ float warp_sum(float v) {

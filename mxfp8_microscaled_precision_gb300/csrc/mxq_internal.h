@@ -29,14 +29,19 @@ cudaError_t current_device_is_supported(bool* yes);
 // before it on the stream (clipping 6 gradients 8.7 us to 8.2 us, 16384 x 64 layer norm backward 11.2 us to 10.6 us then; letting its
 // blocks start before that end changes nothing more).
 template <typename... Params>
-inline cudaError_t launch_behind(void (*kernel)(Params...), unsigned grid, unsigned block, cudaStream_t stream,
-                                 const std::remove_cv_t<Params>&... args) {
+inline cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, unsigned block, unsigned shared,
+                                 cudaStream_t stream, const std::remove_cv_t<Params>&... args) {
+    if (shared > 48 * 1024) {   // a constant of the kernel at each call
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchAttribute attribute{};
     attribute.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attribute.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t config{};
-    config.gridDim = dim3(grid);
+    config.gridDim = grid;
     config.blockDim = dim3(block);
+    config.dynamicSmemBytes = shared;
     config.stream = stream;
     config.attrs = &attribute;
     config.numAttrs = 1;
@@ -49,6 +54,11 @@ inline cudaError_t launch_behind(void (*kernel)(Params...), unsigned grid, unsig
 bool encode_tensor_map_2d(CUtensorMap* map, const void* base, bool two_byte_elems, uint64_t inner,
                           uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner,
                           uint32_t box_outer, bool swizzle_128b);
+
+// Bytes [rows, row_bytes] (row_bytes a multiple of 128) as [chunk][row][128 bytes], boxes of box_chunks x box_rows x
+// 128 with the 128-byte swizzle.
+bool encode_tensor_map_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows,
+                              uint32_t box_chunks);
 
 // 3-D tensor map [outer, mid, inner], box [1, box_mid, box_inner], no swizzle.
 // BF16 [rows, cols] (row stride ld elements) for 32 x 32 tiled stores with the

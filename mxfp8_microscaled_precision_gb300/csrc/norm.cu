@@ -892,7 +892,7 @@ cudaError_t norm_backward_launch(const NormBackwardArgs& a, cudaStream_t stream)
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || (a.dweight == nullptr && a.dshift == nullptr)) return e;
-    return launch_behind(norm_reduce_kernel, static_cast<unsigned>((2 * a.cols + 31) / 32), 1024, stream, a.partial,
+    return launch_behind(norm_reduce_kernel, static_cast<unsigned>((2 * a.cols + 31) / 32), 1024, 0, stream, a.partial,
                          static_cast<int>(parts), static_cast<int>(a.cols), a.dweight, a.dshift);
 }
 

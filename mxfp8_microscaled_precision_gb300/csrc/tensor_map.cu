@@ -63,6 +63,19 @@ bool encode_tensor_map_2d(CUtensorMap* map, const void* base, bool two_byte_elem
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tensor_map_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows,
+                              uint32_t box_chunks) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rows == 0 || row_bytes == 0 || row_bytes % 128 != 0) return false;
+    const cuuint64_t dims[3] = {128u, rows, row_bytes / 128};
+    const cuuint64_t strides[2] = {row_bytes, 128u};
+    const cuuint32_t box[3] = {128u, box_rows, box_chunks};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // BF16 matrix [rows, cols] with a row stride of ld elements, as the target of
 // tiled stores of 32 x 32 boxes from shared memory laid out with the 64-byte
 // swizzle (16-byte chunk j of box row r at chunk position j ^ ((r >> 1) & 3)).

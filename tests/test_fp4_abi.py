@@ -47,7 +47,7 @@ def test_values(L):
                 dict(lds=1), dict(ldo=39), dict(q=None), dict(s=None), dict(out=None), dict(out=ODD), dict(out=HALF, dtype=1),
                 dict(elem=2, ldq=31), dict(elem=2, ldq=34), dict(elem=2, q=HALF, ldq=32)):
         assert d(**bad) == 1, bad
-    assert d(rows=BIG) == 2 and d(rows=1 << 30, cols=1 << 20, ldq=1 << 20, lds=1 << 15, ldo=1 << 20) == 2
+    assert d(rows=BIG) == 2 and d(cols=1 << 24, ldq=1 << 24, lds=1 << 19, ldo=1 << 24) == 2
 
 
 def test_products(L):
