@@ -140,13 +140,13 @@ __device__ __forceinline__ void store_codes(uint8_t* out, bool tiled, int64_t r,
     }
 }
 
-// Eight rows r, r + step, .. of `rows` rows of n elements: their elements [c, c + 8), 0 outside the matrix.  What a vector
+// kRows rows r, r + step, .. of `rows` rows of n elements: their elements [c, c + 8), 0 outside the matrix.  What a vector
 // load may touch comes first, all of it in flight at once; the ends that it may not, element by element, last.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load_rows(Eight<T> (&v)[8], const T* x, int64_t ld, int64_t r, int step, int64_t rows, int c, int n) {
+template <typename T, bool kVec, int kRows>
+__device__ __forceinline__ void load_rows(Eight<T> (&v)[kRows], const T* x, int64_t ld, int64_t r, int step, int64_t rows, int c, int n) {
     bool ends = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kRows; ++j) {
         const int64_t row = r + j * step;
         const T* p = x + j * step * ld;
 #pragma unroll
@@ -164,7 +164,7 @@ __device__ __forceinline__ void load_rows(Eight<T> (&v)[8], const T* x, int64_t 
     }
     if (!ends) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kRows; ++j) {
         const int64_t row = r + j * step;
 #pragma unroll
         for (int i = 0; i < Eight<T>::kWords; ++i) {
@@ -200,30 +200,33 @@ __device__ __forceinline__ bool is_whole(const Quant4Args& a, int64_t r0, int ro
     return c0 + cols <= a.cols && (kVec ? r0 + rows <= a.rows : r0 > 0 && r0 + rows < a.rows);
 }
 
-// Row copy alone: 64 rows of 256 elements a block.  A warp has a row of it at a time, eight elements a lane, and stores
-// its 128 bytes of payload together; all loads of a thread are issued before the first is used.
-constexpr int kRowTile = 64, kColTile = 256;
+// Row copy alone: 64 rows (FP32: 32) of 256 elements a block.  A warp has a row of it at a time, eight elements a lane, and
+// stores its 128 bytes of payload together; all loads of a thread are issued before the first is used.
+constexpr int kColTile = 256;
+template <typename T>
+constexpr int kRowTile = 128 / static_cast<int>(sizeof(T));
 
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_rows_kernel(const Quant4Args a, const Shape s) {
-    __shared__ uint32_t s_codes[kRowTile][2];   // four scale codes of every row and 128 columns
-    __shared__ int64_t s_at[kRowTile];          // grouped: the row in the scales, -1: none
+__global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const Quant4Args a, const Shape s) {
+    __shared__ uint32_t s_codes[kRowTile<T>][2];   // four scale codes of every row and 128 columns
+    __shared__ int64_t s_at[kRowTile<T>];          // grouped: the row in the scales, -1: none
     let_next_start();
     wait_for_previous();
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     const int b = static_cast<int>(blockIdx.x) / s.per_batch, local = static_cast<int>(blockIdx.x) - b * s.per_batch;
     const int tr = local / s.tiles_c, tc = local - tr * s.tiles_c;
-    const int64_t r0 = static_cast<int64_t>(tr) * kRowTile, c0 = static_cast<int64_t>(tc) * kColTile;
+    const int64_t r0 = static_cast<int64_t>(tr) * kRowTile<T>, c0 = static_cast<int64_t>(tc) * kColTile;
     const int64_t groups = (a.cols + 31) >> 5;
     const T* x = static_cast<const T*>(a.x) + b * a.batch_stride + (r0 + w) * a.ld;
-    Eight<T> v[8];
-    if (is_whole<kVec>(a, r0, kRowTile, c0, kColTile)) {
+    constexpr int kPer = kRowTile<T> / 8;   // rows of a warp
+    Eight<T> v[kPer];
+    if (is_whole<kVec>(a, r0, kRowTile<T>, c0, kColTile)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j].template load_whole<kVec>(x + 8 * j * a.ld, static_cast<int>(c0) + 8 * lane);
+        for (int j = 0; j < kPer; ++j) v[j].template load_whole<kVec>(x + 8 * j * a.ld, static_cast<int>(c0) + 8 * lane);
     } else {
-        load_rows<T, kVec>(v, x, a.ld, r0 + w, 8, a.rows, static_cast<int>(c0) + 8 * lane, static_cast<int>(a.cols));
+        load_rows<T, kVec, kPer>(v, x, a.ld, r0 + w, 8, a.rows, static_cast<int>(c0) + 8 * lane, static_cast<int>(a.cols));
     }
-    if (a.offsets != nullptr && t < kRowTile) {   // tiled by expert: its first row starts a band
+    if (a.offsets != nullptr && t < kRowTile<T>) {   // tiled by expert: its first row starts a band
         const int64_t r = r0 + t;
         int lo = 0, hi = a.G;   // the last expert that starts at or before the row
         while (hi - lo > 1) {
@@ -236,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_rows_k
     const int64_t g = (c0 >> 5) + (lane >> 2);
     uint8_t* q = static_cast<uint8_t*>(a.q_row) + (b * a.rows + r0 + w) * groups * 16 + c0 / 2 + 4 * lane;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kPer; ++j) {
         const int64_t r = r0 + w + 8 * j;
         uint32_t code;
         const uint32_t o = group_codes(v[j], &code);
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_rows_k
             reinterpret_cast<uint8_t*>(s_codes[w + 8 * j])[lane >> 2] = in ? static_cast<uint8_t>(code) : 0;
     }
     __syncthreads();
-    if (t < 2 * kRowTile) {
+    if (t < 2 * kRowTile<T>) {
         const int row = t >> 1, part = t & 1;
         const int64_t first = (c0 >> 5) + 4 * part;   // of the four groups
         uint8_t* out = static_cast<uint8_t*>(a.s_row) + b * a.s_row_bytes;
@@ -257,8 +260,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_rows_k
 }
 
 // Column copy, alone or with the row copy: a 128 x 128 tile in shared memory, its loads in flight at once (rows that start
-// on 16 bytes: without passing registers), several blocks on an SM.  Rows: thread t takes the elements
-// 8 (t % 16) .. of the rows t / 16 + 16 j.  Columns: a thread takes 32 rows of a column (BF16: of two
+// on 16 bytes: without passing registers), several blocks on an SM.  Rows: a thread takes a group of 32 of a row (FP32:
+// eight elements, four threads a group).  Columns: a thread takes 32 rows of a column (BF16: of two
 // neighbouring ones, in packed operations), and the payload goes out through shared memory, 64 bytes of a
 // column together.
 template <typename T, bool kRow, bool kVec>
@@ -281,11 +284,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_tile_k
         const int at = t % kPer, rows_step = kThreads / kPer;
         const int64_t c = c0 + at * kVec16<T>, left = (a.cols - c) * static_cast<int64_t>(sizeof(T));
         const uint32_t bytes = left >= 16 ? 16u : (left > 0 ? static_cast<uint32_t>(left) : 0u);
+        const T* from = x + (r0 + t / kPer) * a.ld + c;
+        const uint32_t to = smem_u32(tile + t / kPer * kTile + at * kVec16<T>);
+        const int left_rows = static_cast<int>(min(a.rows - r0, static_cast<int64_t>(kTile))) - t / kPer;
 #pragma unroll
         for (int i = 0; i < kTile / rows_step; ++i) {
-            const int row = t / kPer + rows_step * i;
-            const bool in = r0 + row < a.rows && bytes > 0;
-            cp_async16(smem_u32(tile + row * kTile + at * kVec16<T>), in ? x + (r0 + row) * a.ld + c : x, in ? bytes : 0u);
+            const bool in = rows_step * i < left_rows && bytes > 0;
+            cp_async16(to + static_cast<uint32_t>(i * rows_step * kTile * sizeof(T)), in ? from : x, in ? bytes : 0u);
+            from += rows_step * a.ld;
         }
         cp_async_wait_all();
     } else {
@@ -295,13 +301,66 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_tile_k
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j].template load_whole<kVec>(p + 16 * j * a.ld, static_cast<int>(c0) + 8 * chunk);
         } else {
-            load_rows<T, kVec>(v, p, a.ld, r0 + (t >> 4), 16, a.rows, static_cast<int>(c0) + 8 * chunk, static_cast<int>(a.cols));
+            load_rows<T, kVec, 8>(v, p, a.ld, r0 + (t >> 4), 16, a.rows, static_cast<int>(c0) + 8 * chunk, static_cast<int>(a.cols));
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j].to_shared(tile + ((t >> 4) + 16 * j) * kTile + 8 * chunk);
     }
     __syncthreads();
-    if constexpr (kRow) {
+    if constexpr (kRow && sizeof(T) == 2) {
+        // A thread takes the groups t % 4 of the rows t / 4 and t / 4 + 64, each as four 16-byte chunks in the order
+        // i ^ rot, so that the eight lanes of a load (two rows, four groups) hit different banks.
+        const int group = t & 3, rot = (group & 2) | ((t >> 2) & 1);
+        const int64_t g = (c0 >> 5) + group;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int tile_row = (t >> 2) + 64 * j;
+            const uint32_t from = smem_u32(tile + tile_row * kTile + 32 * group);
+            uint4 v[4];   // v[i]: chunk i ^ rot
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = lds128(from + 16u * static_cast<uint32_t>(i ^ rot));
+            uint32_t m2 = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                m2 = max_abs_bf16x2(m2, max_abs_bf16x2(max_abs_bf16x2(v[i].x, v[i].y), max_abs_bf16x2(v[i].z, v[i].w)));
+            m2 &= 0x7FFF7FFFu;
+            const uint32_t m = max(m2 & 0xFFFFu, m2 >> 16) << 16;
+            uint32_t o[4], code;
+            if (m >= kInfBits) {
+                code = 0xFFu;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float f[8];
+                    unpack<T>(v[i], f);
+                    o[i] = bad_codes(f);
+                }
+            } else {
+                const int e = rceil_exponent_f32<kE2M1>(m);
+                code = static_cast<uint32_t>(e + 127);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    Eight<T> eight;
+                    eight.w[0] = v[i];
+                    float f[8];
+                    eight.scaled(e, f);
+                    o[i] = cvt_e2m1x8(f);
+                }
+            }
+            if (rot & 1) {   // back into order, a bit of the XOR at a time
+                uint32_t x = o[0]; o[0] = o[1]; o[1] = x;
+                x = o[2]; o[2] = o[3]; o[3] = x;
+            }
+            if (rot & 2) {
+                uint32_t x = o[0]; o[0] = o[2]; o[2] = x;
+                x = o[1]; o[1] = o[3]; o[3] = x;
+            }
+            const bool in = r0 + tile_row < a.rows && g < row_groups;
+            if (in)
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.q_row) + ((b * a.rows + r0 + tile_row) * row_groups + g) * 16) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            reinterpret_cast<uint8_t*>(s_row_codes)[4 * tile_row + group] = in ? static_cast<uint8_t>(code) : 0;
+        }
+    } else if constexpr (kRow) {
         const int64_t g = (c0 >> 5) + (chunk >> 2);
         uint8_t* q = static_cast<uint8_t*>(a.q_row) + (b * a.rows + r0 + (t >> 4)) * row_groups * 16 + c0 / 2 + 4 * chunk;
 #pragma unroll
@@ -406,7 +465,7 @@ cudaError_t launch_quant_t(const Quant4Args& a, cudaStream_t stream) {
     // tiled scales: whole 512-byte atoms, with their padding
     const int64_t rows = a.tiled ? (a.rows + kTile - 1) / kTile * kTile : a.rows;
     const int64_t tiles_c = rows_only ? (a.cols + kColTile - 1) / kColTile : (a.cols + kTile - 1) / kTile;
-    const int64_t per_batch = tiles_c * (rows_only ? (rows + kRowTile - 1) / kRowTile : (a.rows + kTile - 1) / kTile);
+    const int64_t per_batch = tiles_c * (rows_only ? (rows + kRowTile<T> - 1) / kRowTile<T> : (a.rows + kTile - 1) / kTile);
     const int64_t blocks = a.batch * per_batch;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const Shape s{static_cast<int>(tiles_c), static_cast<int>(per_batch)};
@@ -439,15 +498,19 @@ __device__ __forceinline__ void values8(uint32_t lo, uint32_t hi, float s, float
     }
 }
 
-__device__ __forceinline__ uint32_t scale_code(const Dequant4Args& a, int64_t r, int64_t g, int64_t groups) {
-    const uint8_t* s = static_cast<const uint8_t*>(a.s);
-    return a.tiled ? s[tiled_scale_offset(r, g, groups)] : s[r * a.lds + g];
-}
+// The scale codes of row r.
+struct RowScales {
+    const uint8_t* first;
+    bool tiled;
+    __device__ __forceinline__ RowScales(const Dequant4Args& a, int64_t r)
+        : first(static_cast<const uint8_t*>(a.s) + (a.tiled ? tiled_scale_offset(r, 0, (a.cols + 31) >> 5) : r * a.lds)), tiled(a.tiled) {}
+    __device__ __forceinline__ uint32_t operator[](int g) const { return first[tiled ? (g >> 2) * 512 + (g & 3) : g]; }
+};
 
 template <int kFormat, typename T>
 __global__ void __launch_bounds__(kThreads) dequant_kernel(const Dequant4Args a, int log_row) {
     const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads >> log_row) + (threadIdx.x >> log_row);
-    const int64_t c = ((static_cast<int64_t>(blockIdx.y) << log_row) + (threadIdx.x & ((1 << log_row) - 1))) * 16;
+    const int c = static_cast<int>((blockIdx.y << log_row) + (threadIdx.x & ((1u << log_row) - 1u))) * 16;
     if (r >= a.rows || c >= a.cols) return;
     const uint8_t* q = static_cast<const uint8_t*>(a.q) + r * a.ldq + (kFormat == kE2M1 ? c / 2 : c);
     uint32_t w[4];
@@ -458,7 +521,7 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const Dequant4Args a,
         const uint4 v = *reinterpret_cast<const uint4*>(q);
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     }
-    const float s = scale_of(scale_code(a, r, c >> 5, (a.cols + 31) >> 5));
+    const float s = scale_of(RowScales(a, r)[c >> 5]);
     T* out = static_cast<T*>(a.out) + r * a.ldo + c;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -474,57 +537,54 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const Dequant4Args a,
     }
 }
 
-// Element i of a row.
-template <int kFormat>
-__device__ __forceinline__ uint32_t code_at(const uint8_t* q, int64_t i) {
-    return kFormat == kE2M1 ? (q[i >> 1] >> (4 * (i & 1))) & 15u : q[i];
-}
-
 template <int kFormat, typename T>
 __global__ void __launch_bounds__(kThreads) dequant_any_kernel(const Dequant4Args a, int log_row) {
     const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads >> log_row) + (threadIdx.x >> log_row);
     if (r >= a.rows) return;
     T* out = static_cast<T*>(a.out) + r * a.ldo;
     const uint8_t* q = static_cast<const uint8_t*>(a.q) + r * a.ldq;
-    const int64_t groups = (a.cols + 31) >> 5;
+    const int cols = static_cast<int>(a.cols), groups = (cols + 31) >> 5;   // at most 2^23
+    const RowScales scales(a, r);
     // eight elements from i on, which lies on the output's 16-byte grid
-    const int64_t i = ((static_cast<int64_t>(blockIdx.y) << log_row) + (threadIdx.x & ((1 << log_row) - 1))) * 8 -
-                      lead_of<sizeof(T)>(out);
-    if (i >= a.cols) return;
-    if (i < 0 || i + 8 > a.cols) {   // a row's ends, which it shares with its neighbours
-        for (int64_t k = i < 0 ? 0 : i; k < i + 8 && k < a.cols; ++k) {
-            float f[8];
-            values8<kFormat>(code_at<kFormat>(q, k), 0u, scale_of(scale_code(a, r, k >> 5, groups)), f);
-            out[k] = from_float<T>(f[0]);
-        }
-        return;
-    }
-    const int64_t g = i >> 5;
-    const int in_first = static_cast<int>(32 - (i & 31));   // elements that the first of at most two groups has here
-    const float s0 = scale_of(scale_code(a, r, g, groups));
-    const float s1 = in_first < 8 ? scale_of(scale_code(a, r, g + 1, groups)) : s0;
+    const int i = static_cast<int>((blockIdx.y << log_row) + (threadIdx.x & ((1u << log_row) - 1u))) * 8 - lead_of<sizeof(T)>(out);
+    if (i >= cols) return;
+    const bool whole = i >= 0 && i + 8 <= cols;   // no end of the row, which it shares with its neighbours
+    const int g = i >> 5;
+    const int in_first = 32 - (i & 31);   // elements that the first of at most two groups has here
+    const uint32_t c0 = g >= 0 ? scales[g] : 0u;
+    const float s0 = scale_of(c0), s1 = scale_of(in_first < 8 && g + 1 < groups ? scales[g + 1] : c0);
     uint32_t lo, hi = 0u;
     if constexpr (kFormat == kE2M1) {   // the payload's rows start on words: two of them, shifted by elements
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(q) + (i >> 3);
-        const int at = static_cast<int>(i & 7);
-        lo = __funnelshift_r(w[0], at != 0 ? w[1] : 0u, 4 * at);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(q);
+        const int first = i >> 3;   // -1: before the row
+        const uint32_t w0 = first >= 0 ? w[first] : 0u, w1 = first + 1 < 4 * groups ? w[first + 1] : 0u;
+        lo = __funnelshift_r(w0, w1, 4 * (i & 7));
     } else {
         const uint8_t* p = q + i;
         const unsigned at = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 3u);
-        if (at == 0 || (i >= 4 && i + 12 <= a.cols)) {   // whole words around it lie in the row
+        if (whole && (at == 0 || (i >= 4 && i + 12 <= cols))) {   // whole words around it lie in the row
             const uint32_t* w = reinterpret_cast<const uint32_t*>(p - at);
             const uint32_t mid = w[1];
             lo = __funnelshift_r(w[0], mid, 8 * at);
             hi = __funnelshift_r(mid, at != 0 ? w[2] : 0u, 8 * at);
         } else {
-            lo = p[0] | (p[1] << 8) | (p[2] << 16) | (static_cast<uint32_t>(p[3]) << 24);
-            hi = p[4] | (p[5] << 8) | (p[6] << 16) | (static_cast<uint32_t>(p[7]) << 24);
+            uint32_t byte[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) byte[k] = i + k >= 0 && i + k < cols ? p[k] : 0u;
+            lo = byte[0] | (byte[1] << 8) | (byte[2] << 16) | (byte[3] << 24);
+            hi = byte[4] | (byte[5] << 8) | (byte[6] << 16) | (byte[7] << 24);
         }
     }
     float f[8];
     values8<kFormat>(lo, hi, 1.0f, f);   // exact: the scale follows
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] *= k < in_first ? s0 : s1;
+    if (!whole) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i + k >= 0 && i + k < cols) out[i + k] = from_float<T>(f[k]);
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < 8 / kVec16<T>; ++k) {
         float part[kVec16<T>];

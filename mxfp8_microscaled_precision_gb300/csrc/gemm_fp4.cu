@@ -109,13 +109,19 @@ __device__ __forceinline__ int mmas_of(int64_t k_padded, int64_t kb) {
 //
 // Output tiles of 256 x 256 per pair of SMs (cta_group::2).  CTA r of the pair loads 128 rows of A, its 128-row half
 // of B, its two A scale atoms, and multicasts the two scale atoms of its half of B to both (each tensor
-// core needs the scales of all 256 B rows).  One thread of the even CTA issues, per stage, six scale copies
-// and four 256 x 256 x 64 instructions of 128 cycles each.
+// core needs the scales of all 256 B rows).  One thread of the even CTA issues, per stage, six scale copies and four
+// 256 x 256 x 64 instructions of 128 cycles each; it asks for the next stage's bytes before them and reads the answer
+// behind them.
 //
-// Tensor memory (512 columns): two accumulators of 256 columns that share 64 of them, at 0 and 192, and two
-// slots of 24 columns of scales.  The epilogue of a tile reads the shared columns first and hands them back,
-// so the next tile's instructions wait for a quarter of it only.  A scale slot is written again when the
-// instructions of two stages before have completed.
+// What bounds it (16384^3: 1250 us, 7.0 PFLOP/s, 1.9 GHz): a stage takes about 700 cycles instead of the 512 of its
+// instructions.  The same kernel without the operands' loads takes 984 us, without the instructions 1004 us (35 KB a
+// stage and SM, 64 bytes a cycle), without the scale copies 1207 us: loads and instructions meet in shared
+// memory.  Tried without gain: scale copies by a second warp (1490 us), scale copies a stage ahead (1278 us),
+// clusters of two pairs that share B's loads (1280 to 1380 us; 8192 x 4096 x 4096 47.4 us against 47.7 us).
+//
+// Tensor memory (512 columns): two accumulators of 256 columns that share 128 of them, at 0 and 128, and a slot of 24
+// columns of scales for each stage.  The epilogue of a tile reads the shared columns first and hands them back,
+// so the next tile's instructions wait for half of it only.
 struct PairCfg {
     static constexpr int kStages = 5;
     static constexpr int kEpiWarps = 8;
@@ -132,15 +138,13 @@ struct PairCfg {
     static constexpr int kNumBars = 2 * kStages + 3;   // full, empty, accumulator full / handed back, drain
     static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
-    static constexpr int kOffEpiFlag = kOffAbort + 4;
-    static constexpr int kOffPrefix = kOffEpiFlag + 4;
+    static constexpr int kOffPrefix = kOffAbort + 4;
     static constexpr int kBytes = kOffPrefix + 4 * (kMaxExperts + 1);
     static constexpr int kAlloc = kBytes + 1024;
     static constexpr int kTmemCols = 512;
-    static constexpr int kAcc1 = 192;                 // second accumulator
-    static constexpr int kShared = 256 - kAcc1;       // columns of both
+    static constexpr int kAcc1 = 128;                 // second accumulator
     static constexpr int kTmemScales = kAcc1 + 256, kScaleCols = 24;
-    static_assert(kTmemScales + 2 * kScaleCols <= kTmemCols, "tensor memory budget");
+    static_assert(kTmemScales + kScaleCols * kStages <= kTmemCols, "tensor memory budget");
     static_assert(kAlloc <= 227 * 1024, "shared memory budget");
     static_assert(kOffStage % 1024 == 0, "swizzle atoms");
 };
@@ -188,14 +192,23 @@ __device__ __forceinline__ PairTile pair_tile(const Args& p, const int* prefix, 
     return ti;
 }
 
-// 32 x 32 results of a warp (lane l: output row row0 + l, columns n .. n + 31) through its staging buffer: 16-byte
-// chunk j of row r sits at position j ^ ((r >> 1) & 3), the 64-byte swizzle of a tiled bulk copy.  Rows that are
-// all stored leave with one such copy (the map clips columns past N); otherwise by rows, in vectors or
-// element by element.
-__device__ __forceinline__ void store_chunk(const Args& p, const uint32_t (&v)[32], uint32_t stage, int64_t row0,
-                                            int64_t row_lo, int64_t row_hi, int64_t n, int lane, const CUtensorMap* map) {
-    if (n >= p.N) return;
-    if (lane == 0) bulk_wait_read_but_one();   // the copy before the last one has read this buffer
+// 32 x 32 results of a warp (lane l: output row row0 + l, columns n .. n + 31) through one of its two staging buffers
+// (`buffers`, taken in turns): 16-byte chunk j of row r sits at position j ^ ((r >> 1) & 3), the 64-byte swizzle of a
+// tiled bulk copy.  Rows that are all stored leave with one such copy (the map clips columns past N); otherwise
+// by rows, in vectors or element by element.
+__device__ __forceinline__ void store_chunk(const Args& p, const uint32_t (&v)[32], uint32_t buffers, uint32_t& turn,
+                                            int64_t row0, int64_t row_lo, int64_t row_hi, int64_t n, int lane,
+                                            const CUtensorMap* map) {
+    if (n >= p.N) return;   // and the next chunk takes this one's buffer
+    const bool tiled = p.y_tma && row0 >= row_lo && row0 + 32 <= row_hi;
+    const uint32_t stage = buffers + (turn & 1u) * PairCfg::kStageWarpBytes;
+    ++turn;
+    // Copies alternate between the buffers: all but the last one have to have read theirs.  Chunks that leave by rows
+    // use the buffers without a copy, after which nothing is said about which buffer the last copy reads.
+    if (lane == 0) {
+        if (tiled) bulk_wait_read_but_one();
+        else bulk_wait_read_all();
+    }
     __syncwarp();
     const uint32_t wrow = stage + 64u * static_cast<uint32_t>(lane), swz = static_cast<uint32_t>((lane >> 1) & 3);
 #pragma unroll
@@ -207,7 +220,7 @@ __device__ __forceinline__ void store_chunk(const Args& p, const uint32_t (&v)[3
         o.w = cvt_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
         sts128(wrow + 16u * (static_cast<uint32_t>(j) ^ swz), o);
     }
-    if (p.y_tma && row0 >= row_lo && row0 + 32 <= row_hi) {
+    if (tiled) {
         fence_proxy_async_smem();   // the buffer is read by the bulk copy (async proxy)
         __syncwarp();
         if (lane == 0) {
@@ -234,13 +247,30 @@ __device__ __forceinline__ void store_chunk(const Args& p, const uint32_t (&v)[3
                 for (int c = 0; c < 8 && col + c < p.N; ++c) to[c] = static_cast<uint16_t>(w[c >> 1] >> (16 * (c & 1)));
             }
         }
-    } else if (n + lane < p.N) {
-        for (int r = 0; r < 32; ++r) {
-            if (row0 + r < row_lo || row0 + r >= row_hi) continue;
-            const uint32_t at = stage + 64u * static_cast<uint32_t>(r) +
-                                16u * (static_cast<uint32_t>(lane >> 3) ^ static_cast<uint32_t>((r >> 1) & 3)) +
-                                4u * static_cast<uint32_t>((lane & 7) >> 1);
-            p.y[(row0 + r) * p.ldy + n + lane] = static_cast<uint16_t>(lds32(at) >> (16 * (lane & 1)));
+    } else {
+        // Rows that start anywhere, two of them at a time: their columns in pairs on the memory's 4-byte grid, which starts
+        // at the row's first or second column, then the columns that have no partner.
+        const int lo = static_cast<int>(max(row_lo - row0, int64_t(0))), hi = static_cast<int>(min(row_hi - row0, int64_t(32)));
+        const int cols = static_cast<int>(min(p.N - n, int64_t(32)));
+        uint16_t* to = p.y + row0 * p.ldy + n;
+        const int first = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1) & 1, step = static_cast<int>(p.ldy & 1);
+        auto word = [&](int r, int w) {   // columns 2 w and 2 w + 1 of row r
+            return lds32(stage + 64u * static_cast<uint32_t>(r) + 16u * static_cast<uint32_t>((w >> 2) ^ ((r >> 1) & 3)) +
+                         4u * static_cast<uint32_t>(w & 3));
+        };
+        const int w = lane & 15;
+#pragma unroll 8
+        for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + (lane >> 4), odd = first ^ (step & r), c = 2 * w + odd;
+            const uint32_t here = word(r, w), next = word(r, w < 15 ? w + 1 : 15);
+            if (r >= lo && r < hi && c + 2 <= cols)
+                *reinterpret_cast<uint32_t*>(to + r * p.ldy + c) = odd ? __funnelshift_r(here, next, 16) : here;
+        }
+        const int odd = first ^ (step & lane);
+        if (lane >= lo && lane < hi) {
+            if (odd) to[lane * p.ldy] = static_cast<uint16_t>(word(lane, 0));
+            const int last = cols - 1;
+            if (last >= odd && ((cols - odd) & 1)) to[lane * p.ldy + last] = static_cast<uint16_t>(word(lane, last >> 1) >> (16 * (last & 1)));
         }
     }
     __syncwarp();
@@ -262,7 +292,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     const uint32_t tfull_bar = bar0 + 8u * (2 * STAGES), tempty_bar = tfull_bar + 8u, drain_bar = tfull_bar + 16u;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffAbort);
-    volatile int* epi_flag = reinterpret_cast<volatile int*>(smem + L::kOffEpiFlag);
     int* prefix = reinterpret_cast<int*>(smem + L::kOffPrefix);
     const WaitGuard guard{abort_flag, p.status, p.wait_limit_ns};
 
@@ -339,26 +368,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
             const uint64_t b_desc0 = make_smem_desc(sbase + L::kOffB, 16, 1024, 2);
             const uint64_t sfa_desc0 = make_smem_desc(sbase + L::kOffSfa, 0, 128, 0);
             const uint64_t sfb_desc0 = make_smem_desc(sbase + L::kOffSfb, 0, 128, 0);
-            int stage = 0, before = STAGES - 2;   // this stage and the one two before
-            uint32_t phase = 0, before_phase = 1, acc = 0, acc_phase = 0, slot = 0;
-            bool ok = true;
+            int stage = 0;
+            uint32_t phase = 0, acc = 0, acc_phase = 0;
+            bool ok = true, landed = false;   // the stage's bytes, seen already
             for (int t = pair_id; t < total && ok; t += n_pairs) {
                 if (!warp_waits(lane, [&] { return spin_phase(tempty_bar, acc_phase ^ 1u, guard); })) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * L::kAcc1;
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    // the slot's scales have been read: the stage two before has completed (before the
-                    // first two stages a fresh barrier's odd phase counts as complete)
-                    if (!warp_waits(lane, [&] {
-                            return wait_phase(full_bar(stage), phase, guard) && wait_phase(empty_bar(before), before_phase, guard);
-                        })) { ok = false; break; }
+                    if (!landed && !warp_waits(lane, [&] { return wait_phase(full_bar(stage), phase, guard); })) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t sfa_t = tmem_base + L::kTmemScales + L::kScaleCols * slot, sfb_t = sfa_t + 8;
+                    const uint32_t sfa_t = tmem_base + L::kTmemScales + L::kScaleCols * stage, sfb_t = sfa_t + 8;
                     const uint64_t a_desc = a_desc0 + static_cast<uint64_t>((stage * kBandBytes) >> 4);
                     const uint64_t b_desc = b_desc0 + static_cast<uint64_t>((stage * kBandBytes) >> 4);
                     const uint64_t sfa_d = sfa_desc0 + static_cast<uint64_t>((stage * L::kSfaBytes) >> 4);
                     const uint64_t sfb_d = sfb_desc0 + static_cast<uint64_t>((stage * L::kSfbBytes) >> 4);
                     const int mmas = mmas_of<kBK>(p.k_padded, kb);
+                    const uint32_t this_empty = empty_bar(stage);
+                    // ask for the next stage now and look at the answer behind the instructions
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    const bool next = mbar_test_wait(full_bar(stage), phase);
                     if (elect_one()) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {   // atom i: K elements 128 i .. of the stage
@@ -372,12 +401,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
                                 tc_mma_mxf4_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k,
                                                  make_idesc_mxf4(256, 256, 2 * (k & 1)), sfa_t + 4 * (k >> 1),
                                                  sfb_t + 8 * (k >> 1), (kb > 0 || k > 0) ? 1u : 0u);
-                        tc_commit_pair_multicast(empty_bar(stage), 0x3);   // frees the slot in both CTAs
+                        tc_commit_pair_multicast(this_empty, 0x3);   // frees the slot in both CTAs
                     }
                     __syncwarp();
-                    slot ^= 1u;
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                    if (++before == STAGES) { before = 0; before_phase ^= 1u; }
+                    landed = __all_sync(0xFFFFFFFFu, next) != 0;
                 }
                 if (!ok) break;
                 if (elect_one()) tc_commit_pair_multicast(tfull_bar, 0x3);
@@ -385,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
                 acc ^= 1u;
                 acc_phase ^= 1u;
             }
-            // Drain: every MMA and copy issued above completes before teardown.
+            // Drain: every MMA issued above completes before teardown.
             if (lane == 0) {
                 tc_commit_pair(drain_bar);
                 WaitGuard g2 = guard;
@@ -399,29 +426,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
         // ---- epilogue (both CTAs; warps 2..9) ----------------------------------------
         const int quad = warp & 3, half = (warp - 2) >> 2;
         const uint32_t tempty_leader = leader ? tempty_bar : mapa_shared(tempty_bar, 0);
-        const uint32_t buffer = sbase + L::kOffStage + (warp - 2) * 2 * L::kStageWarpBytes;
+        const uint32_t buffers = sbase + L::kOffStage + (warp - 2) * 2 * L::kStageWarpBytes;
         uint32_t acc = 0, acc_phase = 0, turn = 0;
         for (int t = pair_id; t < total; t += n_pairs) {
             const PairTile ti = pair_tile<kGrouped>(p, prefix, t, rank);
-            // One thread waits (suspending), the other epilogue warps sleep on a
-            // named barrier; barrier 2 keeps the verdict until every warp read it.
-            if (warp == 2 && lane == 0) *epi_flag = wait_phase(tfull_bar, acc_phase, guard) ? 1 : 0;
-            named_bar_sync(1, 32 * L::kEpiWarps);
-            const int ok = *epi_flag;
-            named_bar_sync(2, 32 * L::kEpiWarps);
-            if (!ok) break;
+            if (!warp_waits(lane, [&] { return wait_phase(tfull_bar, acc_phase, guard); })) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + acc * L::kAcc1;
             const int64_t row0 = ti.m0 + 32 * quad;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                // the columns that the other accumulator shares come first: the last 64 of the first
-                // accumulator, the first 64 of the second
-                const int col = c == 0 ? (acc ? 0 : L::kAcc1) + 32 * half : (acc ? L::kShared : 0) + 96 * half + 32 * (c - 1);
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(taddr + col, v);
+            for (int part = 0; part < 2; ++part) {
+                // the columns that the other accumulator shares come first: the upper half of the first
+                // accumulator, the lower half of the second
+                const int col = (part == static_cast<int>(acc) ? 128 : 0) + 64 * half;
+                uint32_t v[2][32];
+                tmem_ld_32x32b_x32(taddr + col, v[0]);
+                tmem_ld_32x32b_x32(taddr + col + 32, v[1]);
                 tmem_ld_wait();
-                if (c == 0) {
+                if (part == 0) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -429,8 +451,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
                         else mbar_arrive_cluster(tempty_leader);
                     }
                 }
-                store_chunk(p, v, buffer + (turn & 1u) * L::kStageWarpBytes, row0, ti.row_lo, ti.row_hi, ti.n0 + col, lane, &maps.y);
-                ++turn;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    store_chunk(p, v[c], buffers, turn, row0, ti.row_lo, ti.row_hi, ti.n0 + col + 32 * c, lane, &maps.y);
             }
             acc ^= 1u;
             acc_phase ^= 1u;

@@ -195,6 +195,23 @@ def test_a_nan_scale_makes_its_row_or_column_nan(M, N, K):
     assert torch.equal(nan, want)
 
 
+@pytest.mark.parametrize("M,N,K,ld", [(1024, 200, 320, 200), (1000, 456, 320, 456), (770, 232, 512, 240), (1024, 2024, 256, 2024)])
+def test_ragged_widths_many_times(M, N, K, ld):
+    """A last column tile that ends inside: chunks of the epilogue are left out, some rows leave in tiles and some by rows,
+    and a buffer that was rewritten before its copy had read it would show now and then only."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    rng = np.random.default_rng(N)
+    a_q, a_s, a = _operand(rng, M, K)
+    b_q, b_s, b = _operand(rng, N, K)
+    want = _fp4.bf16((a.cuda() @ b.cuda().t()).cpu().numpy()).cuda()
+    y = torch.empty(M, ld, dtype=torch.bfloat16, device="cuda")[:, :N]
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(100):
+        y.zero_()
+        wrong += (mxq.gemm_mxfp4(a_q, a_s, b_q, b_s, M, N, K, out=y) != want).sum()
+    assert int(wrong) == 0
+
+
 def test_empty_products():
     from mxfp8_microscaled_precision_gb300 import mxq
     empty = torch.empty(0, dtype=torch.uint8, device="cuda")
