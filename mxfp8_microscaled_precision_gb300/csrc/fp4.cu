@@ -264,8 +264,14 @@ __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const Quant4Arg
 // eight elements, four threads a group).  Columns: a thread takes 32 rows of a column (BF16: of two
 // neighbouring ones, in packed operations), and the payload goes out through shared memory, 64 bytes of a
 // column together.
+// FP32 rows that start anywhere: a tile is long work for 256 threads where there are few tiles (777 x 2085: 9.3 us with 256
+// threads, 7.7 us with 512); of rows that start on 16 bytes more tiles fit an SM with 256 (16384 x 7168: 100 us, 122 us).
+template <typename T, bool kVec>
+constexpr int kTileThreads = sizeof(T) == 4 && !kVec ? 512 : 256;
+
 template <typename T, bool kRow, bool kVec>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_tile_kernel(const Quant4Args a, const Shape s) {
+__global__ void __launch_bounds__(kTileThreads<T, kVec>, sizeof(T) == 2 ? 4 : 2) quant_tile_kernel(const Quant4Args a, const Shape s) {
+    constexpr int kNT = kTileThreads<T, kVec>, kStep = kNT / 16, kPasses = kTile / kStep;   // rows of 16 threads each at once
     extern __shared__ __align__(16) uint8_t s_memory[];
     T* tile = reinterpret_cast<T*>(s_memory);
     uint4* s_out = reinterpret_cast<uint4*>(s_memory + kTile * kTile * sizeof(T));
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_tile_k
     const int chunk = t & 15;
     if (kVec) {   // 16 bytes a copy, neighbouring threads side by side; what lies outside is filled up with zeros
         constexpr int kPer = kTile / kVec16<T>;   // copies of a row
-        const int at = t % kPer, rows_step = kThreads / kPer;
+        const int at = t % kPer, rows_step = kNT / kPer;
         const int64_t c = c0 + at * kVec16<T>, left = (a.cols - c) * static_cast<int64_t>(sizeof(T));
         const uint32_t bytes = left >= 16 ? 16u : (left > 0 ? static_cast<uint32_t>(left) : 0u);
         const T* from = x + (r0 + t / kPer) * a.ld + c;
@@ -295,16 +301,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_tile_k
         }
         cp_async_wait_all();
     } else {
-        Eight<T> v[8];
+        Eight<T> v[kPasses];
         const T* p = x + (r0 + (t >> 4)) * a.ld;
         if (is_whole<kVec>(a, r0, kTile, c0, kTile)) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j].template load_whole<kVec>(p + 16 * j * a.ld, static_cast<int>(c0) + 8 * chunk);
+            for (int j = 0; j < kPasses; ++j) v[j].template load_whole<kVec>(p + kStep * j * a.ld, static_cast<int>(c0) + 8 * chunk);
         } else {
-            load_rows<T, kVec, 8>(v, p, a.ld, r0 + (t >> 4), 16, a.rows, static_cast<int>(c0) + 8 * chunk, static_cast<int>(a.cols));
+            load_rows<T, kVec, kPasses>(v, p, a.ld, r0 + (t >> 4), kStep, a.rows, static_cast<int>(c0) + 8 * chunk, static_cast<int>(a.cols));
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j].to_shared(tile + ((t >> 4) + 16 * j) * kTile + 8 * chunk);
+        for (int j = 0; j < kPasses; ++j) v[j].to_shared(tile + ((t >> 4) + kStep * j) * kTile + 8 * chunk);
     }
     __syncthreads();
     if constexpr (kRow && sizeof(T) == 2) {
@@ -364,14 +370,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_tile_k
         const int64_t g = (c0 >> 5) + (chunk >> 2);
         uint8_t* q = static_cast<uint8_t*>(a.q_row) + (b * a.rows + r0 + (t >> 4)) * row_groups * 16 + c0 / 2 + 4 * chunk;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int tile_row = (t >> 4) + 16 * j;
+        for (int j = 0; j < kPasses; ++j) {
+            const int tile_row = (t >> 4) + kStep * j;
             Eight<T> v;
             v.from_shared(tile + tile_row * kTile + 8 * chunk);
             uint32_t code;
             const uint32_t o = group_codes(v, &code);
             const bool in = r0 + tile_row < a.rows && g < row_groups;
-            if (in) *reinterpret_cast<uint32_t*>(q + 16 * j * row_groups * 16) = o;
+            if (in) *reinterpret_cast<uint32_t*>(q + kStep * j * row_groups * 16) = o;
             if ((chunk & 3) == 0)
                 reinterpret_cast<uint8_t*>(s_row_codes)[4 * tile_row + (chunk >> 2)] = in ? static_cast<uint8_t>(code) : 0;
         }
@@ -427,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_tile_k
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int c = t & (kTile - 1), block = (t >> 7) + 2 * k;
+            for (int k = 0; k < 4 * kTile / kNT; ++k) {
+                const int c = t & (kTile - 1), block = (t >> 7) + kNT / kTile * k;
                 float f[32];
                 uint32_t m = 0u, code;
 #pragma unroll
@@ -443,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) quant_tile_k
         __syncthreads();
         uint8_t* q = static_cast<uint8_t*>(a.q_col) + b * a.cols * col_groups * 16;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int c = (t >> 2) + 64 * k, block = t & 3;
+        for (int k = 0; k < 4 * kTile / kNT; ++k) {
+            const int c = (t >> 2) + kNT / 4 * k, block = t & 3;
             const int64_t g = (r0 >> 5) + block;
             if (c0 + c < a.cols && g < col_groups)
                 *reinterpret_cast<uint4*>(q + ((c0 + c) * col_groups + g) * 16) = s_out[place_of(c, block)];
@@ -472,8 +478,8 @@ cudaError_t launch_quant_t(const Quant4Args& a, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(blocks));
     if (rows_only) return launch_behind(quant_rows_kernel<T, kVec>, grid, kThreads, 0, stream, a, s);
     constexpr unsigned kShared = kTile * kTile * sizeof(T) + 4 * kTile * sizeof(uint4);
-    if (a.q_row == nullptr) return launch_behind(quant_tile_kernel<T, false, kVec>, grid, kThreads, kShared, stream, a, s);
-    return launch_behind(quant_tile_kernel<T, true, kVec>, grid, kThreads, kShared, stream, a, s);
+    if (a.q_row == nullptr) return launch_behind(quant_tile_kernel<T, false, kVec>, grid, kTileThreads<T, kVec>, kShared, stream, a, s);
+    return launch_behind(quant_tile_kernel<T, true, kVec>, grid, kTileThreads<T, kVec>, kShared, stream, a, s);
 }
 
 // ---- values ----------------------------------------------------------------------------
