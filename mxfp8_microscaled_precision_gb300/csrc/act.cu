@@ -229,19 +229,18 @@ __device__ __forceinline__ uint32_t lane_e4m3(float f, uint32_t* code) {
     return 0x7Fu | ((__float_as_uint(f) >> 24) & 0x80u);
 }
 
-// The first group and the row of a warp: kSpan groups, the blocks' y along a row.
+// The first group and the row of a warp: kSpan groups, `per_row` such warps a row, row after row.
 struct Span {
     int64_t row, group;
 };
-__device__ __forceinline__ Span span_of(int log_row) {   // 1 << log_row warps of a block lie along a row
-    const int w = threadIdx.x >> 5;
-    return {static_cast<int64_t>(blockIdx.x) * ((kThreads / 32) >> log_row) + (w >> log_row),
-            ((static_cast<int64_t>(blockIdx.y) << log_row) + (w & ((1 << log_row) - 1))) * kSpan};
+__device__ __forceinline__ Span span_of(int per_row) {
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), row = w / per_row;
+    return {row, (w - row * per_row) * kSpan};
 }
 
 template <typename T, int kKind, bool kGated, bool kKeep>
-__global__ void __launch_bounds__(kThreads) act_any_kernel(const ActArgs a, int log_row) {
-    const Span at = span_of(log_row);
+__global__ void __launch_bounds__(kThreads) act_any_kernel(const ActArgs a, int per_row) {
+    const Span at = span_of(per_row);
     if (at.row >= a.rows) return;   // a whole warp
     constexpr int kParts = kGated ? 2 : 1;
     const int lane = threadIdx.x & 31;
@@ -277,8 +276,8 @@ __global__ void __launch_bounds__(kThreads) act_any_kernel(const ActArgs a, int 
 }
 
 template <typename T, int kKind, bool kGated>
-__global__ void __launch_bounds__(kThreads) act_backward_any_kernel(const ActBackwardArgs a, int log_row) {
-    const Span at = span_of(log_row);
+__global__ void __launch_bounds__(kThreads) act_backward_any_kernel(const ActBackwardArgs a, int per_row) {
+    const Span at = span_of(per_row);
     if (at.row >= a.rows) return;
     constexpr int kParts = kGated ? 2 : 1;
     const int lane = threadIdx.x & 31;
@@ -314,18 +313,29 @@ __global__ void __launch_bounds__(kThreads) act_backward_any_kernel(const ActBac
 
 // ---- host ----------------------------------------------------------------------------------------
 
-// Units along a row (threads of eight elements, or warps of kSpan groups) and rows, as a grid: 1 << log_row of a
-// block's `per_block` units lie along a row, the least power of two that holds it or all.
+// Whole vectors: 1 << log_row of a block's threads lie along a row, the least power of two that holds it or all.
 struct Grid {
     dim3 blocks;
-    int log_row = 0;
-    bool fits = true;
-    Grid(int64_t rows, int64_t units, int per_block, int least_log) {
-        log_row = least_log;
-        while ((1 << log_row) < per_block && (1 << log_row) < units) ++log_row;
-        const int64_t down = per_block >> log_row, x = (rows + down - 1) / down, y = (units + (1 << log_row) - 1) >> log_row;
+    int log_row;
+    bool fits;
+    Grid(int64_t rows, int64_t inter, int least_log) : log_row(least_log) {
+        const int64_t units = inter / 8;
+        while ((1 << log_row) < kThreads && (1 << log_row) < units) ++log_row;
+        const int64_t down = kThreads >> log_row, x = (rows + down - 1) / down, y = (units + (1 << log_row) - 1) >> log_row;
         fits = x <= 0x7FFFFFFF && y <= 65535;
         blocks = dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
+    }
+};
+
+// Any rows: warps of kSpan groups, row after row.
+struct AnyGrid {
+    unsigned blocks;
+    int per_row;
+    bool fits;
+    AnyGrid(int64_t rows, int64_t inter) : per_row(static_cast<int>((inter + 32 * kSpan - 1) / (32 * kSpan))) {
+        const int64_t n = (rows * per_row + kThreads / 32 - 1) / (kThreads / 32);
+        fits = n <= 0x7FFFFFFF;
+        blocks = static_cast<unsigned>(n);
     }
 };
 
@@ -336,27 +346,33 @@ inline bool whole(const void* p, int64_t ld, int64_t size) {
 template <typename T, int kKind, bool kGated>
 cudaError_t launch_act_t(const ActArgs& a, cudaStream_t stream) {
     constexpr int64_t kSize = sizeof(T);
-    const bool vec = a.inter % 8 == 0 && whole(a.z, a.ldz, kSize) && whole(a.y, a.ldy, kSize);
-    const Grid grid = vec ? Grid(a.rows, a.inter / 8, kThreads, 2)   // a group's four threads in one row
-                          : Grid(a.rows, (a.inter + 32 * kSpan - 1) / (32 * kSpan), kThreads / 32, 0);
-    if (!grid.fits) return cudaErrorInvalidValue;
-    if (vec && a.q != nullptr) act_kernel<T, kKind, kGated, true><<<grid.blocks, kThreads, 0, stream>>>(a, grid.log_row);
-    else if (vec) act_kernel<T, kKind, kGated, false><<<grid.blocks, kThreads, 0, stream>>>(a, grid.log_row);
-    else if (a.q != nullptr) act_any_kernel<T, kKind, kGated, true><<<grid.blocks, kThreads, 0, stream>>>(a, grid.log_row);
-    else act_any_kernel<T, kKind, kGated, false><<<grid.blocks, kThreads, 0, stream>>>(a, grid.log_row);
+    if (a.inter % 8 == 0 && whole(a.z, a.ldz, kSize) && whole(a.y, a.ldy, kSize)) {
+        const Grid grid(a.rows, a.inter, 2);   // a group's four threads in one row
+        if (!grid.fits) return cudaErrorInvalidValue;
+        if (a.q != nullptr) act_kernel<T, kKind, kGated, true><<<grid.blocks, kThreads, 0, stream>>>(a, grid.log_row);
+        else act_kernel<T, kKind, kGated, false><<<grid.blocks, kThreads, 0, stream>>>(a, grid.log_row);
+    } else {
+        const AnyGrid grid(a.rows, a.inter);
+        if (!grid.fits) return cudaErrorInvalidValue;
+        if (a.q != nullptr) act_any_kernel<T, kKind, kGated, true><<<grid.blocks, kThreads, 0, stream>>>(a, grid.per_row);
+        else act_any_kernel<T, kKind, kGated, false><<<grid.blocks, kThreads, 0, stream>>>(a, grid.per_row);
+    }
     return cudaGetLastError();
 }
 
 template <typename T, int kKind, bool kGated>
 cudaError_t launch_backward_t(const ActBackwardArgs& a, cudaStream_t stream) {
     constexpr int64_t kSize = sizeof(T);
-    const bool vec = a.inter % 8 == 0 && whole(a.dy, a.lddy, kSize) && whole(a.dz, a.lddz, kSize) &&
-                     (a.y == nullptr || whole(a.y, a.ldy, kSize));
-    const Grid grid = vec ? Grid(a.rows, a.inter / 8, kThreads, 0)
-                          : Grid(a.rows, (a.inter + 32 * kSpan - 1) / (32 * kSpan), kThreads / 32, 0);
-    if (!grid.fits) return cudaErrorInvalidValue;
-    if (vec) act_backward_kernel<T, kKind, kGated><<<grid.blocks, kThreads, 0, stream>>>(a, grid.log_row);
-    else act_backward_any_kernel<T, kKind, kGated><<<grid.blocks, kThreads, 0, stream>>>(a, grid.log_row);
+    if (a.inter % 8 == 0 && whole(a.dy, a.lddy, kSize) && whole(a.dz, a.lddz, kSize) &&
+        (a.y == nullptr || whole(a.y, a.ldy, kSize))) {
+        const Grid grid(a.rows, a.inter, 0);
+        if (!grid.fits) return cudaErrorInvalidValue;
+        act_backward_kernel<T, kKind, kGated><<<grid.blocks, kThreads, 0, stream>>>(a, grid.log_row);
+    } else {
+        const AnyGrid grid(a.rows, a.inter);
+        if (!grid.fits) return cudaErrorInvalidValue;
+        act_backward_any_kernel<T, kKind, kGated><<<grid.blocks, kThreads, 0, stream>>>(a, grid.per_row);
+    }
     return cudaGetLastError();
 }
 
