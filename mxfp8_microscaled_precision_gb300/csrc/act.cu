@@ -125,7 +125,7 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
         float s[kVec16<T>];
 #pragma unroll
         for (int j = 0; j < kVec16<T>; ++j) s[j] = f[i * kVec16<T> + j];
-        __stcs(reinterpret_cast<uint4*>(p) + i, pack<T>(s));
+        reinterpret_cast<uint4*>(p)[i] = pack<T>(s);   // what follows reads it; the checkpoint, read much later, streams
     }
 }
 
