@@ -123,7 +123,7 @@ __device__ __forceinline__ int mmas_of(int64_t k_padded, int64_t kb) {
 // columns of scales for each stage.  The epilogue of a tile reads the shared columns first and hands them back,
 // so the next tile's instructions wait for half of it only.
 struct PairCfg {
-    static constexpr int kStages = 5;
+    static constexpr int kStages = 6;
     static constexpr int kEpiWarps = 8;
     static constexpr int kThreads = 64 + 32 * kEpiWarps;
     static constexpr int kSfaBytes = 2 * kAtom, kSfbBytes = 4 * kAtom;
@@ -133,8 +133,8 @@ struct PairCfg {
     static constexpr int kOffSfa = kOffA + kStages * kBandBytes;
     static constexpr int kOffSfb = kOffSfa + kStages * kSfaBytes;
     static constexpr int kOffStage = kOffSfb + kStages * kSfbBytes;   // 1024-byte aligned
-    static constexpr int kStageWarpBytes = 32 * 32 * 2;               // a BF16 chunk of 32 rows, twice a warp
-    static constexpr int kOffBar = kOffStage + 2 * kEpiWarps * kStageWarpBytes;
+    static constexpr int kStageWarpBytes = 32 * 16 * 2;               // a BF16 chunk of 32 rows
+    static constexpr int kOffBar = kOffStage + kEpiWarps * kStageWarpBytes;
     static constexpr int kNumBars = 2 * kStages + 3;   // full, empty, accumulator full / handed back, drain
     static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
@@ -142,9 +142,11 @@ struct PairCfg {
     static constexpr int kBytes = kOffPrefix + 4 * (kMaxExperts + 1);
     static constexpr int kAlloc = kBytes + 1024;
     static constexpr int kTmemCols = 512;
-    static constexpr int kAcc1 = 128;                 // second accumulator
+    static constexpr int kAcc1 = 96;                  // second accumulator
+    static constexpr int kShared = 256 - kAcc1;       // columns of both
     static constexpr int kTmemScales = kAcc1 + 256, kScaleCols = 24;
     static_assert(kTmemScales + kScaleCols * kStages <= kTmemCols, "tensor memory budget");
+    static_assert(kShared % 32 == 0, "chunks of 16 columns of two halves");
     static_assert(kAlloc <= 227 * 1024, "shared memory budget");
     static_assert(kOffStage % 1024 == 0, "swizzle atoms");
 };
@@ -192,34 +194,27 @@ __device__ __forceinline__ PairTile pair_tile(const Args& p, const int* prefix, 
     return ti;
 }
 
-// 32 x 32 results of a warp (lane l: output row row0 + l, columns n .. n + 31) through one of its two staging buffers
-// (`buffers`, taken in turns): 16-byte chunk j of row r sits at position j ^ ((r >> 1) & 3), the 64-byte swizzle of a
-// tiled bulk copy.  Rows that are all stored leave with one such copy (the map clips columns past N); otherwise
-// by rows, in vectors or element by element.
-__device__ __forceinline__ void store_chunk(const Args& p, const uint32_t (&v)[32], uint32_t buffers, uint32_t& turn,
-                                            int64_t row0, int64_t row_lo, int64_t row_hi, int64_t n, int lane,
-                                            const CUtensorMap* map) {
-    if (n >= p.N) return;   // and the next chunk takes this one's buffer
+// 32 x 16 results of a warp (lane l: output row row0 + l, columns n .. n + 15) through its staging buffer of 1 KB: 16-byte
+// chunk j of row r sits at position j ^ ((r >> 2) & 1), the 32-byte swizzle of a tiled bulk copy.  Rows that are all
+// stored leave with one such copy (the map clips columns past N); otherwise by rows, in vectors or in pairs
+// of columns.  The buffer is small so that the ring is large.
+__device__ __forceinline__ void store_chunk(const Args& p, const uint32_t* v, uint32_t stage, int64_t row0, int64_t row_lo,
+                                            int64_t row_hi, int64_t n, int lane, const CUtensorMap* map) {
+    if (n >= p.N) return;
     const bool tiled = p.y_tma && row0 >= row_lo && row0 + 32 <= row_hi;
-    const uint32_t stage = buffers + (turn & 1u) * PairCfg::kStageWarpBytes;
-    ++turn;
-    // Copies alternate between the buffers: all but the last one have to have read theirs.  Chunks that leave by rows
-    // use the buffers without a copy, after which nothing is said about which buffer the last copy reads.
-    if (lane == 0) {
-        if (tiled) bulk_wait_read_but_one();
-        else bulk_wait_read_all();
-    }
-    __syncwarp();
-    const uint32_t wrow = stage + 64u * static_cast<uint32_t>(lane), swz = static_cast<uint32_t>((lane >> 1) & 3);
+    uint4 o[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint4 o;
-        o.x = cvt_bf16x2(__uint_as_float(v[8 * j + 0]), __uint_as_float(v[8 * j + 1]));
-        o.y = cvt_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
-        o.z = cvt_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
-        o.w = cvt_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
-        sts128(wrow + 16u * (static_cast<uint32_t>(j) ^ swz), o);
+    for (int j = 0; j < 2; ++j) {
+        o[j].x = cvt_bf16x2(__uint_as_float(v[8 * j + 0]), __uint_as_float(v[8 * j + 1]));
+        o[j].y = cvt_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
+        o[j].z = cvt_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
+        o[j].w = cvt_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
     }
+    if (lane == 0) bulk_wait_read_all();   // the copy before has read the buffer
+    __syncwarp();
+    const uint32_t swz = static_cast<uint32_t>((lane >> 2) & 1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sts128(stage + 32u * static_cast<uint32_t>(lane) + 16u * (static_cast<uint32_t>(j) ^ swz), o[j]);
     if (tiled) {
         fence_proxy_async_smem();   // the buffer is read by the bulk copy (async proxy)
         __syncwarp();
@@ -230,39 +225,37 @@ __device__ __forceinline__ void store_chunk(const Args& p, const uint32_t (&v)[3
         return;
     }
     __syncwarp();
+    const int lo = static_cast<int>(max(row_lo - row0, int64_t(0))), hi = static_cast<int>(min(row_hi - row0, int64_t(32)));
+    const int cols = static_cast<int>(min(p.N - n, int64_t(16)));
+    uint16_t* to = p.y + row0 * p.ldy + n;
     if (p.y_vec) {
-        const int jj = lane & 3;
-        const int64_t col = n + 8 * jj;
+        const int jj = lane & 1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2);
-            const uint4 x = lds128_ordered(stage + 64u * static_cast<uint32_t>(r) +
-                                           16u * (static_cast<uint32_t>(jj) ^ static_cast<uint32_t>((r >> 1) & 3)));
-            if (row0 + r < row_lo || row0 + r >= row_hi) continue;
-            uint16_t* to = p.y + (row0 + r) * p.ldy + col;
-            if (col + 8 <= p.N) {
-                *reinterpret_cast<uint4*>(to) = x;
+        for (int i = 0; i < 2; ++i) {
+            const int r = 16 * i + (lane >> 1);
+            const uint4 x = lds128_ordered(stage + 32u * static_cast<uint32_t>(r) + 16u * static_cast<uint32_t>(jj ^ ((r >> 2) & 1)));
+            if (r < lo || r >= hi) continue;
+            uint16_t* at = to + r * p.ldy + 8 * jj;
+            if (8 * jj + 8 <= cols) {
+                *reinterpret_cast<uint4*>(at) = x;
             } else {
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                for (int c = 0; c < 8 && col + c < p.N; ++c) to[c] = static_cast<uint16_t>(w[c >> 1] >> (16 * (c & 1)));
+                for (int c = 0; c < 8 && 8 * jj + c < cols; ++c) at[c] = static_cast<uint16_t>(w[c >> 1] >> (16 * (c & 1)));
             }
         }
     } else {
-        // Rows that start anywhere, two of them at a time: their columns in pairs on the memory's 4-byte grid, which starts
+        // Rows that start anywhere, four of them at a time: their columns in pairs on the memory's 4-byte grid, which starts
         // at the row's first or second column, then the columns that have no partner.
-        const int lo = static_cast<int>(max(row_lo - row0, int64_t(0))), hi = static_cast<int>(min(row_hi - row0, int64_t(32)));
-        const int cols = static_cast<int>(min(p.N - n, int64_t(32)));
-        uint16_t* to = p.y + row0 * p.ldy + n;
         const int first = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1) & 1, step = static_cast<int>(p.ldy & 1);
         auto word = [&](int r, int w) {   // columns 2 w and 2 w + 1 of row r
-            return lds32(stage + 64u * static_cast<uint32_t>(r) + 16u * static_cast<uint32_t>((w >> 2) ^ ((r >> 1) & 3)) +
+            return lds32(stage + 32u * static_cast<uint32_t>(r) + 16u * static_cast<uint32_t>((w >> 2) ^ ((r >> 2) & 1)) +
                          4u * static_cast<uint32_t>(w & 3));
         };
-        const int w = lane & 15;
-#pragma unroll 8
-        for (int i = 0; i < 16; ++i) {
-            const int r = 2 * i + (lane >> 4), odd = first ^ (step & r), c = 2 * w + odd;
-            const uint32_t here = word(r, w), next = word(r, w < 15 ? w + 1 : 15);
+        const int w = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), odd = first ^ (step & r), c = 2 * w + odd;
+            const uint32_t here = word(r, w), next = word(r, w < 7 ? w + 1 : 7);
             if (r >= lo && r < hi && c + 2 <= cols)
                 *reinterpret_cast<uint32_t*>(to + r * p.ldy + c) = odd ? __funnelshift_r(here, next, 16) : here;
         }
@@ -426,34 +419,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
         // ---- epilogue (both CTAs; warps 2..9) ----------------------------------------
         const int quad = warp & 3, half = (warp - 2) >> 2;
         const uint32_t tempty_leader = leader ? tempty_bar : mapa_shared(tempty_bar, 0);
-        const uint32_t buffers = sbase + L::kOffStage + (warp - 2) * 2 * L::kStageWarpBytes;
-        uint32_t acc = 0, acc_phase = 0, turn = 0;
+        const uint32_t buffer = sbase + L::kOffStage + (warp - 2) * L::kStageWarpBytes;
+        // chunks of 16 columns of a half: of the columns that the other accumulator shares, the upper ones of the first
+        // accumulator and the lower ones of the second, and of the others
+        constexpr int kFirst = L::kShared / 32, kRest = 8 - kFirst;
+        uint32_t acc = 0, acc_phase = 0;
         for (int t = pair_id; t < total; t += n_pairs) {
             const PairTile ti = pair_tile<kGrouped>(p, prefix, t, rank);
             if (!warp_waits(lane, [&] { return wait_phase(tfull_bar, acc_phase, guard); })) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + acc * L::kAcc1;
             const int64_t row0 = ti.m0 + 32 * quad;
-#pragma unroll 1
-            for (int part = 0; part < 2; ++part) {
-                // the columns that the other accumulator shares come first: the upper half of the first
-                // accumulator, the lower half of the second
-                const int col = (part == static_cast<int>(acc) ? 128 : 0) + 64 * half;
-                uint32_t v[2][32];
-                tmem_ld_32x32b_x32(taddr + col, v[0]);
-                tmem_ld_32x32b_x32(taddr + col + 32, v[1]);
+            auto store = [&](const uint32_t* v, int col) {
+                store_chunk(p, v, buffer, row0, ti.row_lo, ti.row_hi, ti.n0 + col, lane, &maps.y);
+            };
+            {
+                const int col = (acc ? 0 : L::kAcc1) + 16 * kFirst * half;
+                uint32_t v[kFirst][16];
+#pragma unroll
+                for (int c = 0; c < kFirst; ++c) tmem_ld_32x32b_x16(taddr + col + 16 * c, v[c]);
                 tmem_ld_wait();
-                if (part == 0) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (leader) mbar_arrive(tempty_bar);
-                        else mbar_arrive_cluster(tempty_leader);
-                    }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader) mbar_arrive(tempty_bar);
+                    else mbar_arrive_cluster(tempty_leader);
                 }
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    store_chunk(p, v[c], buffers, turn, row0, ti.row_lo, ti.row_hi, ti.n0 + col + 32 * c, lane, &maps.y);
+                for (int c = 0; c < kFirst; ++c) store(v[c], col + 16 * c);
+            }
+            {
+                const int col = (acc ? L::kShared : 0) + 16 * kRest * half;
+                uint32_t v[kRest][16];
+#pragma unroll
+                for (int c = 0; c < kRest; ++c) tmem_ld_32x32b_x16(taddr + col + 16 * c, v[c]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < kRest; ++c) store(v[c], col + 16 * c);
             }
             acc ^= 1u;
             acc_phase ^= 1u;
@@ -847,7 +849,7 @@ cudaError_t launch_pair(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
     args.m_tiles = static_cast<int>(m_tiles);
     args.n_tiles = static_cast<int>(n_tiles);
     args.y_vec = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0;
-    args.y_tma = args.y_vec && encode_tensor_map_bf16_store(&maps.y, g.y, static_cast<uint64_t>(g.N),
+    args.y_tma = args.y_vec && encode_tensor_map_bf16_store16(&maps.y, g.y, static_cast<uint64_t>(g.N),
                                                             static_cast<uint64_t>(g.M), static_cast<uint64_t>(g.ldy));
     int64_t pairs = dev.sm_count / 2;
     if (!kGrouped && m_tiles * n_tiles < pairs) pairs = m_tiles * n_tiles;

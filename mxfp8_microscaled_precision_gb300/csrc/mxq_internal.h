@@ -65,6 +65,8 @@ bool encode_tensor_map_chunks(CUtensorMap* map, const void* base, uint64_t rows,
 // 64-byte swizzle.
 bool encode_tensor_map_bf16_store(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                                   uint64_t ld);
+// The same for 32 x 16 tiled stores with the 32-byte swizzle.
+bool encode_tensor_map_bf16_store16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t ld);
 // Bytes [rows, cols] (row stride ld bytes) for 32 x 32 tiled stores, no swizzle.
 bool encode_tensor_map_u8_store(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t ld);
 bool encode_tensor_map_3d(CUtensorMap* map, const void* base, bool two_byte_elems, uint64_t inner,
