@@ -729,6 +729,20 @@ mxq_status mxq_quant_mxfp4_grouped(const void* x, mxq_dtype dtype, int64_t rows,
                                    mxq_stream_t stream);
 
 /*
+ * The column copy inside each expert, the operand form of the experts' weight gradients (dW_g = dY_g^T X_g contracts over
+ * the expert's rows).  Expert g's rows [off[g], off[g+1]) take the slot positions from 128 * (floor(off[g] / 128) + g) on,
+ * in groups of 32 of their own; the slot is filled up to a multiple of 128 with zeros (code 0, scale code 0).
+ *
+ * q         payload [cols, capacity / 2 bytes]: row c, slot position p.
+ * s         MMA-tiled scales of [cols, capacity].
+ * capacity  slot positions, a multiple of 128, at least 128 * (ceil(rows/128) + G).  Positions of no slot are not written.
+ * group_offsets as for mxq_quant_mxfp4_grouped.
+ */
+mxq_status mxq_quant_mxfp4_cols_grouped(const void* x, mxq_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                                        const int64_t* group_offsets, int32_t G, int64_t capacity, void* q, void* s,
+                                        mxq_stream_t stream);
+
+/*
  * The values that a payload [rows, cols] and its scales (one per 32 elements of a row) stand for:
  * out = q * 2^(s - 127), NaN where the scale is 0xFF.  E2M1, E4M3 and E5M2 payloads, those of
  * this library's quantizers and of mxq_activation among them.
@@ -770,6 +784,16 @@ mxq_status mxq_gemm_mxfp4(const void* a_q, const void* a_s, const void* b_q, con
 mxq_status mxq_grouped_gemm_mxfp4(const void* a_q, const void* a_s, int64_t a_bands_cap, const void* b_q,
                                   const void* b_s, const int64_t* group_offsets, int32_t G, int64_t M_total, int64_t N,
                                   int64_t K, void* y, int64_t ldy, mxq_stream_t stream);
+
+/*
+ * The experts' weight gradients: y[g][m, n] = sum over expert g's rows r of deq(A)[m, r] * deq(B)[n, r], with A = dY's and
+ * B = X's column copies of mxq_quant_mxfp4_cols_grouped (payloads [M, capacity / 2] and [N, capacity / 2] bytes, the same
+ * group_offsets, rows M_total and capacity).  y: BF16 [G, M, N], row stride ldy >= N, expert g at y + g * M * ldy; zeros
+ * for an expert without rows.  1 <= G <= 1024, G * M up to 2^31 - 4096.
+ */
+mxq_status mxq_grouped_gemm_mxfp4_wgrad(const void* a_q, const void* a_s, const void* b_q, const void* b_s,
+                                        const int64_t* group_offsets, int32_t G, int64_t M_total, int64_t capacity,
+                                        int64_t M, int64_t N, void* y, int64_t ldy, mxq_stream_t stream);
 
 typedef enum {
     MXQ_ACT_SILU = 0,   /* f(g) = g / (1 + exp(-g)) */

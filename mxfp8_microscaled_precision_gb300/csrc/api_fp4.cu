@@ -76,6 +76,24 @@ mxq_status mxq_quant_mxfp4_grouped(const void* x, mxq_dtype dtype, int64_t rows,
     return from_cuda(launch_quant_mxfp4(a, dtype == MXQ_F32, cu(stream)));
 }
 
+mxq_status mxq_quant_mxfp4_cols_grouped(const void* x, mxq_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                                        const int64_t* group_offsets, int32_t G, int64_t capacity, void* q, void* s,
+                                        mxq_stream_t stream) {
+    if (bad_dtype(dtype) || rows < 0 || cols < 0 || ld < cols || G < 1 || capacity < 0) return MXQ_ERR_INVALID_ARG;
+    if (G > kMaxExperts || rows > kMaxRows || cols > kMaxRows || capacity > kMaxRows || capacity % 128 != 0 ||
+        capacity / 128 * bands_of(cols) > 0x7FFFFFFF)
+        return MXQ_ERR_UNSUPPORTED_SHAPE;
+    if (capacity / 128 < bands_of(rows) + G) return MXQ_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return MXQ_OK;
+    if (!x || !group_offsets || !q || !s || !aligned(x, size_of(dtype)) || !aligned(group_offsets, 8) || !aligned(q, 16) ||
+        !aligned(s, 16))
+        return MXQ_ERR_INVALID_ARG;
+    const mxq_status st = device_ok();
+    if (st != MXQ_OK) return st;
+    const Quant4Args a{x, 1, rows, cols, ld, 0, nullptr, nullptr, q, s, 0, 0, true, group_offsets, G, capacity / 128};
+    return from_cuda(launch_quant_mxfp4(a, dtype == MXQ_F32, cu(stream)));
+}
+
 mxq_status mxq_dequant_1x32(const void* q, const void* s, mxq_element element, int64_t rows, int64_t cols, int64_t ldq,
                             int64_t lds, mxq_scale_layout layout, void* out, mxq_dtype dtype, int64_t ldo,
                             mxq_stream_t stream) {
@@ -123,6 +141,23 @@ mxq_status mxq_grouped_gemm_mxfp4(const void* a_q, const void* a_s, int64_t a_ba
     if (st != MXQ_OK) return st;
     return from_cuda(launch_gemm_mxfp4(dev, {a_q, a_s, b_q, b_s, M_total, N, K, y, ldy, group_offsets, G, a_bands_cap},
                                        cu(stream)));
+}
+
+mxq_status mxq_grouped_gemm_mxfp4_wgrad(const void* a_q, const void* a_s, const void* b_q, const void* b_s,
+                                        const int64_t* group_offsets, int32_t G, int64_t M_total, int64_t capacity,
+                                        int64_t M, int64_t N, void* y, int64_t ldy, mxq_stream_t stream) {
+    if (G < 1 || M_total < 0 || capacity < 0 || M < 0 || N < 0 || ldy < N) return MXQ_ERR_INVALID_ARG;
+    if (G > kMaxExperts || M_total > kMaxRows || capacity > kMaxRows || capacity % 128 != 0 || N > kMaxRows || M > kMaxRows / G)
+        return MXQ_ERR_UNSUPPORTED_SHAPE;
+    if (capacity / 128 < bands_of(M_total) + G) return MXQ_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return MXQ_OK;
+    if (!y || !aligned(y, 2) || !group_offsets || !aligned(group_offsets, 8) || bad_operands(a_q, a_s, b_q, b_s))
+        return MXQ_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    const mxq_status st = device_ok(&dev);
+    if (st != MXQ_OK) return st;
+    return from_cuda(launch_grouped_wgrad_mxfp4(dev, {a_q, a_s, b_q, b_s, M, N, capacity, y, ldy, group_offsets, G, 0}, M_total,
+                                                cu(stream)));
 }
 
 mxq_status mxq_activation(const void* z, mxq_dtype dtype, int64_t rows, int64_t inter, int64_t ldz, mxq_act kind,

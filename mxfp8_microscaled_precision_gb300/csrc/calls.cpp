@@ -652,6 +652,22 @@ PyObject* quant_mxfp4_grouped(Args a) {
     return got.tuple();
 }
 
+// (x, offsets, out)
+PyObject* quant_mxfp4_cols_grouped(Args a) {
+    const at::Tensor& like = tensor(a[0], "x");
+    const Matrix x = matrix(like, "x");
+    const int64_t* offsets;
+    const int32_t G = offsets_of(a[1], &offsets, "mxq_quant_mxfp4_cols_grouped");
+    const int64_t capacity = 128 * ((x.rows + 127) / 128 + G);
+    const Given out(a[2], 2);
+    Results got;
+    void* q = got.dense(out[0], "q", like, at::kByte, {x.cols, capacity / 2});
+    void* s = got.dense(out[1], "s", like, at::kByte, {scale_bytes(x.cols, capacity, MXQ_SCALE_MMA_TILED)});
+    check(mxq_quant_mxfp4_cols_grouped(x.data, x.type, x.rows, x.cols, x.ld, offsets, G, capacity, q, s, stream_of(like)),
+          "mxq_quant_mxfp4_cols_grouped");
+    return got.tuple();
+}
+
 // (q, s, cols, element, layout, dtype, out)
 PyObject* dequant_1x32(Args a) {
     const at::Tensor& q = tensor(a[0], "q");
@@ -718,6 +734,26 @@ PyObject* grouped_gemm_mxfp4(Args a) {
     void* y = matrix_out(got, a[7], "out", like, MXQ_BF16, M, N, &ld);
     check(mxq_grouped_gemm_mxfp4(a_q, a_s, bands, b_q, b_s, offsets, G, M, N, K, y, ld, stream_of(like)),
           "mxq_grouped_gemm_mxfp4");
+    return got.one();
+}
+
+// (a_q, a_s, b_q, b_s, offsets, M_total, out)
+PyObject* grouped_gemm_mxfp4_wgrad(Args a) {
+    const at::Tensor& like = tensor(a[0], "a_q");
+    const at::Tensor& b = tensor(a[2], "b_q");
+    if (like.dim() != 2 || b.dim() != 2) throw Refused{"a_q and b_q must be 2-D"};
+    const int64_t M = like.size(0), N = b.size(0), rows = size_arg(a[5], "M_total");
+    const int64_t* offsets;
+    const int32_t G = offsets_of(a[4], &offsets, "mxq_grouped_gemm_mxfp4_wgrad");
+    const int64_t capacity = 128 * ((rows + 127) / 128 + G);
+    const void* a_q = bytes_of(a[0], "a_q", M * (capacity / 2));
+    const void* a_s = bytes_of(a[1], "a_s", scale_bytes(M, capacity, MXQ_SCALE_MMA_TILED));
+    const void* b_q = bytes_of(a[2], "b_q", N * (capacity / 2));
+    const void* b_s = bytes_of(a[3], "b_s", scale_bytes(N, capacity, MXQ_SCALE_MMA_TILED));
+    Results got;
+    void* y = got.dense(a[6], "out", like, at::kBFloat16, {G, M, N});
+    check(mxq_grouped_gemm_mxfp4_wgrad(a_q, a_s, b_q, b_s, offsets, G, rows, capacity, M, N, y, N, stream_of(like)),
+          "mxq_grouped_gemm_mxfp4_wgrad");
     return got.one();
 }
 
@@ -809,7 +845,8 @@ PyMethodDef methods[] = {ENTRY(route, 11), ENTRY(route_backward, 7), ENTRY(moe_p
                          ENTRY(moe_combine, 4), ENTRY(moe_combine_backward, 5), ENTRY(layer_norm, 5),
                          ENTRY(layer_norm_backward, 6), ENTRY(grad_norm, 1), ENTRY(clip_grad_norm, 4),
                          ENTRY(quant_mxfp4, 5), ENTRY(quant_mxfp4_grouped, 3), ENTRY(dequant_1x32, 7),
-                         ENTRY(gemm_mxfp4, 8), ENTRY(grouped_gemm_mxfp4, 8), ENTRY(activation, 5),
+                         ENTRY(quant_mxfp4_cols_grouped, 3), ENTRY(gemm_mxfp4, 8), ENTRY(grouped_gemm_mxfp4, 8),
+                         ENTRY(grouped_gemm_mxfp4_wgrad, 7), ENTRY(activation, 5),
                          ENTRY(activation_backward, 7), ENTRY(set_error, 1), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mxqcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

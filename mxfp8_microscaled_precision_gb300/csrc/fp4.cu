@@ -196,8 +196,8 @@ __device__ __forceinline__ uint32_t group_codes(const Eight<T>& v, uint32_t* cod
 
 // Whether a tile's elements, and of rows that start anywhere the 16 bytes around each row's part, lie in the matrix.
 template <bool kVec>
-__device__ __forceinline__ bool is_whole(const Quant4Args& a, int64_t r0, int rows, int64_t c0, int cols) {
-    return c0 + cols <= a.cols && (kVec ? r0 + rows <= a.rows : r0 > 0 && r0 + rows < a.rows);
+__device__ __forceinline__ bool is_whole(int64_t rows, int64_t cols, int64_t r0, int height, int64_t c0, int width) {
+    return c0 + width <= cols && (kVec ? r0 + height <= rows : r0 > 0 && r0 + height < rows);
 }
 
 // Row copy alone: 64 rows (FP32: 32) of 256 elements a block.  A warp has a row of it at a time, eight elements a lane, and
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const Quant4Arg
     const T* x = static_cast<const T*>(a.x) + b * a.batch_stride + (r0 + w) * a.ld;
     constexpr int kPer = kRowTile<T> / 8;   // rows of a warp
     Eight<T> v[kPer];
-    if (is_whole<kVec>(a, r0, kRowTile<T>, c0, kColTile)) {
+    if (is_whole<kVec>(a.rows, a.cols, r0, kRowTile<T>, c0, kColTile)) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) v[j].template load_whole<kVec>(x + 8 * j * a.ld, static_cast<int>(c0) + 8 * lane);
     } else {
@@ -281,8 +281,26 @@ __global__ void __launch_bounds__(kTileThreads<T, kVec>, sizeof(T) == 2 ? 4 : 2)
     const int t = threadIdx.x;
     const int b = static_cast<int>(blockIdx.x) / s.per_batch, local = static_cast<int>(blockIdx.x) - b * s.per_batch;
     const int tr = local / s.tiles_c, tc = local - tr * s.tiles_c;
-    const int64_t r0 = static_cast<int64_t>(tr) * kTile, c0 = static_cast<int64_t>(tc) * kTile;
-    const int64_t row_groups = (a.cols + 31) >> 5, col_groups = (a.rows + 31) >> 5;
+    const int64_t c0 = static_cast<int64_t>(tc) * kTile;
+    const int64_t row_groups = (a.cols + 31) >> 5;
+    // rows [r0, rows) of the matrix, as the column copy's groups g0 .. of col_groups
+    int64_t r0 = static_cast<int64_t>(tr) * kTile, rows = a.rows, g0 = r0 >> 5, col_groups = (a.rows + 31) >> 5;
+    if (!kRow && a.offsets != nullptr) {   // band tr of the experts: whose it is, all of them asked at once
+        __shared__ int s_expert;
+        if (threadIdx.x == 0) s_expert = -1;
+        __syncthreads();
+        for (int g = threadIdx.x; g < a.G; g += kNT) {
+            const int64_t lo = a.offsets[g], hi = a.offsets[g + 1], band = lo / kTile + g;
+            if (lo >= 0 && hi <= a.rows && band <= tr && tr < band + (hi - lo + kTile - 1) / kTile) s_expert = g;
+        }
+        __syncthreads();
+        if (s_expert < 0) return;
+        const int64_t lo = a.offsets[s_expert];
+        r0 = lo + (tr - (lo / kTile + s_expert)) * kTile;
+        rows = a.offsets[s_expert + 1];
+        g0 = 4 * static_cast<int64_t>(tr);
+        col_groups = 4 * a.bands_cap;
+    }
     const T* x = static_cast<const T*>(a.x) + b * a.batch_stride;
     const int chunk = t & 15;
     if (kVec) {   // 16 bytes a copy, neighbouring threads side by side; what lies outside is filled up with zeros
@@ -292,7 +310,7 @@ __global__ void __launch_bounds__(kTileThreads<T, kVec>, sizeof(T) == 2 ? 4 : 2)
         const uint32_t bytes = left >= 16 ? 16u : (left > 0 ? static_cast<uint32_t>(left) : 0u);
         const T* from = x + (r0 + t / kPer) * a.ld + c;
         const uint32_t to = smem_u32(tile + t / kPer * kTile + at * kVec16<T>);
-        const int left_rows = static_cast<int>(min(a.rows - r0, static_cast<int64_t>(kTile))) - t / kPer;
+        const int left_rows = static_cast<int>(min(rows - r0, static_cast<int64_t>(kTile))) - t / kPer;
 #pragma unroll
         for (int i = 0; i < kTile / rows_step; ++i) {
             const bool in = rows_step * i < left_rows && bytes > 0;
@@ -303,11 +321,11 @@ __global__ void __launch_bounds__(kTileThreads<T, kVec>, sizeof(T) == 2 ? 4 : 2)
     } else {
         Eight<T> v[kPasses];
         const T* p = x + (r0 + (t >> 4)) * a.ld;
-        if (is_whole<kVec>(a, r0, kTile, c0, kTile)) {
+        if (is_whole<kVec>(rows, a.cols, r0, kTile, c0, kTile)) {
 #pragma unroll
             for (int j = 0; j < kPasses; ++j) v[j].template load_whole<kVec>(p + kStep * j * a.ld, static_cast<int>(c0) + 8 * chunk);
         } else {
-            load_rows<T, kVec, kPasses>(v, p, a.ld, r0 + (t >> 4), kStep, a.rows, static_cast<int>(c0) + 8 * chunk, static_cast<int>(a.cols));
+            load_rows<T, kVec, kPasses>(v, p, a.ld, r0 + (t >> 4), kStep, rows, static_cast<int>(c0) + 8 * chunk, static_cast<int>(a.cols));
         }
 #pragma unroll
         for (int j = 0; j < kPasses; ++j) v[j].to_shared(tile + ((t >> 4) + kStep * j) * kTile + 8 * chunk);
@@ -429,7 +447,7 @@ __global__ void __launch_bounds__(kTileThreads<T, kVec>, sizeof(T) == 2 ? 4 : 2)
             for (int k = 0; k < 2; ++k) {
                 const int c = 2 * pair + k;
                 s_out[place_of(c, block)] = o[k];
-                codes8[4 * c + block] = c0 + c < a.cols && (r0 >> 5) + block < col_groups ? static_cast<uint8_t>(code[k]) : 0;
+                codes8[4 * c + block] = c0 + c < a.cols && g0 + block < col_groups ? static_cast<uint8_t>(code[k]) : 0;
             }
         } else {
 #pragma unroll
@@ -443,7 +461,7 @@ __global__ void __launch_bounds__(kTileThreads<T, kVec>, sizeof(T) == 2 ? 4 : 2)
                     m = max(m, abs_bits(f[i]));
                 }
                 s_out[place_of(c, block)] = column_codes(f, m, &code);
-                codes8[4 * c + block] = c0 + c < a.cols && (r0 >> 5) + block < col_groups ? static_cast<uint8_t>(code) : 0;
+                codes8[4 * c + block] = c0 + c < a.cols && g0 + block < col_groups ? static_cast<uint8_t>(code) : 0;
             }
         }
         __syncthreads();
@@ -451,12 +469,12 @@ __global__ void __launch_bounds__(kTileThreads<T, kVec>, sizeof(T) == 2 ? 4 : 2)
 #pragma unroll
         for (int k = 0; k < 4 * kTile / kNT; ++k) {
             const int c = (t >> 2) + kNT / 4 * k, block = t & 3;
-            const int64_t g = (r0 >> 5) + block;
+            const int64_t g = g0 + block;
             if (c0 + c < a.cols && g < col_groups)
                 *reinterpret_cast<uint4*>(q + ((c0 + c) * col_groups + g) * 16) = s_out[place_of(c, block)];
         }
         if (t < kTile) {
-            store_codes(static_cast<uint8_t*>(a.s_col) + b * a.s_col_bytes, a.tiled, c0 + t, a.cols, r0 >> 5, col_groups,
+            store_codes(static_cast<uint8_t*>(a.s_col) + b * a.s_col_bytes, a.tiled, c0 + t, a.cols, g0, col_groups,
                         s_col_codes[t]);
             if (kRow)
                 store_codes(static_cast<uint8_t*>(a.s_row) + b * a.s_row_bytes, a.tiled, r0 + t, a.rows, c0 >> 5, row_groups,
@@ -471,7 +489,7 @@ cudaError_t launch_quant_t(const Quant4Args& a, cudaStream_t stream) {
     // tiled scales: whole 512-byte atoms, with their padding
     const int64_t rows = a.tiled ? (a.rows + kTile - 1) / kTile * kTile : a.rows;
     const int64_t tiles_c = rows_only ? (a.cols + kColTile - 1) / kColTile : (a.cols + kTile - 1) / kTile;
-    const int64_t per_batch = tiles_c * (rows_only ? (rows + kRowTile<T> - 1) / kRowTile<T> : (a.rows + kTile - 1) / kTile);
+    const int64_t per_batch = tiles_c * (rows_only ? (rows + kRowTile<T> - 1) / kRowTile<T> : a.offsets != nullptr ? a.bands_cap : (a.rows + kTile - 1) / kTile);
     const int64_t blocks = a.batch * per_batch;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const Shape s{static_cast<int>(tiles_c), static_cast<int>(per_batch)};

@@ -1,4 +1,4 @@
-// gemm_fp4.cu -- products of MXFP4 operands with BF16 output, dense and grouped by expert.
+// gemm_fp4.cu -- products of MXFP4 operands with BF16 output: dense, the experts' products, their weight gradients.
 //
 //   y[m, n] = sum_k (qa[m, k] 2^ea[m, k/32]) (qb[n, k] 2^eb[n, k/32])
 //
@@ -36,6 +36,7 @@ struct Args {
     int m_tiles, n_tiles;      // dense
     int64_t b_bands;           // 128-row bands of an expert's (of B's) scales
     const int64_t* offsets;    // grouped: [G + 1] on the device
+    int64_t offset_limit;      // rows that they may point to
     int G;
     int64_t bands_cap;         // grouped: bands of A's scales
     int y_tma, y_vec;          // the output has a map; its rows hold whole vectors (16 bytes, rows kernel 8)
@@ -44,10 +45,10 @@ struct Args {
     uint64_t wait_limit_ns;
 };
 
-// Offset g, inside [0, M] whatever it holds.
+// Offset g, inside [0, offset_limit] whatever it holds.
 __device__ __forceinline__ int64_t offset_at(const Args& p, int g) {
     const int64_t o = p.offsets[g];
-    return o < 0 ? int64_t(0) : (o > p.M ? p.M : o);
+    return o < 0 ? int64_t(0) : (o > p.offset_limit ? p.offset_limit : o);
 }
 
 // A wait by one lane, its verdict as a vote: the compiler sees that a vote is the same in all lanes, so that the loops of
@@ -155,26 +156,45 @@ struct PairMaps {
     CUtensorMap a, b, sfa, sfb, y;
 };
 
+// What a launch computes: one product; the experts' products, their rows of A by offsets; the experts' weight gradients,
+// the contraction by offsets and a full grid of tiles each.
+constexpr int kDense = 0, kExperts = 1, kGradients = 2;
+
 struct PairTile {
     int64_t m0;              // this CTA's first A row (may lie past the matrix)
     int64_t a_band;          // its A scale band
-    int64_t row_lo, row_hi;  // rows that are stored (empty: none)
+    int64_t y_row;           // the output row of m0
+    int64_t row_lo, row_hi;  // output rows that are stored (empty: none)
     int64_t n0;              // first output column
     int64_t b_row, b_band;   // first B row of the pair's tile and its scale band
+    int k_atom;              // where the contraction starts, in 128 K elements
+    int num_kb;              // its K blocks (0: the tile is zero) and K elements
+    int64_t k_padded;
 };
 
-template <bool kGrouped>
+template <int kMode>
 __device__ __forceinline__ PairTile pair_tile(const Args& p, const int* prefix, int t, uint32_t rank) {
     PairTile ti;
-    if constexpr (!kGrouped) {
+    ti.k_atom = 0;
+    ti.k_padded = p.k_padded;
+    if constexpr (kMode != kExperts) {
+        int g = 0;
+        if constexpr (kMode == kGradients) {
+            const int per = p.m_tiles * p.n_tiles;
+            g = t / per;
+            t -= g * per;
+            const int64_t lo = offset_at(p, g), hi = offset_at(p, g + 1);
+            ti.k_atom = static_cast<int>(first_band(lo, g));
+            ti.k_padded = hi > lo && ti.k_atom + (hi - lo + 127) / 128 <= p.k_atoms ? (hi - lo + 31) / 32 * 32 : 0;
+        }
         constexpr int kBand = 4;   // raster: bands of 1024 rows, columns inside a band
         const int per_band = kBand * p.n_tiles, band = t / per_band, within = t - band * per_band;
         const int height = min(kBand, p.m_tiles - band * kBand), n = within / height;
         ti.m0 = static_cast<int64_t>(band * kBand + within - n * height) * 256 + 128 * rank;
         ti.n0 = static_cast<int64_t>(n) * 256;
         ti.a_band = ti.m0 / 128;
-        ti.row_lo = ti.m0;
-        ti.row_hi = min(ti.m0 + 128, p.M);
+        ti.y_row = ti.row_lo = g * p.M + ti.m0;
+        ti.row_hi = g * p.M + min(ti.m0 + 128, p.M);
         ti.b_row = ti.n0;
         ti.b_band = ti.n0 / 128;
     } else {
@@ -186,11 +206,12 @@ __device__ __forceinline__ PairTile pair_tile(const Args& p, const int* prefix, 
         const bool any = lo + 128 * i < hi;   // an odd number of row tiles leaves the last odd CTA without rows
         ti.m0 = any ? lo + 128 * i : lo;
         ti.a_band = first_band(lo, g) + (any ? i : 0);
-        ti.row_lo = ti.m0;
+        ti.y_row = ti.row_lo = ti.m0;
         ti.row_hi = any ? min(ti.m0 + 128, hi) : ti.m0;
         ti.b_row = static_cast<int64_t>(g) * p.N + ti.n0;
         ti.b_band = static_cast<int64_t>(g) * p.b_bands + ti.n0 / 128;
     }
+    ti.num_kb = static_cast<int>((ti.k_padded + kBK - 1) / kBK);
     return ti;
 }
 
@@ -269,7 +290,7 @@ __device__ __forceinline__ void store_chunk(const Args& p, const uint32_t* v, ui
     __syncwarp();
 }
 
-template <bool kGrouped>
+template <int kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1)
     gemm_mxfp4_pair_kernel(const __grid_constant__ PairMaps maps, const Args p) {
     using L = PairCfg;
@@ -310,17 +331,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     }
     wait_for_previous();
     int total = p.m_tiles * p.n_tiles;
-    if constexpr (kGrouped) {
+    if constexpr (kMode == kExperts) {
         build_prefix(p, 256, prefix);
         total = prefix[p.G];
     }
+    if constexpr (kMode == kGradients) total *= p.G;
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();   // both CTAs' barriers initialised and tensor memory allocated
     tc_fence_after();
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + L::kOffTmemSlot);
     const int pair_id = static_cast<int>(blockIdx.x >> 1), n_pairs = static_cast<int>(gridDim.x >> 1);
-    const int num_kb = static_cast<int>((p.k_padded + kBK - 1) / kBK);
 
     if (warp == 0) {
         // ---- producer (both CTAs) --------------------------------------------------
@@ -330,15 +351,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
             const uint32_t full0 = leader ? full_bar(0) : mapa_shared(full_bar(0), 0);
             bool stop = false;
             for (int t = pair_id; t < total && !stop && !*abort_flag; t += n_pairs) {
-                const PairTile ti = pair_tile<kGrouped>(p, prefix, t, rank);
+                const PairTile ti = pair_tile<kMode>(p, prefix, t, rank);
                 const int32_t ma = static_cast<int32_t>(ti.m0), nb = static_cast<int32_t>(ti.b_row + 128 * rank);
-                const int32_t sfa_row = static_cast<int32_t>(2 * ti.a_band * p.k_atoms);
-                const int32_t sfb_row = static_cast<int32_t>(2 * (ti.b_band + rank) * p.k_atoms);
-                for (int kb = 0; kb < num_kb; ++kb) {
+                const int32_t sfa_row = static_cast<int32_t>(2 * (ti.a_band * p.k_atoms + ti.k_atom));
+                const int32_t sfb_row = static_cast<int32_t>(2 * ((ti.b_band + rank) * p.k_atoms + ti.k_atom));
+                for (int kb = 0; kb < ti.num_kb; ++kb) {
                     if (!wait_phase(empty_bar(stage), phase ^ 1u, guard)) { stop = true; break; }
                     const uint32_t fb = full0 + 8u * stage;
                     if (leader) mbar_arrive_expect_tx(fb, 2u * L::kStageBytes);
-                    const int32_t kx = 128 * kb, ks = 4 * kb;
+                    const int32_t kx = 64 * ti.k_atom + 128 * kb, ks = 4 * kb;
                     tma_load_2d_pair(sbase + L::kOffA + stage * kBandBytes, &maps.a, kx, ma, fb);
                     tma_load_2d_pair(sbase + L::kOffB + stage * kBandBytes, &maps.b, kx, nb, fb);
                     tma_load_2d_pair(sbase + L::kOffSfa + stage * L::kSfaBytes, &maps.sfa, 0, sfa_row + ks, fb);
@@ -367,8 +388,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
             for (int t = pair_id; t < total && ok; t += n_pairs) {
                 if (!warp_waits(lane, [&] { return spin_phase(tempty_bar, acc_phase ^ 1u, guard); })) { ok = false; break; }
                 tc_fence_after();
+                const PairTile ti = pair_tile<kMode>(p, prefix, t, 0u);
                 const uint32_t d_tmem = tmem_base + acc * L::kAcc1;
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = 0; kb < ti.num_kb; ++kb) {
                     if (!landed && !warp_waits(lane, [&] { return wait_phase(full_bar(stage), phase, guard); })) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sfa_t = tmem_base + L::kTmemScales + L::kScaleCols * stage, sfb_t = sfa_t + 8;
@@ -376,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
                     const uint64_t b_desc = b_desc0 + static_cast<uint64_t>((stage * kBandBytes) >> 4);
                     const uint64_t sfa_d = sfa_desc0 + static_cast<uint64_t>((stage * L::kSfaBytes) >> 4);
                     const uint64_t sfb_d = sfb_desc0 + static_cast<uint64_t>((stage * L::kSfbBytes) >> 4);
-                    const int mmas = mmas_of<kBK>(p.k_padded, kb);
+                    const int mmas = mmas_of<kBK>(ti.k_padded, kb);
                     const uint32_t this_empty = empty_bar(stage);
                     // ask for the next stage now and look at the answer behind the instructions
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -425,12 +447,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
         constexpr int kFirst = L::kShared / 32, kRest = 8 - kFirst;
         uint32_t acc = 0, acc_phase = 0;
         for (int t = pair_id; t < total; t += n_pairs) {
-            const PairTile ti = pair_tile<kGrouped>(p, prefix, t, rank);
+            const PairTile ti = pair_tile<kMode>(p, prefix, t, rank);
             if (!warp_waits(lane, [&] { return wait_phase(tfull_bar, acc_phase, guard); })) break;
             tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + acc * L::kAcc1;
-            const int64_t row0 = ti.m0 + 32 * quad;
-            auto store = [&](const uint32_t* v, int col) {
+            const int64_t row0 = ti.y_row + 32 * quad;
+            auto store = [&](uint32_t* v, int col) {
+                if (kMode == kGradients && ti.num_kb == 0) {   // an expert without rows
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = 0u;
+                }
                 store_chunk(p, v, buffer, row0, ti.row_lo, ti.row_hi, ti.n0 + col, lane, &maps.y);
             };
             {
@@ -832,28 +858,29 @@ cudaError_t allow_smem(Kernel* kernel, int bytes, int device, int* configured) {
     return e;
 }
 
-template <bool kGrouped>
+template <int kMode>
 cudaError_t launch_pair(const DeviceInfo& dev, const Gemm4Args& g, Args args, cudaStream_t stream) {
     using L = PairCfg;
     static thread_local int configured = -1;
-    const cudaError_t e = allow_smem(gemm_mxfp4_pair_kernel<kGrouped>, L::kAlloc, dev.device, &configured);
+    const cudaError_t e = allow_smem(gemm_mxfp4_pair_kernel<kMode>, L::kAlloc, dev.device, &configured);
     if (e != cudaSuccess) return e;
-    const int64_t row_bytes = args.k_padded / 2, experts = kGrouped ? g.G : 1;
+    const int64_t row_bytes = args.k_padded / 2, experts = kMode == kExperts ? g.G : 1;
     PairMaps maps;
     if (!payload_map(&maps.a, g.a_q, g.M, row_bytes, 128) || !payload_map(&maps.b, g.b_q, experts * g.N, row_bytes, 128) ||
-        !scale_map(&maps.sfa, g.a_s, kGrouped ? g.bands_cap : (g.M + 127) / 128, args.k_atoms) ||
+        !scale_map(&maps.sfa, g.a_s, kMode == kExperts ? g.bands_cap : (g.M + 127) / 128, args.k_atoms) ||
         !scale_map(&maps.sfb, g.b_s, experts * args.b_bands, args.k_atoms))
         return cudaErrorInvalidValue;
     const int64_t m_tiles = (g.M + 255) / 256, n_tiles = (g.N + 255) / 256;
-    if ((kGrouped ? m_tiles + g.G : m_tiles) * n_tiles > kMostItems) return cudaErrorInvalidValue;
+    const int64_t y_rows = kMode == kGradients ? g.G * g.M : g.M;
+    const int64_t items = kMode == kDense ? m_tiles * n_tiles : kMode == kExperts ? (m_tiles + g.G) * n_tiles : g.G * m_tiles * n_tiles;
+    if (items > kMostItems) return cudaErrorInvalidValue;
     args.m_tiles = static_cast<int>(m_tiles);
     args.n_tiles = static_cast<int>(n_tiles);
     args.y_vec = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0;
     args.y_tma = args.y_vec && encode_tensor_map_bf16_store16(&maps.y, g.y, static_cast<uint64_t>(g.N),
-                                                            static_cast<uint64_t>(g.M), static_cast<uint64_t>(g.ldy));
-    int64_t pairs = dev.sm_count / 2;
-    if (!kGrouped && m_tiles * n_tiles < pairs) pairs = m_tiles * n_tiles;
-    return launch(gemm_mxfp4_pair_kernel<kGrouped>, 2 * pairs, L::kThreads, L::kAlloc, 0, stream, maps, args);
+                                                              static_cast<uint64_t>(y_rows), static_cast<uint64_t>(g.ldy));
+    const int64_t pairs = items < dev.sm_count / 2 ? items : dev.sm_count / 2;
+    return launch(gemm_mxfp4_pair_kernel<kMode>, 2 * pairs, L::kThreads, L::kAlloc, 0, stream, maps, args);
 }
 
 // Clusters of 1 << log_split CTAs of the rows kernel that the device holds at once (looked up once per device and thread).
@@ -937,7 +964,9 @@ bool fills_pairs(const Gemm4Args& g) {
 
 }  // namespace
 
-cudaError_t launch_gemm_mxfp4(const DeviceInfo& dev, const Gemm4Args& g, cudaStream_t stream) {
+namespace {
+
+Args args_of(const DeviceInfo& dev, const Gemm4Args& g) {
     Args a{};
     a.a_s = static_cast<const uint8_t*>(g.a_s);
     a.b_s = static_cast<const uint8_t*>(g.b_s);
@@ -947,13 +976,27 @@ cudaError_t launch_gemm_mxfp4(const DeviceInfo& dev, const Gemm4Args& g, cudaStr
     a.k_atoms = (a.k_padded + 127) / 128;
     a.b_bands = (g.N + 127) / 128;
     a.offsets = g.offsets;
+    a.offset_limit = g.M;
     a.G = g.G;
     a.bands_cap = g.bands_cap;
     a.split = 1;
     a.status = dev.status;
     a.wait_limit_ns = kDefaultWaitLimitNs;
-    return g.offsets != nullptr ? (fills_pairs<true>(g) ? launch_pair<true>(dev, g, a, stream) : launch_rows<true>(dev, g, a, stream))
-                                : (fills_pairs<false>(g) ? launch_pair<false>(dev, g, a, stream) : launch_rows<false>(dev, g, a, stream));
+    return a;
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_mxfp4(const DeviceInfo& dev, const Gemm4Args& g, cudaStream_t stream) {
+    const Args a = args_of(dev, g);
+    return g.offsets != nullptr ? (fills_pairs<true>(g) ? launch_pair<kExperts>(dev, g, a, stream) : launch_rows<true>(dev, g, a, stream))
+                                : (fills_pairs<false>(g) ? launch_pair<kDense>(dev, g, a, stream) : launch_rows<false>(dev, g, a, stream));
+}
+
+cudaError_t launch_grouped_wgrad_mxfp4(const DeviceInfo& dev, const Gemm4Args& g, int64_t rows, cudaStream_t stream) {
+    Args a = args_of(dev, g);
+    a.offset_limit = rows;
+    return launch_pair<kGradients>(dev, g, a, stream);
 }
 
 }  // namespace mxq

@@ -231,8 +231,9 @@ cudaError_t launch_clip(const ClipTensor* tensors, int count, bool scale_too, fl
 
 // ---- MXFP4, and activations kept in 8 bits (fp4.cu, gemm_fp4.cu, act.cu) ----
 
-// MXFP4 quantization of `batch` matrices (see mxq_quant_mxfp4).  offsets (one matrix, row copy only): the
-// scales tiled by expert in bands_cap bands (see mxq_quant_mxfp4_grouped).
+// MXFP4 quantization of `batch` matrices (see mxq_quant_mxfp4).  offsets, with one matrix and one copy: of the row copy the
+// scales tiled by expert in bands_cap bands (see mxq_quant_mxfp4_grouped); the column copy inside each expert, in bands_cap
+// slots of 128 rows (see mxq_quant_mxfp4_cols_grouped).
 struct Quant4Args {
     const void* x;
     int64_t batch, rows, cols, ld, batch_stride;
@@ -266,6 +267,9 @@ struct Gemm4Args {
     int64_t bands_cap;
 };
 cudaError_t launch_gemm_mxfp4(const DeviceInfo& dev, const Gemm4Args& a, cudaStream_t stream);
+// Weight gradients of the experts (see mxq_grouped_gemm_mxfp4_wgrad): K is the capacity, y [G, M, N]; rows: of the
+// token-sorted inputs.
+cudaError_t launch_grouped_wgrad_mxfp4(const DeviceInfo& dev, const Gemm4Args& a, int64_t rows, cudaStream_t stream);
 
 // The activation between two products (see mxq_activation); q and s null: nothing is kept.
 struct ActArgs {

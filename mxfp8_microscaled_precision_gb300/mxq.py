@@ -108,6 +108,8 @@ def lib() -> ctypes.CDLL:
         L.mxq_grad_norm_workspace_size.restype = SZ
         L.mxq_quant_mxfp4.argtypes = [P, S, I64, I64, I64, I64, I64, P, P, P, P, S, P]
         L.mxq_quant_mxfp4_grouped.argtypes = [P, S, I64, I64, I64, P, I32, I64, P, P, P]
+        L.mxq_quant_mxfp4_cols_grouped.argtypes = [P, S, I64, I64, I64, P, I32, I64, P, P, P]
+        L.mxq_grouped_gemm_mxfp4_wgrad.argtypes = [P, P, P, P, P, I32, I64, I64, I64, I64, P, I64, P]
         L.mxq_dequant_1x32.argtypes = [P, P, S, I64, I64, I64, I64, S, P, S, I64, P]
         L.mxq_gemm_mxfp4.argtypes = [P, P, P, P, I64, I64, I64, P, I64, P]
         L.mxq_grouped_gemm_mxfp4.argtypes = [P, P, I64, P, P, P, I32, I64, I64, I64, P, I64, P]
@@ -123,7 +125,7 @@ def lib() -> ctypes.CDLL:
                   "mxq_route", "mxq_route_backward", "mxq_moe_plan", "mxq_moe_dispatch", "mxq_moe_combine",
                   "mxq_moe_combine_backward", "mxq_layer_norm", "mxq_layer_norm_backward", "mxq_grad_norm",
                   "mxq_clip_grad_norm", "mxq_quant_mxfp4", "mxq_quant_mxfp4_grouped", "mxq_dequant_1x32", "mxq_gemm_mxfp4",
-                  "mxq_grouped_gemm_mxfp4", "mxq_activation", "mxq_activation_backward"):
+                  "mxq_grouped_gemm_mxfp4", "mxq_quant_mxfp4_cols_grouped", "mxq_grouped_gemm_mxfp4_wgrad", "mxq_activation", "mxq_activation_backward"):
             getattr(L, f).restype = S
         _lib = L
         return L
@@ -647,6 +649,13 @@ def quant_mxfp4_grouped(x: torch.Tensor, offsets: torch.Tensor, out=None):
     return _calls().quant_mxfp4_grouped(x, offsets, out)
 
 
+def quant_mxfp4_cols_grouped(x: torch.Tensor, offsets: torch.Tensor, out=None):
+    """The column copy of rows sorted by expert inside each expert (see mxq_quant_mxfp4_cols_grouped), an operand of
+    grouped_gemm_mxfp4_wgrad: x [M, C], offsets int64 [experts + 1].  Returns (q [C, capacity / 2], s), capacity =
+    128 (ceil(M / 128) + experts) slot positions; those of no expert are not written."""
+    return _calls().quant_mxfp4_cols_grouped(x, offsets, out)
+
+
 def dequant_1x32(q: torch.Tensor, s: torch.Tensor, cols: int, fmt="e4m3", layout="tiled", dtype=torch.bfloat16,
                  out=None) -> torch.Tensor:
     """The values [R, cols] that a payload q [R, .] with one scale per 32 elements of a row stands for (see
@@ -667,6 +676,12 @@ def grouped_gemm_mxfp4(a_q, a_s, b_q, b_s, offsets: torch.Tensor, N: int, K: int
     the same offsets, b_q, b_s the row copies (of the transposed weights: the column copies) of quant_mxfp4 on
     stacked weights [experts, N, K].  Returns y [M, N] bf16; rows of no expert are not written."""
     return _calls().grouped_gemm_mxfp4(a_q, a_s, b_q, b_s, offsets, N, K, out)
+
+
+def grouped_gemm_mxfp4_wgrad(a_q, a_s, b_q, b_s, offsets: torch.Tensor, M_total: int, out=None) -> torch.Tensor:
+    """Per-expert y[g] = A_g B_g^T over each expert's rows (see mxq_grouped_gemm_mxfp4_wgrad): a_q [M, .] and b_q [N, .] from
+    quant_mxfp4_cols_grouped on the gradient and the input of M_total rows.  Returns y bf16 [experts, M, N]."""
+    return _calls().grouped_gemm_mxfp4_wgrad(a_q, a_s, b_q, b_s, offsets, M_total, out)
 
 
 def activation(z: torch.Tensor, kind="silu", gated: bool = True, checkpoint: bool = True, out=None):

@@ -39,6 +39,24 @@ def test_quantization(L):
     assert g(G=1025, cap=2000) == 2 and g(rows=BIG, cap=BIG) == 2
 
 
+def test_weight_gradients(L):
+    def q(x=FAKE, dtype=0, rows=300, cols=40, ld=40, off=FAKE, G=4, cap=896, q=FAKE, s=FAKE):
+        return L.mxq_quant_mxfp4_cols_grouped(x, dtype, rows, cols, ld, off, G, cap, q, s, None)
+    assert q(rows=0, cap=512) == 0
+    for bad in (dict(dtype=2), dict(rows=-1), dict(cols=-1), dict(ld=39), dict(G=0), dict(cap=768), dict(cap=-128), dict(x=None),
+                dict(off=None), dict(q=None), dict(s=None), dict(x=ODD), dict(off=HALF), dict(q=HALF), dict(s=HALF)):
+        assert q(**bad) == 1, bad
+    assert q(G=1025, cap=1 << 20) == 2 and q(cap=900) == 2 and q(rows=BIG, cap=BIG) == 2
+
+    def w(aq=FAKE, as_=FAKE, bq=FAKE, bs=FAKE, off=FAKE, G=4, rows=300, cap=896, M=24, N=40, y=FAKE, ldy=40):
+        return L.mxq_grouped_gemm_mxfp4_wgrad(aq, as_, bq, bs, off, G, rows, cap, M, N, y, ldy, None)
+    assert w(M=0) == 0 and w(N=0) == 0
+    for bad in (dict(G=0), dict(rows=-1), dict(cap=-1), dict(cap=768), dict(M=-1), dict(N=-1), dict(ldy=39), dict(aq=None), dict(as_=None),
+                dict(bq=None), dict(bs=None), dict(off=None), dict(y=None), dict(y=ODD), dict(off=HALF), dict(aq=HALF)):
+        assert w(**bad) == 1, bad
+    assert w(G=1025, cap=1 << 20) == 2 and w(cap=900) == 2 and w(M=1 << 30) == 2 and w(N=BIG, ldy=BIG) == 2
+
+
 def test_values(L):
     def d(q=FAKE, s=FAKE, elem=0, rows=4, cols=40, ldq=40, lds=2, layout=0, out=FAKE, dtype=0, ldo=40):
         return L.mxq_dequant_1x32(q, s, elem, rows, cols, ldq, lds, layout, out, dtype, ldo, None)

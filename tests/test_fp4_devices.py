@@ -25,12 +25,16 @@ def _calls():
         "gemm": (lambda a, s, b, t, y: mxq.gemm_mxfp4(a, s, b, t, M, N, K, out=y), [q, s, ((N, K // 2), U8), s, ((M, N), B)]),
         "grouped_gemm": (lambda a, s, b, t, o, y: mxq.grouped_gemm_mxfp4(a, s, b, t, o, N, K, out=y),
                          [q, grouped, ((G * N, K // 2), U8), ((G * ATOM,), U8), off, ((M, N), B)]),
+        "quant_cols_grouped": (lambda x, o, q, s: mxq.quant_mxfp4_cols_grouped(x, o, out=(q, s)),
+                               [x, off, ((K, 64 * (1 + G)), U8), (((1 + G) * ATOM,), U8)]),
+        "wgrad": (lambda a, s, b, t, o, y: mxq.grouped_gemm_mxfp4_wgrad(a, s, b, t, o, M, out=y),
+                  [((N, 64 * (1 + G)), U8), grouped, ((K, 64 * (1 + G)), U8), grouped, off, ((G, N, K), B)]),
         "activation": (lambda z, y, q, s: mxq.activation(z, out=(y, q, s)), [x, act, kept, scales]),
         "activation_backward": (lambda d, q, s, z, y: mxq.activation_backward(d, q, s, out=(z, y)), [act, kept, scales, x, act]),
     }
 
 
-NAMES = ["quant", "quant_grouped", "dequant", "dequant_plain", "gemm", "grouped_gemm", "activation", "activation_backward"]
+NAMES = ["quant", "quant_grouped", "quant_cols_grouped", "wgrad", "dequant", "dequant_plain", "gemm", "grouped_gemm", "activation", "activation_backward"]
 
 
 @pytest.mark.parametrize("name", NAMES)

@@ -278,6 +278,70 @@ def test_experts_products(counts, behind, N, K):
     assert mxq.get_device_status() == 0
 
 
+@pytest.mark.parametrize("counts,behind,M,N", [([5], 0, 64, 96), ([0], 4, 40, 33), ([1, 1, 1], 0, 128, 8), ([0, 3, 0, 0, 70, 1, 0], 0, 130, 160),
+                                                ([128, 128], 0, 256, 256), ([129, 127, 1, 256], 3, 200, 300), ([300, 0, 40, 513], 7, 264, 520),
+                                                ([1, 0] * 100, 0, 24, 40), ([33, 64, 65, 31, 32], 60, 513, 257), ([17] * 64, 0, 72, 1)],
+                         ids=lambda v: str(len(v)) + "x" + str(max(v)) if isinstance(v, list) else None)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_experts_weight_gradients(counts, behind, M, N, dtype):
+    """The column copies inside each expert bit by bit, and the products over its rows: of so few values and rows that FP32
+    holds every partial sum."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    G, R = len(counts), sum(counts) + behind
+    off = torch.tensor(np.cumsum([0] + counts), device="cuda")
+    rng = np.random.default_rng(R + N)
+    x, d = (torch.from_numpy(rng.integers(-12, 13, (R, n)) / 2.0).to(dtype).cuda() for n in (N, M))
+    for t in (x, d):
+        t[sum(counts):] = float("nan")
+    bands = -(-R // 128) + G
+    guard = torch.full((N * bands * 64 + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    a_q, a_s = mxq.quant_mxfp4_cols_grouped(d, off)
+    b_q, b_s = mxq.quant_mxfp4_cols_grouped(x, off, out=(guard[256:-256].view(N, bands * 64), None))
+    assert bool((guard[:256] == 0x5A).all()) and bool((guard[-256:] == 0x5A).all())
+    y = mxq.grouped_gemm_mxfp4_wgrad(a_q, a_s, b_q, b_s, off, R)
+    assert y.shape == (G, M, N)
+    used = torch.full((N, bands * 64), False)
+    for g in range(G):
+        lo, hi = int(off[g]), int(off[g + 1])
+        if hi == lo:
+            assert bool((y[g] == 0).all())
+            continue
+        v = []
+        for t in (d, x):
+            codes, scales = _fp4.quantize(_fp4.f64(t[lo:hi].t()), "e2m1")
+            v.append(_fp4.values(codes, scales, hi - lo, "e2m1"))
+        slot, size = lo // 128 + g, -(-(hi - lo) // 128)
+        want = np.zeros((N, 64 * size), np.uint8)
+        want[:, :codes.shape[1] // 2] = _fp4.pack(codes)
+        assert np.array_equal(b_q[:, 64 * slot:64 * (slot + size)].cpu().numpy(), want)
+        used[:, 64 * slot:64 * (slot + size)] = True
+        full = np.zeros((N, 4 * size), np.uint8)
+        full[:, :scales.shape[1]] = scales
+        atoms = b_s.view(-1, bands, 512)[:, slot:slot + size].reshape(-1).cpu().numpy()
+        assert np.array_equal(atoms, _fp4.tiled(full))
+        assert torch.equal(y[g].cpu(), _fp4.bf16(v[0] @ v[1].T)), g
+    assert bool((b_q.cpu()[~used] == 0x5A).all())   # what is no expert's stays as it was
+    assert mxq.get_device_status() == 0
+
+
+def test_experts_input_gradients():
+    """dX = dY W_g from the column copies of the stacked weights."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    G, R, N, K = 5, 300, 200, 330
+    off = torch.tensor([0, 100, 100, 129, 299, 300], device="cuda")
+    g = torch.Generator().manual_seed(2)
+    w, dy = torch.randn(G, N, K, generator=g).cuda(), torch.randn(R, N, generator=g).cuda()
+    _, _, w_q, w_s = mxq.quant_mxfp4(w, row=False)
+    dx = mxq.grouped_gemm_mxfp4(*mxq.quant_mxfp4_grouped(dy, off), w_q, w_s, off, K, N)
+    dq, ds, _, _ = mxq.quant_mxfp4(dy, col=False, layout="rowmajor")
+    d = mxq.dequant_1x32(dq, ds, N, fmt="e2m1", layout="rowmajor").double()
+    for e in range(G):
+        lo, hi = int(off[e]), int(off[e + 1])
+        v = mxq.dequant_1x32(w_q[e], w_s[e], N, fmt="e2m1").double()
+        ref, size = d[lo:hi] @ v.t(), d[lo:hi].abs() @ v.abs().t()
+        assert bool(((dx[lo:hi].double() - ref).abs() <= (N / 32 + 64) * 2.0 ** -22 * size + 2.0 ** -8 * ref.abs()).all())
+
+
 @pytest.mark.parametrize("off", [[3, 50, 100], [0, 120, 60], [0, 50, 5000], [-10, 20, 100], [2 ** 62, -2 ** 62, 7], [100, 0, 0]])
 def test_offsets_that_break_the_rule_stay_inside(off):
     """Rows are unspecified; what lies around the buffers stays as it was."""
@@ -292,8 +356,14 @@ def test_offsets_that_break_the_rule_stay_inside(off):
     w = mxq.quant_mxfp4(torch.randn(G, N, K, device="cuda"), col=False)
     y = torch.full((M + 64, N), 9.0, dtype=torch.bfloat16, device="cuda")
     mxq.grouped_gemm_mxfp4(q, s, w[0], w[1], off, N, K, out=y[32:32 + M])
+    sizes = [K * 64 * (1 + G), 2 * (1 + G) * 512]
+    guard += [torch.full((n + 2048,), 0xA5, dtype=torch.uint8, device="cuda") for n in sizes]
+    c, cs = guard[2][1024:-1024].view(K, -1), guard[3][1024:-1024]
+    mxq.quant_mxfp4_cols_grouped(x, off, out=(c, cs))
+    dw = torch.full((G + 2, K, K), 9.0, dtype=torch.bfloat16, device="cuda")
+    mxq.grouped_gemm_mxfp4_wgrad(c, cs, c, cs, off, M, out=dw[1:1 + G])
     torch.cuda.synchronize()
-    assert bool((y[:32] == 9).all()) and bool((y[32 + M:] == 9).all())
+    assert bool((y[:32] == 9).all()) and bool((y[32 + M:] == 9).all()) and bool((dw[0] == 9).all()) and bool((dw[-1] == 9).all())
     for g in guard:
         assert bool((g[:1024] == 0xA5).all()) and bool((g[-1024:] == 0xA5).all())
     assert mxq.get_device_status() == 0
