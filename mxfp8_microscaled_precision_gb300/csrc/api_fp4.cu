@@ -101,11 +101,11 @@ mxq_status mxq_dequant_1x32(const void* q, const void* s, mxq_element element, i
     if (element != MXQ_ELEM_E4M3 && element != MXQ_ELEM_E5M2 && element != MXQ_ELEM_E2M1) return MXQ_ERR_INVALID_ARG;
     if (rows < 0 || cols < 0 || ldo < cols) return MXQ_ERR_INVALID_ARG;
     const bool four = element == MXQ_ELEM_E2M1;
-    if (ldq < (four ? 16 * groups_of(cols) : cols) || (four && ldq % 4 != 0)) return MXQ_ERR_INVALID_ARG;
+    if (ldq < (four ? 16 * groups_of(cols) : cols)) return MXQ_ERR_INVALID_ARG;
     if (layout == MXQ_SCALE_ROWMAJOR && lds < groups_of(cols)) return MXQ_ERR_INVALID_ARG;
     if (rows > kMaxRows || cols > kMaxCols) return MXQ_ERR_UNSUPPORTED_SHAPE;
     if (rows == 0 || cols == 0) return MXQ_OK;
-    if (!q || !s || !out || !aligned(out, size_of(dtype)) || (four && !aligned(q, 4))) return MXQ_ERR_INVALID_ARG;
+    if (!q || !s || !out || !aligned(out, size_of(dtype)) || (four && (!aligned(q, 4) || ldq % 4 != 0))) return MXQ_ERR_INVALID_ARG;
     const mxq_status st = device_ok();
     if (st != MXQ_OK) return st;
     const Dequant4Args a{q, s, rows, cols, ldq, lds, layout == MXQ_SCALE_MMA_TILED, out, ldo};

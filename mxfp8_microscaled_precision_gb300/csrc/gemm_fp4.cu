@@ -114,15 +114,21 @@ __device__ __forceinline__ int mmas_of(int64_t k_padded, int64_t kb) {
 // 256 x 256 x 64 instructions of 128 cycles each; it asks for the next stage's bytes before them and reads the answer
 // behind them.
 //
-// What bounds it (16384^3: 1250 us, 7.0 PFLOP/s, 1.9 GHz): a stage takes about 700 cycles instead of the 512 of its
-// instructions.  The same kernel without the operands' loads takes 984 us, without the instructions 1004 us (35 KB a
-// stage and SM, 64 bytes a cycle), without the scale copies 1207 us: loads and instructions meet in shared
-// memory.  Tried without gain: scale copies by a second warp (1490 us), scale copies a stage ahead (1278 us),
-// clusters of two pairs that share B's loads (1280 to 1380 us; 8192 x 4096 x 4096 47.4 us against 47.7 us).
+// Measured: 16384^3 1193 us (7.37 PFLOP/s), 16384 x 7168 x 7168 229 us, 8192 x 4096 x 4096 45 to 46 us, 2048 x 4096 x 4096
+// 16.7 us; experts' products of 131072 rows (128 experts of 4096 x 4096, unequal loads) 746 us, their weight gradients
+// 1248 us.
 //
-// Tensor memory (512 columns): two accumulators of 256 columns that share 128 of them, at 0 and 128, and a slot of 24
+// What bounds it: a stage takes about 660 cycles (1.9 GHz) instead of the 512 of its instructions.  With five stages
+// it took 690 (16384^3: 1256 us; 8192 x 4096 x 4096: 48.4 us); there the same kernel without the operands' loads
+// took 984 us, without the instructions 1004 us (35 KB a stage and SM, 64 bytes a cycle), without the scale copies
+// 1207 us: loads and instructions meet in shared memory, and bytes in flight are part of it.  Tried without gain, with five
+// stages: scale copies by a second warp (1490 us), scale copies a stage ahead (1278 us), clusters of two pairs that
+// share B's loads (1280 to 1380 us; 8192 x 4096 x 4096 47.4 us against 47.7 us); with six: operands and scales
+// loaded by two warps (1225 us).
+//
+// Tensor memory (512 columns): two accumulators of 256 columns, at 0 and 96, that share 160 of them, and a slot of 24
 // columns of scales for each stage.  The epilogue of a tile reads the shared columns first and hands them back,
-// so the next tile's instructions wait for half of it only.
+// so the next tile's instructions wait for these only.
 struct PairCfg {
     static constexpr int kStages = 6;
     static constexpr int kEpiWarps = 8;
@@ -509,6 +515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
 // its thread about 90 cycles, a scale copy or an instruction of the tensor core about 50.  So a slot is 512 K elements
 // (of B 32 KB), loaded by four copies where a row's payload is a multiple of 128 bytes: B, A, and the four scale
 // atoms of each; as many slots as shared memory holds.  A comes in boxes of 16 rows or of tok_cap.
+// Measured: 16 x 16384 x 16384 26.5 us (B at 5.4 TB/s), 1 x 7168 x 7168 9.2 us, 8 x 4096 x 4096 5.5 us.
 //
 // split > 1 (a cluster, one tile): CTA r takes the r-th part of K; the parts' sums are joined through
 // distributed shared memory in the order of the parts.  split == 1: persistent over tiles, two accumulators.
@@ -947,19 +954,24 @@ cudaError_t launch_rows(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
     return launch(gemm_mxfp4_rows_kernel<kGrouped>, grid, L::kThreads, smem, split > 1 ? split : 0, stream, maps, args);
 }
 
-// Which kernel.  Few rows leave most of a 256-row tile's instructions idle and the device without tiles; many rows make
-// the rows kernel read B once for each 128 of them.  Measured, rows kernel / pairs (us, in a graph, N x K):
-//   M = 16    5.7 / 9.9 (4096 x 4096)    4.8 / 5.9 (4096 x 1024)   26 / 33 (16384 x 16384)
-//   M = 64    6.7 / 9.8                  6.3 / 5.8                 29 / 33
-//   M = 128   8.4 / 10.1                 8.0 / 6.1                 36 / 34
-//   M = 256   10.6 / 10.0                8.4 / 6.1                 53 / 34
-// Grouped, 128 experts of 4096 x 4096: 0.5 rows an expert 53 / 63, 16: 191 / 203, 64: 227 / 224, 256: 411 / 318.
+// Which kernel.  Few rows leave most of a 256-row tile's instructions idle; where there are few tiles, a cluster of the
+// rows kernel splits K of each and more SMs work than there are pairs.  Measured, rows kernel / pairs (us, in a graph):
+//   N x K           M = 16      64            128           256           512           1024
+//   4096 x 1024     5.1 / 7.1   6.2 / 7.1     7.8 / 7.2     8.2 / 7.2     8.1 / 7.3     12.1 / 7.5
+//   2048 x 2048     -           5.7 / 8.1     7.2 / 8.3     7.7 / 8.2     8.8 / 8.3     9.1 / 8.4
+//   1024 x 7168     5.6 / 13.4  6.6 / 13.4    8.0 / 13.5    8.8 / 13.4    9.2 / 13.5    11.5 / 13.6
+//   4096 x 4096     5.7 / 10.5  6.6 / 10.5    8.2 / 10.6    9.9 / 10.5    11.8 / 11.0   17.1 / 11.6
+//   7168 x 7168     9.6 / 14.9  11.6 / 14.9   14.5 / 15.0   17.9 / 14.9   26.1 / 15.4   34.3 / 23.9
+//   16384 x 16384   26.5 / 31.1 29.1 / 31.4   36.2 / 31.8   54.7 / 32.6   91.1 / 48.0   145 / 85.1
+// Grouped, 4096 x 4096: 128 experts of unequal loads, 16 rows each 186 / 188, 32: 203 / 196, 64: 227 / 209, 256: 413 / 295;
+// 8 experts, 32 rows each 15 / 17, 128: 21 / 18.
 template <bool kGrouped>
-bool fills_pairs(const Gemm4Args& g) {
+bool fills_pairs(const DeviceInfo& dev, const Gemm4Args& g) {
     if (kGrouped) return g.M > 48 * static_cast<int64_t>(g.G);
-    if (g.M <= 32) return false;
-    if (g.M > 128 || g.K < 2048) return true;
-    return g.M > 64 && g.N > 8192;
+    if (g.M <= 64) return false;
+    const int64_t tiles = ((g.M + 127) / 128) * ((g.N + 127) / 128);
+    if (g.K >= 4096) return 2 * tiles > dev.sm_count;
+    return g.K < 2048 || 4 * tiles > dev.sm_count;
 }
 
 }  // namespace
@@ -989,8 +1001,8 @@ Args args_of(const DeviceInfo& dev, const Gemm4Args& g) {
 
 cudaError_t launch_gemm_mxfp4(const DeviceInfo& dev, const Gemm4Args& g, cudaStream_t stream) {
     const Args a = args_of(dev, g);
-    return g.offsets != nullptr ? (fills_pairs<true>(g) ? launch_pair<kExperts>(dev, g, a, stream) : launch_rows<true>(dev, g, a, stream))
-                                : (fills_pairs<false>(g) ? launch_pair<kDense>(dev, g, a, stream) : launch_rows<false>(dev, g, a, stream));
+    return g.offsets != nullptr ? (fills_pairs<true>(dev, g) ? launch_pair<kExperts>(dev, g, a, stream) : launch_rows<true>(dev, g, a, stream))
+                                : (fills_pairs<false>(dev, g) ? launch_pair<kDense>(dev, g, a, stream) : launch_rows<false>(dev, g, a, stream));
 }
 
 cudaError_t launch_grouped_wgrad_mxfp4(const DeviceInfo& dev, const Gemm4Args& g, int64_t rows, cudaStream_t stream) {

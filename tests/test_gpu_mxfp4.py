@@ -5,6 +5,10 @@ sum of up to 4096 terms is a multiple of 2^-4 below 2^20 times that and FP32 hol
 exact sum rounded to BF16 once, and has to be equal.  With scales over a wide range the sum is off by at most
 (K/32 + 64) 2^-22 of the sum of the terms' sizes (a rounding or truncation of the running sum for each instruction's
 64 terms and for each joining of partial sums), plus 2^-8 of the result for BF16."""
+import subprocess
+import sys
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -180,6 +184,23 @@ def test_product_with_scales_of_every_size(M, N, K):
     assert bool(((got - ref).abs() <= (K / 32 + 64) * 2.0 ** -22 * size + 2.0 ** -8 * ref.abs()).all())
 
 
+@pytest.mark.parametrize("M,N,K", [(129, 8, 2048), (500, 520, 2113), (1024, 1024, 4128), (130, 4097, 4096), (1031, 129, 4500), (65, 1000, 4096),
+                                   (257, 1500, 2050), (600, 31, 8192)])
+def test_few_tiles_of_many_rows(M, N, K):
+    """More rows than a tile has, K split over clusters: the exact sums (of up to 8192 terms: below 2^21 times their unit), into
+    rows that leave in vectors and one by one."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    rng = np.random.default_rng(M * N)
+    a_q, a_s, a = _operand(rng, M, K)
+    b_q, b_s, b = _operand(rng, N, K)
+    want = _fp4.bf16((a.cuda() @ b.cuda().t()).cpu().numpy())
+    for ld in (N, N + 5):
+        wide = torch.full((M + 1, ld), 7.0, dtype=torch.bfloat16, device="cuda")
+        mxq.gemm_mxfp4(a_q, a_s, b_q, b_s, M, N, K, out=wide[:M, :N])
+        assert torch.equal(wide[:M, :N].cpu(), want)
+        assert (wide[M] == 7).all() and (wide[:, N:] == 7).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(2, 200, 160), (300, 300, 300)])
 def test_a_nan_scale_makes_its_row_or_column_nan(M, N, K):
     from mxfp8_microscaled_precision_gb300 import mxq
@@ -276,6 +297,98 @@ def test_experts_products(counts, behind, N, K):
     odd = torch.full((M * (N + 3) + 1,), 9.0, dtype=torch.bfloat16, device="cuda")[1:].view(M, N + 3)
     assert torch.equal(mxq.grouped_gemm_mxfp4(a_q, a_s, b_q, b_s, off, N, K, out=odd[:, :N]), y[:, :N]) and bool((odd[:, N:] == 9).all())
     assert mxq.get_device_status() == 0
+
+
+@pytest.mark.parametrize("K,ld,dtype", [(256, 256, torch.bfloat16), (300, 300, torch.bfloat16), (300, 317, torch.bfloat16), (520, 520, torch.float32),
+                                        (45, 45, torch.float32)])
+@pytest.mark.parametrize("counts,behind", [([3, 0, 70], 5), ([0, 0], 40), ([128], 1), ([64, 1], 200), ([500, 12], 0)])
+def test_rows_of_no_expert_are_not_written(counts, behind, K, ld, dtype):
+    """Payload rows behind the last expert and scales of rows that no expert has, whatever the rows hold."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    live, M, G = sum(counts), sum(counts) + behind, len(counts)
+    x = torch.randn(M, ld, device="cuda").to(dtype)[:, :K]
+    x[live:] = float("inf")
+    off = torch.tensor(np.cumsum([0] + counts), device="cuda")
+    bands, atoms = -(-M // 128) + G, -(-K // 128)
+    q = torch.full((M, 16 * -(-K // 32)), 0x5A, dtype=torch.uint8, device="cuda")
+    s = torch.full((bands * atoms * 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    mxq.quant_mxfp4_grouped(x, off, out=(q, s))
+    assert bool((q[live:] == 0x5A).all())
+    plain = mxq.quant_mxfp4(x, col=False, layout="rowmajor")
+    assert torch.equal(q[:live], plain[0][:live])
+    # byte of row r, group g of a band's atom: 16 (r % 32) + 4 (r / 32) + g
+    r = torch.arange(128, device="cuda")
+    at = (16 * (r % 32) + 4 * (r // 32))[:, None] + torch.arange(4, device="cuda")
+    rows = s.view(bands, atoms, 512)[:, :, at]   # [band, atom, row, group]
+    mine = torch.zeros(bands, 128, dtype=torch.bool, device="cuda")
+    for g, n in enumerate(counts):
+        first = int(off[g]) // 128 + g
+        mine.view(-1)[128 * first:128 * first + n] = True
+    assert bool((rows.permute(0, 2, 1, 3)[~mine] == 0x5A).all())
+
+
+def test_no_rows_at_all():
+    from mxfp8_microscaled_precision_gb300 import mxq
+    off = torch.zeros(4, dtype=torch.int64, device="cuda")
+    none = torch.empty(0, 96, dtype=torch.bfloat16, device="cuda")
+    q, s = mxq.quant_mxfp4_cols_grouped(none, off)
+    assert q.shape == (96, 3 * 64)
+    y = torch.full((3, 96, 96), 9.0, dtype=torch.bfloat16, device="cuda")
+    assert bool((mxq.grouped_gemm_mxfp4_wgrad(q.fill_(0x77), s.fill_(255), q, s, off, 0, out=y) == 0).all())
+    q, s = mxq.quant_mxfp4_grouped(none, off)
+    w, ws, _, _ = mxq.quant_mxfp4(torch.randn(3, 40, 96, device="cuda"), col=False)
+    assert mxq.grouped_gemm_mxfp4(q, s, w, ws, off, 40, 96).shape == (0, 40)
+    for shape in ((0, 64), (64, 0), (0, 0)):
+        got = mxq.quant_mxfp4(torch.empty(shape, device="cuda"))
+        assert got[0].shape == (shape[0], shape[1] // 2) and got[2].shape == (shape[1], shape[0] // 2)
+        assert mxq.dequant_1x32(got[0], got[1], shape[1], fmt="e2m1").shape == shape
+    assert mxq.get_device_status() == 0
+
+
+CAPTURE = """
+import sys, torch
+from mxfp8_microscaled_precision_gb300 import mxq
+x, w = torch.randn(200, 4096, device="cuda").bfloat16(), torch.randn(2, 300, 4096, device="cuda").bfloat16()
+off = torch.tensor([0, 150, 200], device="cuda")
+z, dy = torch.randn(50, 512, device="cuda").bfloat16(), torch.randn(50, 256, device="cuda").bfloat16()
+side = torch.cuda.Stream()
+def step():
+    main = torch.cuda.current_stream()
+    side.wait_stream(main)
+    with torch.cuda.stream(side):                      # weights there, rows here
+        k = mxq.quant_mxfp4(w)
+        c = mxq.quant_mxfp4_cols_grouped(x[:, :300], off)
+    q = mxq.quant_mxfp4(x.clone(), col=False)
+    g = mxq.quant_mxfp4_grouped(x, off)
+    main.wait_stream(side)
+    few, many = mxq.gemm_mxfp4(q[0], q[1], k[0][0], k[1][0], 200, 300, 4096), mxq.gemm_mxfp4(k[2][0], k[3][0], k[2][1], k[3][1], 4096, 4096, 300)
+    y = mxq.grouped_gemm_mxfp4(*g, k[0], k[1], off, 300, 4096)
+    dw = mxq.grouped_gemm_mxfp4_wgrad(*c, *c, off, 200)
+    a, zq, zs = mxq.activation(z)
+    return (few, many, y, dw, a, *mxq.activation_backward(dy, zq, zs), mxq.dequant_1x32(k[0][0], k[1][0], 4096, fmt="e2m1"))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):                          # no call was made before
+    held = step()
+for seed in range(3):
+    for t in (x, w, z, dy):
+        t.copy_(torch.randn(t.shape, generator=torch.Generator().manual_seed(seed)))
+    for t in held:
+        t.fill_(float("nan"))
+    graph.replay()
+    want = step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(held, want)), [torch.equal(a, b) for a, b in zip(held, want)]
+assert mxq.get_device_status() == 0
+print("captured")
+"""
+
+
+def test_first_calls_inside_a_capture_that_forks():
+    """In a process of its own: kernels' limits and the device's shape are looked up while the stream is captured, and
+    launches follow copies and joins of streams there."""
+    done = subprocess.run([sys.executable, "-c", CAPTURE], cwd=Path(__file__).resolve().parents[1], capture_output=True, text=True,
+                          timeout=300)
+    assert done.returncode == 0 and "captured" in done.stdout, done.stdout[-500:] + done.stderr[-2000:]
 
 
 @pytest.mark.parametrize("counts,behind,M,N", [([5], 0, 64, 96), ([0], 4, 40, 33), ([1, 1, 1], 0, 128, 8), ([0, 3, 0, 0, 70, 1, 0], 0, 130, 160),
