@@ -200,35 +200,39 @@ __device__ __forceinline__ bool is_whole(int64_t rows, int64_t cols, int64_t r0,
     return c0 + width <= cols && (kVec ? r0 + height <= rows : r0 > 0 && r0 + height < rows);
 }
 
-// Row copy alone: 64 rows (FP32: 32) of 256 elements a block.  A warp has a row of it at a time, eight elements a lane, and
+// Row copy alone: 64 rows (FP32: 32; few rows: 8) of 256 elements a block.  A warp has a row of it at a time, eight elements a lane, and
 // stores its 128 bytes of payload together; all loads of a thread are issued before the first is used.
 // Bound by memory: 131072 x 4096 BF16 208 us (96% of the copy rate), 16384 x 7168 FP32 77 us, 16381 x 7167 BF16 68 us (64%).
 constexpr int kColTile = 256;
 template <typename T>
 constexpr int kRowTile = 128 / static_cast<int>(sizeof(T));
+// Few rows: blocks of 8 rows, a row a warp, as long as one wave holds them (8 blocks on each of 152 SMs).  Such calls are
+// bound by latency, the fetching of instructions in it.  Measured, tall blocks / these (us, in a graph): 1 x 7168 BF16
+// 2.4 / 1.4, 64 x 4096 2.5 / 1.5, 64 x 4099 5.1 / 1.8, 512 x 4096 3.8 / 2.9, 1024 x 4096 (two waves) 3.9 / 4.6.
+constexpr int kFewRows = 8, kFewBlocks = 8 * 152;
 
-template <typename T, bool kVec>
+template <typename T, bool kVec, int kHeight>
 __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const Quant4Args a, const Shape s) {
-    __shared__ uint32_t s_codes[kRowTile<T>][2];   // four scale codes of every row and 128 columns
-    __shared__ int64_t s_at[kRowTile<T>];          // grouped: the row in the scales, -1: none
+    __shared__ uint32_t s_codes[kHeight][2];   // four scale codes of every row and 128 columns
+    __shared__ int64_t s_at[kHeight];          // grouped: the row in the scales, -1: none
     let_next_start();
     wait_for_previous();
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     const int b = static_cast<int>(blockIdx.x) / s.per_batch, local = static_cast<int>(blockIdx.x) - b * s.per_batch;
     const int tr = local / s.tiles_c, tc = local - tr * s.tiles_c;
-    const int64_t r0 = static_cast<int64_t>(tr) * kRowTile<T>, c0 = static_cast<int64_t>(tc) * kColTile;
+    const int64_t r0 = static_cast<int64_t>(tr) * kHeight, c0 = static_cast<int64_t>(tc) * kColTile;
     const int64_t groups = (a.cols + 31) >> 5;
     const T* x = static_cast<const T*>(a.x) + b * a.batch_stride + (r0 + w) * a.ld;
-    constexpr int kPer = kRowTile<T> / 8;   // rows of a warp
+    constexpr int kPer = kHeight / 8;   // rows of a warp
     Eight<T> v[kPer];
-    if (is_whole<kVec>(a.rows, a.cols, r0, kRowTile<T>, c0, kColTile)) {
+    if (is_whole<kVec>(a.rows, a.cols, r0, kHeight, c0, kColTile)) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) v[j].template load_whole<kVec>(x + 8 * j * a.ld, static_cast<int>(c0) + 8 * lane);
     } else {
         load_rows<T, kVec, kPer>(v, x, a.ld, r0 + w, 8, a.rows, static_cast<int>(c0) + 8 * lane, static_cast<int>(a.cols));
     }
     const int64_t live = a.offsets != nullptr ? min(a.rows, a.offsets[a.G]) : a.rows;   // rows that are written
-    if (a.offsets != nullptr && t < kRowTile<T>) {   // tiled by expert: its first row starts a band
+    if (a.offsets != nullptr && t < kHeight) {   // tiled by expert: its first row starts a band
         const int64_t r = r0 + t;
         int lo = 0, hi = a.G;   // the last expert that starts at or before the row
         while (hi - lo > 1) {
@@ -251,13 +255,16 @@ __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const Quant4Arg
             reinterpret_cast<uint8_t*>(s_codes[w + 8 * j])[lane >> 2] = in ? static_cast<uint8_t>(code) : 0;
     }
     __syncthreads();
-    if (t < 2 * kRowTile<T>) {
-        const int row = t >> 1, part = t & 1;
-        const int64_t first = (c0 >> 5) + 4 * part;   // of the four groups
-        uint8_t* out = static_cast<uint8_t*>(a.s_row) + b * a.s_row_bytes;
-        if (first >= groups) return;
+    const int row = t >> 1, part = t & 1;
+    const int64_t first = (c0 >> 5) + 4 * part;   // of the four groups
+    uint8_t* out = static_cast<uint8_t*>(a.s_row) + b * a.s_row_bytes;
+    if (first >= groups) return;
+    if (t < 2 * kHeight) {
         if (a.offsets == nullptr) store_codes(out, a.tiled, r0 + row, a.rows, first, groups, s_codes[row][part]);
         else if (s_at[row] >= 0) store_codes(out, true, s_at[row], 0, first, groups, s_codes[row][part]);
+    } else if (kHeight == kFewRows && a.offsets == nullptr && a.tiled && r0 + kHeight >= a.rows) {
+        // the last rows: no block of their own for the padding up to 128
+        if (r0 + row < (a.rows + kTile - 1) / kTile * kTile) store_codes(out, true, r0 + row, 0, first, groups, 0u);
     }
 }
 
@@ -490,16 +497,24 @@ __global__ void __launch_bounds__(kTileThreads<T, kVec>, sizeof(T) == 2 ? 4 : 2)
 
 template <typename T, bool kVec>
 cudaError_t launch_quant_t(const Quant4Args& a, cudaStream_t stream) {
-    const bool rows_only = a.q_col == nullptr;
-    // tiled scales: whole 512-byte atoms, with their padding
-    const int64_t rows = a.tiled ? (a.rows + kTile - 1) / kTile * kTile : a.rows;
-    const int64_t tiles_c = rows_only ? (a.cols + kColTile - 1) / kColTile : (a.cols + kTile - 1) / kTile;
-    const int64_t per_batch = tiles_c * (rows_only ? (rows + kRowTile<T> - 1) / kRowTile<T> : a.offsets != nullptr ? a.bands_cap : (a.rows + kTile - 1) / kTile);
+    if (a.q_col == nullptr) {
+        const int64_t tiles_c = (a.cols + kColTile - 1) / kColTile, few = (a.rows + kFewRows - 1) / kFewRows;
+        // tiled scales: whole 512-byte atoms, with their padding
+        const int64_t many = ((a.tiled ? (a.rows + kTile - 1) / kTile * kTile : a.rows) + kRowTile<T> - 1) / kRowTile<T>;
+        const bool is_few = a.batch * few * tiles_c <= kFewBlocks;
+        const int64_t per_batch = tiles_c * (is_few ? few : many), blocks = a.batch * per_batch;
+        if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+        const Shape s{static_cast<int>(tiles_c), static_cast<int>(per_batch)};
+        const dim3 grid(static_cast<unsigned>(blocks));
+        return is_few ? launch_behind(quant_rows_kernel<T, kVec, kFewRows>, grid, kThreads, 0, stream, a, s)
+                      : launch_behind(quant_rows_kernel<T, kVec, kRowTile<T>>, grid, kThreads, 0, stream, a, s);
+    }
+    const int64_t tiles_c = (a.cols + kTile - 1) / kTile;
+    const int64_t per_batch = tiles_c * (a.offsets != nullptr ? a.bands_cap : (a.rows + kTile - 1) / kTile);
     const int64_t blocks = a.batch * per_batch;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const Shape s{static_cast<int>(tiles_c), static_cast<int>(per_batch)};
     const dim3 grid(static_cast<unsigned>(blocks));
-    if (rows_only) return launch_behind(quant_rows_kernel<T, kVec>, grid, kThreads, 0, stream, a, s);
     constexpr unsigned kShared = kTile * kTile * sizeof(T) + 4 * kTile * sizeof(uint4);
     if (a.offsets != nullptr) return launch_behind(quant_tile_kernel<T, false, kVec, true>, grid, kTileThreads<T, kVec>, kShared, stream, a, s);
     if (a.q_row == nullptr) return launch_behind(quant_tile_kernel<T, false, kVec, false>, grid, kTileThreads<T, kVec>, kShared, stream, a, s);

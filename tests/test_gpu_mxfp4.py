@@ -67,6 +67,22 @@ def test_quantization_along_both_axes(R, C, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R,C", [(1, 40), (5, 4099), (8, 7168), (9, 300), (120, 256), (127, 4096), (129, 7000), (1216, 2048), (1217, 2048), (1000, 4097)])
+def test_row_copies_of_few_rows(R, C, dtype):
+    """Given outputs full of other values: the padding of tiled scales up to 128 rows and 4 groups is zero, whoever writes it."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    x = _matrix(R, C, dtype, R + C)
+    codes, scales = _fp4.quantize(_fp4.f64(x), "e2m1")
+    size = -(-R // 128) * -(-C // 128) * 512
+    q, s = torch.full((R, 16 * -(-C // 32)), 0x5A, dtype=torch.uint8, device="cuda"), torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")
+    mxq.quant_mxfp4(x.cuda(), col=False, out=(q, s, None, None))
+    assert np.array_equal(q.cpu().numpy(), _fp4.pack(codes))
+    assert np.array_equal(s.cpu().numpy(), _fp4.tiled(scales))
+    many = mxq.quant_mxfp4(x.cuda().expand(3, R, C), col=False)
+    assert all(torch.equal(many[0][i], q) and torch.equal(many[1][i], s) for i in range(3))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("off,ld", [(0, 168), (1, 161), (2, 163), (8, 160), (3, 200), (5, 173)])
 def test_rows_that_start_anywhere(off, ld, dtype):
     """Views into a wider buffer of NaN: what lies outside the rows is neither read into a group nor written."""
