@@ -515,7 +515,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
 // its thread about 90 cycles, a scale copy or an instruction of the tensor core about 50.  So a slot is 512 K elements
 // (of B 32 KB), loaded by four copies where a row's payload is a multiple of 128 bytes: B, A, and the four scale
 // atoms of each; as many slots as shared memory holds.  A comes in boxes of 16 rows or of tok_cap.
-// Measured: 16 x 16384 x 16384 26.5 us (B at 5.4 TB/s), 1 x 7168 x 7168 9.2 us, 8 x 4096 x 4096 5.5 us.
+// Measured: 16 x 16384 x 16384 26.5 us (B at 5.4 TB/s), 1 x 7168 x 7168 9.2 us, 8 x 4096 x 4096 5.5 us.  Tried without
+// gain: sums sent to the CTA that adds them, each counted on a barrier there, instead of fetched between two
+// barriers of the cluster (8 x 4096 x 4096 5.6 us to 7.0 us, 64 rows 6.9 us to 11.9 us).
 //
 // split > 1 (a cluster, one tile): CTA r takes the r-th part of K; the parts' sums are joined through
 // distributed shared memory in the order of the parts.  split == 1: persistent over tiles, two accumulators.
@@ -815,6 +817,9 @@ __global__ void __launch_bounds__(RowsCfg::kThreads, 1)
 
 // ---- host --------------------------------------------------------------------------------------
 
+// Output rows that start on 16 bytes.
+bool whole_rows(const Gemm4Args& g) { return (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0; }
+
 constexpr int64_t kMostItems = (int64_t(1) << 31) - 4096;   // tiles of a launch: 32-bit counters step past the last one
 
 // Payload [rows, row_bytes], boxes of box_rows x 128 bytes, 128-byte swizzle.
@@ -883,7 +888,7 @@ cudaError_t launch_pair(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
     if (items > kMostItems) return cudaErrorInvalidValue;
     args.m_tiles = static_cast<int>(m_tiles);
     args.n_tiles = static_cast<int>(n_tiles);
-    args.y_vec = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0;
+    args.y_vec = whole_rows(g);
     args.y_tma = args.y_vec && encode_tensor_map_bf16_store16(&maps.y, g.y, static_cast<uint64_t>(g.N),
                                                               static_cast<uint64_t>(y_rows), static_cast<uint64_t>(g.ldy));
     const int64_t pairs = items < dev.sm_count / 2 ? items : dev.sm_count / 2;
@@ -963,6 +968,8 @@ cudaError_t launch_rows(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
 //   4096 x 4096     5.7 / 10.5  6.6 / 10.5    8.2 / 10.6    9.9 / 10.5    11.8 / 11.0   17.1 / 11.6
 //   7168 x 7168     9.6 / 14.9  11.6 / 14.9   14.5 / 15.0   17.9 / 14.9   26.1 / 15.4   34.3 / 23.9
 //   16384 x 16384   26.5 / 31.1 29.1 / 31.4   36.2 / 31.8   54.7 / 32.6   91.1 / 48.0   145 / 85.1
+// Output rows that do not start on 16 bytes cost the pairs 2 to 4 us and the rows kernel nothing: 777 x 1003 (K 2085) 9.5 / 11.3,
+// 777 x 2085 (K 1003) 7.8 / 10.2, 300 x 4099 (K 4096) 10.5 / 13.5, but 2000 x 2085 (K 1003), two waves of tiles, 11.9 / 11.0.
 // Grouped, 4096 x 4096: 128 experts of unequal loads, 16 rows each 186 / 188, 32: 203 / 196, 64: 227 / 209, 256: 413 / 295;
 // 8 experts, 32 rows each 15 / 17, 128: 21 / 18.
 template <bool kGrouped>
@@ -970,6 +977,7 @@ bool fills_pairs(const DeviceInfo& dev, const Gemm4Args& g) {
     if (kGrouped) return g.M > 48 * static_cast<int64_t>(g.G);
     if (g.M <= 64) return false;
     const int64_t tiles = ((g.M + 127) / 128) * ((g.N + 127) / 128);
+    if (!whole_rows(g)) return tiles > dev.sm_count;
     if (g.K >= 4096) return 2 * tiles > dev.sm_count;
     return g.K < 2048 || 4 * tiles > dev.sm_count;
 }
