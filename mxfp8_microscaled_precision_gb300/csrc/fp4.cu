@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "mxq_elem.cuh"
 #include "mxq_internal.h"
@@ -18,6 +19,7 @@ namespace mxq {
 namespace {
 
 constexpr int kTile = 128;
+constexpr int kFewTiles = 2 * 152;   // two on each SM
 constexpr int kThreads = 256;
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
@@ -141,38 +143,49 @@ __device__ __forceinline__ void store_codes(uint8_t* out, bool tiled, int64_t r,
 }
 
 // kRows rows r, r + step, .. of `rows` rows of n elements: their elements [c, c + 8), 0 outside the matrix.  What a vector
-// load may touch comes first, all of it in flight at once; the ends that it may not, element by element, last.
+// load may touch comes first, as many loads in flight as registers hold and nothing between them; then what lies outside
+// is cut off; the ends that a vector may not touch (of a matrix's first and last row) come last, element by element.
 template <typename T, bool kVec, int kRows>
 __device__ __forceinline__ void load_rows(Eight<T> (&v)[kRows], const T* x, int64_t ld, int64_t r, int step, int64_t rows, int c, int n) {
-    bool ends = false;
+    constexpr int kWords = Eight<T>::kWords, kAtOnce = 2;   // rows of which the loads are in flight
+    static_assert(kRows % kAtOnce == 0 || kRows == 1, "rows in groups");
+    uint32_t ends = 0;
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-        const int64_t row = r + j * step;
-        const T* p = x + j * step * ld;
+    for (int j0 = 0; j0 < kRows; j0 += kAtOnce) {
+        uint4 q[kAtOnce][kWords][2];
 #pragma unroll
-        for (int i = 0; i < Eight<T>::kWords; ++i) {
-            const int at = c + i * kVec16<T>;
-            v[j].w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (row >= rows || at >= n) continue;
-            if (kVec ? at + kVec16<T> <= n : is_between<sizeof(T)>(row, rows, n) || is_inner<sizeof(T)>(at, n)) {
-                v[j].w[i] = kVec ? *reinterpret_cast<const uint4*>(p + at) : load_inner<sizeof(T)>(p, at);
-                if (!kVec && at + kVec16<T> > n) v[j].w[i] = inside<sizeof(T)>(v[j].w[i], at, n);
-            } else {
-                ends = true;
+        for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const int64_t row = r + (j0 + j) * step;
+                const int at = c + i * kVec16<T>;
+                const bool in = j0 + j < kRows && row < rows && at < n;
+                const bool whole = kVec ? at + kVec16<T> <= n : is_between<sizeof(T)>(row, rows, n) || is_inner<sizeof(T)>(at, n);
+                const char* p = reinterpret_cast<const char*>(x + (j0 + j) * step * ld + at);
+                const uint4* from = reinterpret_cast<const uint4*>(p - (kVec ? 0u : static_cast<unsigned>(reinterpret_cast<uintptr_t>(p) & 15u)));
+                q[j][i][0] = q[j][i][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (in && whole) q[j][i][0] = from[0];
+                if (!kVec && in && whole) q[j][i][1] = from[1];
+                if (in && !whole) ends |= 1u << ((j0 + j) * kWords + i);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                if (j0 + j >= kRows) continue;
+                const int at = c + i * kVec16<T>;
+                const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(x + (j0 + j) * step * ld + at) & 15u);
+                v[j0 + j].w[i] = kVec ? q[j][i][0] : inside<sizeof(T)>(shift16(q[j][i][0], q[j][i][1], off), at, n);
             }
         }
     }
-    if (!ends) return;
+    if (ends == 0) return;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-        const int64_t row = r + j * step;
 #pragma unroll
-        for (int i = 0; i < Eight<T>::kWords; ++i) {
-            const int at = c + i * kVec16<T>;
-            if (row < rows && at < n &&
-                !(kVec ? at + kVec16<T> <= n : is_between<sizeof(T)>(row, rows, n) || is_inner<sizeof(T)>(at, n)))
-                v[j].w[i] = load_ends<sizeof(T)>(x + j * step * ld, at, n);
-        }
+        for (int i = 0; i < kWords; ++i)
+            if (ends >> (j * kWords + i) & 1) v[j].w[i] = load_ends<sizeof(T)>(x + j * step * ld, c + i * kVec16<T>, n);
     }
 }
 
@@ -273,17 +286,17 @@ __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const Quant4Arg
 // eight elements, four threads a group).  Columns: a thread takes 32 rows of a column (BF16: of two
 // neighbouring ones, in packed operations), and the payload goes out through shared memory, 64 bytes of a
 // column together.
-// FP32 rows that start anywhere: a tile is long work for 256 threads where there are few tiles (777 x 2085: 9.3 us with 256
-// threads, 7.7 us with 512); of rows that start on 16 bytes more tiles fit an SM with 256 (16384 x 7168: 100 us, 122 us).
+// FP32: 512 threads where the tiles are few, since a tile is long work; of many tiles more fit an SM with 256.  Both copies
+// with 256 / 512 threads (us, in a graph): 2048 x 2048 (256 tiles) 6.9 / 5.4, 777 x 2085 7.8 / 6.2, 4096 x 1280 (320 tiles)
+// 6.9 / 7.7, 4096 x 4096 14.8 / 17.0.
+// Rows that start anywhere: FP32 by asynchronous copies of single elements, which need no shift and no ends (4099 x 1111:
+// 6.4 us, 8.5 us by shifted vectors); BF16 by vectors shifted in registers (6.5 us).
 // Bound by memory, with both copies nearly by instructions too (73% of the issue slots): 16384 x 7168 BF16 63 us (84%
 // of the copy rate), the column copy alone 48 us (91%); 131072 x 4096 272 us (89%) and 203 us (99%).
-template <typename T, bool kVec>
-constexpr int kTileThreads = sizeof(T) == 4 && !kVec ? 512 : 256;
-
 // kExperts (column copy alone): the rows of each expert as a slot of their own.
-template <typename T, bool kRow, bool kVec, bool kExperts>
-__global__ void __launch_bounds__(kTileThreads<T, kVec>, sizeof(T) == 2 ? 4 : 2) quant_tile_kernel(const Quant4Args a, const Shape s) {
-    constexpr int kNT = kTileThreads<T, kVec>, kStep = kNT / 16, kPasses = kTile / kStep;   // rows of 16 threads each at once
+template <typename T, bool kRow, bool kVec, bool kExperts, int kNT>
+__global__ void __launch_bounds__(kNT, sizeof(T) == 2 ? 4 : 2) quant_tile_kernel(const Quant4Args a, const Shape s) {
+    constexpr int kStep = kNT / 16, kPasses = kTile / kStep;   // rows of 16 threads each at once
     extern __shared__ __align__(16) uint8_t s_memory[];
     T* tile = reinterpret_cast<T*>(s_memory);
     uint4* s_out = reinterpret_cast<uint4*>(s_memory + kTile * kTile * sizeof(T));
@@ -328,6 +341,22 @@ __global__ void __launch_bounds__(kTileThreads<T, kVec>, sizeof(T) == 2 ? 4 : 2)
             const bool in = rows_step * i < left_rows && bytes > 0;
             cp_async16(to + static_cast<uint32_t>(i * rows_step * kTile * sizeof(T)), in ? from : x, in ? bytes : 0u);
             from += rows_step * a.ld;
+        }
+        cp_async_wait_all();
+    } else if constexpr (sizeof(T) == 4) {   // an element a copy, a warp's side by side
+        const int lane = t & 31, warp = t >> 5;
+        const int left_rows = static_cast<int>(min(rows - r0, static_cast<int64_t>(kTile))), left = static_cast<int>(min(a.cols - c0, static_cast<int64_t>(kTile)));
+        const T* from = x + (r0 + warp) * a.ld + c0 + lane;
+        uint32_t to = smem_u32(tile + warp * kTile + lane);
+#pragma unroll 4
+        for (int row = warp; row < kTile; row += kNT / 32) {
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k) {
+                const bool in = row < left_rows && lane + 32 * k < left;
+                cp_async4(to + 128u * k, in ? from + 32 * k : x, in ? 4u : 0u);
+            }
+            from += kNT / 32 * a.ld;
+            to += kNT / 32 * kTile * static_cast<uint32_t>(sizeof(T));
         }
         cp_async_wait_all();
     } else {
@@ -516,9 +545,16 @@ cudaError_t launch_quant_t(const Quant4Args& a, cudaStream_t stream) {
     const Shape s{static_cast<int>(tiles_c), static_cast<int>(per_batch)};
     const dim3 grid(static_cast<unsigned>(blocks));
     constexpr unsigned kShared = kTile * kTile * sizeof(T) + 4 * kTile * sizeof(uint4);
-    if (a.offsets != nullptr) return launch_behind(quant_tile_kernel<T, false, kVec, true>, grid, kTileThreads<T, kVec>, kShared, stream, a, s);
-    if (a.q_row == nullptr) return launch_behind(quant_tile_kernel<T, false, kVec, false>, grid, kTileThreads<T, kVec>, kShared, stream, a, s);
-    return launch_behind(quant_tile_kernel<T, true, kVec, false>, grid, kTileThreads<T, kVec>, kShared, stream, a, s);
+    const auto go = [&](auto threads) {
+        constexpr int kNT = decltype(threads)::value;
+        if (a.offsets != nullptr) return launch_behind(quant_tile_kernel<T, false, kVec, true, kNT>, grid, kNT, kShared, stream, a, s);
+        if (a.q_row == nullptr) return launch_behind(quant_tile_kernel<T, false, kVec, false, kNT>, grid, kNT, kShared, stream, a, s);
+        return launch_behind(quant_tile_kernel<T, true, kVec, false, kNT>, grid, kNT, kShared, stream, a, s);
+    };
+    if constexpr (sizeof(T) == 4) {
+        if (blocks <= kFewTiles) return go(std::integral_constant<int, 512>{});
+    }
+    return go(std::integral_constant<int, 256>{});
 }
 
 // ---- values ----------------------------------------------------------------------------
