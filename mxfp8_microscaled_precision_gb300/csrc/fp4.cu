@@ -215,7 +215,7 @@ __device__ __forceinline__ bool is_whole(int64_t rows, int64_t cols, int64_t r0,
 
 // Row copy alone: 64 rows (FP32: 32; few rows: 8) of 256 elements a block.  A warp has a row of it at a time, eight elements a lane, and
 // stores its 128 bytes of payload together; all loads of a thread are issued before the first is used.
-// Bound by memory: 131072 x 4096 BF16 208 us (96% of the copy rate), 16384 x 7168 FP32 77 us, 16381 x 7167 BF16 68 us (64%).
+// Bound by memory: 131072 x 4096 BF16 210 us (95% of the copy rate), 16384 x 7168 FP32 77 us, 16381 x 7167 BF16 65 us (68%).
 constexpr int kColTile = 256;
 template <typename T>
 constexpr int kRowTile = 128 / static_cast<int>(sizeof(T));
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const Quant4Arg
 // Rows that start anywhere: FP32 by asynchronous copies of single elements, which need no shift and no ends (4099 x 1111:
 // 6.4 us, 8.5 us by shifted vectors); BF16 by vectors shifted in registers (6.5 us).
 // Bound by memory, with both copies nearly by instructions too (73% of the issue slots): 16384 x 7168 BF16 63 us (84%
-// of the copy rate), the column copy alone 48 us (91%); 131072 x 4096 272 us (89%) and 203 us (99%).
+// of the copy rate), the column copy alone 47 us (93%); 131072 x 4096 272 us (89%) and 203 us (99%).
 // kExperts (column copy alone): the rows of each expert as a slot of their own.
 template <typename T, bool kRow, bool kVec, bool kExperts, int kNT>
 __global__ void __launch_bounds__(kNT, sizeof(T) == 2 ? 4 : 2) quant_tile_kernel(const Quant4Args a, const Shape s) {
@@ -561,7 +561,7 @@ cudaError_t launch_quant_t(const Quant4Args& a, cudaStream_t stream) {
 //
 // Bound by the values that are written.  Rows that hold whole vectors: 16 elements a thread, one 8- or 16-byte load and
 // 32 or 64 bytes of values.  Any other rows: 16 elements a thread on the 16-byte grid of the values, the payload's words
-// shifted to them; element by element at a row's ends only (16381 x 7167 98 us, 44% of the copy rate).
+// shifted to them; element by element at a row's ends only (16381 x 7167 74 us, 59% of the copy rate).
 
 template <int kFormat>
 __device__ __forceinline__ void values8(uint32_t lo, uint32_t hi, float s, float (&f)[8]) {
