@@ -315,16 +315,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     int* prefix = reinterpret_cast<int*>(smem + L::kOffPrefix);
     const WaitGuard guard{abort_flag, p.status, p.wait_limit_ns};
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full_bar(s), 1);    // the even CTA's producer (with both CTAs' bytes)
-            mbar_init(empty_bar(s), 1);   // the even CTA's commit
-        }
-        mbar_init(tfull_bar, 1);
-        mbar_init(tempty_bar, 2 * L::kEpiWarps);   // every epilogue warp of both CTAs
-        mbar_init(drain_bar, 1);
-        *abort_flag = 0;
+    if (warp == 0) {   // a lane a barrier: one after the other they take 40 cycles each
+        if (lane < STAGES) mbar_init(full_bar(lane), 1);   // the even CTA's producer (with both CTAs' bytes)
+        else if (lane < 2 * STAGES) mbar_init(empty_bar(lane - STAGES), 1);   // the even CTA's commit
+        else if (lane == 2 * STAGES) mbar_init(tfull_bar, 1);
+        else if (lane == 2 * STAGES + 1) mbar_init(tempty_bar, 2 * L::kEpiWarps);   // every epilogue warp of both CTAs
+        else if (lane == 2 * STAGES + 2) mbar_init(drain_bar, 1);
+        else if (lane == 2 * STAGES + 3) *abort_flag = 0;
         fence_mbar_init();
+    } else if (warp == 2 && lane == 0) {
         prefetch_tensormap(&maps.a);
         prefetch_tensormap(&maps.b);
         prefetch_tensormap(&maps.sfa);
@@ -352,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     if (warp == 0) {
         // ---- producer (both CTAs) --------------------------------------------------
         if (lane == 0) {
-            int stage = 0;
+            int stage = 0, fresh = STAGES;   // slots that have never been used
             uint32_t phase = 0;
             const uint32_t full0 = leader ? full_bar(0) : mapa_shared(full_bar(0), 0);
             bool stop = false;
@@ -362,7 +361,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
                 const int32_t sfa_row = static_cast<int32_t>(2 * (ti.a_band * p.k_atoms + ti.k_atom));
                 const int32_t sfb_row = static_cast<int32_t>(2 * ((ti.b_band + rank) * p.k_atoms + ti.k_atom));
                 for (int kb = 0; kb < ti.num_kb; ++kb) {
-                    if (!wait_phase(empty_bar(stage), phase ^ 1u, guard)) { stop = true; break; }
+                    if (fresh > 0) --fresh;
+                    else if (!wait_phase(empty_bar(stage), phase ^ 1u, guard)) { stop = true; break; }
                     const uint32_t fb = full0 + 8u * stage;
                     if (leader) mbar_arrive_expect_tx(fb, 2u * L::kStageBytes);
                     const int32_t kx = 64 * ti.k_atom + 128 * kb, ks = 4 * kb;
@@ -595,18 +595,16 @@ __global__ void __launch_bounds__(RowsCfg::kThreads, 1)
     int* prefix = reinterpret_cast<int*>(tail + 16);
     const WaitGuard guard{abort_flag, p.status, p.wait_limit_ns};
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), 1);
-        }
-        for (uint32_t a = 0; a < 2; ++a) {
-            mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), 4);   // the epilogue warps
-        }
-        mbar_init(drain_bar, 1);
-        *abort_flag = 0;
+    if (warp == 0) {   // a lane a barrier: one after the other they took 600 to 1100 cycles
+        constexpr int S = L::kMaxStages;
+        if (lane < S) mbar_init(full_bar(lane), 1);
+        else if (lane < 2 * S) mbar_init(empty_bar(lane - S), 1);
+        else if (lane < 2 * S + 2) mbar_init(tfull_bar(lane - 2 * S), 1);
+        else if (lane < 2 * S + 4) mbar_init(tempty_bar(lane - 2 * S - 2), 4);   // the epilogue warps
+        else if (lane == 2 * S + 4) mbar_init(drain_bar, 1);
+        else if (lane == 2 * S + 5) *abort_flag = 0;
         fence_mbar_init();
+    } else if (warp == 2 && lane == 0) {
         prefetch_tensormap(&maps.a);
         prefetch_tensormap(&maps.a16);
         prefetch_tensormap(&maps.b);
@@ -652,7 +650,8 @@ __global__ void __launch_bounds__(RowsCfg::kThreads, 1)
             if (!waited) wait_for_previous();   // nothing above reads what the kernel before wrote
             waited = true;
             for (int kb = kb_lo; kb < kb_hi; ++kb) {
-                if (!warp_waits(lane, [&] { return wait_phase(empty_bar(stage), phase ^ 1u, guard); })) { stop = true; break; }
+                if (issued >= stages &&   // the slots are free at first
+                    !warp_waits(lane, [&] { return wait_phase(empty_bar(stage), phase ^ 1u, guard); })) { stop = true; break; }
                 const uint32_t fb = full_bar(stage), at = sbase + stage * stage_bytes, at_a = at + 2 * kBandBytes;
                 const uint32_t scales = atoms >= 4 ? 4 * kAtom : kAtom * static_cast<uint32_t>(atoms);
                 if (elect_one()) {
