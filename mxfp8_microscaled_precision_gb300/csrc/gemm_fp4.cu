@@ -114,7 +114,7 @@ __device__ __forceinline__ int mmas_of(int64_t k_padded, int64_t kb) {
 // 256 x 256 x 64 instructions of 128 cycles each; it asks for the next stage's bytes before them and reads the answer
 // behind them.
 //
-// Measured: 16384^3 1193 us (7.37 PFLOP/s), 16384 x 7168 x 7168 229 us, 8192 x 4096 x 4096 45 to 46 us, 2048 x 4096 x 4096
+// Measured: 16384^3 1170 to 1193 us (7.4 to 7.5 PFLOP/s), 16384 x 7168 x 7168 224 to 229 us, 8192 x 4096 x 4096 45 to 46 us, 2048 x 4096 x 4096
 // 16.7 us; experts' products of 131072 rows (128 experts of 4096 x 4096, unequal loads) 746 us, their weight gradients
 // 1248 us.
 //
@@ -315,15 +315,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     int* prefix = reinterpret_cast<int*>(smem + L::kOffPrefix);
     const WaitGuard guard{abort_flag, p.status, p.wait_limit_ns};
 
-    if (warp == 0) {   // a lane a barrier: one after the other they take 40 cycles each
-        if (lane < STAGES) mbar_init(full_bar(lane), 1);   // the even CTA's producer (with both CTAs' bytes)
-        else if (lane < 2 * STAGES) mbar_init(empty_bar(lane - STAGES), 1);   // the even CTA's commit
-        else if (lane == 2 * STAGES) mbar_init(tfull_bar, 1);
-        else if (lane == 2 * STAGES + 1) mbar_init(tempty_bar, 2 * L::kEpiWarps);   // every epilogue warp of both CTAs
-        else if (lane == 2 * STAGES + 2) mbar_init(drain_bar, 1);
-        else if (lane == 2 * STAGES + 3) *abort_flag = 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);    // the even CTA's producer (with both CTAs' bytes)
+            mbar_init(empty_bar(s), 1);   // the even CTA's commit
+        }
+        mbar_init(tfull_bar, 1);
+        mbar_init(tempty_bar, 2 * L::kEpiWarps);   // every epilogue warp of both CTAs
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
         fence_mbar_init();
-    } else if (warp == 2 && lane == 0) {
         prefetch_tensormap(&maps.a);
         prefetch_tensormap(&maps.b);
         prefetch_tensormap(&maps.sfa);
@@ -351,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
     if (warp == 0) {
         // ---- producer (both CTAs) --------------------------------------------------
         if (lane == 0) {
-            int stage = 0, fresh = STAGES;   // slots that have never been used
+            int stage = 0;
             uint32_t phase = 0;
             const uint32_t full0 = leader ? full_bar(0) : mapa_shared(full_bar(0), 0);
             bool stop = false;
@@ -361,8 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
                 const int32_t sfa_row = static_cast<int32_t>(2 * (ti.a_band * p.k_atoms + ti.k_atom));
                 const int32_t sfb_row = static_cast<int32_t>(2 * ((ti.b_band + rank) * p.k_atoms + ti.k_atom));
                 for (int kb = 0; kb < ti.num_kb; ++kb) {
-                    if (fresh > 0) --fresh;
-                    else if (!wait_phase(empty_bar(stage), phase ^ 1u, guard)) { stop = true; break; }
+                    if (!wait_phase(empty_bar(stage), phase ^ 1u, guard)) { stop = true; break; }
                     const uint32_t fb = full0 + 8u * stage;
                     if (leader) mbar_arrive_expect_tx(fb, 2u * L::kStageBytes);
                     const int32_t kx = 64 * ti.k_atom + 128 * kb, ks = 4 * kb;
@@ -515,7 +515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
 // its thread about 90 cycles, a scale copy or an instruction of the tensor core about 50.  So a slot is 512 K elements
 // (of B 32 KB), loaded by four copies where a row's payload is a multiple of 128 bytes: B, A, and the four scale
 // atoms of each; as many slots as shared memory holds.  A comes in boxes of 16 rows or of tok_cap.
-// Measured: 16 x 16384 x 16384 26.5 us (B at 5.4 TB/s), 1 x 7168 x 7168 9.2 us, 8 x 4096 x 4096 5.5 us.  Tried without
+// Measured: 16 x 16384 x 16384 26 us (B at 5.5 TB/s), 1 x 7168 x 7168 9.2 us, 8 x 4096 x 4096 5.5 us.  Tried without
 // gain: sums sent to the CTA that adds them, each counted on a barrier there, instead of fetched between two
 // barriers of the cluster (8 x 4096 x 4096 5.6 us to 7.0 us, 64 rows 6.9 us to 11.9 us).
 //
@@ -595,16 +595,18 @@ __global__ void __launch_bounds__(RowsCfg::kThreads, 1)
     int* prefix = reinterpret_cast<int*>(tail + 16);
     const WaitGuard guard{abort_flag, p.status, p.wait_limit_ns};
 
-    if (warp == 0) {   // a lane a barrier: one after the other they took 600 to 1100 cycles
-        constexpr int S = L::kMaxStages;
-        if (lane < S) mbar_init(full_bar(lane), 1);
-        else if (lane < 2 * S) mbar_init(empty_bar(lane - S), 1);
-        else if (lane < 2 * S + 2) mbar_init(tfull_bar(lane - 2 * S), 1);
-        else if (lane < 2 * S + 4) mbar_init(tempty_bar(lane - 2 * S - 2), 4);   // the epilogue warps
-        else if (lane == 2 * S + 4) mbar_init(drain_bar, 1);
-        else if (lane == 2 * S + 5) *abort_flag = 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (uint32_t a = 0; a < 2; ++a) {
+            mbar_init(tfull_bar(a), 1);
+            mbar_init(tempty_bar(a), 4);   // the epilogue warps
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
         fence_mbar_init();
-    } else if (warp == 2 && lane == 0) {
         prefetch_tensormap(&maps.a);
         prefetch_tensormap(&maps.a16);
         prefetch_tensormap(&maps.b);
@@ -961,16 +963,16 @@ cudaError_t launch_rows(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
 // Which kernel.  Few rows leave most of a 256-row tile's instructions idle; where there are few tiles, a cluster of the
 // rows kernel splits K of each and more SMs work than there are pairs.  Measured, rows kernel / pairs (us, in a graph):
 //   N x K           M = 16      64            128           256           512           1024
-//   4096 x 1024     5.1 / 7.1   6.2 / 7.1     7.8 / 7.2     8.2 / 7.2     8.1 / 7.3     12.1 / 7.5
-//   2048 x 2048     -           5.7 / 8.1     7.2 / 8.3     7.7 / 8.2     8.8 / 8.3     9.1 / 8.4
-//   1024 x 7168     5.6 / 13.4  6.6 / 13.4    8.0 / 13.5    8.8 / 13.4    9.2 / 13.5    11.5 / 13.6
-//   4096 x 4096     5.7 / 10.5  6.6 / 10.5    8.2 / 10.6    9.9 / 10.5    11.8 / 11.0   17.1 / 11.6
-//   7168 x 7168     9.6 / 14.9  11.6 / 14.9   14.5 / 15.0   17.9 / 14.9   26.1 / 15.4   34.3 / 23.9
-//   16384 x 16384   26.5 / 31.1 29.1 / 31.4   36.2 / 31.8   54.7 / 32.6   91.1 / 48.0   145 / 85.1
+//   4096 x 1024     4.9 / 7.1   6.1 / 7.3     7.9 / 7.5     8.1 / 7.3     8.1 / 7.5     12.2 / 7.7
+//   2048 x 2048     4.9 / 8.3   5.9 / 8.2     7.2 / 8.5     7.6 / 8.4     8.9 / 8.4     9.1 / 8.5
+//   1024 x 7168     5.7 / 13.5  6.7 / 13.5    8.0 / 13.7    8.8 / 13.6    9.3 / 13.7    11.4 / 13.9
+//   4096 x 4096     5.8 / 10.8  6.8 / 10.8    8.2 / 10.9    9.9 / 10.8    11.7 / 11.1   16.6 / 12.0
+//   7168 x 7168     9.7 / 15.2  11.3 / 15.2   13.8 / 15.5   17.0 / 15.3   24.6 / 16.2   33.1 / 24.6
+//   16384 x 16384   25.9 / 31.1 28.6 / 31.3   33.9 / 31.9   50.3 / 32.4   85.7 / 48.8   139 / 86.6
 // Output rows that do not start on 16 bytes cost the pairs 2 to 4 us and the rows kernel nothing: 777 x 1003 (K 2085) 9.5 / 11.3,
 // 777 x 2085 (K 1003) 7.8 / 10.2, 300 x 4099 (K 4096) 10.5 / 13.5, but 2000 x 2085 (K 1003), two waves of tiles, 11.9 / 11.0.
-// Grouped, 4096 x 4096: 128 experts of unequal loads, 16 rows each 186 / 188, 32: 203 / 196, 64: 227 / 209, 256: 413 / 295;
-// 8 experts, 32 rows each 15 / 17, 128: 21 / 18.
+// Grouped, 4096 x 4096: 128 experts of unequal loads, 16 rows each 182 / 185, 32: 194 / 195, 64: 219 / 209, 256: 395 / 295;
+// 8 experts, 32 rows each 13 / 18, 128: 22 / 19.
 template <bool kGrouped>
 bool fills_pairs(const DeviceInfo& dev, const Gemm4Args& g) {
     if (kGrouped) return g.M > 48 * static_cast<int64_t>(g.G);
