@@ -223,12 +223,13 @@ __device__ __forceinline__ PairTile pair_tile(const Args& p, const int* prefix, 
 
 // 32 x 16 results of a warp (lane l: output row row0 + l, columns n .. n + 15) through its staging buffer of 1 KB: 16-byte
 // chunk j of row r sits at position j ^ ((r >> 2) & 1), the 32-byte swizzle of a tiled bulk copy.  Rows that are all
-// stored leave with one such copy (the map clips columns past N); otherwise by rows, in vectors or in pairs
+// stored leave with one such copy; otherwise by rows, in vectors or in pairs
 // of columns.  The buffer is small so that the ring is large.
 __device__ __forceinline__ void store_chunk(const Args& p, const uint32_t* v, uint32_t stage, int64_t row0, int64_t row_lo,
                                             int64_t row_hi, int64_t n, int lane, const CUtensorMap* map) {
     if (n >= p.N) return;
-    const bool tiled = p.y_tma && row0 >= row_lo && row0 + 32 <= row_hi;
+    // not across N: the copy leaves out columns past it by 16 bytes only, and what follows them in a row is the caller's
+    const bool tiled = p.y_tma && row0 >= row_lo && row0 + 32 <= row_hi && n + 16 <= p.N;
     uint4 o[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {

@@ -249,6 +249,41 @@ def test_ragged_widths_many_times(M, N, K, ld):
     assert int(wrong) == 0
 
 
+@pytest.mark.parametrize("offset,pad", [(0, 0), (1, 0), (0, 1), (1, 1), (1, 2), (0, 3), (3, 8)])
+@pytest.mark.parametrize("width", range(16))
+def test_many_tiles_whose_rows_start_anywhere(width, offset, pad):
+    """Every length of a row's last chunk of columns, on rows that start on a word and on rows that do not."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    M, N, K = 1291, 2033 + width, 96
+    rng = np.random.default_rng(width)
+    a_q, a_s, a = _operand(rng, M, K)
+    b_q, b_s, b = _operand(rng, N, K)
+    want = (a.cuda() @ b.cuda().t()).to(torch.bfloat16)   # sums of 96 terms: exact in 64 bits and in 32, rounded once
+    ld = N + pad
+    flat = torch.full((offset + M * ld + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = flat[offset:offset + M * ld].view(M, ld)
+    mxq.gemm_mxfp4(a_q, a_s, b_q, b_s, M, N, K, out=y[:, :N])
+    assert torch.equal(y[:, :N], want)
+    assert bool((y[:, N:] == 7).all()) and bool((flat[:offset] == 7).all()) and bool((flat[offset + M * ld:] == 7).all())
+
+
+@pytest.mark.parametrize("N,ld", [(4, 8), (13, 16), (2037, 2040), (250, 256), (1001, 1008)])
+def test_experts_rows_wider_than_their_columns(N, ld):
+    """Rows that start on 16 bytes with columns up to the middle of 16 bytes: what follows them stays."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    rng = np.random.default_rng(N)
+    K, off = 96, torch.tensor([0, 500, 1100], device="cuda")
+    x = torch.from_numpy(rng.integers(-12, 13, (1100, K)) / 2.0).bfloat16().cuda()
+    b = [_operand(rng, N, K) for _ in range(2)]
+    q, s = mxq.quant_mxfp4_grouped(x, off)
+    v = mxq.dequant_1x32(*mxq.quant_mxfp4(x, col=False, layout="rowmajor")[:2], K, fmt="e2m1", layout="rowmajor").double()
+    y = torch.full((1100, ld), 7.0, dtype=torch.bfloat16, device="cuda")
+    mxq.grouped_gemm_mxfp4(q, s, torch.cat([e[0] for e in b]), torch.cat([e[1] for e in b]), off, N, K, out=y[:, :N])
+    assert bool((y[:, N:] == 7).all())
+    for g, (lo, hi) in enumerate(((0, 500), (500, 1100))):
+        assert torch.equal(y[lo:hi, :N], (v[lo:hi] @ b[g][2].cuda().t()).to(torch.bfloat16))
+
+
 def test_empty_products():
     from mxfp8_microscaled_precision_gb300 import mxq
     empty = torch.empty(0, dtype=torch.uint8, device="cuda")
