@@ -223,13 +223,18 @@ __device__ __forceinline__ PairTile pair_tile(const Args& p, const int* prefix, 
 
 // 32 x 16 results of a warp (lane l: output row row0 + l, columns n .. n + 15) through its staging buffer of 1 KB: 16-byte
 // chunk j of row r sits at position j ^ ((r >> 2) & 1), the 32-byte swizzle of a tiled bulk copy.  Rows that are all
-// stored leave with one such copy; otherwise by rows, in vectors or in pairs
-// of columns.  The buffer is small so that the ring is large.
+// stored leave with one such copy; otherwise by rows, in vectors or, where rows start
+// anywhere, in words on the memory's 4-byte grid: where that starts at a row's second column, the row's words hold the
+// columns -1 and 0, 1 and 2, ..; column -1 is the last one of the chunk before (*carry).  Single columns are left at the
+// ends of a run of chunks (start, last) only: a store of one column of 32 rows costs as much as four of words
+// (15143 x 3615 x 77: 71 us with such ends at every chunk, 49 us).  The buffer is small so that the ring is large.
+template <bool kAny>
 __device__ __forceinline__ void store_chunk(const Args& p, const uint32_t* v, uint32_t stage, int64_t row0, int64_t row_lo,
-                                            int64_t row_hi, int64_t n, int lane, const CUtensorMap* map) {
+                                            int64_t row_hi, int64_t n, int lane, const CUtensorMap* map, bool start, bool last,
+                                            uint32_t* carry) {
     if (n >= p.N) return;
     // not across N: the copy leaves out columns past it by 16 bytes only, and what follows them in a row is the caller's
-    const bool tiled = p.y_tma && row0 >= row_lo && row0 + 32 <= row_hi && n + 16 <= p.N;
+    const bool tiled = !kAny && p.y_tma && row0 >= row_lo && row0 + 32 <= row_hi && n + 16 <= p.N;
     uint4 o[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -237,6 +242,17 @@ __device__ __forceinline__ void store_chunk(const Args& p, const uint32_t* v, ui
         o[j].y = cvt_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
         o[j].z = cvt_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
         o[j].w = cvt_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
+    }
+    uint16_t* to = p.y + row0 * p.ldy + n;
+    const int first = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1) & 1, step = static_cast<int>(p.ldy & 1);
+    const int odd = kAny ? first ^ (step & lane) : 0;   // of this lane's row
+    const uint32_t column0 = o[0].x, before = *carry;
+    *carry = o[1].w >> 16;
+    if (kAny && odd) {
+        const uint32_t w[8] = {o[0].x, o[0].y, o[0].z, o[0].w, o[1].x, o[1].y, o[1].z, o[1].w};
+        o[0] = make_uint4(before | (w[0] << 16), __funnelshift_r(w[0], w[1], 16), __funnelshift_r(w[1], w[2], 16), __funnelshift_r(w[2], w[3], 16));
+        o[1] = make_uint4(__funnelshift_r(w[3], w[4], 16), __funnelshift_r(w[4], w[5], 16), __funnelshift_r(w[5], w[6], 16),
+                          __funnelshift_r(w[6], w[7], 16));
     }
     if (lane == 0) bulk_wait_read_all();   // the copy before has read the buffer
     __syncwarp();
@@ -255,8 +271,7 @@ __device__ __forceinline__ void store_chunk(const Args& p, const uint32_t* v, ui
     __syncwarp();
     const int lo = static_cast<int>(max(row_lo - row0, int64_t(0))), hi = static_cast<int>(min(row_hi - row0, int64_t(32)));
     const int cols = static_cast<int>(min(p.N - n, int64_t(16)));
-    uint16_t* to = p.y + row0 * p.ldy + n;
-    if (p.y_vec) {
+    if constexpr (!kAny) {
         const int jj = lane & 1;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -272,32 +287,30 @@ __device__ __forceinline__ void store_chunk(const Args& p, const uint32_t* v, ui
             }
         }
     } else {
-        // Rows that start anywhere, four of them at a time: their columns in pairs on the memory's 4-byte grid, which starts
-        // at the row's first or second column, then the columns that have no partner.
-        const int first = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1) & 1, step = static_cast<int>(p.ldy & 1);
-        auto word = [&](int r, int w) {   // columns 2 w and 2 w + 1 of row r
+        auto word = [&](int r, int w) {
             return lds32(stage + 32u * static_cast<uint32_t>(r) + 16u * static_cast<uint32_t>((w >> 2) ^ ((r >> 2) & 1)) +
                          4u * static_cast<uint32_t>(w & 3));
         };
         const int w = lane & 7;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3), odd = first ^ (step & r), c = 2 * w + odd;
-            const uint32_t here = word(r, w), next = word(r, w < 7 ? w + 1 : 7);
-            if (r >= lo && r < hi && c + 2 <= cols)
-                *reinterpret_cast<uint32_t*>(to + r * p.ldy + c) = odd ? __funnelshift_r(here, next, 16) : here;
+        for (int i = 0; i < 8; ++i) {   // four rows at a time
+            const int r = 4 * i + (lane >> 3), at = 2 * w - (first ^ (step & r));   // the word's first column
+            const uint32_t x = word(r, w);
+            if (r >= lo && r < hi && at + 2 <= cols && (at >= 0 || !start)) *reinterpret_cast<uint32_t*>(to + r * p.ldy + at) = x;
         }
-        const int odd = first ^ (step & lane);
         if (lane >= lo && lane < hi) {
-            if (odd) to[lane * p.ldy] = static_cast<uint16_t>(word(lane, 0));
-            const int last = cols - 1;
-            if (last >= odd && ((cols - odd) & 1)) to[lane * p.ldy + last] = static_cast<uint16_t>(word(lane, last >> 1) >> (16 * (last & 1)));
+            uint16_t* row = to + lane * p.ldy;
+            if (odd && start) row[0] = static_cast<uint16_t>(column0);
+            // the last column where it has no partner: the first one of a word, or of the one behind the last
+            if (last && ((cols - odd) & 1))
+                row[cols - 1] = static_cast<uint16_t>(cols == 16 ? *carry : word(lane, cols >> 1));
         }
     }
     __syncwarp();
 }
 
-template <int kMode>
+// kAny: output rows that do not start on 16 bytes.
+template <int kMode, bool kAny>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1)
     gemm_mxfp4_pair_kernel(const __grid_constant__ PairMaps maps, const Args p) {
     using L = PairCfg;
@@ -459,12 +472,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
             tc_fence_after();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * quad) << 16) + acc * L::kAcc1;
             const int64_t row0 = ti.y_row + 32 * quad;
-            auto store = [&](uint32_t* v, int col) {
+            uint32_t carry = 0u;
+            auto store = [&](uint32_t* v, int col, bool start, bool last) {
                 if (kMode == kGradients && ti.num_kb == 0) {   // an expert without rows
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = 0u;
                 }
-                store_chunk(p, v, buffer, row0, ti.row_lo, ti.row_hi, ti.n0 + col, lane, &maps.y);
+                store_chunk<kAny>(p, v, buffer, row0, ti.row_lo, ti.row_hi, ti.n0 + col, lane, &maps.y, start, last || ti.n0 + col + 16 >= p.N, &carry);
             };
             {
                 const int col = (acc ? 0 : L::kAcc1) + 16 * kFirst * half;
@@ -479,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
                     else mbar_arrive_cluster(tempty_leader);
                 }
 #pragma unroll
-                for (int c = 0; c < kFirst; ++c) store(v[c], col + 16 * c);
+                for (int c = 0; c < kFirst; ++c) store(v[c], col + 16 * c, c == 0, c == kFirst - 1);
             }
             {
                 const int col = (acc ? L::kShared : 0) + 16 * kRest * half;
@@ -488,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::kThreads, 1
                 for (int c = 0; c < kRest; ++c) tmem_ld_32x32b_x16(taddr + col + 16 * c, v[c]);
                 tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < kRest; ++c) store(v[c], col + 16 * c);
+                for (int c = 0; c < kRest; ++c) store(v[c], col + 16 * c, c == 0, c == kRest - 1);
             }
             acc ^= 1u;
             acc_phase ^= 1u;
@@ -872,11 +886,11 @@ cudaError_t allow_smem(Kernel* kernel, int bytes, int device, int* configured) {
     return e;
 }
 
-template <int kMode>
-cudaError_t launch_pair(const DeviceInfo& dev, const Gemm4Args& g, Args args, cudaStream_t stream) {
+template <int kMode, bool kAny>
+cudaError_t launch_pair_of(const DeviceInfo& dev, const Gemm4Args& g, Args args, cudaStream_t stream) {
     using L = PairCfg;
     static thread_local int configured = -1;
-    const cudaError_t e = allow_smem(gemm_mxfp4_pair_kernel<kMode>, L::kAlloc, dev.device, &configured);
+    const cudaError_t e = allow_smem(gemm_mxfp4_pair_kernel<kMode, kAny>, L::kAlloc, dev.device, &configured);
     if (e != cudaSuccess) return e;
     const int64_t row_bytes = args.k_padded / 2, experts = kMode == kExperts ? g.G : 1;
     PairMaps maps;
@@ -890,11 +904,15 @@ cudaError_t launch_pair(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
     if (items > kMostItems) return cudaErrorInvalidValue;
     args.m_tiles = static_cast<int>(m_tiles);
     args.n_tiles = static_cast<int>(n_tiles);
-    args.y_vec = whole_rows(g);
-    args.y_tma = args.y_vec && encode_tensor_map_bf16_store16(&maps.y, g.y, static_cast<uint64_t>(g.N),
+    args.y_tma = !kAny && encode_tensor_map_bf16_store16(&maps.y, g.y, static_cast<uint64_t>(g.N),
                                                               static_cast<uint64_t>(y_rows), static_cast<uint64_t>(g.ldy));
     const int64_t pairs = items < dev.sm_count / 2 ? items : dev.sm_count / 2;
-    return launch(gemm_mxfp4_pair_kernel<kMode>, 2 * pairs, L::kThreads, L::kAlloc, 0, stream, maps, args);
+    return launch(gemm_mxfp4_pair_kernel<kMode, kAny>, 2 * pairs, L::kThreads, L::kAlloc, 0, stream, maps, args);
+}
+
+template <int kMode>
+cudaError_t launch_pair(const DeviceInfo& dev, const Gemm4Args& g, const Args& args, cudaStream_t stream) {
+    return whole_rows(g) ? launch_pair_of<kMode, false>(dev, g, args, stream) : launch_pair_of<kMode, true>(dev, g, args, stream);
 }
 
 // Clusters of 1 << log_split CTAs of the rows kernel that the device holds at once (looked up once per device and thread).
