@@ -114,8 +114,8 @@ __device__ __forceinline__ int mmas_of(int64_t k_padded, int64_t kb) {
 // 256 x 256 x 64 instructions of 128 cycles each; it asks for the next stage's bytes before them and reads the answer
 // behind them.
 //
-// Measured: 16384^3 1170 to 1193 us (7.4 to 7.5 PFLOP/s), 16384 x 7168 x 7168 224 to 229 us, 8192 x 4096 x 4096 45 to 46 us, 2048 x 4096 x 4096
-// 16.7 us; experts' products of 131072 rows (128 experts of 4096 x 4096, unequal loads) 746 us, their weight gradients
+// Measured: 16384^3 1160 us (7.58 PFLOP/s), 16384 x 7168 x 7168 223 us, 8192 x 4096 x 4096 45 us, 2048 x 4096 x 4096
+// 16.8 us; experts' products of 131072 rows (128 experts of 4096 x 4096, unequal loads) 746 us, their weight gradients
 // 1248 us.
 //
 // What bounds it: a stage takes about 660 cycles (1.9 GHz) instead of the 512 of its instructions.  With five stages
@@ -227,7 +227,7 @@ __device__ __forceinline__ PairTile pair_tile(const Args& p, const int* prefix, 
 // anywhere, in words on the memory's 4-byte grid: where that starts at a row's second column, the row's words hold the
 // columns -1 and 0, 1 and 2, ..; column -1 is the last one of the chunk before (*carry).  Single columns are left at the
 // ends of a run of chunks (start, last) only: a store of one column of 32 rows costs as much as four of words
-// (15143 x 3615 x 77: 71 us with such ends at every chunk, 49 us).  The buffer is small so that the ring is large.
+// (15143 x 3615 x 77: 71 us with such ends at every chunk, 46 us).  The buffer is small so that the ring is large.
 template <bool kAny>
 __device__ __forceinline__ void store_chunk(const Args& p, const uint32_t* v, uint32_t stage, int64_t row0, int64_t row_lo,
                                             int64_t row_hi, int64_t n, int lane, const CUtensorMap* map, bool start, bool last,
@@ -988,8 +988,9 @@ cudaError_t launch_rows(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
 //   4096 x 4096     5.8 / 10.8  6.8 / 10.8    8.2 / 10.9    9.9 / 10.8    11.7 / 11.1   16.6 / 12.0
 //   7168 x 7168     9.7 / 15.2  11.3 / 15.2   13.8 / 15.5   17.0 / 15.3   24.6 / 16.2   33.1 / 24.6
 //   16384 x 16384   25.9 / 31.1 28.6 / 31.3   33.9 / 31.9   50.3 / 32.4   85.7 / 48.8   139 / 86.6
-// Output rows that do not start on 16 bytes cost the pairs 2 to 4 us and the rows kernel nothing: 777 x 1003 (K 2085) 9.5 / 11.3,
-// 777 x 2085 (K 1003) 7.8 / 10.2, 300 x 4099 (K 4096) 10.5 / 13.5, but 2000 x 2085 (K 1003), two waves of tiles, 11.9 / 11.0.
+// Output rows that do not start on 16 bytes cost the pairs up to 1 us more and the rows kernel nothing: 777 x 2085 (K 1003)
+// 7.8 / 8.2, 300 x 4099 (K 4096) 10.5 / 11.3, 777 x 1003 (K 300) 7.3 / 7.4, (K 2085) 9.5 / 9.2, but 2000 x 2085 (K 1003), two
+// waves of tiles, 11.9 / 8.4.
 // Grouped, 4096 x 4096: 128 experts of unequal loads, 16 rows each 182 / 185, 32: 194 / 195, 64: 219 / 209, 256: 395 / 295;
 // 8 experts, 32 rows each 13 / 18, 128: 22 / 19.
 template <bool kGrouped>
