@@ -34,6 +34,7 @@ struct Args {
     int64_t k_atoms;           // scale atoms of a 128-row band
     int64_t k_padded;          // K up to a multiple of 32
     int m_tiles, n_tiles;      // dense
+    int items;                 // grouped: work items of a launch at most
     int64_t b_bands;           // 128-row bands of an expert's (of B's) scales
     const int64_t* offsets;    // grouped: [G + 1] on the device
     int64_t offset_limit;      // rows that they may point to
@@ -63,27 +64,30 @@ __device__ __forceinline__ bool warp_waits(int lane, Wait wait) {
 __device__ __forceinline__ int64_t first_band(int64_t first_row, int g) { return first_row / 128 + g; }
 
 // Grouped: prefix[g] = work items of the experts before g; `rows` rows of A an item.  All threads of the block.
+// Sums stop at p.items, which offsets that keep the rule never pass.  Others may have one row in the ranges of many experts:
+// their items past that are left out, or the sums would leave 32 bits and a cluster of a split product meet a second tile.
 __device__ __forceinline__ void build_prefix(const Args& p, int rows, int* prefix) {
+    const uint32_t most = static_cast<uint32_t>(p.items);   // below 2^31: the sum of two of them fits
     for (int g = threadIdx.x; g < p.G; g += blockDim.x) {
         const int64_t lo = offset_at(p, g), hi = offset_at(p, g + 1);
         int64_t n = hi > lo ? (hi - lo + rows - 1) / rows : 0;
         if (first_band(lo, g) + (hi - lo + 127) / 128 > p.bands_cap) n = 0;   // offsets that break the rule
-        prefix[g + 1] = static_cast<int>(n * p.n_tiles);
+        prefix[g + 1] = static_cast<int>(min(n * p.n_tiles, static_cast<int64_t>(most)));
     }
     if (threadIdx.x == 0) prefix[0] = 0;
     __syncthreads();
     if (threadIdx.x < 32) {
-        int carry = 0;
+        uint32_t carry = 0;
         for (int base = 0; base < p.G; base += 32) {
             const int g = base + static_cast<int>(threadIdx.x);
-            int v = g < p.G ? prefix[g + 1] : 0;
+            uint32_t v = g < p.G ? static_cast<uint32_t>(prefix[g + 1]) : 0u;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int up = __shfl_up_sync(0xFFFFFFFFu, v, d);
-                if (static_cast<int>(threadIdx.x) >= d) v += up;
+                const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, v, d);
+                if (static_cast<int>(threadIdx.x) >= d) v = min(v + up, most);
             }
-            if (g < p.G) prefix[g + 1] = carry + v;
-            carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+            if (g < p.G) prefix[g + 1] = static_cast<int>(min(carry + v, most));
+            carry = min(carry + __shfl_sync(0xFFFFFFFFu, v, 31), most);
         }
     }
     __syncthreads();
@@ -902,6 +906,7 @@ cudaError_t launch_pair_of(const DeviceInfo& dev, const Gemm4Args& g, Args args,
     const int64_t y_rows = kMode == kGradients ? g.G * g.M : g.M;
     const int64_t items = kMode == kDense ? m_tiles * n_tiles : kMode == kExperts ? (m_tiles + g.G) * n_tiles : g.G * m_tiles * n_tiles;
     if (items > kMostItems) return cudaErrorInvalidValue;
+    args.items = static_cast<int>(items);
     args.m_tiles = static_cast<int>(m_tiles);
     args.n_tiles = static_cast<int>(n_tiles);
     args.y_tma = !kAny && encode_tensor_map_bf16_store16(&maps.y, g.y, static_cast<uint64_t>(g.N),
@@ -953,6 +958,7 @@ cudaError_t launch_rows(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
     // tiles, at most: grouped, of the experts with rows, each with one partly filled tile
     const int64_t tiles = (kGrouped ? (g.M < g.G ? g.M : g.G) + g.M / 128 : m_tiles) * n_tiles;
     if (tiles > kMostItems) return cudaErrorInvalidValue;
+    args.items = static_cast<int>(tiles);
     args.m_tiles = static_cast<int>(m_tiles);
     args.n_tiles = static_cast<int>(n_tiles);
     args.y_vec = (reinterpret_cast<uintptr_t>(g.y) & 7u) == 0 && g.ldy % 4 == 0;
