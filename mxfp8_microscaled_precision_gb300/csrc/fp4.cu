@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(kNT, sizeof(T) == 2 ? 4 : 2) quant_tile_kernel
         __syncthreads();
         for (int g = threadIdx.x; g < a.G; g += kNT) {
             const int64_t lo = a.offsets[g], hi = a.offsets[g + 1], band = lo / kTile + g;
-            if (lo >= 0 && hi <= a.rows && band <= tr && tr < band + (hi - lo + kTile - 1) / kTile) s_expert = g;
+            // lo < hi first: of offsets that break the rule the difference may not fit 64 bits
+            if (lo >= 0 && lo < hi && hi <= a.rows && band <= tr && tr < band + (hi - lo + kTile - 1) / kTile) s_expert = g;
         }
         __syncthreads();
         if (s_expert < 0) return;

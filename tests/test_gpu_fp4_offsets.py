@@ -38,3 +38,20 @@ def test_no_more_tiles_than_the_launch_holds(M, G, N, K, last):
     size = -(-M // 128) * atoms * 512
     assert torch.equal(y, mxq.gemm_mxfp4(a_q, a_s[:size], b_q[0], b_s[0], M, N, K))
     assert mxq.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("off", [[100, -2 ** 63, 100], [0, -2 ** 63, -2 ** 63 + 5], [2 ** 63 - 1, -2 ** 63, 2 ** 63 - 1], [99, -2 ** 63 + 1, 0]])
+def test_ranges_that_end_before_they_start_have_no_columns(off, dtype):
+    """However far before: the difference of such offsets may wrap around in 64 bits, and a range that seems long would be read
+    behind the matrix."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    M, K, G = 100, 160, 2
+    x = torch.randn(M, K, device="cuda").to(dtype)
+    slots = -(-M // 128) + G
+    q, s = torch.full((K, 64 * slots), 0x5A, dtype=torch.uint8, device="cuda"), torch.full((2 * slots * 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    mxq.quant_mxfp4_cols_grouped(x, torch.tensor(off, device="cuda"), out=(q, s))
+    assert bool((q == 0x5A).all()) and bool((s == 0x5A).all())
+    dw = mxq.grouped_gemm_mxfp4_wgrad(q, s, q, s, torch.tensor(off, device="cuda"), M)
+    assert dw.shape == (G, K, K)
+    assert mxq.get_device_status() == 0
