@@ -1028,7 +1028,9 @@ Args args_of(const DeviceInfo& dev, const Gemm4Args& g) {
     a.bands_cap = g.bands_cap;
     a.split = 1;
     a.status = dev.status;
-    a.wait_limit_ns = kDefaultWaitLimitNs;
+    // The epilogue waits for a tile's whole contraction, which takes about 0.35 us a stage: of an expert's 1.5e9 rows and more
+    // the default limit alone would run out on work that goes on.
+    a.wait_limit_ns = kDefaultWaitLimitNs + static_cast<uint64_t>(a.k_padded / kBK) * 1000u;
     return a;
 }
 
