@@ -30,23 +30,43 @@ constexpr int kThreads = 256;
 constexpr int kSilu = 0, kGelu = 1;
 constexpr int kSpan = 8;   // groups of 32 that a warp of the second form has at once
 
-// f(g) and, where asked for, f'(g).
-template <int kKind, bool kSlope>
+// exp(-(x + rest)), x in [0, 200], rest small.  What the product x log2(e) loses to its rounding (Dekker's exact product, by
+// one fused operation), log2(e)'s own next digits and rest come back as a factor 1 + d ln 2.
+__device__ __forceinline__ float exp_minus(float x, float rest) {
+    constexpr float kLog2e = 1.44269502162933349609375f, kLow = 1.9259629911266175e-8f, kLn2 = 0.693147182464599609375f;
+    const float t = x * -kLog2e, d = fmaf(x, -kLow, fmaf(x, -kLog2e, -t)), e = exp2f(t);
+    return fmaf(e, fmaf(d, kLn2, -rest), e);
+}
+
+// f(g) and, where asked for, f'(g), as precise as results of T show.  BF16: the fast exponential, whose argument's rounding costs
+// |g| (GELU: g^2 / 2) roundings in the tails, 63 units of 2^-24 at -80 and 124 at -12; a result rounds by 2^16 of them.  FP32:
+// exp_minus, 6 and 10 units at most, for which rows that start anywhere pay (65536 x 2 x 2047 kept, SiLU 336 us to 363 us, GELU
+// 373 us to 396 us; 4099 x 1111 GELU 11.8 us to 12.6 us).  CUDA's expf and division cost more there (408, 447 and 14.5 us).
+template <typename T, int kKind, bool kSlope>
 __device__ __forceinline__ float act(float g, float* slope) {
+    constexpr bool kFull = sizeof(T) == 4;
     if constexpr (kKind == kSilu) {
         // from exp(-|g|), which neither overflows nor loses the far side's digits to 1 - sig
-        const float e = __expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e), far = e * r;
+        const float e = kFull ? exp_minus(fminf(fabsf(g), 200.0f), 0.0f) : __expf(-fabsf(g));
+        const float r = __fdividef(1.0f, 1.0f + e), far = e * r;
         const float sig = g < 0.0f ? far : r;
         if (kSlope) *slope = sig * (1.0f + g * (g < 0.0f ? r : far));   // f' = s(g) (1 + g s(-g))
         return g * sig;
     } else {
         // The normal distribution's far side, exp(-g^2/2) h(|g|) with h(a) = exp(a^2/2) erfc(a / sqrt 2) / 2: the bell
         // that the slope needs too times a smooth function, here t P(t), t = k / (a + k), P by least squares on
-        // Chebyshev points of [0, 15] weighted towards equal relative errors: 1.5e-8 at most.
+        // Chebyshev points of [0, 15] weighted towards equal relative errors: 4.4e-8 at most with these coefficients.
         constexpr float kP[9] = {0.10640031844377518f, 0.10602681338787079f, 0.10231088101863861f,
                                  0.06455493718385696f, 0.12730126082897186f, -0.10002311319112778f,
                                  0.20164304971694946f, -0.1384870558977127f, 0.030272917822003365f};
-        const float a = fabsf(g), t = __fdividef(3.75f, a + 3.75f), e = __expf(-0.5f * g * g);
+        const float a = fabsf(g), t = __fdividef(3.75f, a + 3.75f);
+        float e;
+        if constexpr (kFull) {   // at 20 it is zero already
+            const float b = fminf(a, 20.0f), half = 0.5f * b, square = half * b;
+            e = exp_minus(square, fmaf(half, b, -square));
+        } else {
+            e = __expf(-0.5f * g * g);
+        }
         float h = kP[8];
 #pragma unroll
         for (int i = 7; i >= 0; --i) h = fmaf(h, t, kP[i]);
@@ -74,9 +94,14 @@ __device__ __forceinline__ bool e4m3_scale(uint32_t amax, uint32_t* code, float*
 template <typename T>
 struct Eight {
     uint4 w[sizeof(T) / 2];
+    // FP32 without the hint that they are read once: two loads take the halves of a thread's sectors, and the hint lets go of
+    // some between them (L1 hits 38% instead of 50%; SiLU not kept, 65536 x 2 x 2048: 251 us, 226 us without it)
     __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+            const uint4* from = reinterpret_cast<const uint4*>(p) + i;
+            w[i] = sizeof(T) == 2 ? __ldcs(from) : *from;
+        }
     }
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -161,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) act_kernel(const ActArgs a, int log_
         u.get(fu);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float f = act<kKind, false>(fg[k], nullptr);
+            const float f = act<T, kKind, false>(fg[k], nullptr);
             y[k] = kGated ? f * fu[k] : f;
         }
         store8(static_cast<T*>(a.y) + at.row * a.ldy + at.col, y);
@@ -213,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) act_backward_kernel(const ActBackwar
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         float slope;
-        const float f = act<kKind, true>(g[k], &slope);
+        const float f = act<T, kKind, true>(g[k], &slope);
         y[k] = kGated ? f * u[k] : f;
         dg[k] = (kGated ? dy[k] * u[k] : dy[k]) * slope;
         du[k] = dy[k] * f;
@@ -261,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) act_any_kernel(const ActArgs a, int 
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) {
         const int64_t c = c0 + 32 * i;
-        const float f = act<kKind, false>(g[i], nullptr);
+        const float f = act<T, kKind, false>(g[i], nullptr);
         if (c < a.inter) static_cast<T*>(a.y)[at.row * a.ldy + c] = from_float<T>(kGated ? f * u[i] : f);
         if constexpr (kKeep) {
             uint8_t* q = static_cast<uint8_t*>(a.q) + at.row * kParts * a.inter + c;
@@ -309,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) act_backward_any_kernel(const ActBac
         const float g = f16_lo(cvt_f16_fp8x2<kE4M3>(qg[i])) * scale_of(sg[i]);
         const float u = kGated ? f16_lo(cvt_f16_fp8x2<kE4M3>(qu[i])) * scale_of(su[i]) : 1.0f;
         float slope;
-        const float f = act<kKind, true>(g, &slope);
+        const float f = act<T, kKind, true>(g, &slope);
         dz[c] = from_float<T>((kGated ? dy[i] * u : dy[i]) * slope);
         if (kGated) dz[a.inter + c] = from_float<T>(dy[i] * f);
         if (a.y != nullptr) static_cast<T*>(a.y)[at.row * a.ldy + c] = from_float<T>(kGated ? f * u : f);
