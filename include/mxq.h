@@ -809,7 +809,7 @@ typedef enum {
  *       and plain E8M0 scales [rows, 2 ceil(inter/32)] or [rows, ceil(inter/32)], dense; g and u in groups of
  *       32 of their own.  8.25 bits instead of the input's 16 or 32.  A group with a NaN or an infinity
  *       comes back as NaN.
- * FP32 results hold FP32's digits down to f of 2^-119,
+ * f(inf) is inf; f(-inf) is NaN, minus infinity times zero.  FP32 results hold FP32's digits down to f of 2^-119,
  * off by at most 16 (SiLU) and 30 (GELU) roundings.
  */
 mxq_status mxq_activation(const void* z, mxq_dtype dtype, int64_t rows, int64_t inter, int64_t ldz, mxq_act kind,
