@@ -69,22 +69,29 @@ cudaError_t current_device_info(DeviceInfo* info) {
     return cudaSuccess;
 }
 
-cudaError_t current_device_is_supported(bool* yes) {
-    static std::atomic<signed char> known[kMaxDevices];   // 0 unknown, 1 sm_103, -1 another
+cudaError_t current_device_sms(int* sms) {
+    static std::atomic<int> known[kMaxDevices];   // 0 unknown, -1 no sm_103
     int dev = -1;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    signed char k = known[dev].load(std::memory_order_relaxed);
+    int k = known[dev].load(std::memory_order_relaxed);
     if (k == 0) {
         DeviceInfo info;
         const cudaError_t err = current_device_info(&info);
         if (err != cudaSuccess) return err;
-        k = info.cc_major == 10 && info.cc_minor == 3 ? 1 : -1;
+        k = info.cc_major == 10 && info.cc_minor == 3 ? info.sm_count : -1;
         known[dev].store(k, std::memory_order_relaxed);
     }
-    *yes = k > 0;
+    *sms = k > 0 ? k : 0;
     return cudaSuccess;
+}
+
+cudaError_t current_device_is_supported(bool* yes) {
+    int sms = 0;
+    const cudaError_t e = current_device_sms(&sms);
+    *yes = sms > 0;
+    return e;
 }
 
 }  // namespace mxq

@@ -50,12 +50,13 @@ mxq_status mxq_quant_mxfp4(const void* x, mxq_dtype dtype, int64_t batch, int64_
     if (!x || (!q_row && !q_col) || !q_row != !s_row || !q_col != !s_col) return MXQ_ERR_INVALID_ARG;
     if (!aligned(x, size_of(dtype)) || !aligned(q_row, 16) || !aligned(s_row, 16) || !aligned(q_col, 16) || !aligned(s_col, 16))
         return MXQ_ERR_INVALID_ARG;
-    const mxq_status st = device_ok();
+    int sms = 0;
+    const mxq_status st = device_ok(&sms);
     if (st != MXQ_OK) return st;
     const Quant4Args a{x, batch, rows, cols, ld, batch > 1 ? batch_stride : 0, q_row, s_row, q_col, s_col,
                        static_cast<int64_t>(mxq_scale_bytes(rows, 32 * groups_of(cols), layout)),
                        static_cast<int64_t>(mxq_scale_bytes(cols, 32 * groups_of(rows), layout)),
-                       layout == MXQ_SCALE_MMA_TILED, nullptr, 0, 0};
+                       layout == MXQ_SCALE_MMA_TILED, nullptr, 0, 0, sms};
     return from_cuda(launch_quant_mxfp4(a, dtype == MXQ_F32, cu(stream)));
 }
 
@@ -70,9 +71,10 @@ mxq_status mxq_quant_mxfp4_grouped(const void* x, mxq_dtype dtype, int64_t rows,
     if (!x || !group_offsets || !q || !s || !aligned(x, size_of(dtype)) || !aligned(group_offsets, 8) || !aligned(q, 16) ||
         !aligned(s, 16))
         return MXQ_ERR_INVALID_ARG;
-    const mxq_status st = device_ok();
+    int sms = 0;
+    const mxq_status st = device_ok(&sms);
     if (st != MXQ_OK) return st;
-    const Quant4Args a{x, 1, rows, cols, ld, 0, q, s, nullptr, nullptr, 0, 0, true, group_offsets, G, bands_cap};
+    const Quant4Args a{x, 1, rows, cols, ld, 0, q, s, nullptr, nullptr, 0, 0, true, group_offsets, G, bands_cap, sms};
     return from_cuda(launch_quant_mxfp4(a, dtype == MXQ_F32, cu(stream)));
 }
 
@@ -88,9 +90,10 @@ mxq_status mxq_quant_mxfp4_cols_grouped(const void* x, mxq_dtype dtype, int64_t 
     if (!x || !group_offsets || !q || !s || !aligned(x, size_of(dtype)) || !aligned(group_offsets, 8) || !aligned(q, 16) ||
         !aligned(s, 16))
         return MXQ_ERR_INVALID_ARG;
-    const mxq_status st = device_ok();
+    int sms = 0;
+    const mxq_status st = device_ok(&sms);
     if (st != MXQ_OK) return st;
-    const Quant4Args a{x, 1, rows, cols, ld, 0, nullptr, nullptr, q, s, 0, 0, true, group_offsets, G, capacity / 128};
+    const Quant4Args a{x, 1, rows, cols, ld, 0, nullptr, nullptr, q, s, 0, 0, true, group_offsets, G, capacity / 128, sms};
     return from_cuda(launch_quant_mxfp4(a, dtype == MXQ_F32, cu(stream)));
 }
 

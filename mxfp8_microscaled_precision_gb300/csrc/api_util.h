@@ -27,6 +27,11 @@ inline mxq_status device_ok() {
     return yes ? MXQ_OK : MXQ_ERR_UNSUPPORTED_DEVICE;
 }
 
+inline mxq_status device_ok(int* sms) {
+    if (current_device_sms(sms) != cudaSuccess) return MXQ_ERR_CUDA;
+    return *sms > 0 ? MXQ_OK : MXQ_ERR_UNSUPPORTED_DEVICE;
+}
+
 // The runtime keeps an error for the next cudaGetLastError: it is taken here, or it would be read as that
 // of a later call's launch.
 inline mxq_status from_cuda(cudaError_t e) {

@@ -19,7 +19,7 @@ namespace mxq {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kFewTiles = 2 * 152;   // two on each SM
+constexpr int kFewTiles = 2;   // on each SM
 constexpr int kThreads = 256;
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
@@ -219,10 +219,10 @@ __device__ __forceinline__ bool is_whole(int64_t rows, int64_t cols, int64_t r0,
 constexpr int kColTile = 256;
 template <typename T>
 constexpr int kRowTile = 128 / static_cast<int>(sizeof(T));
-// Few rows: blocks of 8 rows, a row a warp, as long as one wave holds them (8 blocks on each of 152 SMs).  Such calls are
+// Few rows: blocks of 8 rows, a row a warp, as long as one wave holds them (8 blocks on each SM, of which GB300 has 152).  Such calls are
 // bound by latency, the fetching of instructions in it.  Measured, tall blocks / these (us, in a graph): 1 x 7168 BF16
 // 2.4 / 1.4, 64 x 4096 2.5 / 1.5, 64 x 4099 5.1 / 1.8, 512 x 4096 3.8 / 2.9, 1024 x 4096 (two waves) 3.9 / 4.6.
-constexpr int kFewRows = 8, kFewBlocks = 8 * 152;
+constexpr int kFewRows = 8, kFewBlocks = 8;
 
 template <typename T, bool kVec, int kHeight>
 __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const Quant4Args a, const Shape s) {
@@ -531,7 +531,7 @@ cudaError_t launch_quant_t(const Quant4Args& a, cudaStream_t stream) {
         const int64_t tiles_c = (a.cols + kColTile - 1) / kColTile, few = (a.rows + kFewRows - 1) / kFewRows;
         // tiled scales: whole 512-byte atoms, with their padding
         const int64_t many = ((a.tiled ? (a.rows + kTile - 1) / kTile * kTile : a.rows) + kRowTile<T> - 1) / kRowTile<T>;
-        const bool is_few = a.batch * few * tiles_c <= kFewBlocks;
+        const bool is_few = a.batch * few * tiles_c <= static_cast<int64_t>(kFewBlocks) * a.sms;
         const int64_t per_batch = tiles_c * (is_few ? few : many), blocks = a.batch * per_batch;
         if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
         const Shape s{static_cast<int>(tiles_c), static_cast<int>(per_batch)};
@@ -553,7 +553,7 @@ cudaError_t launch_quant_t(const Quant4Args& a, cudaStream_t stream) {
         return launch_behind(quant_tile_kernel<T, true, kVec, false, kNT>, grid, kNT, kShared, stream, a, s);
     };
     if constexpr (sizeof(T) == 4) {
-        if (blocks <= kFewTiles) return go(std::integral_constant<int, 512>{});
+        if (blocks <= static_cast<int64_t>(kFewTiles) * a.sms) return go(std::integral_constant<int, 512>{});
     }
     return go(std::integral_constant<int, 256>{});
 }

@@ -24,6 +24,8 @@ cudaError_t current_device_info(DeviceInfo* info);
 // Whether the current device is an sm_103 (GB300): the one question of the calls that are
 // made for single tokens, without the lookups of the above.
 cudaError_t current_device_is_supported(bool* yes);
+// The same with the device's SMs as the answer, 0 for another device.
+cudaError_t current_device_sms(int* sms);
 
 // Launches a kernel that begins with wait_for_previous(), so that its launch overlaps the end of the kernel
 // before it on the stream (clipping 6 gradients 8.7 us to 8.2 us, 16384 x 64 layer norm backward 11.2 us to 10.6 us then; letting its
@@ -243,6 +245,7 @@ struct Quant4Args {
     const int64_t* offsets;
     int G;
     int64_t bands_cap;
+    int sms;                                  // of the device
 };
 cudaError_t launch_quant_mxfp4(const Quant4Args& a, bool f32, cudaStream_t stream);
 
