@@ -946,6 +946,9 @@ int64_t clusters_of(const DeviceInfo& dev, int log_split) {
     return known[log_split];
 }
 
+// Grouped: tiles of the rows kernel at most, of the experts with rows, each with one partly filled tile.
+int64_t most_tiles(const Gemm4Args& g) { return ((g.M < g.G ? g.M : g.G) + g.M / 128) * ((g.N + 127) / 128); }
+
 template <bool kGrouped>
 cudaError_t launch_rows(const DeviceInfo& dev, const Gemm4Args& g, Args args, cudaStream_t stream) {
     using L = RowsCfg;
@@ -955,8 +958,7 @@ cudaError_t launch_rows(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
     const int64_t row_bytes = args.k_padded / 2, experts = kGrouped ? g.G : 1;
     RowsMaps maps;
     const int64_t m_tiles = (g.M + 127) / 128, n_tiles = (g.N + 127) / 128;
-    // tiles, at most: grouped, of the experts with rows, each with one partly filled tile
-    const int64_t tiles = (kGrouped ? (g.M < g.G ? g.M : g.G) + g.M / 128 : m_tiles) * n_tiles;
+    const int64_t tiles = kGrouped ? most_tiles(g) : m_tiles * n_tiles;
     if (tiles > kMostItems) return cudaErrorInvalidValue;
     args.items = static_cast<int>(tiles);
     args.m_tiles = static_cast<int>(m_tiles);
@@ -997,14 +999,28 @@ cudaError_t launch_rows(const DeviceInfo& dev, const Gemm4Args& g, Args args, cu
 // Output rows that do not start on 16 bytes cost the pairs up to 1 us more and the rows kernel nothing: 777 x 2085 (K 1003)
 // 7.8 / 8.2, 300 x 4099 (K 4096) 10.5 / 11.3, 777 x 1003 (K 300) 7.3 / 7.4, (K 2085) 9.5 / 9.2, but 2000 x 2085 (K 1003), two
 // waves of tiles, 11.9 / 8.4.
-// Grouped, 4096 x 4096: 128 experts of unequal loads, 16 rows each 182 / 185, 32: 194 / 195, 64: 219 / 209, 256: 395 / 295;
-// 8 experts, 32 rows each 13 / 18, 128: 22 / 19.
+// Grouped, up to 48 rows an expert the rows kernel, past that as for a dense product, of the most tiles that the rows can make.
+// Rows an expert, experts of equal loads:
+//   experts of N x K      64             128            256            512
+//   1 of 4096 x 4096      7.4 / 13.4     10.1 / 13.6    11.2 / 10.6    11.3 / 10.7
+//   1 of 2048 x 2048      6.5 / 8.3      7.8 / 8.4      9.1 / 8.4      9.3 / 8.5
+//   1 of 1024 x 7168      7.2 / 13.8     9.3 / 13.9     9.4 / 14.4     11.4 / 14.0
+//   4 of 1024 x 7168      9.9 / 13.7     11.7 / 13.9    14.2 / 13.9    14.5 / 14.1
+//   4 of 768 x 4096       7.5 / 10.5     10.2 / 10.6    10.4 / 10.6    11.3 / 10.7
+//   8 of 4096 x 4096      14.2 / 16.8    17.6 / 17.3    28.7 / 17.8    48.3 / 31.1
+//   16 of 2048 x 2048     10.4 / 12.0    14.2 / 12.1    23.1 / 12.2    37.3 / 19.3
+//   128 of 4096 x 4096    193 / 209      209 / 220      343 / 232      633 / 394
+//   128 of 4096 x 1024    80 / 72        131 / 76       255 / 103      505 / 145
+// and with loads as 1, 2^-1.1, 3^-1.1, ..:
+//   128 of 4096 x 4096    225 / 227      278 / 257      398 / 326      657 / 475
+//   32 of 4096 x 4096     61 / 61        74 / 68        106 / 82       173 / 115
+//   8 of 1024 x 7168      14.1 / 14.1    14.2 / 14.2    14.5 / 14.3    22.4 / 15.2
+// 48 rows: between 10% for the rows kernel (equal loads) and 10% for pairs (unequal ones of 128 x 4096 x 1024).
 template <bool kGrouped>
 bool fills_pairs(const DeviceInfo& dev, const Gemm4Args& g) {
-    if (kGrouped) return g.M > 48 * static_cast<int64_t>(g.G);
-    if (g.M <= 64) return false;
-    const int64_t tiles = ((g.M + 127) / 128) * ((g.N + 127) / 128);
-    if (!whole_rows(g)) return tiles > dev.sm_count;
+    if (g.M <= (kGrouped ? 48 * static_cast<int64_t>(g.G) : 64)) return false;
+    const int64_t tiles = kGrouped ? most_tiles(g) : ((g.M + 127) / 128) * ((g.N + 127) / 128);
+    if (!kGrouped && !whole_rows(g)) return tiles > dev.sm_count;
     if (g.K >= 4096) return 2 * tiles > dev.sm_count;
     return g.K < 2048 || 4 * tiles > dev.sm_count;
 }

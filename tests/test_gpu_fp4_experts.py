@@ -42,6 +42,33 @@ def test_one_expert_is_the_dense_product(M, N, K):
     assert torch.equal(dense, (va @ vb.t()).to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("N,K", [(768, 4096), (300, 2085), (1024, 4064), (130, 4000)])
+@pytest.mark.parametrize("counts,behind", [([200], 0), ([130, 0, 1], 7), ([1, 255], 0), ([500], 30), ([0, 129, 128, 127], 0), ([300, 300], 100)])
+def test_few_experts_of_many_rows_and_long_rows(counts, behind, N, K):
+    """Few tiles, each with K split over a cluster, of experts that start and end inside a tile; rows of no expert stay."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    G, live = len(counts), sum(counts)
+    M = live + behind
+    gen = torch.Generator(device="cuda").manual_seed(M + K)
+    off = torch.tensor(np.cumsum([0] + counts), device="cuda")
+    # halves up to 6, with a 6 in each group of 32: scales of 1, values as they are
+    x, w = (torch.randint(-8, 9, (n, K), generator=gen, device="cuda").double() / 2 for n in (M, G * N))
+    x[:, ::32], w[:, ::32] = 6, 6
+    for t in (x, w):
+        t[t.abs() == 3.5] = 4.0
+        t[t.abs() == 2.5] = 2.0
+    y = torch.full((M, N + 8), 9.0, dtype=torch.bfloat16, device="cuda")
+    x[live:] = float("inf")
+    q = mxq.quant_mxfp4_grouped(x.bfloat16(), off)
+    wq, ws, _, _ = mxq.quant_mxfp4(w.bfloat16().view(G, N, K), col=False)
+    mxq.grouped_gemm_mxfp4(*q, wq, ws, off, N, K, out=y[:, :N])
+    assert bool((y[live:] == 9).all()) and bool((y[:, N:] == 9).all())
+    for g, n in enumerate(counts):
+        lo = int(off[g])
+        assert torch.equal(y[lo:lo + n, :N], (x[lo:lo + n] @ w[g * N:(g + 1) * N].t()).to(torch.bfloat16))
+    assert mxq.get_device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("counts,behind,N,K", [([1, 0, 2], 1, 64, 96), ([48, 48, 0], 0, 130, 515), ([100, 49, 3], 5, 257, 320),
                                                ([0, 0, 300], 40, 1000, 77), ([700, 1, 0], 0, 520, 1024)])
