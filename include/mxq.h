@@ -745,7 +745,8 @@ mxq_status mxq_quant_mxfp4_cols_grouped(const void* x, mxq_dtype dtype, int64_t 
 /*
  * The values that a payload [rows, cols] and its scales (one per 32 elements of a row) stand for:
  * out = q * 2^(s - 127), NaN where the scale is 0xFF.  E2M1, E4M3 and E5M2 payloads, those of
- * this library's quantizers and of mxq_activation among them.
+ * this library's quantizers and of mxq_activation among them.  What mxq_quant_mxfp4_grouped made, one expert at a time: its
+ * rows of q, and s from its first band on.
  *
  * ldq   row stride of q in bytes (E2M1: at least 16 * ceil(cols/32), q 4-byte aligned and ldq a multiple of 4).
  * lds   row stride of plain scales (at least ceil(cols/32)); ignored for tiled ones.

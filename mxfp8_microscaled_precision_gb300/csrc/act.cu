@@ -10,10 +10,12 @@
 // element of a group, a warp several groups, so that its accesses are contiguous wherever a row starts.
 // Arithmetic in FP32, one rounding.
 //
-// 131072 x 2 x 2048 BF16, SiLU with a gate: 351 us forward (91% of the copy rate), 228 us without a checkpoint, 385 us
-// backward; GELU 423, 271 and 419 us (forward by its instructions).  Rows of 2047: 652, 286 and 717 us, the checkpoint
-// by single bytes.  Tried there without gain: eight elements a lane from shifted vectors, results through shared memory
-// onto the 16-byte grid of their rows (673, 424 and 813 us; 4099 x 1111 FP32 GELU forward 14.8 us instead of 14.6 us).
+// 131072 x 2 x 2048 BF16, SiLU with a gate: 351 us forward (91% of the copy rate), 228 us without a checkpoint, 386 us
+// backward; GELU 423, 271 and 425 us (forward by its instructions).  65536 x 2 x 2048 FP32: SiLU 270, 226 and 371 us, GELU 272, 226
+// and 359 us (the copy rate, but for SiLU backward, 96%).  BF16 rows of 2047: 652, 286 and 717 us, the checkpoint
+// by single bytes; FP32 SiLU 364, 227 and 466 us.  Tried on such rows without gain: eight elements a lane from shifted vectors, results
+// through shared memory onto the 16-byte grid of their rows (673, 424 and 813 us; 4099 x 1111 FP32 GELU forward 14.8 us when the
+// kernel took 14.6 us, now 12.6).
 
 #include <cuda_runtime.h>
 

@@ -205,8 +205,6 @@ __device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bul
 // Until the issuing thread's bulk groups have read their shared-memory sources.
 __device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
-// Until at most one of them has not.
-
 // Until the issuing thread's bulk groups have completed.
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 

@@ -28,8 +28,9 @@ cudaError_t current_device_is_supported(bool* yes);
 cudaError_t current_device_sms(int* sms);
 
 // Launches a kernel that begins with wait_for_previous(), so that its launch overlaps the end of the kernel
-// before it on the stream (clipping 6 gradients 8.7 us to 8.2 us, 16384 x 64 layer norm backward 11.2 us to 10.6 us then; letting its
-// blocks start before that end changes nothing more).
+// before it on the stream (clipping 6 gradients 8.7 us to 8.2 us, 16384 x 64 layer norm backward 11.2 us to 10.6 us then).  Letting its
+// blocks start before that end changes nothing more for these; the quantizers of MXFP4 do (let_next_start), for the products
+// behind them.
 template <typename... Params>
 inline cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, unsigned block, unsigned shared,
                                  cudaStream_t stream, const std::remove_cv_t<Params>&... args) {

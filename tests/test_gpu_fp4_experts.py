@@ -94,3 +94,20 @@ def test_input_gradients(counts, behind, N, K, dtype):
             ref, size = d[lo:lo + n] @ v.t(), d[lo:lo + n].abs() @ v.abs().t()
             assert bool(((dx[lo:lo + n, :K].double() - ref).abs() <= (N / 32 + 64) * 2.0 ** -22 * size + 2.0 ** -8 * ref.abs()).all())
     assert mxq.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("counts,K", [([3, 0, 70, 128], 96), ([129, 300, 1], 515), ([0, 40], 1000)])
+def test_values_of_one_experts_rows(counts, K, dtype):
+    """A payload with scales by expert, read back an expert at a time: its rows, and the scales from its first band on."""
+    from mxfp8_microscaled_precision_gb300 import mxq
+    off = torch.tensor(np.cumsum([0] + counts), device="cuda")
+    x = torch.randn(sum(counts), K, device="cuda").to(dtype)
+    q, s = mxq.quant_mxfp4_grouped(x, off)
+    atoms = -(-K // 128) * 512
+    for g, n in enumerate(counts):
+        lo = int(off[g])
+        first = lo // 128 + g
+        want = mxq.quant_mxfp4(x[lo:lo + n], col=False, layout="rowmajor")[:2]
+        got = mxq.dequant_1x32(q[lo:lo + n], s[first * atoms:(first + -(-n // 128)) * atoms], K, fmt="e2m1", dtype=torch.float32)
+        assert torch.equal(got, mxq.dequant_1x32(*want, K, fmt="e2m1", layout="rowmajor", dtype=torch.float32))
